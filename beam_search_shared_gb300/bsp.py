@@ -23,6 +23,7 @@ DTYPES = {"bf16": 0, "fp16": 1, torch.bfloat16: 0, torch.float16: 1}
 FLAG_LSE_BASE2 = 1
 FLAG_CHECK = 2
 FLAG_GRAPH = 4
+FLAG_ACCUMULATE = 8
 MAX_TAIL = 8
 MAX_GROUP = 8
 STATUS_BYTES = 256  # device status words ahead of the plan image in the workspace
@@ -66,12 +67,28 @@ class RopeConfig(ctypes.Structure):
                 ("interleaved", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class TokenMask(ctypes.Structure):
+    _fields_ = [("bits", ctypes.c_void_p), ("stride", ctypes.c_int64), ("index", ctypes.c_void_p),
+                ("rows", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class _LogitsParams(ctypes.Structure):
+    _fields_ = [("prompt_tokens", ctypes.c_void_p), ("prompt_len", ctypes.c_void_p), ("prompt_stride", ctypes.c_int64),
+                ("tokens", ctypes.c_void_p), ("token_len", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("bias_tokens", ctypes.c_void_p), ("bias_values", ctypes.c_void_p), ("bias_len", ctypes.c_void_p),
+                ("bias_stride", ctypes.c_int64), ("repetition_penalty", ctypes.c_void_p),
+                ("frequency_penalty", ctypes.c_void_p), ("presence_penalty", ctypes.c_void_p),
+                ("temperature", ctypes.c_void_p), ("mask", TokenMask), ("prompt_cols", ctypes.c_int32),
+                ("token_cols", ctypes.c_int32), ("bias_cols", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 _lib = None
 EXPORTS = ["bsp_status_string", "bsp_bucket_rows", "bsp_workspace_size", "bsp_plan_build", "bsp_plan",
            "bsp_append_kv", "bsp_decode_attn", "bsp_read_device_status", "bsp_decode_attn_noalloc",
            "bsp_plan_prefill_build", "bsp_plan_prefill", "bsp_prefill_attn", "bsp_rope_cos_sin",
            "bsp_rope_append_kv", "bsp_append_kv_fp8", "bsp_rope_append_kv_fp8", "bsp_plan_update_tails",
-           "bsp_decode_attn_fp8"]
+           "bsp_decode_attn_fp8", "bsp_process_logits", "bsp_beam_select_workspace_size", "bsp_beam_select",
+           "bsp_beam_advance", "bsp_key_weights", "bsp_key_weights_fp8", "bsp_evict_prefix"]
 NOALLOC_SCRATCH_MIB = 32
 
 
@@ -135,6 +152,20 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
     lib.bsp_decode_attn_noalloc.restype = i32
     lib.bsp_decode_attn_noalloc.argtypes = [P(Geometry), i32, i32, vp, vp, vp, i32, i32, vp, vp, vp, vp, i32, vp, i32,
                                             ctypes.c_float, i32, vp, vp, vp]
+    lib.bsp_process_logits.restype = i32
+    lib.bsp_process_logits.argtypes = [P(Plan), vp, i32, i64, i32, P(_LogitsParams), vp, i64, vp, vp]
+    lib.bsp_beam_select_workspace_size.restype = i32
+    lib.bsp_beam_select_workspace_size.argtypes = [i32, i32, i32, i32, P(sz)]
+    lib.bsp_beam_select.restype = i32
+    lib.bsp_beam_select.argtypes = [P(Plan), vp, i32, i64, i32, vp, vp, i64, P(TokenMask), i32, vp, vp, vp, vp, sz, vp]
+    lib.bsp_beam_advance.restype = i32
+    lib.bsp_beam_advance.argtypes = [P(Plan), vp, vp, i64, vp, vp, i32, vp, vp, i64, i32, vp, vp]
+    lib.bsp_key_weights.restype = i32
+    lib.bsp_key_weights.argtypes = [P(Plan), vp, vp, vp, f32, i32, i32, vp, i64, vp]
+    lib.bsp_key_weights_fp8.restype = i32
+    lib.bsp_key_weights_fp8.argtypes = [P(Plan), vp, vp, vp, f32, f32, i32, i32, vp, i64, vp]
+    lib.bsp_evict_prefix.restype = i32
+    lib.bsp_evict_prefix.argtypes = [P(Plan), vp, i64, vp, vp, i32, i32, vp, vp, vp, vp, vp, i64, vp]
     _lib = lib
     return lib
 
@@ -438,3 +469,244 @@ def decode_attn_noalloc(geo: Geometry, batch, beam_width, prefix_len, tail_len, 
         ctypes.byref(geo), int(batch), int(beam_width), _ptr(pl), _ptr(tl), _ptr(pp), pp.shape[1], int(max_tail),
         _dptr(q), _dptr(k_pool), _dptr(v_pool), _dptr(beam_pages), bps, _dptr(cache_indirection), max_seq,
         float(softmax_scale), int(flags), _dptr(o), _dptr(lse), _stream(stream)))
+
+
+# ---------------------------------------------------------------- around the attention of a step
+
+LOGITS_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _table(name: str, t: torch.Tensor, dtype, shape, exact_last: bool = True):
+    """Checks a table's type and shape (None: any extent) and that its rows are contiguous and evenly spaced;
+    returns the row stride in elements."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} is {t.dtype}, not {dtype}")
+    n = t.dim()
+    if n != len(shape) or any(w is not None and (t.shape[i] != w if exact_last or i < n - 1 else t.shape[i] < w)
+                              for i, w in enumerate(shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the rows of {name} are not contiguous")
+    # the stride of a dimension of one entry says nothing: torch leaves it arbitrary
+    steps = [(t.stride(i), t.shape[i]) for i in range(n - 1) if t.shape[i] > 1]
+    for (outer, _), (inner, count) in zip(steps, steps[1:]):
+        if outer != inner * count:
+            raise ValueError(f"the rows of {name} are not evenly spaced")
+    return steps[-1][0] if steps else t.shape[-1]
+
+
+def token_mask(bits: Optional[torch.Tensor], index: Optional[torch.Tensor]) -> TokenMask:
+    """Grammar masks: ``bits`` int32 [states, words] (bit t % 32 of word t // 32: token t is allowed), ``index``
+    int32 [batch * beam_width], the row's state or -1."""
+    if bits is None:
+        return TokenMask()
+    stride = _table("mask", bits, torch.int32, (None, None))
+    if index is None:
+        raise ValueError("a mask needs mask_index")
+    _table("mask_index", index, torch.int32, (None,))
+    return TokenMask(bits.data_ptr(), stride, index.data_ptr(), bits.shape[0], 0)
+
+
+class LogitsParams:
+    """What ``process_logits`` does to a row, checked once; tensors' contents may change between calls, the
+    tensors may not. prompt_tokens int32 [batch, n] with prompt_token_len [batch]; tokens int32
+    [batch * beam_width, n] with token_len [batch * beam_width]; bias_tokens int32 and bias_values fp32
+    [batch, n], bias_len int32 [batch] or None (all n); penalties and temperature fp32 [batch]; mask,
+    mask_index as ``token_mask``. None leaves a step out."""
+
+    def __init__(self, prompt_tokens=None, prompt_token_len=None, tokens=None, token_len=None,
+                 repetition_penalty=None, frequency_penalty=None, presence_penalty=None, temperature=None,
+                 bias_tokens=None, bias_values=None, bias_len=None, mask=None, mask_index=None):
+        c = _LogitsParams()
+        i32, f32 = torch.int32, torch.float32
+        self.batch, self.rows = None, None
+
+        def lead(what, n):
+            old = getattr(self, what)
+            if old is not None and old != n:
+                raise ValueError(f"lists for {n} and for {old} {what}")
+            setattr(self, what, n)
+
+        for name, t, lens, what in (("prompt_tokens", prompt_tokens, prompt_token_len, "batch"),
+                                    ("tokens", tokens, token_len, "rows")):
+            if t is None:
+                continue
+            short = "prompt" if what == "batch" else "token"
+            setattr(c, short + "_stride", _table(name, t, i32, (None, None)))
+            setattr(c, short + "_cols", t.shape[1])
+            if lens is None:
+                raise ValueError(f"{name} need their lengths")
+            _table(short + "_len", lens, i32, (t.shape[0],))
+            lead(what, t.shape[0])
+            setattr(c, name, t.data_ptr())
+            setattr(c, short + "_len", lens.data_ptr())
+        if bias_tokens is not None:
+            c.bias_stride = _table("bias_tokens", bias_tokens, i32, (None, None))
+            if bias_values is None or _table("bias_values", bias_values, f32, tuple(bias_tokens.shape)) != c.bias_stride:
+                raise ValueError("bias_values must be laid out as bias_tokens")
+            lead("batch", bias_tokens.shape[0])
+            c.bias_cols = bias_tokens.shape[1]
+            c.bias_tokens, c.bias_values = bias_tokens.data_ptr(), bias_values.data_ptr()
+            if bias_len is not None:
+                _table("bias_len", bias_len, i32, (bias_tokens.shape[0],))
+                c.bias_len = bias_len.data_ptr()
+        for name, t in (("repetition_penalty", repetition_penalty), ("frequency_penalty", frequency_penalty),
+                        ("presence_penalty", presence_penalty), ("temperature", temperature)):
+            if t is not None:
+                _table(name, t, f32, (None,))
+                lead("batch", t.shape[0])
+                setattr(c, name, t.data_ptr())
+        if mask is not None:
+            c.mask = token_mask(mask, mask_index)
+            lead("rows", mask_index.shape[0])
+            self.mask_tokens = 32 * mask.shape[1]
+        else:
+            self.mask_tokens = None
+        self.c = c
+        self._keep = (prompt_tokens, prompt_token_len, tokens, token_len, repetition_penalty, frequency_penalty,
+                      presence_penalty, temperature, bias_tokens, bias_values, bias_len, mask, mask_index)
+
+
+def process_logits(plan_: Plan, logits: torch.Tensor, params: LogitsParams, out: Optional[torch.Tensor] = None,
+                   lse: Optional[torch.Tensor] = None, stream=None):
+    """bsp_process_logits: logits [batch * beam_width, vocab] (bf16, fp16 or fp32) into ``out`` (None: in place),
+    and each processed row's log-sum-exp into lse fp32 [batch * beam_width]."""
+    rows = plan_.total_rows
+    out = logits if out is None else out
+    if logits.dtype not in LOGITS_DTYPES:
+        raise ValueError(f"logits are {logits.dtype}")
+    stride = _table("logits", logits, logits.dtype, (rows, None))
+    out_stride = stride if out is logits else _table("out", out, logits.dtype, tuple(logits.shape))
+    if params.rows not in (None, rows) or params.batch not in (None, plan_.batch):
+        raise ValueError(f"lists for {params.batch} requests and {params.rows} rows, a plan of {plan_.batch} and {rows}")
+    if params.mask_tokens is not None and params.mask_tokens < logits.shape[1]:
+        raise ValueError(f"a mask of {params.mask_tokens} tokens for a vocabulary of {logits.shape[1]}")
+    if lse is not None:
+        _table("lse", lse, torch.float32, (rows,))
+    _check("bsp_process_logits", load().bsp_process_logits(
+        ctypes.byref(plan_), logits.data_ptr(), LOGITS_DTYPES[logits.dtype], stride, logits.shape[1],
+        ctypes.byref(params.c), out.data_ptr(), out_stride, _dptr(lse), _stream(stream)))
+
+
+def beam_select_workspace(batch: int, beam_width: int, vocab: int, num_candidates: int, device="cuda") -> torch.Tensor:
+    """Device workspace of ``beam_select`` (bsp_beam_select_workspace_size bytes)."""
+    n = ctypes.c_size_t()
+    _check("bsp_beam_select_workspace_size", load().bsp_beam_select_workspace_size(
+        int(batch), int(beam_width), int(vocab), int(num_candidates), ctypes.byref(n)))
+    return torch.empty(max(16, n.value), dtype=torch.uint8, device=device)
+
+
+def beam_select(plan_: Plan, logits: torch.Tensor, lse: torch.Tensor, cum_scores: torch.Tensor, scores: torch.Tensor,
+                parents: torch.Tensor, tokens: torch.Tensor, workspace: torch.Tensor,
+                mask: Optional[torch.Tensor] = None, mask_index: Optional[torch.Tensor] = None, stream=None):
+    """bsp_beam_select: the best continuations of each request over its beams' vocabularies, into scores fp32,
+    parents int32 and tokens int32 [batch, num_candidates], best first. lse fp32 [batch * beam_width],
+    cum_scores fp32 [batch, beam_width] (or wider rows, the first beam_width read)."""
+    rows, batch = plan_.total_rows, plan_.batch
+    if logits.dtype not in LOGITS_DTYPES:
+        raise ValueError(f"logits are {logits.dtype}")
+    stride = _table("logits", logits, logits.dtype, (rows, None))
+    _table("lse", lse, torch.float32, (rows,))
+    cum_stride = _table("cum_scores", cum_scores, torch.float32, (batch, plan_.beam_width), exact_last=False)
+    num = scores.shape[-1]
+    for name, t, dt in (("scores", scores, torch.float32), ("parents", parents, torch.int32),
+                        ("tokens", tokens, torch.int32)):
+        if _table(name, t, dt, (batch, num)) != num:
+            raise ValueError(f"{name} must be contiguous")
+    m = None
+    if mask is not None:
+        m = token_mask(mask, mask_index)
+        if 32 * mask.shape[1] < logits.shape[1] or mask_index.shape[0] != rows:
+            raise ValueError("the mask does not cover the vocabulary, or its index the rows")
+        m = ctypes.byref(m)
+    _check("bsp_beam_select", load().bsp_beam_select(
+        ctypes.byref(plan_), logits.data_ptr(), LOGITS_DTYPES[logits.dtype], stride, logits.shape[1], lse.data_ptr(),
+        cum_scores.data_ptr(), cum_stride, m, num, scores.data_ptr(), parents.data_ptr(), tokens.data_ptr(),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def beam_advance(plan_: Plan, parents: torch.Tensor, chosen: torch.Tensor,
+                 cache_indirection: Optional[torch.Tensor] = None, cache_indirection_out: Optional[torch.Tensor] = None,
+                 tokens: Optional[torch.Tensor] = None, tokens_out: Optional[torch.Tensor] = None,
+                 token_len: Optional[torch.Tensor] = None, stream=None):
+    """bsp_beam_advance: cache_indirection int32 [batch, beam_width, max_seq] and tokens int32
+    [batch * beam_width, n] re-ordered by the chosen parents and extended by the new position (outputs None: in
+    place). parents, chosen: int32 [batch, >= beam_width], the first beam_width of a row read."""
+    batch, W, rows = plan_.batch, plan_.beam_width, plan_.total_rows
+    i32 = torch.int32
+    stride = _table("parents", parents, i32, (batch, W), exact_last=False)
+    if _table("chosen", chosen, i32, (batch, W), exact_last=False) != stride:
+        raise ValueError("parents and chosen must have the same row stride")
+    max_seq = token_stride = token_cols = 0
+    if cache_indirection is not None:
+        cache_indirection_out = cache_indirection if cache_indirection_out is None else cache_indirection_out
+        max_seq = cache_indirection.shape[-1]
+        for name, t in (("cache_indirection", cache_indirection), ("cache_indirection_out", cache_indirection_out)):
+            if _table(name, t, i32, (batch, W, max_seq)) != max_seq:
+                raise ValueError(f"{name} must be contiguous")
+    if tokens is not None:
+        tokens_out = tokens if tokens_out is None else tokens_out
+        token_cols = tokens.shape[-1]
+        token_stride = _table("tokens", tokens, i32, (rows, None))
+        if _table("tokens_out", tokens_out, i32, tuple(tokens.shape)) != token_stride:
+            raise ValueError("tokens and tokens_out must have the same row stride")
+    if token_len is not None:
+        _table("token_len", token_len, i32, (rows,))
+    _check("bsp_beam_advance", load().bsp_beam_advance(
+        ctypes.byref(plan_), parents.data_ptr(), chosen.data_ptr(), stride, _dptr(cache_indirection),
+        _dptr(cache_indirection_out), max_seq, _dptr(tokens), _dptr(tokens_out), token_stride, token_cols,
+        _dptr(token_len), _stream(stream)))
+
+
+def _key_table(plan_: Plan, name: str, t: torch.Tensor, dtype):
+    return _table(name, t, dtype, (plan_.batch, plan_.geo.num_kv_heads, plan_.max_prefix_len), exact_last=False)
+
+
+def _rows_ok(plan_: Plan, q: torch.Tensor, lse: torch.Tensor):
+    want = torch.bfloat16 if plan_.geo.dtype == 0 else torch.float16
+    if q.dtype != want or q.numel() != plan_.total_rows * plan_.geo.num_q_heads * plan_.geo.head_dim or not q.is_contiguous():
+        raise ValueError(f"q must be contiguous {want} [{plan_.total_rows}, {plan_.geo.num_q_heads}, {plan_.geo.head_dim}]")
+    if lse.dtype != torch.float32 or lse.numel() != plan_.total_rows * plan_.geo.num_q_heads or not lse.is_contiguous():
+        raise ValueError(f"lse must be contiguous fp32 [{plan_.total_rows}, {plan_.geo.num_q_heads}]")
+
+
+def key_weights(plan_: Plan, q: torch.Tensor, k_pool: torch.Tensor, lse: torch.Tensor, softmax_scale: float,
+                weights: torch.Tensor, window: int = 0, flags: int = 0, stream=None):
+    """bsp_key_weights: the attention weight each prompt key received from the plan's query rows, into weights
+    fp32 [batch, num_kv_heads, >= longest prompt] (flags FLAG_ACCUMULATE: added to it)."""
+    _rows_ok(plan_, q, lse)
+    stride = _key_table(plan_, "weights", weights, torch.float32)
+    _check("bsp_key_weights", load().bsp_key_weights(
+        ctypes.byref(plan_), q.data_ptr(), k_pool.data_ptr(), lse.data_ptr(), float(softmax_scale), int(window),
+        int(flags), weights.data_ptr(), stride, _stream(stream)))
+
+
+def key_weights_fp8(plan_: Plan, q: torch.Tensor, k_pool: torch.Tensor, lse: torch.Tensor, softmax_scale: float,
+                    k_scale: float, weights: torch.Tensor, window: int = 0, flags: int = 0, stream=None):
+    """bsp_key_weights_fp8: key_weights over a uint8 E4M3 pool (key = code x k_scale)."""
+    _rows_ok(plan_, q, lse)
+    stride = _key_table(plan_, "weights", weights, torch.float32)
+    _check("bsp_key_weights_fp8", load().bsp_key_weights_fp8(
+        ctypes.byref(plan_), q.data_ptr(), k_pool.data_ptr(), lse.data_ptr(), float(softmax_scale), float(k_scale),
+        int(window), int(flags), weights.data_ptr(), stride, _stream(stream)))
+
+
+def evict_prefix(plan_: Plan, weights: torch.Tensor, keep_len: torch.Tensor, sinks: int, recent: int,
+                 k_pool: torch.Tensor, v_pool: torch.Tensor, kept: torch.Tensor,
+                 positions: Optional[torch.Tensor] = None, weights_out: Optional[torch.Tensor] = None,
+                 positions_out: Optional[torch.Tensor] = None, stream=None):
+    """bsp_evict_prefix: per (request, kv head) the keep_len[b] rows of largest weight move to the front of the
+    request's pages, in place. weights fp32, positions and kept int32 [batch, num_kv_heads, >= longest prompt]."""
+    i32 = torch.int32
+    stride = _key_table(plan_, "weights", weights, torch.float32)
+    out_stride = _key_table(plan_, "kept", kept, i32)
+    _table("keep_len", keep_len, i32, (plan_.batch,))
+    if positions is not None and _key_table(plan_, "positions", positions, i32) != stride:
+        raise ValueError("positions must have the row stride of weights")
+    for name, t, dt in (("weights_out", weights_out, torch.float32), ("positions_out", positions_out, i32)):
+        if t is not None and _key_table(plan_, name, t, dt) != out_stride:
+            raise ValueError(f"{name} must have the row stride of kept")
+    _check("bsp_evict_prefix", load().bsp_evict_prefix(
+        ctypes.byref(plan_), weights.data_ptr(), stride, _dptr(positions), keep_len.data_ptr(), int(sinks), int(recent),
+        k_pool.data_ptr(), v_pool.data_ptr(), kept.data_ptr(), _dptr(weights_out), _dptr(positions_out), out_stride,
+        _stream(stream)))

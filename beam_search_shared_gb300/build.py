@@ -11,8 +11,11 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libbsp.so")
-SOURCES = ["bsp_host.cpp", "bsp_append.cu", "bsp_rope.cu", "bsp_tail.cu", "bsp_prefix.cu", "bsp_wide.cu", "bsp_alt.cu", "bsp_noalloc.cu"]
-HEADERS = ["bsp_internal.h", "bsp_ptx.cuh", "bsp_prompt.cuh", "bsp_write.h"]
+SOURCES = ["bsp_host.cpp", "bsp_append.cu", "bsp_rope.cu", "bsp_tail.cu", "bsp_prefix.cu", "bsp_wide.cu", "bsp_alt.cu", "bsp_noalloc.cu",
+           "bsp_step.cpp", "bsp_logits.cu", "bsp_beams.cu", "bsp_weights.cu", "bsp_evict.cu"]
+# built without fast-math: their stored results are single IEEE operations in a fixed order
+EXACT_MATH = {"bsp_logits.cu", "bsp_beams.cu", "bsp_weights.cu", "bsp_evict.cu"}
+HEADERS = ["bsp_internal.h", "bsp_ptx.cuh", "bsp_prompt.cuh", "bsp_topk.cuh", "bsp_write.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -48,7 +51,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
-        extra = ["-use_fast_math", "-Xptxas", "-v"] if src.endswith(".cu") else []
+        extra = ["-Xptxas", "-v"] if src.endswith(".cu") else []
+        if extra and src not in EXACT_MATH:
+            extra = ["-use_fast_math"] + extra
         cmd = [nvcc] + common + extra + ["-c", os.path.join(CSRC, src), "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:

@@ -91,12 +91,18 @@ bool plan_is_current(const bsp_plan_t* plan) {
            hdr->ws_device == reinterpret_cast<uint64_t>(plan->ws_device);
 }
 
+}  // namespace
+
+namespace bsp {
 bsp_status check_plan(const bsp_plan_t* plan) {
     if (!plan) return BSP_ERR_INVALID_ARG;
     if (plan->generation == 0 || !plan->ws_device || !plan->ws_host) return BSP_ERR_INVALID_ARG;
     if (!plan_is_current(plan)) return BSP_ERR_STALE_PLAN;
     return check_geometry(&plan->geo);
 }
+}  // namespace bsp
+
+namespace {
 
 // Device memory (or managed) pointer, 16-byte aligned.
 bool device_ptr_ok(const void* p) {
@@ -121,10 +127,13 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     return fn;
 }
 
+}  // namespace
+
+namespace bsp {
 // A tiled tensor map of 16-bit elements with 128-byte swizzle (the MMA operand layout), or with
 // e4m3 = true of one-byte elements without swizzle (E4M3 tiles that the kernel widens itself).
 bool encode_map(CUtensorMap* m, int dtype, int rank, const void* base, const cuuint64_t* dims,
-                const cuuint64_t* strides_bytes, const cuuint32_t* box, bool e4m3 = false) {
+                const cuuint64_t* strides_bytes, const cuuint32_t* box, bool e4m3) {
     auto enc = tensor_map_encoder();
     if (!enc) return false;
     cuuint32_t es[3] = {1, 1, 1};
@@ -136,6 +145,9 @@ bool encode_map(CUtensorMap* m, int dtype, int rank, const void* base, const cuu
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
+}  // namespace bsp
+
+namespace {
 
 // Records a timing event; under stream capture it becomes an external event-record node.
 bool record_event(void* const* events, int i, cudaStream_t s) {

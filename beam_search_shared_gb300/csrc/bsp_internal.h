@@ -153,6 +153,123 @@ cudaError_t launch_alt(int head_dim, bool bf16, int ctas, const CUtensorMap& tq,
 cudaError_t prepare_wide(int head_dim, bool bf16, bool fp8 = false);
 cudaError_t launch_wide(int head_dim, bool bf16, int ctas, const CUtensorMap& tq, const CUtensorMap& tk,
                         const CUtensorMap& tv, const PrefixParams& p, cudaStream_t stream, bool fp8 = false);
+// ---------------------------------------------------------------- the operators around a step (bsp_step.cpp)
+
+// Whether the plan staged now has the shape a launch was made for: a launch replayed from a CUDA graph reads
+// the lengths of the latest plan. hdr: the image header ([2] batch, [4] beam width, [6] kind).
+#ifdef __CUDACC__
+__device__ __forceinline__ bool plan_matches(const int32_t* hdr, int batch, int w, int kind) {
+    return __ldg(hdr + 2) == batch && __ldg(hdr + 4) == w && __ldg(hdr + 6) == kind;
+}
+#endif
+
+struct TokenMask {
+    const uint32_t* bits;  // [rows][stride]: bit t of a row: token t is allowed; null: no masks
+    long long stride;      // words
+    const int32_t* index;  // [query rows]: row of `bits`, -1: none
+    int rows;
+};
+
+struct ProcessParams {
+    const void* x;
+    void* out;
+    long long x_stride, out_stride;  // elements
+    float* lse;
+    const int32_t* prompt_tokens;
+    const int32_t* prompt_len;
+    const int32_t* tokens;
+    const int32_t* token_len;
+    const int32_t* bias_tokens;
+    const float* bias_values;
+    const int32_t* bias_len;
+    long long prompt_stride, token_stride, bias_stride;
+    const float *repetition, *frequency, *presence, *temperature;
+    TokenMask mask;
+    int32_t* status;
+    int vocab, W, rows, prompt_cols, token_cols, bias_cols;
+    int bitmap_words;  // words of each of the three bitmaps of a CTA's slice
+    int hash_slots;    // slots of the table of counts and biases (a power of two), 0: none
+};
+constexpr int kProcessSlotBytes = 12;
+cudaError_t launch_process(int dtype, const ProcessParams& p, int cluster, size_t smem, cudaStream_t stream);
+
+struct SelectParams {
+    const void* x;
+    long long x_stride;  // elements
+    const float* lse;
+    const float* cum;
+    long long cum_stride;
+    TokenMask mask;
+    uint64_t* part_keys;   // [batch][splits][K]
+    int32_t* part_count;   // [batch][splits]
+    float* scores;
+    int32_t* parents;
+    int32_t* tokens;
+    int32_t* status;
+    int batch, W, vocab, K, splits, segments, limit;
+};
+int select_unit_elems(int dtype);
+cudaError_t launch_select(int dtype, const SelectParams& p, cudaStream_t stream);
+
+struct AdvanceParams {
+    const int32_t* req;
+    const int32_t* plan_hdr;
+    const int32_t* parents;
+    const int32_t* chosen;
+    long long cand_stride;
+    const int32_t* ci_in;
+    int32_t* ci_out;
+    const int32_t* tok_in;
+    int32_t* tok_out;
+    int32_t* token_len;
+    int32_t* status;
+    long long tok_stride;
+    int batch, W, max_seq, tok_cols;
+    int cols;  // tail columns of both tables staged at a time
+};
+cudaError_t launch_advance(const AdvanceParams& p, cudaStream_t stream);
+
+struct WeightsParams {
+    const int32_t* req;
+    const int32_t* pages;
+    const int32_t* plan_hdr;
+    const float* lse;
+    float* weights;
+    long long stride;
+    int32_t* status;
+    int batch, plan_w, plan_kind, Hq, Hkv, G, ps_log2, num_pages, max_keys, window, accumulate;
+    int block_rows;  // beams (prompt tokens) of a Q block
+    int mma_n;       // its rows for the MMA: block_rows * G rounded up to 16
+    int q_slots, k_slots, strided;
+    float scale_log2, lse_mul;
+};
+constexpr int kWeightsBarBytes = 512;
+cudaError_t launch_weights(int head_dim, bool bf16, bool fp8, const CUtensorMap& tq, const CUtensorMap& tk,
+                           const WeightsParams& p, int ctas, size_t smem, cudaStream_t stream);
+
+struct EvictParams {
+    const int32_t* req;
+    const int32_t* pages;
+    const int32_t* plan_hdr;
+    const float* weights;
+    const int32_t* positions;
+    const int32_t* keep;
+    uint8_t* k_pool;
+    uint8_t* v_pool;
+    int32_t* kept;
+    float* weights_out;
+    int32_t* positions_out;
+    long long stride, out_stride;
+    int32_t* status;
+    int batch, plan_w, plan_kind, Hkv, ps_log2, row_bytes, max_keys, sinks, recent;
+};
+cudaError_t launch_evict(const EvictParams& p, int num_sms, cudaStream_t stream);
+
+// bsp_host.cpp, for bsp_step.cpp
+bsp_status check_plan(const bsp_plan_t* plan);
+bool encode_map(CUtensorMap* m, int dtype, int rank, const void* base, const cuuint64_t* dims,
+                const cuuint64_t* strides_bytes, const cuuint32_t* box, bool e4m3 = false);
+
 cudaError_t prepare_append();
 cudaError_t launch_append(const AppendParams& p, cudaStream_t stream);
 

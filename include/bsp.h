@@ -11,6 +11,9 @@
  *                   beams (tensor cores), each beam's own tail through
  *                   cache_indirection, and merges the two by log-sum-exp,
  *                   returning O and LSE.
+ * Around it: bsp_process_logits, bsp_beam_select and bsp_beam_advance take the
+ * step's logits to the next step's beams; bsp_key_weights and bsp_evict_prefix
+ * shorten the prompts' cache to the rows that the attention looked at.
  * The method: TensorRT-LLM PR #21738, "Add opt-in cascade attention for wide
  * beam search on KVCM V2" (description, "Solution"); the valid-prefix bound:
  * TensorRT-Model-Connect PR #2202, "prefill and decode over the cached prefix,
@@ -74,10 +77,11 @@ enum { BSP_DTYPE_BF16 = 0, BSP_DTYPE_FP16 = 1 };
    [page][kv head][slot][head_dim] layout */
 enum { BSP_KV_DTYPE_SAME = 0, BSP_KV_DTYPE_E4M3 = 1 };
 
-/* bsp_decode_attn flags */
+/* Launch flags (bsp_decode_attn, bsp_prefill_attn; bsp_key_weights takes LSE_BASE2, CHECK and ACCUMULATE) */
 enum {
     BSP_FLAG_LSE_BASE2 = 1, /* write LSE as log2-sum-exp2 instead of the natural log */
     BSP_FLAG_CHECK = 2,     /* synchronise after the launches and report device status */
+    BSP_FLAG_ACCUMULATE = 8, /* bsp_key_weights only: add to `weights` instead of writing it */
     BSP_FLAG_GRAPH = 4      /* bsp_decode_attn only, not with BSP_FLAG_CHECK: launch shapes that do not
                                depend on the plan's lengths, so that the launches may be captured in a
                                CUDA graph once and replayed after every later bsp_plan on the same
@@ -553,6 +557,172 @@ BSP_API bsp_status bsp_decode_attn_noalloc(const bsp_geometry* geo, int32_t batc
                                            const void* v_pool, const int32_t* beam_pages, int32_t beam_pages_stride,
                                            const int32_t* cache_indirection, int32_t max_seq, float softmax_scale,
                                            int32_t flags, void* o, float* lse, void* stream);
+
+/* ------------------------------------------------------------------------------------------------------
+ * Around the attention of a step: from logits to beams, and from attention weights to a shorter cache.
+ * (These entry points have no counterpart on the pages the method comes from.)
+ *
+ * These calls take the plan of the step for its batch, beam width, lengths, prompt pages and status word.
+ * They follow the conventions above: host-checkable errors return before any launch; nothing is allocated or
+ * synchronised; indices in device memory are checked by the kernels. Their logits, scores, lists and tables
+ * need the alignment of their element only (q, the pools and workspaces: 16 bytes), and every pointer must be
+ * memory of the current device (or managed memory). They may be captured into a CUDA graph: the lengths are
+ * read from the staged plan, so a replay follows later plans of the same batch and beam width (decode plans);
+ * a replay that finds a plan of another shape, or lengths past the tables it was captured with, leaves what
+ * it would write and sets BSP_DEVFLAG_GRAPH.
+ */
+
+enum { BSP_LOGITS_BF16 = 0, BSP_LOGITS_FP16 = 1, BSP_LOGITS_FP32 = 2 };
+
+#define BSP_MAX_VOCAB (1 << 21)
+#define BSP_MAX_LISTED 8192          /* token_cols (with frequency or presence penalties) + bias_cols */
+#define BSP_MAX_CANDIDATES 512       /* continuations per request of bsp_beam_select */
+#define BSP_MAX_ADVANCE_BEAMS 16384
+#define BSP_MAX_WEIGHTS_BATCH 4096
+#define BSP_MAX_EVICT_ROWS (1 << 19) /* prompt rows per request of bsp_evict_prefix */
+
+/* Grammar masks, packed: token t is allowed by state s when bit t % 32 of bits[s * stride + t / 32] is set.
+   index[r] is beam row r's state; -1 leaves the row unmasked (so does an index >= rows, which is flagged as
+   BSP_DEVFLAG_PAGE_INDEX). bits NULL: no masks. */
+typedef struct bsp_token_mask {
+    const uint32_t* bits;   /* device [rows][stride] */
+    int64_t stride;         /* words, >= ceil(vocab / 32) */
+    const int32_t* index;   /* device [batch * beam_width] */
+    int32_t rows;
+    int32_t reserved;       /* 0 */
+} bsp_token_mask;
+
+/* What bsp_process_logits does to a row. All device pointers; NULL leaves the step out. Tokens outside
+   [0, vocab) in the lists are padding and are passed over; lengths are cut to [0, cols]. */
+typedef struct bsp_logits_params {
+    const int32_t* prompt_tokens;   /* [batch][prompt_stride]: the request's prompt, shared by its beams */
+    const int32_t* prompt_len;      /* [batch] */
+    int64_t prompt_stride;
+    const int32_t* tokens;          /* [batch * beam_width][token_stride]: what the beam generated */
+    const int32_t* token_len;       /* [batch * beam_width] */
+    int64_t token_stride;
+    const int32_t* bias_tokens;     /* [batch][bias_stride]; an id given twice: its first value counts */
+    const float* bias_values;       /* [batch][bias_stride] */
+    const int32_t* bias_len;        /* [batch], or NULL: bias_cols entries each */
+    int64_t bias_stride;
+    const float* repetition_penalty; /* [batch], > 0 */
+    const float* frequency_penalty;  /* [batch] */
+    const float* presence_penalty;   /* [batch] */
+    const float* temperature;        /* [batch], > 0 */
+    bsp_token_mask mask;
+    int32_t prompt_cols, token_cols, bias_cols; /* columns of the lists */
+    int32_t reserved;               /* 0 */
+} bsp_logits_params;
+
+/*
+ * Penalties, biases, temperature and grammar masks on the logits of every beam row, with the log-sum-exp of
+ * each processed row, in one pass. In fp32, in this order, for token t of row r of request b:
+ *   1. t in the prompt or in the row's generated tokens: x = x > 0 ? x / repetition : x * repetition;
+ *   2. t generated c > 0 times: x = x - frequency * c, then x = x - presence;
+ *   3. t in the bias list: x = x + bias;
+ *   4. x = x / temperature (as the product with its rounded reciprocal);
+ *   5. t not allowed by the row's grammar state: x = -inf, whatever it was (NaN and infinities included).
+ * The result is rounded once to the logits' type. lse[r] (fp32, natural log; may be NULL) is that of the stored
+ * values: -inf for a row without a finite one, +inf with +inf in the row, NaN with a NaN.
+ *   logits, out     [batch * beam_width] rows of vocab elements, logits_stride / out_stride elements apart
+ *                   (>= vocab). out may be logits itself (same stride): only vectors that change are written
+ *                   then; any other overlap is BSP_ERR_INVALID_ARG
+ * A tensor-parallel or padded head's columns past vocab are neither read nor written.
+ */
+BSP_API bsp_status bsp_process_logits(const bsp_plan_t* plan, const void* logits, int32_t logits_dtype,
+                                      int64_t logits_stride, int32_t vocab, const bsp_logits_params* params,
+                                      void* out, int64_t out_stride, float* lse, void* stream);
+
+/*
+ * The best continuations of each request over the vocabularies of all of its beams: the num_candidates largest
+ * of
+ *   score(w, t) = fl(fl(x[b * W + w][t] - lse[b * W + w]) + cum_scores[b][w])
+ * (two fp32 operations, so the choice is exactly reproducible), in descending order; equal scores (-0 and +0
+ * among them) go by the lower beam, then the lower token. A token the mask rejects, and a score of -inf or
+ * NaN, is no candidate; a beam whose cumulative score is -inf or NaN is not read. Places without a candidate
+ * get score -inf, parent -1 and token -1.
+ *   cum_scores      device [batch] rows of beam_width fp32, cum_stride apart (the scores of the step before)
+ *   mask            NULL, or the grammar masks: rejected logits are then not read. Logits that
+ *                   bsp_process_logits has masked need none
+ *   scores, parents, tokens   device [batch][num_candidates]; may not overlap the inputs
+ *   workspace       16-byte aligned device memory of bsp_beam_select_workspace_size bytes; its contents need not
+ *                   be kept or cleared. Calls whose GPU work overlaps (two graphs too) need one each
+ * beam_width * vocab must be below 2^32.
+ */
+BSP_API bsp_status bsp_beam_select_workspace_size(int32_t batch, int32_t beam_width, int32_t vocab,
+                                                  int32_t num_candidates, size_t* device_bytes);
+BSP_API bsp_status bsp_beam_select(const bsp_plan_t* plan, const void* logits, int32_t logits_dtype,
+                                   int64_t logits_stride, int32_t vocab, const float* lse, const float* cum_scores,
+                                   int64_t cum_stride, const bsp_token_mask* mask, int32_t num_candidates,
+                                   float* scores, int32_t* parents, int32_t* tokens, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/*
+ * The beams' tables after a step's choice, for the step that follows: with p = parents[b][w], P = P_b and
+ * T = T_b of the plan (the tail positions that exist),
+ *   ci_out[b][w][P + j]      = ci_in[b][p][P + j], j < T;     ci_out[b][w][P + T] = w
+ *   tokens_out[b * W + w][j] = tokens_in[b * W + p][j], j < T; tokens_out[b * W + w][T] = chosen[b][w]
+ *   token_len[b * W + w]     = T + 1
+ * Other entries stay as they were. Each output may be its input (no other overlap). A parent of -1 (a place
+ * without a candidate) keeps the beam's own rows; one outside [-1, beam_width) does so too and is flagged as
+ * BSP_DEVFLAG_PAGE_INDEX.
+ *   parents, chosen  device [batch] rows, cand_stride (>= beam_width) apart, the first beam_width of each read
+ *   ci_in, ci_out    device [batch][beam_width][max_seq], max_seq > max(P_b + T_b); both NULL: left out
+ *   tokens_in, tokens_out  device [batch * beam_width] rows of token_cols (> max T_b) entries, token_stride
+ *                    apart; both NULL: left out
+ *   token_len        device [batch * beam_width] or NULL
+ */
+BSP_API bsp_status bsp_beam_advance(const bsp_plan_t* plan, const int32_t* parents, const int32_t* chosen,
+                                    int64_t cand_stride, const int32_t* ci_in, int32_t* ci_out, int32_t max_seq,
+                                    const int32_t* tokens_in, int32_t* tokens_out, int64_t token_stride,
+                                    int32_t token_cols, int32_t* token_len, void* stream);
+
+/*
+ * The attention weight that each prompt key received from the plan's query rows: for request b, kv head g and
+ * key j of its prompt (a decode plan: j < P_b; a prefill plan: j < cached + prompt rows),
+ *   weights[b][g][j] = sum over rows r of b and query heads h of g of exp(softmax_scale * q[r][h] . k[j] - lse[r][h])
+ * with lse from the attention of the same rows (bsp_decode_attn: the whole sequence's, tail included; base 2
+ * with BSP_FLAG_LSE_BASE2). A row with lse -inf adds nothing. A causal prefill's row adds to the keys it sees.
+ *   window        a prefill plan: only the last `window` prompt rows of each request are summed (0: all);
+ *                 a decode plan: 0
+ *   flags         BSP_FLAG_LSE_BASE2, BSP_FLAG_CHECK, BSP_FLAG_ACCUMULATE (add to weights)
+ *   weights       device fp32 [batch][num_kv_heads][weights_stride], weights_stride >= the plan's longest
+ *                 prompt; entries past a request's keys (all entries of one without rows) stay as they were
+ * One pass over K on the tensor cores; each sum is taken in one order, so repeated calls agree bit for bit.
+ * The _fp8 form reads E4M3 pools (key = code * k_scale; head_dim 64 or 128, decode plans).
+ */
+BSP_API bsp_status bsp_key_weights(const bsp_plan_t* plan, const void* q, const void* k_pool, const float* lse,
+                                   float softmax_scale, int32_t window, int32_t flags, float* weights,
+                                   int64_t weights_stride, void* stream);
+BSP_API bsp_status bsp_key_weights_fp8(const bsp_plan_t* plan, const void* q, const void* k_pool, const float* lse,
+                                       float softmax_scale, float k_scale, int32_t window, int32_t flags,
+                                       float* weights, int64_t weights_stride, void* stream);
+
+/*
+ * Evicts prompt rows from the cache, per (request, kv head): the keep = clamp(keep_len[b], 0, P_b) slots of
+ * largest weight stay, and those of them behind the first `keep` slots move, K and V, into the evicted slots
+ * before them (the i-th evicted slot takes the i-th such row), within the request's own prompt pages and the
+ * pools' element size. Attention does not depend on the order of its keys, so a plan with prompt length keep
+ * over the first ceil(keep / page_size) of the same pages reads exactly the rows kept; the other pages are
+ * free. Equal weights (-0 and +0 among them) go by the lower slot; a NaN counts below every number. Slots whose
+ * position is < sinks or among the last `recent` (>= the highest position held + 1 - recent) rank above all
+ * weights.
+ *   plan           a decode plan without tail rows (they would follow the old length: BSP_ERR_INVALID_ARG) or
+ *                  a prefill plan (a request without prompt rows is left as it is), whose requests share no
+ *                  page with one another
+ *   positions      device int32 [batch][num_kv_heads][weights_stride]: the slots' logical positions, or NULL:
+ *                  the slot numbers (a cache that nothing was evicted from)
+ *   keep_len       device int32 [batch]
+ *   kept           device int32 [batch][num_kv_heads][out_stride] out: slot i < keep now holds the row that
+ *                  was in slot kept[i]
+ *   weights_out, positions_out   NULL, or [batch][num_kv_heads][out_stride]: the kept slots' weights and
+ *                  positions (each may be its input when the strides agree)
+ * Entries of the outputs from `keep` on stay as they were. weights_stride, out_stride >= the longest prompt.
+ */
+BSP_API bsp_status bsp_evict_prefix(const bsp_plan_t* plan, const float* weights, int64_t weights_stride,
+                                    const int32_t* positions, const int32_t* keep_len, int32_t sinks, int32_t recent,
+                                    void* k_pool, void* v_pool, int32_t* kept, float* weights_out,
+                                    int32_t* positions_out, int64_t out_stride, void* stream);
 
 #ifdef __cplusplus
 }
