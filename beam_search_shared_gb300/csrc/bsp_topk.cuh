@@ -62,7 +62,8 @@ __device__ uint64_t topk_threshold(int n, int K, TopkScratch<NT>& s, Key key) {
     }
     for (int i = tid; i < 256; i += NT) s.hist[i] = 0;
     __syncthreads();
-    while (!s.done) {
+    // (a round takes 8 bits off the range: at most 8 of them)
+    for (int round = 0; round < 9 && !s.done; ++round) {
         const uint64_t r0 = s.range_lo, r1 = s.range_hi;
         const int need = s.need;
         const int bits = 64 - __clzll(static_cast<long long>(r1 - r0));  // (r1 - r0) >> shift < 256
@@ -93,9 +94,9 @@ __device__ uint64_t topk_threshold(int n, int K, TopkScratch<NT>& s, Key key) {
                 for (int j = 7; j >= 0; --j) {
                     if (above < static_cast<uint32_t>(need) && above + c[j] >= static_cast<uint32_t>(need)) {
                         const uint64_t e0 = r0 + (static_cast<uint64_t>(8 * lane + j) << shift);
-                        const uint64_t e1 = e0 + ((1ull << shift) - 1);
+                        const uint64_t width = (1ull << shift) - 1;
                         s.range_lo = e0;
-                        s.range_hi = e1 < r1 ? e1 : r1;
+                        s.range_hi = r1 - e0 > width ? e0 + width : r1;  // (e0 + width may pass 2^64)
                         s.need = need - static_cast<int>(above);
                         s.done = above + c[j] == static_cast<uint32_t>(need) || shift == 0;
                         break;
