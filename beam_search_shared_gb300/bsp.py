@@ -209,6 +209,8 @@ def _ptr(a: Optional[np.ndarray]):
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        if torch.cuda.is_initialized():  # the raw handle, without building a Stream object for each call
+            return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
 
@@ -479,8 +481,10 @@ LOGITS_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 def _table(name: str, t: torch.Tensor, dtype, shape, exact_last: bool = True):
     """Checks a table's type and shape (None: any extent) and that its rows are contiguous and evenly spaced;
     returns the row stride in elements."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} is {t.dtype}, not {dtype}")
+    if t.shape == shape and t.is_contiguous():  # the usual case
+        return shape[-1]
     n = t.dim()
     if n != len(shape) or any(w is not None and (t.shape[i] != w if exact_last or i < n - 1 else t.shape[i] < w)
                               for i, w in enumerate(shape)):

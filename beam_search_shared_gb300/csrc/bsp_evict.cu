@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kPickThreads) evict_select_kernel(const EvictP
         const uint32_t o = at < p.sinks || at >= recent0 ? ~0u : isnan(w) ? 0u : float_order(w);
         return (static_cast<uint64_t>(o) << 32) | static_cast<uint32_t>(~i);
     };
-    const uint64_t edge = keep < P ? topk_threshold<kPickThreads>(P, keep, s_top, key) : 0;
+    const uint64_t edge = keep < P ? topk_threshold<kPickThreads>(P, keep, 0, s_top, key) : 0;
 
     uint32_t* s_kept = s_dyn;
     const int words = (P + 31) >> 5;

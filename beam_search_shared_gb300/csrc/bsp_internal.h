@@ -200,16 +200,21 @@ struct SelectParams {
     const float* cum;
     long long cum_stride;
     TokenMask mask;
-    uint64_t* part_keys;   // [batch][splits][K]
-    int32_t* part_count;   // [batch][splits]
+    uint64_t* part_keys;   // [ctas + batch][K]: the list of (scanning CTA, request) at their sum
+    uint64_t* part_head;   // [ctas + batch][2]: its length, and a bound below the request's best K or 0
     float* scores;
     int32_t* parents;
     int32_t* tokens;
     int32_t* status;
-    int batch, W, vocab, K, splits, segments, limit;
+    int batch, W, vocab, K;
+    int ctas;      // scanning CTAs
+    int segments;  // scanning units of a row
+    int cap;       // keys of a scanning CTA's buffer
 };
 int select_unit_elems(int dtype);
-cudaError_t launch_select(int dtype, const SelectParams& p, cudaStream_t stream);
+int select_unit_warps();
+int select_buffer(int K);
+cudaError_t launch_select(int dtype, const SelectParams& p, int most_lists, cudaStream_t stream);
 
 struct AdvanceParams {
     const int32_t* req;

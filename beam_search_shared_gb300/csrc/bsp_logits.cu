@@ -30,6 +30,15 @@ struct Logit<BSP_LOGITS_BF16> {
     static constexpr int E = 8;
     static constexpr uint32_t kNegInfPair = 0xff80ff80u;
     static __device__ __forceinline__ float get(T v) { return __bfloat162float(v); }
+    // the larger values of two words, and the largest value of a word (NaN passed over, unless there is
+    // nothing else)
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+        const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+        return *reinterpret_cast<const uint32_t*>(&m);
+    }
+    static __device__ __forceinline__ float top(uint32_t a) {
+        return fmaxf(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
+    }
     static __device__ __forceinline__ T put(float v) { return __float2bfloat16_rn(v); }
     static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -55,6 +64,14 @@ struct Logit<BSP_LOGITS_FP16> {
     static constexpr int E = 8;
     static constexpr uint32_t kNegInfPair = 0xfc00fc00u;
     static __device__ __forceinline__ float get(T v) { return __half2float(v); }
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+        const __half2 m = __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+        return *reinterpret_cast<const uint32_t*>(&m);
+    }
+    static __device__ __forceinline__ float top(uint32_t a) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&a));
+        return fmaxf(f.x, f.y);
+    }
     static __device__ __forceinline__ T put(float v) { return __float2half_rn(v); }
     static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -81,6 +98,10 @@ struct Logit<BSP_LOGITS_FP32> {
     static constexpr int E = 4;
     static constexpr uint32_t kNegInfPair = 0xff800000u;
     static __device__ __forceinline__ float get(T v) { return v; }
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+        return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    }
+    static __device__ __forceinline__ float top(uint32_t a) { return __uint_as_float(a); }
     static __device__ __forceinline__ T put(float v) { return v; }
     static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[4]) {
         f[0] = __uint_as_float(v.x);
@@ -456,7 +477,9 @@ cudaError_t launch_process_t(const ProcessParams& p, int cluster, size_t smem, c
 // ---------------------------------------------------------------- select
 
 constexpr int kSelThreads = 256;
-constexpr int kSelU = 2;  // vectors per thread and unit
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelU = 8;       // vectors per lane and unit
+constexpr int kSelRounds = 4;  // units per warp of the sample that sets the first floor
 
 // Candidates as 64-bit keys: the score's order in the high half, the flat index (beam * vocab + token)
 // complemented in the low half, so that the larger key is the better candidate and equal scores go by the
@@ -465,159 +488,371 @@ __device__ __forceinline__ uint64_t candidate_key(float score, uint32_t flat) {
     return (static_cast<uint64_t>(float_order(score)) << 32) | static_cast<uint32_t>(~flat);
 }
 
+// The best K of each request in one pass over the logits. The units of all requests (32 * kSelU vectors of a
+// row) are one sequence, cut evenly among the CTAs, whatever the batch; a CTA that crosses into another
+// request leaves its list and begins anew. Inside a CTA the warps scan on their own. A unit costs a packed
+// maximum over the lane's vectors and one comparison with the logit below which the row cannot reach the
+// floor; where a lane passes, its elements are tried and the candidates go to a buffer in shared memory, each
+// lane's next one at a time. When that is full the warps meet, cut it to the best K and raise the floor to the
+// K-th. Rows with a sparse mask are read by its bits.
+//
+// The first floor is guessed from a sample of units spread over the CTA's: if K of n vectors hold a candidate
+// of the best K, a share K / n of the sample's do, and the floor is the sample's vector maximum some four
+// deviations further down. It lets through a few times K candidates in all. If fewer than K come through, the
+// CTA scans its part of the request once more under the sample's K-th maximum, which is a sure bound.
+// Bound by reading the logits.
 template <int DT>
-__global__ void __launch_bounds__(kSelThreads) beam_scan_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kSelThreads, 2) beam_scan_kernel(const SelectParams p) {
     using L = Logit<DT>;
     using T = typename L::T;
     constexpr int E = L::E, U = kSelU;
-    // [limit + kSelThreads * U * E + 16]: the candidates held, and the most one unit can add (a row's ragged
-    // ends: below 16)
-    extern __shared__ uint64_t s_buf[];
+    constexpr uint32_t ALL = (1u << E) - 1;
+    extern __shared__ uint64_t s_buf[];  // [p.cap], cap >= the sample's keys (4 per thread) and > K
     __shared__ TopkScratch<kSelThreads> s_top;
     __shared__ int s_count;
+    __shared__ volatile int s_full;      // a warp waits for the buffer to be cut
 
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int b = blockIdx.y, S = gridDim.x;
-    const int limit = p.limit;             // candidates held when a unit begins: at most this many (>= K)
-    if (tid == 0) s_count = 0;
-    __syncthreads();
-    uint64_t floor_key = 0;                // only larger keys are candidates (a lower bound of the best K)
-    float floor_score = kNegInf;
-    bool have = false;                     // floor_key is set
-    const int nseg = p.segments;           // units of a row
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int nseg = p.segments;         // units of a row
+    const long long per_request = static_cast<long long>(p.W) * nseg;
+    const long long total = per_request * p.batch;
+    long long at = total * blockIdx.x / gridDim.x;
+    const long long end = total * (blockIdx.x + 1) / gridDim.x;
+    const int mwords = (p.vocab + 31) >> 5;
+    bool sure = false;                   // the floor is no guess
 
-    for (int u = blockIdx.x; u < p.W * nseg; u += S) {
-        const int w = u / nseg, seg = u - w * nseg;
-        const int r = b * p.W + w;
-        const float cum = __ldg(p.cum + static_cast<long long>(b) * p.cum_stride + w);
-        const float lse = __ldg(p.lse + r);
-        if (!(cum > kNegInf)) continue;    // uniform: a dead beam (or a NaN score) has no candidates
-        const T* x = static_cast<const T*>(p.x) + static_cast<long long>(r) * p.x_stride;
-        const int head = min(lead_elems<E>(x), p.vocab);
-        const int nv = (p.vocab - head) / E;
-        const int v0 = static_cast<int>(static_cast<long long>(nv) * seg / nseg);
-        const int v1 = static_cast<int>(static_cast<long long>(nv) * (seg + 1) / nseg);
-        const uint32_t* mrow = mask_row(p.mask, r, p.status, tid == 0 && seg == 0);
-        const int mwords = (p.vocab + 31) >> 5;
-        const uint4* xv = reinterpret_cast<const uint4*>(x + head);
-        float f[U][E], g = kNegInf;        // scores (-inf: not a candidate); g: a ragged element
-        int tg = -1;
+    while (at < end) {  // one request at a time
+        const int b = static_cast<int>(at / per_request);
+        const int u_begin = static_cast<int>(at - b * per_request);
+        const int u_end = static_cast<int>(min(per_request, end - b * per_request));
+        uint64_t floor_key = 0;  // only larger keys are candidates
+        bool have = false;       // it is set
+        if (tid == 0) {
+            s_count = 0;
+            s_full = 0;
+        }
+        __syncthreads();
+
+        // the present row: beam, logits, mask, scores' terms, elements before the first 16-byte boundary, vectors,
+        // and the logit below which its scores stay under the floor
+        int w = -1, head = 0, nv = 0;
+        const T* x = nullptr;     // null: a beam without candidates (a cumulative score of -inf or NaN)
+        const uint32_t* mrow = nullptr;
+        float cum = 0.f, lse = 0.f, reach = 0.f;
+        auto set_reach = [&]() {
+            // less a margin that covers the score's two roundings (2^-24 of |score| + |cum| + |lse| each)
+            const float fl = have ? order_float(static_cast<uint32_t>(floor_key >> 32)) : kNegInf;
+            const float room = (fabsf(fl) + fabsf(cum) + fabsf(lse)) * 0x1p-20f;
+            reach = have && room < 1e30f ? fl - cum + lse - room : kNegInf;  // (room: false for NaN)
+        };
+        auto open_row = [&](int to, bool flag) {
+            w = to;
+            const int r = b * p.W + w;
+            cum = __ldg(p.cum + static_cast<long long>(b) * p.cum_stride + w);
+            lse = __ldg(p.lse + r);
+            x = cum > kNegInf ? static_cast<const T*>(p.x) + static_cast<long long>(r) * p.x_stride : nullptr;
+            head = min(lead_elems<E>(x), p.vocab);
+            nv = (p.vocab - head) / E;
+            mrow = mask_row(p.mask, r, p.status, flag);
+            set_reach();
+        };
+        auto score = [&](float v) { return __fadd_rn(__fsub_rn(v, lse), cum); };
+        auto key_of = [&](float sc, int t) {
+            return candidate_key(sc, static_cast<uint32_t>(w) * static_cast<uint32_t>(p.vocab) + t);
+        };
+        // All warps meet: a buffer of more than K is cut to the best K (and up to an eighth of the rest, which
+        // saves passes). Returns whether all of them are done.
+        auto meet = [&](bool done) -> bool {
+            const bool all = __syncthreads_and(done);
+            const int n = min(s_count, p.cap);
+            int left = n;
+            if (n > p.K) {
+                floor_key = topk_compact<kSelThreads>(s_buf, n, p.K, all ? 0 : (p.cap - p.K) >> 3, s_top);
+                have = true;
+                left = s_top.count;
+            }
+            __syncthreads();
+            if (tid == 0) {
+                s_count = left;
+                s_full = 0;
+            }
+            __syncthreads();
+            set_reach();
+            return all;
+        };
+        // Stores each lane's candidate (ok): places in the buffer by one atomic for the warp; when it is full the
+        // warps meet, and what found no place is tried against the new floor. (A NaN score compares false.)
+        auto put = [&](bool ok, float sc, int t) {
+            const uint64_t key = key_of(sc, t);
+            ok = ok && sc > kNegInf && (!have || key > floor_key);
+            for (;;) {
+                const uint32_t who = __ballot_sync(~0u, ok);
+                if (!who) break;
+                int to = 0;
+                if (lane == 0) to = atomicAdd(&s_count, __popc(who));
+                to = __shfl_sync(~0u, to, 0) + __popc(who & ((1u << lane) - 1));
+                if (ok && to < p.cap) {
+                    s_buf[to] = key;
+                    ok = false;
+                }
+                if (!__any_sync(~0u, ok)) break;
+                if (lane == 0) s_full = 1;
+                meet(false);
+                ok = ok && key > floor_key;
+            }
+        };
+        // the lane's vectors of the unit that begins at vector v0, those with an allowed token; their tokens that
+        // count, E bits each
+        auto load = [&](int v0, uint4 (&val)[U]) -> uint64_t {
+            const uint4* xv = reinterpret_cast<const uint4*>(x + head) + v0 + lane;
+            uint64_t keep = 0;
+            if (!mrow && v0 + 32 * U <= nv) {
+#pragma unroll
+                for (int k = 0; k < U; ++k) val[k] = __ldcs(xv + 32 * k);
+                keep = E * U == 64 ? ~0ull : (1ull << (E * U & 63)) - 1;
+            } else {
+#pragma unroll
+                for (int k = 0; k < U; ++k) {
+                    const int v = v0 + lane + 32 * k;
+                    uint32_t m = v < nv ? ALL : 0u;
+                    if (m && mrow) m &= mask_bits(mrow, mwords, head + v * E);
+                    if (m) val[k] = __ldcs(xv + 32 * k);
+                    keep |= static_cast<uint64_t>(m) << (E * k);
+                }
+            }
+            return keep;
+        };
+
+        // ---- the first floor: from each of 32 units spread over the run (round q takes unit
+        // (2 (8 q + warp) + 1) / 64 of the way), or in a shorter run from each warp's first unit
         {
-            uint4 val[U];
-            uint32_t keep[U];
+            const int units = u_end - u_begin;
+            const bool spread = units >= kSelRounds * kSelWarps;
+            const float mean = static_cast<float>(p.K) * min(units, spread ? kSelRounds * kSelWarps : kSelWarps) / units;
+            const int rank = sure ? p.K : min(p.K, static_cast<int>(mean + 4.f * sqrtf(mean)) + 4);
+            uint64_t best[4] = {0, 0, 0, 0};  // the lane's best candidates: of a round, or of a quarter of the unit
 #pragma unroll
-            for (int k = 0; k < U; ++k) {
-                const int v = v0 + tid + k * kSelThreads;
-                keep[k] = v >= v1 ? 0u : mrow ? mask_bits(mrow, mwords, head + v * E) & ((1u << E) - 1) : (1u << E) - 1;
-                if (keep[k]) val[k] = __ldcs(xv + v);
+            for (int q = 0; q < kSelRounds; ++q) {
+                if (!spread && (q > 0 || warp >= units)) break;
+                const int u = u_begin + (spread ? static_cast<int>(static_cast<long long>(units) * (2 * (q * kSelWarps + warp) + 1) /
+                                                                   (2 * kSelRounds * kSelWarps))
+                                                : warp);
+                open_row(u / nseg, false);
+                if (!x) continue;
+                const int v0 = (u - w * nseg) * (32 * U);
+                uint4 val[U];
+                const uint64_t keep = load(v0, val);
+#pragma unroll
+                for (int k = 0; k < U; ++k) {
+                    const uint32_t m = static_cast<uint32_t>(keep >> (E * k)) & ALL;
+                    if (!m) continue;
+                    float f[E], top = kNegInf;
+                    int e0 = 0;
+                    L::unpack(val[k], f);
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        if (((m >> e) & 1u) && f[e] > top) {
+                            top = f[e];
+                            e0 = e;
+                        }
+                    const float sc = score(top);
+                    const uint64_t key = sc > kNegInf ? key_of(sc, head + E * (v0 + lane + 32 * k) + e0) : 0;
+                    const int slot = spread ? q : k / (U / 4);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i == slot && key > best[i]) best[i] = key;
+                }
             }
-            const int n_head = seg == 0 ? head : 0;
-            const int tail0 = head + nv * E;
-            const int n_tail = seg == nseg - 1 ? p.vocab - tail0 : 0;
-            if (tid < n_head + n_tail) {
-                tg = tid < n_head ? tid : tail0 + tid - n_head;
-                if (!mrow || (mask_bits(mrow, mwords, tg) & 1u)) g = __fadd_rn(__fsub_rn(L::get(x[tg]), lse), cum);
+            if (rank <= 64) {  // a lane's best alone: few lanes hold two of so few
+                best[0] = max(max(best[0], best[1]), max(best[2], best[3]));
+                best[1] = best[2] = best[3] = 0;
             }
 #pragma unroll
-            for (int k = 0; k < U; ++k) {
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t who = __ballot_sync(~0u, best[i] != 0);
+                if (!who) continue;
+                int to = 0;
+                if (lane == 0) to = atomicAdd(&s_count, __popc(who));
+                to = __shfl_sync(~0u, to, 0) + __popc(who & ((1u << lane) - 1));
+                if (best[i]) s_buf[to] = best[i];
+            }
+            __syncthreads();
+            const int n = s_count;
+            sure = rank == p.K || n < rank;
+            if (n >= rank) {
+                floor_key = topk_threshold<kSelThreads>(n, rank, 0, s_top, [&](int i) { return s_buf[i]; }) - 1;
+                have = true;
+            }
+            __syncthreads();
+            if (tid == 0) s_count = 0;
+            w = -1;
+            __syncthreads();
+        }
+
+        // ---- the scan
+        int to_w = (u_begin + warp) / nseg, seg = u_begin + warp - to_w * nseg;
+        for (int u = u_begin + warp; u < u_end; u += kSelWarps, seg += kSelWarps) {
+            while (seg >= nseg) {
+                seg -= nseg;
+                ++to_w;
+            }
+            if (to_w != w) open_row(to_w, lane == 0 && seg < kSelWarps);
+            if (s_full) meet(false);
+            if (!x) continue;
+            const int v0 = seg * (32 * U);
+            uint64_t pend = 0;  // the lane's elements that reach the floor
+            bool by_bits = false;
+            if (mrow) {
+                // a word of the mask per lane and 32 * 32 tokens; few allowed: those are read one by one
+                constexpr int N = U * E < 32 ? 1 : U * E / 32;
+                uint32_t bits[N];
+                int n = 0;
 #pragma unroll
-                for (int e = 0; e < E; ++e) f[k][e] = kNegInf;
-                if (keep[k]) {
-                    L::unpack(val[k], f[k]);
+                for (int j = 0; j < N; ++j) {
+                    const int t = head + v0 * E + 32 * (32 * j + lane), left = (U * E < 32 && lane >= U * E ? 0 : head + nv * E - t);
+                    bits[j] = left > 0 ? mask_bits(mrow, mwords, t) & (left < 32 ? (1u << left) - 1 : ~0u) : 0u;
+                    n = max(n, __popc(bits[j]));
+                }
+                n = __reduce_max_sync(~0u, n);
+                by_bits = n <= 8;
+                if (by_bits) {
 #pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        const float s = __fadd_rn(__fsub_rn(f[k][e], lse), cum);
-                        f[k][e] = ((keep[k] >> e) & 1u) ? s : kNegInf;
+                    for (int j = 0; j < N; ++j) {
+                        while (__any_sync(~0u, bits[j] != 0)) {
+                            const int t = head + v0 * E + 32 * (32 * j + lane) + (bits[j] ? __ffs(bits[j]) - 1 : 0);
+                            const float v = bits[j] ? L::get(x[t]) : kNegInf;
+                            const bool ok = bits[j] && v >= reach;
+                            bits[j] &= bits[j] - 1;
+                            if (__any_sync(~0u, ok)) put(ok, score(v), t);
+                        }
                     }
                 }
             }
-        }
-        // candidates: above the floor (before there is one: anything above -inf; NaN compares false)
-        auto passes = [&](float s, int t) -> bool {
-            if (!(s >= floor_score) || !(s > kNegInf)) return false;
-            return !have || candidate_key(s, static_cast<uint32_t>(w) * p.vocab + t) > floor_key;
-        };
-        int mine = 0;
+            if (!by_bits) {
+                uint4 val[U];
+                const uint64_t keep = load(v0, val);
+                bool hit = true;
+                if (!mrow && v0 + 32 * U <= nv) {  // all vectors there: one maximum
+                    uint4 m = val[0];
 #pragma unroll
-        for (int k = 0; k < U; ++k)
-#pragma unroll
-            for (int e = 0; e < E; ++e) mine += passes(f[k][e], head + (v0 + tid + k * kSelThreads) * E + e);
-        mine += tg >= 0 && passes(g, tg);
-        bool full = false;
-        if (__any_sync(~0u, mine)) {
-            int at = mine;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int o = __shfl_up_sync(~0u, at, d);
-                if (lane >= d) at += o;
-            }
-            const int total = __shfl_sync(~0u, at, 31);
-            int first = 0;
-            if (lane == 0) first = atomicAdd(&s_count, total);
-            first = __shfl_sync(~0u, first, 0);
-            full = first + total > limit;
-            at += first - mine;
-            if (mine) {
-#pragma unroll
-                for (int k = 0; k < U; ++k)
-#pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        const int t = head + (v0 + tid + k * kSelThreads) * E + e;
-                        if (passes(f[k][e], t)) s_buf[at++] = candidate_key(f[k][e], static_cast<uint32_t>(w) * p.vocab + t);
+                    for (int k = 1; k < U; ++k) {
+                        m.x = L::max2(m.x, val[k].x);
+                        m.y = L::max2(m.y, val[k].y);
+                        m.z = L::max2(m.z, val[k].z);
+                        m.w = L::max2(m.w, val[k].w);
                     }
-                if (tg >= 0 && passes(g, tg)) s_buf[at++] = candidate_key(g, static_cast<uint32_t>(w) * p.vocab + tg);
+                    hit = L::top(L::max2(L::max2(m.x, m.y), L::max2(m.z, m.w))) >= reach;
+                }
+                if (__any_sync(~0u, hit)) {
+#pragma unroll
+                    for (int k = 0; k < U; ++k) {
+                        const uint32_t m = static_cast<uint32_t>(keep >> (E * k)) & ALL;
+                        const bool some = hit && m && (m != ALL || L::top(L::max2(L::max2(val[k].x, val[k].y), L::max2(val[k].z, val[k].w))) >= reach);
+                        if (!__any_sync(~0u, some)) continue;
+                        float f[E];
+                        L::unpack(val[k], f);
+                        uint32_t got = 0;
+#pragma unroll
+                        for (int e = 0; e < E; ++e) got |= f[e] >= reach ? 1u << e : 0u;
+                        if (some) pend |= static_cast<uint64_t>(got & m) << (E * k);
+                    }
+                }
+            }
+            while (__any_sync(~0u, pend != 0)) {
+                const bool ok = pend != 0;
+                const int bit = ok ? __ffsll(static_cast<long long>(pend)) - 1 : 0;
+                pend &= pend - 1;
+                const int t = head + E * (v0 + lane + 32 * (bit / E)) + bit % E;
+                const float v = ok ? L::get(x[t]) : kNegInf;
+                put(ok, score(v), t);
+            }
+            // the ragged ends of a row: with its first and its last unit
+            const int n_head = seg == 0 ? head : 0;
+            const int tail0 = head + nv * E;
+            const int n_tail = seg == nseg - 1 ? p.vocab - tail0 : 0;
+            if (n_head + n_tail > 0) {
+                const int t = lane < n_head ? lane : tail0 + lane - n_head;
+                const bool ok = lane < n_head + n_tail && (!mrow || (mask_bits(mrow, mwords, t) & 1u));
+                put(ok, score(ok ? L::get(x[t]) : kNegInf), t);
             }
         }
-        if (__syncthreads_or(full)) {
-            const int n = s_count;
-            floor_key = topk_compact<kSelThreads>(s_buf, n, p.K, s_top);
-            floor_score = order_float(static_cast<uint32_t>(floor_key >> 32));
-            have = true;
-            if (tid == 0) s_count = min(n, p.K);
-            __syncthreads();
+        while (!meet(true)) {
         }
+        const int n = s_count;
+        if (n < p.K && !sure) {  // the guess was too high: once more under a sure floor
+            sure = true;
+            __syncthreads();
+            continue;
+        }
+        sure = false;
+        const long long list = static_cast<long long>(blockIdx.x) + b;
+        if (tid == 0) {
+            // the list's length, and for a full one a key that the request's best K exceed
+            p.part_head[2 * list] = n;
+            p.part_head[2 * list + 1] = n == p.K && have ? floor_key : 0;
+        }
+        for (int i = tid; i < n; i += kSelThreads) p.part_keys[list * p.K + i] = s_buf[i];
+        at = b * per_request + u_end;
+        __syncthreads();
     }
-    __syncthreads();
-    int n = s_count;
-    if (n > p.K) {
-        topk_compact<kSelThreads>(s_buf, n, p.K, s_top);
-        n = p.K;
-    }
-    const long long list = static_cast<long long>(b) * S + blockIdx.x;
-    if (tid == 0) p.part_count[list] = n;
-    for (int i = tid; i < n; i += kSelThreads) p.part_keys[list * p.K + i] = s_buf[i];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 constexpr int kMergeThreads = 512;
 
-// One CTA per request: the splits' lists, cut to the best K and put in order.
+// One CTA per request: the lists of the scanning CTAs that met it, cut to the best K and put in order. A list's
+// place is CTA + request: going through the units, one of the two grows at every step. Every full list's
+// K-th key is a bound for all, so most of the others' keys fall away as they are read.
 __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const SelectParams p) {
-    extern __shared__ uint64_t s_buf[];  // [splits * K]
+    extern __shared__ uint64_t s_buf[];  // [most lists of a request * K]
     __shared__ TopkScratch<kMergeThreads> s_top;
     __shared__ int s_count;
+    __shared__ unsigned long long s_floor;
     const int tid = threadIdx.x, lane = tid & 31;
     const int b = blockIdx.x;
-    if (tid == 0) s_count = 0;
+    if (tid == 0) {
+        s_count = 0;
+        s_floor = 0;
+    }
+    const long long per_request = static_cast<long long>(p.W) * p.segments;
+    const long long total = per_request * p.batch;
+    // CTA c scans the units from total * c / ctas on: the last c whose first unit is not behind x
+    auto cta_of = [&](long long x) { return static_cast<int>(((x + 1) * p.ctas - 1) / total); };
+    const int c0 = cta_of(b * per_request), c1 = cta_of((b + 1) * per_request - 1);
+    const int lists = c1 - c0 + 1;
+    const unsigned long long* heads = reinterpret_cast<const unsigned long long*>(p.part_head) + 2 * (static_cast<long long>(c0) + b);
+    const unsigned long long* keys = reinterpret_cast<const unsigned long long*>(p.part_keys) + (static_cast<long long>(c0) + b) * p.K;
     __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const long long list0 = static_cast<long long>(b) * p.splits;
-    for (int i0 = 0; i0 < p.splits * p.K; i0 += kMergeThreads) {
-        const int i = i0 + tid;
-        const int s = i / p.K, j = i - s * p.K;
-        const bool in = s < p.splits && j < __ldcg(p.part_count + list0 + s);
-        uint64_t key = 0;
-        if (in) key = __ldcg(reinterpret_cast<const unsigned long long*>(p.part_keys) + (list0 + s) * p.K + j);
-        const uint32_t who = __ballot_sync(~0u, in);
-        int first = 0;
-        if (lane == 0 && who) first = atomicAdd(&s_count, __popc(who));
-        first = __shfl_sync(~0u, first, 0);
-        if (in) s_buf[first + __popc(who & ((1u << lane) - 1))] = key;
+    for (int s = tid; s < lists; s += kMergeThreads) atomicMax(&s_floor, __ldcg(heads + 2 * s + 1));
+    __syncthreads();
+    const unsigned long long floor = s_floor;
+    constexpr int R = 4;
+    const int slots = lists * p.K;
+    for (int i0 = 0; i0 < slots; i0 += R * kMergeThreads) {
+        unsigned long long key[R], len[R];
+#pragma unroll
+        for (int q = 0; q < R; ++q) {  // (places behind a list's end hold anything, and are passed over)
+            const int i = i0 + q * kMergeThreads + tid;
+            key[q] = i < slots ? __ldcg(keys + i) : 0ull;
+            len[q] = i < slots ? __ldcg(heads + 2 * (i / p.K)) : 0ull;
+        }
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+            const int i = i0 + q * kMergeThreads + tid;
+            const bool in = i < slots && static_cast<unsigned long long>(i % p.K) < len[q] && key[q] > floor;
+            const uint32_t who = __ballot_sync(~0u, in);
+            if (!who) continue;
+            int first = 0;
+            if (lane == 0) first = atomicAdd(&s_count, __popc(who));
+            first = __shfl_sync(~0u, first, 0);
+            if (in) s_buf[first + __popc(who & ((1u << lane) - 1))] = key[q];
+        }
     }
     __syncthreads();
     int n = s_count;
     if (n > p.K) {
-        topk_compact<kMergeThreads>(s_buf, n, p.K, s_top);
+        topk_compact<kMergeThreads>(s_buf, n, p.K, 0, s_top);
         n = p.K;
     }
     // rank = number of larger keys (distinct keys, K <= 512): the output place
@@ -641,12 +876,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const SelectP
 
 template <int DT>
 cudaError_t launch_scan(const SelectParams& p, cudaStream_t stream) {
-    constexpr int E = Logit<DT>::E;
-    const size_t smem = static_cast<size_t>(kSelThreads * kSelU * E + 16 + p.limit) * 8;
-    cudaError_t e = cudaFuncSetAttribute(beam_scan_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-    beam_scan_kernel<DT><<<dim3(p.splits, p.batch), kSelThreads, smem, stream>>>(p);
+    beam_scan_kernel<DT><<<p.ctas, kSelThreads, static_cast<size_t>(p.cap) * 8, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -660,16 +890,24 @@ cudaError_t launch_process(int dtype, const ProcessParams& p, int cluster, size_
     }
 }
 
-int select_unit_elems(int dtype) { return kSelThreads * kSelU * (dtype == BSP_LOGITS_FP32 ? 4 : 8); }
+// Logits of a scanning unit, and the least buffer of a CTA.
+int select_unit_elems(int dtype) { return 32 * kSelU * (dtype == BSP_LOGITS_FP32 ? 4 : 8); }
+int select_unit_warps() { return kSelWarps; }
+int select_buffer(int K) {
+    const int sample = 4 * kSelThreads;
+    return K + 256 > sample ? K + 256 : sample;
+}
 
-cudaError_t launch_select(int dtype, const SelectParams& p, cudaStream_t stream) {
+cudaError_t launch_select(int dtype, const SelectParams& p, int most_lists, cudaStream_t stream) {
     cudaError_t e = dtype == BSP_LOGITS_BF16   ? launch_scan<BSP_LOGITS_BF16>(p, stream)
                     : dtype == BSP_LOGITS_FP16 ? launch_scan<BSP_LOGITS_FP16>(p, stream)
                                                : launch_scan<BSP_LOGITS_FP32>(p, stream);
     if (e != cudaSuccess) return e;
-    const size_t smem = static_cast<size_t>(p.splits) * p.K * 8;
-    e = cudaFuncSetAttribute(beam_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
+    const size_t smem = static_cast<size_t>(most_lists) * p.K * 8;
+    if (smem > 32 * 1024) {
+        e = cudaFuncSetAttribute(beam_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(p.batch);
     cfg.blockDim = dim3(kMergeThreads);

@@ -68,18 +68,21 @@ bsp_status check_mask(const bsp_token_mask* m, int32_t vocab, TokenMask* out) {
 
 constexpr size_t kMaxSmem = 227 * 1024;
 constexpr int64_t kMergeKeys = 16384;  // candidates one merging CTA holds (128 KB)
-constexpr int64_t kSelectCtas = 6;     // scanning CTAs per SM that are resident at once
+constexpr int64_t kSelectCtas = 2;     // scanning CTAs per SM that are resident at once
 
-// How a selection is split: units of a row, and scanning CTAs per request.
+// How a selection is cut: units of a row, scanning CTAs, and the most CTAs that meet one request.
 struct SelectSplit {
-    int segments, splits;
+    int segments, ctas, lists;
 };
 SelectSplit select_split(int batch, int W, int vocab, int K, int dtype, int sms) {
     SelectSplit s;
     s.segments = static_cast<int>(ceil_div(vocab, select_unit_elems(dtype)));
-    const int64_t units = static_cast<int64_t>(W) * s.segments;
-    const int64_t want = std::max<int64_t>(1, kSelectCtas * sms / std::max(1, batch));
-    s.splits = static_cast<int>(std::min({units, want, std::max<int64_t>(1, kMergeKeys / K)}));
+    const int64_t units = static_cast<int64_t>(W) * s.segments * batch;
+    // a unit for each warp at least; a request's lists fit its merging CTA (an even cut of n CTAs over the
+    // batch gives a request at most ceil(n / batch) + 1 of them)
+    const int64_t merge = std::max<int64_t>(1, kMergeKeys / K - 1) * batch;
+    s.ctas = static_cast<int>(std::max<int64_t>(1, std::min({ceil_div(units, select_unit_warps()), kSelectCtas * sms, merge})));
+    s.lists = static_cast<int>(ceil_div(s.ctas, std::max(1, batch)) + 1);
     return s;
 }
 
@@ -195,10 +198,10 @@ bsp_status bsp_beam_select_workspace_size(int32_t batch, int32_t beam_width, int
                                           size_t* device_bytes) {
     if (!device_bytes || batch < 0 || beam_width < 1 || vocab < 1 || num_candidates < 1) return BSP_ERR_INVALID_ARG;
     if (vocab > BSP_MAX_VOCAB || num_candidates > BSP_MAX_CANDIDATES) return BSP_ERR_UNSUPPORTED;
-    // the most splits any logits type and SM count up to 1024 give
-    const SelectSplit s = select_split(1, beam_width, vocab, num_candidates, BSP_LOGITS_FP32, 1024);
-    const int64_t lists = std::min<int64_t>(static_cast<int64_t>(s.splits) * batch, kSelectCtas * 1024 + batch);
-    *device_bytes = static_cast<size_t>(lists) * (static_cast<size_t>(num_candidates) * 8 + 8);
+    // the most lists any logits type and SM count up to 1024 give
+    const SelectSplit s = select_split(std::max(batch, 1), beam_width, vocab, num_candidates, BSP_LOGITS_FP32, 1024);
+    const int64_t lists = static_cast<int64_t>(s.ctas) + batch;
+    *device_bytes = static_cast<size_t>(lists) * (static_cast<size_t>(num_candidates) + 2) * 8;
     return BSP_OK;
 }
 
@@ -224,15 +227,15 @@ bsp_status bsp_beam_select(const bsp_plan_t* plan, const void* logits, int32_t l
     if (!device_sms(&sms)) return BSP_ERR_CUDA;
     const SelectSplit s = select_split(plan->batch, plan->beam_width, vocab, num_candidates, logits_dtype, std::min(sms, 1024));
     if (static_cast<int64_t>(plan->beam_width) * s.segments > (int64_t(1) << 30)) return BSP_ERR_UNSUPPORTED;
-    const int64_t lists = static_cast<int64_t>(s.splits) * plan->batch;
-    if (static_cast<size_t>(lists) * (static_cast<size_t>(num_candidates) * 8 + 4) > workspace_bytes) return BSP_ERR_CAPACITY;
+    const int64_t lists = static_cast<int64_t>(s.ctas) + plan->batch;
+    if (static_cast<size_t>(lists) * (static_cast<size_t>(num_candidates) + 2) * 8 > workspace_bytes) return BSP_ERR_CAPACITY;
     p.x = logits;
     p.x_stride = logits_stride;
     p.lse = lse;
     p.cum = cum_scores;
     p.cum_stride = cum_stride;
     p.part_keys = static_cast<uint64_t*>(workspace);
-    p.part_count = reinterpret_cast<int32_t*>(p.part_keys + lists * num_candidates);
+    p.part_head = p.part_keys + lists * num_candidates;
     p.scores = scores;
     p.parents = parents;
     p.tokens = tokens;
@@ -241,10 +244,10 @@ bsp_status bsp_beam_select(const bsp_plan_t* plan, const void* logits, int32_t l
     p.W = plan->beam_width;
     p.vocab = vocab;
     p.K = num_candidates;
-    p.splits = s.splits;
+    p.ctas = s.ctas;
     p.segments = s.segments;
-    p.limit = std::max(2 * num_candidates, 256);
-    return launched(launch_select(logits_dtype, p, static_cast<cudaStream_t>(stream)));
+    p.cap = select_buffer(num_candidates);
+    return launched(launch_select(logits_dtype, p, s.lists, static_cast<cudaStream_t>(stream)));
 }
 
 bsp_status bsp_beam_advance(const bsp_plan_t* plan, const int32_t* parents, const int32_t* chosen, int64_t cand_stride,

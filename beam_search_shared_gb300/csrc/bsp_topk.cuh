@@ -28,10 +28,10 @@ struct TopkScratch {
 // The K-th largest of the n keys key(0) .. key(n - 1), n >= K >= 1, distinct. All NT threads call it; key(i)
 // may be evaluated several times. Narrows a range of keys by 256 bins at a time: the bins of the present
 // range are counted, and the one that holds the K-th largest becomes the range. It ends as soon as a bin's
-// lower edge has exactly K keys at or above it, which for scattered keys takes two or three passes; then
-// any value between those K keys and the others serves, and the edge is returned.
+// lower edge has K to K + slack keys at or above it, which for scattered keys and no slack takes two or three
+// passes; the edge is returned.
 template <int NT, typename Key>
-__device__ uint64_t topk_threshold(int n, int K, TopkScratch<NT>& s, Key key) {
+__device__ uint64_t topk_threshold(int n, int K, int slack, TopkScratch<NT>& s, Key key) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint64_t lo = ~0ull, hi = 0;
     for (int i = tid; i < n; i += NT) {
@@ -58,7 +58,7 @@ __device__ uint64_t topk_threshold(int n, int K, TopkScratch<NT>& s, Key key) {
         s.range_lo = lo;
         s.range_hi = hi;
         s.need = K;
-        s.done = n == K;
+        s.done = n <= K + slack;
     }
     for (int i = tid; i < 256; i += NT) s.hist[i] = 0;
     __syncthreads();
@@ -98,7 +98,7 @@ __device__ uint64_t topk_threshold(int n, int K, TopkScratch<NT>& s, Key key) {
                         s.range_lo = e0;
                         s.range_hi = r1 - e0 > width ? e0 + width : r1;  // (e0 + width may pass 2^64)
                         s.need = need - static_cast<int>(above);
-                        s.done = above + c[j] == static_cast<uint32_t>(need) || shift == 0;
+                        s.done = above + c[j] <= static_cast<uint32_t>(need + slack) || shift == 0;
                         break;
                     }
                     above += c[j];
@@ -112,13 +112,13 @@ __device__ uint64_t topk_threshold(int n, int K, TopkScratch<NT>& s, Key key) {
     return t;
 }
 
-// Moves the K largest of the n keys in buf to its front (in no order); n <= K leaves them and returns 0. Returns
-// a key above which every further candidate must lie when n > K: the smallest of the K less one. All NT
-// threads call it after a barrier; it ends with one.
+// Moves the K to K + slack largest of the n > K keys in buf to its front (in no order); their number is left in
+// s.count. Returns a key above which every further candidate must lie: the smallest of them less one. All NT
+// threads call it after a barrier; it ends with one. (Not inlined: its callers' loops stay in the
+// instruction cache.)
 template <int NT>
-__device__ uint64_t topk_compact(uint64_t* buf, int n, int K, TopkScratch<NT>& s) {
-    if (n <= K) return 0;
-    const uint64_t edge = topk_threshold<NT>(n, K, s, [&](int i) { return buf[i]; });
+__device__ __noinline__ uint64_t topk_compact(uint64_t* buf, int n, int K, int slack, TopkScratch<NT>& s) {
+    const uint64_t edge = topk_threshold<NT>(n, K, slack, s, [&](int i) { return buf[i]; });
     const int tid = threadIdx.x, lane = tid & 31;
     if (tid == 0) s.count = 0;
     __syncthreads();
