@@ -267,8 +267,10 @@ struct EvictParams {
     long long stride, out_stride;
     int32_t* status;
     int batch, plan_w, plan_kind, Hkv, ps_log2, row_bytes, max_keys, sinks, recent;
+    int cached_keys, cluster;  // set by launch_evict
 };
-cudaError_t launch_evict(const EvictParams& p, int num_sms, cudaStream_t stream);
+// longest: the plan's longest prompt
+cudaError_t launch_evict(EvictParams p, int longest, int num_sms, cudaStream_t stream);
 
 // bsp_host.cpp, for bsp_step.cpp
 bsp_status check_plan(const bsp_plan_t* plan);

@@ -420,7 +420,7 @@ bsp_status bsp_evict_prefix(const bsp_plan_t* plan, const float* weights, int64_
     p.max_keys = static_cast<int>(std::min<int64_t>({weights_stride, out_stride, BSP_MAX_EVICT_ROWS}));
     p.sinks = sinks;
     p.recent = recent;
-    return launched(launch_evict(p, plan->num_sms, static_cast<cudaStream_t>(stream)));
+    return launched(launch_evict(p, plan->max_prefix_len, plan->num_sms, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

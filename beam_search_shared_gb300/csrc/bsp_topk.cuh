@@ -15,29 +15,53 @@ __device__ __forceinline__ float order_float(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
 }
 
+constexpr int kTopkBins = 1024;  // 32 x 32, so that two warp scans find a bin
+
 template <int NT>
 struct TopkScratch {
-    uint32_t hist[256];
+    uint32_t hist[kTopkBins];
+    uint32_t coarse[32];
+    uint64_t list[NT];
     uint64_t lo[NT / 32], hi[NT / 32];
     uint64_t range_lo, range_hi;  // the K-th largest key lies in [range_lo, range_hi]
     int need;                     // how many of the keys in it are wanted
-    int done;
-    int count;
+    int state;                    // 0: narrow further, 1: found, 2: few enough to rank
+    int count, listed;
 };
 
-// The K-th largest of the n keys key(0) .. key(n - 1), n >= K >= 1, distinct. All NT threads call it; key(i)
-// may be evaluated several times. Narrows a range of keys by 256 bins at a time: the bins of the present
-// range are counted, and the one that holds the K-th largest becomes the range. It ends as soon as a bin's
-// lower edge has K to K + slack keys at or above it, which for scattered keys and no slack takes two or three
-// passes; the edge is returned.
+// One bin per lane, higher lanes holding larger keys: the lane in which the count from above, which begins at
+// `above`, reaches `need`. `above` becomes the count of the lanes behind it.
+__device__ __forceinline__ int find_bin(uint32_t mine, uint32_t need, uint32_t& above) {
+    const int lane = threadIdx.x & 31;
+    uint32_t incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t o = __shfl_down_sync(~0u, incl, d);
+        if (lane + d < 32) incl += o;
+    }
+    const uint32_t ok = __ballot_sync(~0u, above + incl >= need);
+    const int l = ok ? 31 - __clz(ok) : 0;
+    above += __shfl_sync(~0u, incl - mine, l);
+    return l;
+}
+
+// The K-th largest of the keys key(0) .. key(n - 1), which are distinct; 0 is no key, and K >= 1 of them are
+// others. All NT threads call it, after a barrier if key() reads shared memory; key(i) may be evaluated
+// several times. The keys of the present range are counted in 1024 bins, and the bin that holds the K-th
+// largest becomes the range: if its lower edge has K to K + slack keys at or above it, the edge is the answer;
+// if it holds at most NT keys they are ranked against one another; else the bin is divided again. Scattered keys
+// take one pass to count and one to rank.
 template <int NT, typename Key>
 __device__ uint64_t topk_threshold(int n, int K, int slack, TopkScratch<NT>& s, Key key) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int NW = NT / 32;
     uint64_t lo = ~0ull, hi = 0;
     for (int i = tid; i < n; i += NT) {
         const uint64_t k = key(i);
-        lo = k < lo ? k : lo;
-        hi = k > hi ? k : hi;
+        if (k) {
+            lo = k < lo ? k : lo;
+            hi = k > hi ? k : hi;
+        }
     }
 #pragma unroll
     for (int d = 16; d; d >>= 1) {
@@ -49,61 +73,74 @@ __device__ uint64_t topk_threshold(int n, int K, int slack, TopkScratch<NT>& s, 
         s.lo[warp] = lo;
         s.hi[warp] = hi;
     }
+    for (int i = tid; i < kTopkBins; i += NT) s.hist[i] = 0;
     __syncthreads();
-    if (tid == 0) {
-        for (int i = 1; i < NT / 32; ++i) {
-            lo = s.lo[i] < lo ? s.lo[i] : lo;
-            hi = s.hi[i] > hi ? s.hi[i] : hi;
+    if (warp == 0) {
+        lo = lane < NW ? s.lo[lane] : ~0ull;
+        hi = lane < NW ? s.hi[lane] : 0ull;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) {
+            const uint64_t a = __shfl_xor_sync(~0u, lo, d), c = __shfl_xor_sync(~0u, hi, d);
+            lo = a < lo ? a : lo;
+            hi = c > hi ? c : hi;
         }
-        s.range_lo = lo;
-        s.range_hi = hi;
-        s.need = K;
-        s.done = n <= K + slack;
+        if (lane == 0) {
+            s.range_lo = lo;
+            s.range_hi = hi;
+            s.need = K;
+            s.state = 0;
+            s.listed = 0;
+        }
     }
-    for (int i = tid; i < 256; i += NT) s.hist[i] = 0;
     __syncthreads();
-    // (a round takes 8 bits off the range: at most 8 of them)
-    for (int round = 0; round < 9 && !s.done; ++round) {
+    // (a round takes 10 bits off the range: at most 7 of them)
+    for (int round = 0; round < 8; ++round) {
         const uint64_t r0 = s.range_lo, r1 = s.range_hi;
-        const int need = s.need;
-        const int bits = 64 - __clzll(static_cast<long long>(r1 - r0));  // (r1 - r0) >> shift < 256
-        const int shift = bits > 8 ? bits - 8 : 0;
+        const uint32_t need = static_cast<uint32_t>(s.need);
+        const int bits = 64 - __clzll(static_cast<long long>(r1 - r0));  // (r1 - r0) >> shift < 1024
+        const int shift = bits > 10 ? bits - 10 : 0;
         for (int i = tid; i < n; i += NT) {
             const uint64_t k = key(i);
             if (k >= r0 && k <= r1) atomicAdd(&s.hist[(k - r0) >> shift], 1u);
         }
         __syncthreads();
+        for (int c = warp; c < 32; c += NW) {
+            const uint32_t sum = __reduce_add_sync(~0u, s.hist[32 * c + lane]);
+            if (lane == 0) s.coarse[c] = sum;
+        }
+        __syncthreads();
         if (warp == 0) {
-            // lane l: bins 8 l .. 8 l + 7; `above`: keys in higher lanes' bins
-            uint32_t c[8], sum = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                c[j] = s.hist[8 * lane + j];
-                s.hist[8 * lane + j] = 0;
-                sum += c[j];
+            // the coarse bin, then the fine one, in which the count from above reaches `need`
+            uint32_t above = 0;
+            const int c = find_bin(s.coarse[lane], need, above);
+            const int bin = 32 * c + find_bin(s.hist[32 * c + lane], need, above);
+            if (lane == 0) {
+                const uint32_t in = s.hist[bin];
+                const uint64_t e0 = r0 + (static_cast<uint64_t>(bin) << shift), width = (1ull << shift) - 1;
+                s.range_lo = e0;
+                s.range_hi = r1 - e0 > width ? e0 + width : r1;  // (e0 + width may pass 2^64)
+                s.need = static_cast<int>(need - above);
+                s.state = above + in <= need + slack || shift == 0 ? 1 : in <= NT ? 2 : 0;
             }
-            uint32_t incl = sum;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const uint32_t o = __shfl_down_sync(~0u, incl, d);
-                if (lane + d < 32) incl += o;
-            }
-            uint32_t above = incl - sum;
-            if (above < static_cast<uint32_t>(need) && incl >= static_cast<uint32_t>(need)) {
-#pragma unroll
-                for (int j = 7; j >= 0; --j) {
-                    if (above < static_cast<uint32_t>(need) && above + c[j] >= static_cast<uint32_t>(need)) {
-                        const uint64_t e0 = r0 + (static_cast<uint64_t>(8 * lane + j) << shift);
-                        const uint64_t width = (1ull << shift) - 1;
-                        s.range_lo = e0;
-                        s.range_hi = r1 - e0 > width ? e0 + width : r1;  // (e0 + width may pass 2^64)
-                        s.need = need - static_cast<int>(above);
-                        s.done = above + c[j] <= static_cast<uint32_t>(need + slack) || shift == 0;
-                        break;
-                    }
-                    above += c[j];
-                }
-            }
+        }
+        __syncthreads();
+        if (s.state) break;
+        for (int i = tid; i < kTopkBins; i += NT) s.hist[i] = 0;
+        __syncthreads();
+    }
+    if (s.state == 2) {
+        const uint64_t r0 = s.range_lo, r1 = s.range_hi;
+        for (int i = tid; i < n; i += NT) {
+            const uint64_t k = key(i);
+            if (k >= r0 && k <= r1) s.list[atomicAdd(&s.listed, 1)] = k;
+        }
+        __syncthreads();
+        const int m = s.listed, need = s.need;
+        if (tid < m) {
+            const uint64_t k = s.list[tid];
+            int larger = 0;
+            for (int j = 0; j < m; ++j) larger += s.list[j] > k;
+            if (larger == need - 1) s.range_lo = k;
         }
         __syncthreads();
     }
@@ -113,7 +150,7 @@ __device__ uint64_t topk_threshold(int n, int K, int slack, TopkScratch<NT>& s, 
 }
 
 // Moves the K to K + slack largest of the n > K keys in buf to its front (in no order); their number is left in
-// s.count. Returns a key above which every further candidate must lie: the smallest of them less one. All NT
+// s.count. Returns a key that exactly these lie above, so that further candidates must too. All NT
 // threads call it after a barrier; it ends with one. (Not inlined: its callers' loops stay in the
 // instruction cache.)
 template <int NT>
@@ -123,7 +160,6 @@ __device__ __noinline__ uint64_t topk_compact(uint64_t* buf, int n, int K, int s
     if (tid == 0) s.count = 0;
     __syncthreads();
     // a round reads its NT keys before it writes the ones that stay, which number no more than were read
-    uint64_t least = ~0ull;
     for (int i0 = 0; i0 < n; i0 += NT) {
         const int i = i0 + tid;
         const uint64_t k = i < n ? buf[i] : 0;
@@ -133,22 +169,10 @@ __device__ __noinline__ uint64_t topk_compact(uint64_t* buf, int n, int K, int s
         int first = 0;
         if (lane == 0 && who) first = atomicAdd(&s.count, __popc(who));
         first = __shfl_sync(~0u, first, 0);
-        if (stay) {
-            buf[first + __popc(who & ((1u << lane) - 1))] = k;
-            least = k < least ? k : least;
-        }
+        if (stay) buf[first + __popc(who & ((1u << lane) - 1))] = k;
     }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) {
-        const uint64_t a = __shfl_xor_sync(~0u, least, d);
-        least = a < least ? a : least;
-    }
-    if (lane == 0) s.lo[tid >> 5] = least;
     __syncthreads();
-    least = s.lo[0];
-    for (int i = 1; i < NT / 32; ++i) least = s.lo[i] < least ? s.lo[i] : least;
-    __syncthreads();
-    return least - 1;
+    return edge - 1;
 }
 
 }  // namespace bsp
