@@ -165,29 +165,62 @@ __device__ __forceinline__ Running join(Running a, Running b) {
     r.s = (a.m == kNegInf && !isnan(a.s) ? 0.f : a.s * fa) + (b.m == kNegInf && !isnan(b.s) ? 0.f : b.s * fb);
     return r;
 }
-template <int N>
-__device__ __forceinline__ void add_values(Running& a, const float (&f)[N]) {
-    float top = f[0];
-#pragma unroll
-    for (int i = 1; i < N; ++i) top = fmaxf(top, f[i]);
-    if (top > a.m) {
-        a.s = a.m == kNegInf && !isnan(a.s) ? 0.f : a.s * exp2_approx((shift_of(a.m) - shift_of(top)) * kLog2e);
-        a.m = top;
-    }
-    // (the difference first: x * log2(e) of a row of lowest values would overflow)
-    const float c = shift_of(a.m);
-    float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-        s0 += exp2_approx((f[i] - c) * kLog2e);
-        if (i + 1 < N) s1 += exp2_approx((f[i + 1] - c) * kLog2e);
-    }
-    a.s += s0 + s1;
+// (d0, d1) = (a0 * b + c, a1 * b + c); (s0, s1) += (a0, a1): two fp32 values an instruction
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b, float c) {
+    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %4};\n\tmov.b64 rc, {%5, %5};\n\t"
+        "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b), "f"(c));
 }
+__device__ __forceinline__ void mul2(float& d0, float& d1, float b) {
+    asm("{\n\t.reg .b64 ra, rb;\n\tmov.b64 ra, {%0, %1};\n\tmov.b64 rb, {%2, %2};\n\t"
+        "mul.rn.f32x2 ra, ra, rb;\n\tmov.b64 {%0, %1}, ra;\n\t}"
+        : "+f"(d0), "+f"(d1) : "f"(b));
+}
+__device__ __forceinline__ void add2(float& s0, float& s1, float a0, float a1) {
+    asm("{\n\t.reg .b64 rs, ra;\n\tmov.b64 rs, {%0, %1};\n\tmov.b64 ra, {%2, %3};\n\t"
+        "add.rn.f32x2 rs, rs, ra;\n\tmov.b64 {%0, %1}, rs;\n\t}"
+        : "+f"(s0), "+f"(s1) : "f"(a0), "f"(a1));
+}
+
+// A running maximum and sum of one thread, the sum in two halves.
+struct RowSum {
+    float m = kNegInf, s0 = 0.f, s1 = 0.f;
+    float c = 0.f;       // -shift * log2(e), where that is well inside fp32
+    bool far = false;    // it is not: a row of lowest (or highest) values, whose x * log2(e) would overflow
+
+    // values of which `top` is the largest
+    template <int N>
+    __device__ __forceinline__ void add(const float (&f)[N], float top) {
+        if (top > m) {
+            const float r = m == kNegInf ? 0.f : exp2_approx((shift_of(m) - shift_of(top)) * kLog2e);
+            // (a sum of 0 stays 0, a NaN stays NaN)
+            s0 = s0 == 0.f ? 0.f : (m == kNegInf ? s0 : s0 * r);
+            s1 = s1 == 0.f ? 0.f : (m == kNegInf ? s1 : s1 * r);
+            m = top;
+            far = fabsf(shift_of(m)) > 1e30f;
+            c = -shift_of(m) * kLog2e;
+        }
+        if (N == 1) {
+            s0 += exp2_approx((f[0] - shift_of(m)) * kLog2e);
+        } else if (!far) {
+#pragma unroll
+            for (int i = 0; i + 1 < N; i += 2) {
+                float d0, d1;
+                fma2(d0, d1, f[i], f[i + 1], kLog2e, c);
+                add2(s0, s1, exp2_approx(d0), exp2_approx(d1));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i + 1 < N; i += 2)
+                add2(s0, s1, exp2_approx((f[i] - shift_of(m)) * kLog2e), exp2_approx((f[i + 1] - shift_of(m)) * kLog2e));
+        }
+    }
+};
 
 // ---------------------------------------------------------------- process
 
-constexpr int kProcThreads = 512;
+constexpr int kProcThreads = 256;
 
 struct HashSlot {
     uint32_t token;  // token + 1; 0: empty
@@ -237,12 +270,16 @@ __device__ __forceinline__ void store_at_rank(const void* p, uint32_t rank, floa
 // One cluster per row, each CTA a slice of the vocabulary. Tokens that the lists name are marked in two
 // bitmaps of the slice (penalised; in the table of counts and biases), so that a 16-byte vector without a
 // marked token costs two shared-memory words; a vector whose tokens the grammar rejects is not read at all.
+// The lists, their lengths and the mask are fetched together, and with no mask the first logits before them:
+// a row is short beside their latencies, which several CTAs per SM hide from one another. Bound by the
+// logits' traffic, and by the exponentials' instructions where nothing is masked.
 template <int DT>
-__global__ void __launch_bounds__(kProcThreads) process_logits_kernel(const ProcessParams p) {
+__global__ void __launch_bounds__(kProcThreads, 4) process_logits_kernel(const ProcessParams p) {
     using L = Logit<DT>;
     using T = typename L::T;
     constexpr int E = L::E;
     constexpr int U = 4;  // vectors in flight per thread
+    constexpr uint32_t ALL = (1u << E) - 1;
     extern __shared__ uint32_t smem[];
     __shared__ Running s_part[kProcThreads / 32];
     __shared__ float s_m[16], s_s[16];
@@ -267,6 +304,7 @@ __global__ void __launch_bounds__(kProcThreads) process_logits_kernel(const Proc
     // bit i of the bitmaps is token base + i; vectors start at multiples of E bits
     const int base = rank == 0 && head > 0 ? head - E : lo;
     const bool vec_out = ((reinterpret_cast<uintptr_t>(out + head)) & 15) == 0;
+    const uint4* xv = reinterpret_cast<const uint4*>(x + head);
 
     uint32_t* bm_pen = smem;
     uint32_t* bm_hot = bm_pen + p.bitmap_words;
@@ -275,63 +313,80 @@ __global__ void __launch_bounds__(kProcThreads) process_logits_kernel(const Proc
     const uint32_t hmask = p.hash_slots - 1;
     const int words = (hi - base + 31) >> 5;
     const bool counts = p.frequency || p.presence;
+    const bool pens = p.repetition && (p.prompt_tokens || p.tokens), hots = p.hash_slots > 0;
 
-    const uint32_t* mrow = mask_row(p.mask, r, p.status, rank == 0 && tid == 0);
-    for (int i = tid; i < words; i += kProcThreads) {
-        bm_pen[i] = 0;
-        bm_hot[i] = 0;
-        if (mrow) bm_mask[i] = mask_bits(mrow, (p.vocab + 31) >> 5, base + 32 * i);
+    uint4 val[U];
+    if (!p.mask.bits) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (v0 + tid + u * kProcThreads < v1) val[u] = __ldcs(xv + v0 + tid + u * kProcThreads);
     }
-    for (int i = tid; i < p.hash_slots; i += kProcThreads) table[i] = HashSlot{0u, 0u, ~0u};
-    __syncthreads();
-    auto mark = [&](uint32_t* bm, int t) { atomicOr(bm + ((t - base) >> 5), 1u << ((t - base) & 31)); };
-    if (p.repetition && p.prompt_tokens) {
-        const int n = max(0, min(__ldg(p.prompt_len + b), p.prompt_cols));
-        const int32_t* list = p.prompt_tokens + static_cast<long long>(b) * p.prompt_stride;
-        for (int i = tid; i < n; i += kProcThreads) {
-            const int t = __ldg(list + i);
-            if (t >= lo && t < hi) mark(bm_pen, t);
-        }
-    }
-    if (p.tokens && (p.repetition || counts)) {
-        const int n = max(0, min(__ldg(p.token_len + r), p.token_cols));
-        const int32_t* list = p.tokens + static_cast<long long>(r) * p.token_stride;
-        for (int i = tid; i < n; i += kProcThreads) {
-            const int t = __ldg(list + i);
-            if (t >= lo && t < hi) {
-                if (p.repetition) mark(bm_pen, t);
-                if (counts) {
-                    mark(bm_hot, t);
-                    if (HashSlot* s = hash_claim(table, hmask, t)) atomicAdd(&s->count, 1u);
-                }
-            }
-        }
-    }
-    if (p.bias_tokens) {
-        const int n = p.bias_len ? max(0, min(__ldg(p.bias_len + b), p.bias_cols)) : p.bias_cols;
-        const int32_t* list = p.bias_tokens + static_cast<long long>(b) * p.bias_stride;
-        for (int i = tid; i < n; i += kProcThreads) {
-            const int t = __ldg(list + i);
-            if (t >= lo && t < hi) {
-                mark(bm_hot, t);
-                // an id given twice: its first value counts
-                if (HashSlot* s = hash_claim(table, hmask, t)) atomicMin(&s->bias, static_cast<uint32_t>(i));
-            }
-        }
-    }
+    // the lists' first entries, whatever their lengths
+    const int32_t* prompt = p.prompt_tokens + static_cast<long long>(b) * p.prompt_stride;
+    const int32_t* made = p.tokens + static_cast<long long>(r) * p.token_stride;
+    const int32_t* biased = p.bias_tokens + static_cast<long long>(b) * p.bias_stride;
+    const int first_p = p.prompt_tokens && tid < p.prompt_cols ? __ldg(prompt + tid) : -1;
+    const int first_t = p.tokens && tid < p.token_cols ? __ldg(made + tid) : -1;
+    const int first_b = p.bias_tokens && tid < p.bias_cols ? __ldg(biased + tid) : -1;
+    const int n_p = p.prompt_tokens ? min(__ldg(p.prompt_len + b), p.prompt_cols) : 0;
+    const int n_t = p.tokens ? min(__ldg(p.token_len + r), p.token_cols) : 0;
+    const int n_b = !p.bias_tokens ? 0 : p.bias_len ? min(__ldg(p.bias_len + b), p.bias_cols) : p.bias_cols;
     const float rep = p.repetition ? __ldg(p.repetition + b) : 1.f;
     const float freq = p.frequency ? __ldg(p.frequency + b) : 0.f;
     const float pres = p.presence ? __ldg(p.presence + b) : 0.f;
+    const float temperature = p.temperature ? __ldg(p.temperature + b) : 1.f;
+    const uint32_t* mrow = mask_row(p.mask, r, p.status, rank == 0 && tid == 0);
+    if (pens)
+        for (int i = tid; i < words; i += kProcThreads) bm_pen[i] = 0;
+    if (hots) {
+        for (int i = tid; i < words; i += kProcThreads) bm_hot[i] = 0;
+        for (int i = tid; i < p.hash_slots; i += kProcThreads) table[i] = HashSlot{0u, 0u, ~0u};
+    }
+    bool dense = !mrow;  // some 32 tokens of the slice have more than 8 allowed ones
+    if (mrow)
+        for (int i = tid; i < words; i += kProcThreads) {
+            const uint32_t m = mask_bits(mrow, (p.vocab + 31) >> 5, base + 32 * i);
+            bm_mask[i] = m;
+            dense |= __popc(m) > 8;
+        }
+    if (pens || hots || mrow) dense = __syncthreads_or(dense);
+    if (pens || hots) {
+        auto mark = [&](uint32_t* bm, int t) { atomicOr(bm + ((t - base) >> 5), 1u << ((t - base) & 31)); };
+        if (pens)
+            for (int i = tid, t = first_p; i < n_p; i += kProcThreads) {
+                if (i != tid) t = __ldg(prompt + i);
+                if (t >= lo && t < hi) mark(bm_pen, t);
+            }
+        for (int i = tid, t = first_t; i < n_t; i += kProcThreads) {
+            if (i != tid) t = __ldg(made + i);
+            if (t < lo || t >= hi) continue;
+            if (pens) mark(bm_pen, t);
+            if (counts) {
+                mark(bm_hot, t);
+                if (HashSlot* s = hash_claim(table, hmask, t)) atomicAdd(&s->count, 1u);
+            }
+        }
+        for (int i = tid, t = first_b; i < n_b; i += kProcThreads) {
+            if (i != tid) t = __ldg(biased + i);
+            if (t < lo || t >= hi) continue;
+            mark(bm_hot, t);
+            // an id given twice: its first value counts
+            if (HashSlot* s = hash_claim(table, hmask, t)) atomicMin(&s->bias, static_cast<uint32_t>(i));
+        }
+        __syncthreads();
+    }
     // the product with the rounded reciprocal: 1.5 half-steps of fp32 from the quotient, one multiplication
     // per logit in place of a division
-    const float inv_t = p.temperature ? __frcp_rn(__ldg(p.temperature + b)) : 1.f;
-    const float* bias = p.bias_values ? p.bias_values + static_cast<long long>(b) * p.bias_stride : nullptr;
-    __syncthreads();
+    const float inv_t = __frcp_rn(temperature);
+    const float* bias = p.bias_values + static_cast<long long>(b) * p.bias_stride;
 
+    auto marked_bits = [&](int i) -> uint32_t {
+        return (pens ? bm_pen[i >> 5] >> (i & 31) : 0u) | (hots ? bm_hot[i >> 5] >> (i & 31) : 0u);
+    };
     auto change = [&](float v, int t) -> float {  // a marked token, before the temperature
         const int i = t - base;
-        if ((bm_pen[i >> 5] >> (i & 31)) & 1u) v = v > 0.f ? __fdiv_rn(v, rep) : __fmul_rn(v, rep);
-        if ((bm_hot[i >> 5] >> (i & 31)) & 1u) {
+        if (pens && ((bm_pen[i >> 5] >> (i & 31)) & 1u)) v = v > 0.f ? __fdiv_rn(v, rep) : __fmul_rn(v, rep);
+        if (hots && ((bm_hot[i >> 5] >> (i & 31)) & 1u)) {
             const HashSlot* s = hash_find(table, hmask, static_cast<uint32_t>(t));
             if (s) {
                 if (s->count) {
@@ -344,7 +399,7 @@ __global__ void __launch_bounds__(kProcThreads) process_logits_kernel(const Proc
         return v;
     };
 
-    Running run{kNegInf, 0.f};
+    RowSum sum;
     const bool temp = p.temperature != nullptr;
     // the ragged ends, one element per thread
     {
@@ -356,60 +411,117 @@ __global__ void __launch_bounds__(kProcThreads) process_logits_kernel(const Proc
             const int i = t - base;
             float f[1] = {kNegInf};
             if (!mrow || ((bm_mask[i >> 5] >> (i & 31)) & 1u)) {
-                f[0] = change(L::get(x[t]), t);
+                f[0] = L::get(x[t]);
+                if (marked_bits(i) & 1u) f[0] = change(f[0], t);
                 if (temp) f[0] = __fmul_rn(f[0], inv_t);
             }
             const T y = L::put(f[0]);
             out[t] = y;
             f[0] = L::get(y);
-            add_values(run, f);
+            sum.add(f, f[0]);
         }
     }
-    const uint4* xv = reinterpret_cast<const uint4*>(x + head);
-    constexpr uint32_t ALL = (1u << E) - 1;
-    for (int vb = v0 + tid; vb < v1; vb += U * kProcThreads) {
-        uint4 val[U];
-        uint32_t keep[U];
+    if (!dense) {
+        // A sparse mask: a warp takes 32 words of it (1024 tokens), a lane a word; the allowed logits are read
+        // one by one into the warp's piece of the output in shared memory, all else of which is -inf.
+        uint4* piece = reinterpret_cast<uint4*>(table + p.hash_slots) + (tid >> 5) * (1024 / E);
+        const int lane = tid & 31;
+        const int first = rank == 0 && head > 0 ? 1 : 0;  // the ragged head stands in the first E bits
+        for (int j0 = (tid >> 5) * 32; j0 < words; j0 += (kProcThreads / 32) * 32) {
+            uint32_t bits = j0 + lane < words ? bm_mask[j0 + lane] : 0u;
+            const int t0 = base + 32 * (j0 + lane);  // token of the word's first bit
+            // only the vectors' tokens
+            const int skip = head + v0 * E - t0, left = head + v1 * E - t0;
+            if (skip > 0) bits &= ~((1u << skip) - 1);
+            if (left < 32) bits &= left > 0 ? (1u << left) - 1 : 0u;
+            const bool some = __any_sync(~0u, bits != 0);
+            const uint4 none = make_uint4(L::kNegInfPair, L::kNegInfPair, L::kNegInfPair, L::kNegInfPair);
+            if (some) {
+#pragma unroll
+                for (int q = 0; q < 32 / E; ++q) piece[lane + 32 * q] = none;
+                __syncwarp();
+                T* mine = reinterpret_cast<T*>(piece) + 32 * lane;
+                while (__any_sync(~0u, bits != 0)) {
+                    if (bits) {
+                        const int e = __ffs(bits) - 1;
+                        bits &= bits - 1;
+                        float f[1] = {L::get(x[t0 + e])};
+                        if (marked_bits(t0 + e - base) & 1u) f[0] = change(f[0], t0 + e);
+                        if (temp) f[0] = __fmul_rn(f[0], inv_t);
+                        const T y = L::put(f[0]);
+                        mine[e] = y;
+                        f[0] = L::get(y);
+                        sum.add(f, f[0]);
+                    }
+                }
+                __syncwarp();
+            }
+#pragma unroll
+            for (int q = 0; q < 32 / E; ++q) {
+                const int v = v0 - first + 32 * j0 / E + lane + 32 * q;
+                if (v < v0 || v >= v1) continue;
+                const uint4 res = some ? piece[lane + 32 * q] : none;
+                if (vec_out) {
+                    __stcs(reinterpret_cast<uint4*>(out + head + v * E), res);
+                } else {
+                    const T* e = reinterpret_cast<const T*>(&res);
+#pragma unroll
+                    for (int k = 0; k < E; ++k) out[head + v * E + k] = e[k];
+                }
+            }
+            __syncwarp();
+        }
+    }
+    bool loaded = !p.mask.bits;  // the first vectors are there
+    for (int vb = v0 + tid; dense && vb < v1; vb += U * kProcThreads) {
+        uint32_t keep = 0;  // E bits per vector
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int v = vb + u * kProcThreads;
             const int i = head + v * E - base;
-            keep[u] = v >= v1 ? 0u : mrow ? (bm_mask[i >> 5] >> (i & 31)) & ALL : ALL;
-            if (keep[u]) val[u] = __ldcs(xv + v);
+            const uint32_t k = v >= v1 ? 0u : mrow ? (bm_mask[i >> 5] >> (i & 31)) & ALL : ALL;
+            if (k && !loaded) val[u] = __ldcs(xv + v);
+            keep |= k << (E * u);
         }
+        loaded = false;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int v = vb + u * kProcThreads;
             if (v >= v1) break;
             const int t0 = head + v * E, i = t0 - base;
+            const uint32_t k = (keep >> (E * u)) & ALL;
             uint4 res = make_uint4(L::kNegInfPair, L::kNegInfPair, L::kNegInfPair, L::kNegInfPair);
             bool changed = true;
-            if (keep[u]) {
+            if (k) {
                 float f[E];
                 L::unpack(val[u], f);
-                const uint32_t marked = ((bm_pen[i >> 5] | bm_hot[i >> 5]) >> (i & 31)) & ALL & keep[u];
-                changed = temp || marked || keep[u] != ALL;
+                const uint32_t marked = marked_bits(i) & k;
+                changed = temp || marked || k != ALL;
                 if (changed) {
-                    if (marked) {
+                    for (uint32_t todo = marked; todo; todo &= todo - 1) {
+                        const int e = __ffs(todo) - 1;
+                        float v = f[0];
 #pragma unroll
-                        for (int e = 0; e < E; ++e)
-                            if ((marked >> e) & 1u) f[e] = change(f[e], t0 + e);
+                        for (int q = 1; q < E; ++q) v = e == q ? f[q] : v;
+                        v = change(v, t0 + e);
+#pragma unroll
+                        for (int q = 0; q < E; ++q) f[q] = e == q ? v : f[q];
                     }
                     if (temp) {
 #pragma unroll
-                        for (int e = 0; e < E; ++e) f[e] = __fmul_rn(f[e], inv_t);
+                        for (int e = 0; e < E; e += 2) mul2(f[e], f[e + 1], inv_t);
                     }
-                    if (keep[u] != ALL) {
+                    if (k != ALL) {
 #pragma unroll
                         for (int e = 0; e < E; ++e)
-                            if (!((keep[u] >> e) & 1u)) f[e] = kNegInf;
+                            if (!((k >> e) & 1u)) f[e] = kNegInf;
                     }
                     res = L::pack(f);
                     L::unpack(res, f);  // the log-sum-exp is that of the stored values
                 } else {
                     res = val[u];
                 }
-                add_values(run, f);
+                sum.add(f, L::top(L::max2(L::max2(res.x, res.y), L::max2(res.z, res.w))));
             }
             if (!in_place || changed) {
                 if (vec_out) {
@@ -417,7 +529,7 @@ __global__ void __launch_bounds__(kProcThreads) process_logits_kernel(const Proc
                 } else {
                     const T* e = reinterpret_cast<const T*>(&res);
 #pragma unroll
-                    for (int k = 0; k < E; ++k) out[t0 + k] = e[k];
+                    for (int q = 0; q < E; ++q) out[t0 + q] = e[q];
                 }
             }
         }
@@ -425,6 +537,7 @@ __global__ void __launch_bounds__(kProcThreads) process_logits_kernel(const Proc
 
     // ---- the row's log-sum-exp: warp, CTA, cluster
     if (!p.lse) return;  // uniform
+    Running run{sum.m, sum.s0 + sum.s1};
 #pragma unroll
     for (int d = 16; d; d >>= 1) {
         Running o;
@@ -881,6 +994,8 @@ cudaError_t launch_scan(const SelectParams& p, cudaStream_t stream) {
 }
 
 }  // namespace
+
+size_t process_piece_bytes(int dtype) { return static_cast<size_t>(kProcThreads / 32) * 1024 * (dtype == BSP_LOGITS_FP32 ? 4 : 2); }
 
 cudaError_t launch_process(int dtype, const ProcessParams& p, int cluster, size_t smem, cudaStream_t stream) {
     switch (dtype) {

@@ -175,7 +175,7 @@ bsp_status bsp_process_logits(const bsp_plan_t* plan, const void* logits, int32_
     p.W = plan->beam_width;
     const int64_t named = (counts ? p.token_cols : 0) + static_cast<int64_t>(p.bias_cols);
     if (named > BSP_MAX_LISTED) return BSP_ERR_UNSUPPORTED;
-    p.hash_slots = named ? 1 << ilog2(static_cast<int>(2 * named)) : 0;
+    p.hash_slots = named ? std::max(4, 1 << ilog2(static_cast<int>(2 * named))) : 0;
 
     // One cluster per row. Many rows fill the SMs with one CTA each; fewer rows are cut into up to 8 slices
     // so that all SMs take part, as far as a slice keeps a vector per thread, and a long row until a CTA's
@@ -186,8 +186,10 @@ bsp_status bsp_process_logits(const bsp_plan_t* plan, const void* logits, int32_
         cluster *= 2;
     size_t smem = 0;
     for (;; cluster *= 2) {
-        p.bitmap_words = static_cast<int>((ceil_div(vocab, cluster) + 48) / 32 + 2);
-        smem = static_cast<size_t>(p.bitmap_words) * 12 + static_cast<size_t>(p.hash_slots) * kProcessSlotBytes;
+        p.bitmap_words = static_cast<int>(((ceil_div(vocab, cluster) + 48) / 32 + 2 + 3) / 4 * 4);
+        // three bitmaps, the table, and for masked rows a piece of the output per warp
+        smem = static_cast<size_t>(p.bitmap_words) * 12 + static_cast<size_t>(p.hash_slots) * kProcessSlotBytes +
+               (p.mask.bits ? process_piece_bytes(logits_dtype) : 0);
         if (smem <= kMaxSmem - 2048) break;
         if (cluster == 8) return BSP_ERR_UNSUPPORTED;
     }
