@@ -191,7 +191,6 @@ struct ProcessParams {
     int hash_slots;    // slots of the table of counts and biases (a power of two), 0: none
 };
 constexpr int kProcessSlotBytes = 12;
-size_t process_piece_bytes(int dtype);
 cudaError_t launch_process(int dtype, const ProcessParams& p, int cluster, size_t smem, cudaStream_t stream);
 
 struct SelectParams {

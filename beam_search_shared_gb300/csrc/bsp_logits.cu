@@ -183,37 +183,39 @@ __device__ __forceinline__ void add2(float& s0, float& s1, float a0, float a1) {
         : "+f"(s0), "+f"(s1) : "f"(a0), "f"(a1));
 }
 
-// A running maximum and sum of one thread, the sum in two halves.
+// One thread's sum of exp(x - m), in two halves. m is a value of the row, at most 16 below the largest so far: it
+// is raised only when one stands further above it, which after the first vector hardly happens, and
+// exp(16) times a vocabulary is well inside fp32.
 struct RowSum {
-    float m = kNegInf, s0 = 0.f, s1 = 0.f;
+    float m = kNegInf, limit = kNegInf, s0 = 0.f, s1 = 0.f;
     float c = 0.f;       // -shift * log2(e), where that is well inside fp32
     bool far = false;    // it is not: a row of lowest (or highest) values, whose x * log2(e) would overflow
 
+    __device__ __noinline__ static RowSum raised(RowSum o, float top) {
+        const float r = o.m == kNegInf ? 1.f : exp2_approx((shift_of(o.m) - shift_of(top)) * kLog2e);
+        o.s0 = o.s0 == 0.f ? 0.f : o.s0 * r;  // (a sum of 0 stays 0, a NaN stays NaN)
+        o.s1 = o.s1 == 0.f ? 0.f : o.s1 * r;
+        o.m = top;
+        o.limit = top + 16.f;
+        o.far = fabsf(shift_of(top)) > 1e30f;
+        o.c = -shift_of(top) * kLog2e;
+        return o;
+    }
     // values of which `top` is the largest
     template <int N>
     __device__ __forceinline__ void add(const float (&f)[N], float top) {
-        if (top > m) {
-            const float r = m == kNegInf ? 0.f : exp2_approx((shift_of(m) - shift_of(top)) * kLog2e);
-            // (a sum of 0 stays 0, a NaN stays NaN)
-            s0 = s0 == 0.f ? 0.f : (m == kNegInf ? s0 : s0 * r);
-            s1 = s1 == 0.f ? 0.f : (m == kNegInf ? s1 : s1 * r);
-            m = top;
-            far = fabsf(shift_of(m)) > 1e30f;
-            c = -shift_of(m) * kLog2e;
-        }
-        if (N == 1) {
-            s0 += exp2_approx((f[0] - shift_of(m)) * kLog2e);
-        } else if (!far) {
+        if (top > limit) *this = raised(*this, top);
+        if (far || N == 1) {
+            const float sh = shift_of(m);
+#pragma unroll
+            for (int i = 0; i < N; ++i) s0 += exp2_approx((f[i] - sh) * kLog2e);
+        } else {
 #pragma unroll
             for (int i = 0; i + 1 < N; i += 2) {
                 float d0, d1;
                 fma2(d0, d1, f[i], f[i + 1], kLog2e, c);
                 add2(s0, s1, exp2_approx(d0), exp2_approx(d1));
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i + 1 < N; i += 2)
-                add2(s0, s1, exp2_approx((f[i] - shift_of(m)) * kLog2e), exp2_approx((f[i + 1] - shift_of(m)) * kLog2e));
         }
     }
 };
@@ -221,6 +223,7 @@ struct RowSum {
 // ---------------------------------------------------------------- process
 
 constexpr int kProcThreads = 256;
+constexpr int kProcListed = 768;  // marked vectors of a slice put aside
 
 struct HashSlot {
     uint32_t token;  // token + 1; 0: empty
@@ -283,6 +286,9 @@ __global__ void __launch_bounds__(kProcThreads, 4) process_logits_kernel(const P
     extern __shared__ uint32_t smem[];
     __shared__ Running s_part[kProcThreads / 32];
     __shared__ float s_m[16], s_s[16];
+    __shared__ uint4 s_vec[kProcListed];  // marked vectors put aside, and their numbers
+    __shared__ int s_list[kProcListed];
+    __shared__ int s_listed;
 
     const int tid = threadIdx.x;
     const int rank = static_cast<int>(cluster_rank()), ranks = static_cast<int>(cluster_size());
@@ -342,6 +348,7 @@ __global__ void __launch_bounds__(kProcThreads, 4) process_logits_kernel(const P
         for (int i = tid; i < words; i += kProcThreads) bm_hot[i] = 0;
         for (int i = tid; i < p.hash_slots; i += kProcThreads) table[i] = HashSlot{0u, 0u, ~0u};
     }
+    if (tid == 0) s_listed = 0;
     bool dense = !mrow;  // some 32 tokens of the slice have more than 8 allowed ones
     if (mrow)
         for (int i = tid; i < words; i += kProcThreads) {
@@ -421,117 +428,166 @@ __global__ void __launch_bounds__(kProcThreads, 4) process_logits_kernel(const P
             sum.add(f, f[0]);
         }
     }
+    // one vector of the output
+    auto store = [&](int v, const uint4& res) {
+        if (vec_out) {
+            __stcs(reinterpret_cast<uint4*>(out + head + v * E), res);
+        } else {
+            const T* e = reinterpret_cast<const T*>(&res);
+#pragma unroll
+            for (int q = 0; q < E; ++q) out[head + v * E + q] = e[q];
+        }
+    };
     if (!dense) {
-        // A sparse mask: a warp takes 32 words of it (1024 tokens), a lane a word; the allowed logits are read
-        // one by one into the warp's piece of the output in shared memory, all else of which is -inf.
-        uint4* piece = reinterpret_cast<uint4*>(table + p.hash_slots) + (tid >> 5) * (1024 / E);
+        // A sparse mask: a warp takes 32 words of it at a time (1024 tokens), a lane a word, and lists the allowed
+        // tokens of as many such chunks as give up to 256; reads their logits, 8 a lane at once; fills the chunks
+        // with -inf; and puts the processed logits in their places.
+        constexpr int R = 8;
         const int lane = tid & 31;
+        int* list = reinterpret_cast<int*>(s_vec) + (tid >> 5) * (32 * R);
         const int first = rank == 0 && head > 0 ? 1 : 0;  // the ragged head stands in the first E bits
-        for (int j0 = (tid >> 5) * 32; j0 < words; j0 += (kProcThreads / 32) * 32) {
+        constexpr int step = kProcThreads;                // words of all warps' chunks
+        int j_from = (tid >> 5) * 32, n = 0;              // the first chunk of the list, and its tokens
+        auto flush = [&](int j_to) {                      // chunks j_from, j_from + step, .. before j_to
+            float f[R];
+#pragma unroll
+            for (int q = 0; q < R; ++q)
+                if (lane + 32 * q < n) f[q] = L::get(x[list[lane + 32 * q]]);
+            __syncwarp();
+            const uint4 none = make_uint4(L::kNegInfPair, L::kNegInfPair, L::kNegInfPair, L::kNegInfPair);
+            for (int j0 = j_from; j0 < j_to; j0 += step)
+#pragma unroll
+                for (int q = 0; q < 32 / E; ++q) {
+                    const int v = v0 - first + 32 * j0 / E + lane + 32 * q;
+                    if (v >= v0 && v < v1) store(v, none);
+                }
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < R; ++q)
+                if (lane + 32 * q < n) {
+                    const int t = list[lane + 32 * q];
+                    float y[1] = {f[q]};
+                    if (marked_bits(t - base) & 1u) y[0] = change(y[0], t);
+                    if (temp) y[0] = __fmul_rn(y[0], inv_t);
+                    const T o = L::put(y[0]);
+                    out[t] = o;
+                    y[0] = L::get(o);
+                    sum.add(y, y[0]);
+                }
+            __syncwarp();
+            n = 0;
+            j_from = j_to;
+        };
+        int j0 = j_from;
+        for (; j0 < words; j0 += step) {
             uint32_t bits = j0 + lane < words ? bm_mask[j0 + lane] : 0u;
             const int t0 = base + 32 * (j0 + lane);  // token of the word's first bit
             // only the vectors' tokens
             const int skip = head + v0 * E - t0, left = head + v1 * E - t0;
             if (skip > 0) bits &= ~((1u << skip) - 1);
             if (left < 32) bits &= left > 0 ? (1u << left) - 1 : 0u;
-            const bool some = __any_sync(~0u, bits != 0);
-            const uint4 none = make_uint4(L::kNegInfPair, L::kNegInfPair, L::kNegInfPair, L::kNegInfPair);
-            if (some) {
+            int at = __popc(bits);
 #pragma unroll
-                for (int q = 0; q < 32 / E; ++q) piece[lane + 32 * q] = none;
-                __syncwarp();
-                T* mine = reinterpret_cast<T*>(piece) + 32 * lane;
-                while (__any_sync(~0u, bits != 0)) {
-                    if (bits) {
-                        const int e = __ffs(bits) - 1;
-                        bits &= bits - 1;
-                        float f[1] = {L::get(x[t0 + e])};
-                        if (marked_bits(t0 + e - base) & 1u) f[0] = change(f[0], t0 + e);
-                        if (temp) f[0] = __fmul_rn(f[0], inv_t);
-                        const T y = L::put(f[0]);
-                        mine[e] = y;
-                        f[0] = L::get(y);
-                        sum.add(f, f[0]);
-                    }
-                }
-                __syncwarp();
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(~0u, at, d);
+                if (lane >= d) at += o;
             }
-#pragma unroll
-            for (int q = 0; q < 32 / E; ++q) {
-                const int v = v0 - first + 32 * j0 / E + lane + 32 * q;
-                if (v < v0 || v >= v1) continue;
-                const uint4 res = some ? piece[lane + 32 * q] : none;
-                if (vec_out) {
-                    __stcs(reinterpret_cast<uint4*>(out + head + v * E), res);
-                } else {
-                    const T* e = reinterpret_cast<const T*>(&res);
-#pragma unroll
-                    for (int k = 0; k < E; ++k) out[head + v * E + k] = e[k];
-                }
-            }
+            const int more = __shfl_sync(~0u, at, 31);
+            if (n + more > 32 * R) flush(j0);
+            at += n - __popc(bits);
+            for (; bits; bits &= bits - 1) list[at++] = t0 + __ffs(bits) - 1;
+            n += more;
             __syncwarp();
         }
+        flush(j0);
     }
-    bool loaded = !p.mask.bits;  // the first vectors are there
-    for (int vb = v0 + tid; dense && vb < v1; vb += U * kProcThreads) {
-        uint32_t keep = 0;  // E bits per vector
+
+    // temperature, mask, rounding, the sum of the stored values, and the store
+    auto finish = [&](int v, uint32_t k, float (&f)[E]) {
+        if (temp) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int v = vb + u * kProcThreads;
-            const int i = head + v * E - base;
-            const uint32_t k = v >= v1 ? 0u : mrow ? (bm_mask[i >> 5] >> (i & 31)) & ALL : ALL;
-            if (k && !loaded) val[u] = __ldcs(xv + v);
-            keep |= k << (E * u);
+            for (int e = 0; e < E; e += 2) mul2(f[e], f[e + 1], inv_t);
         }
-        loaded = false;
+        if (k != ALL) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int v = vb + u * kProcThreads;
-            if (v >= v1) break;
-            const int t0 = head + v * E, i = t0 - base;
-            const uint32_t k = (keep >> (E * u)) & ALL;
-            uint4 res = make_uint4(L::kNegInfPair, L::kNegInfPair, L::kNegInfPair, L::kNegInfPair);
-            bool changed = true;
-            if (k) {
+            for (int e = 0; e < E; ++e)
+                if (!((k >> e) & 1u)) f[e] = kNegInf;
+        }
+        const uint4 res = L::pack(f);
+        L::unpack(res, f);  // the log-sum-exp is that of the stored values
+        sum.add(f, L::top(L::max2(L::max2(res.x, res.y), L::max2(res.z, res.w))));
+        store(v, res);
+    };
+    // a vector with marked tokens
+    auto finish_marked = [&](int v, const uint4& raw) {
+        const int t0 = head + v * E, i = t0 - base;
+        const uint32_t k = mrow ? (bm_mask[i >> 5] >> (i & 31)) & ALL : ALL;
+        float f[E];
+        L::unpack(raw, f);
+        for (uint32_t todo = marked_bits(i) & k; todo; todo &= todo - 1) {
+            const int e = __ffs(todo) - 1;
+            float y = f[0];
+#pragma unroll
+            for (int q = 1; q < E; ++q) y = e == q ? f[q] : y;
+            y = change(y, t0 + e);
+#pragma unroll
+            for (int q = 0; q < E; ++q) f[q] = e == q ? y : f[q];
+        }
+        finish(v, k, f);
+    };
+    if (dense) {
+        // all vectors of the slice but those with a marked token: these are listed, as far as the list goes, so
+        // that afterwards a warp has one for each lane
+        bool loaded = !p.mask.bits;  // the first vectors are there
+        for (int vb = v0 + tid; vb < v1; vb += U * kProcThreads) {
+            uint32_t keep = 0;  // E bits per vector
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int v = vb + u * kProcThreads;
+                const int i = head + v * E - base;
+                const uint32_t k = v >= v1 ? 0u : mrow ? (bm_mask[i >> 5] >> (i & 31)) & ALL : ALL;
+                if (k && !loaded) val[u] = __ldcs(xv + v);
+                keep |= k << (E * u);
+            }
+            loaded = false;
+            uint32_t late = 0;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int v = vb + u * kProcThreads;
+                if (v >= v1) break;
+                const uint32_t k = (keep >> (E * u)) & ALL;
+                if (!k) {
+                    store(v, make_uint4(L::kNegInfPair, L::kNegInfPair, L::kNegInfPair, L::kNegInfPair));
+                    continue;
+                }
+                if ((pens || hots) && (marked_bits(head + v * E - base) & k)) {
+                    const int at = atomicAdd(&s_listed, 1);
+                    if (at < kProcListed) {
+                        s_list[at] = v;
+                        s_vec[at] = val[u];
+                    } else {
+                        late |= 1u << u;
+                    }
+                    continue;
+                }
                 float f[E];
                 L::unpack(val[u], f);
-                const uint32_t marked = marked_bits(i) & k;
-                changed = temp || marked || k != ALL;
-                if (changed) {
-                    for (uint32_t todo = marked; todo; todo &= todo - 1) {
-                        const int e = __ffs(todo) - 1;
-                        float v = f[0];
-#pragma unroll
-                        for (int q = 1; q < E; ++q) v = e == q ? f[q] : v;
-                        v = change(v, t0 + e);
-#pragma unroll
-                        for (int q = 0; q < E; ++q) f[q] = e == q ? v : f[q];
-                    }
-                    if (temp) {
-#pragma unroll
-                        for (int e = 0; e < E; e += 2) mul2(f[e], f[e + 1], inv_t);
-                    }
-                    if (k != ALL) {
-#pragma unroll
-                        for (int e = 0; e < E; ++e)
-                            if (!((k >> e) & 1u)) f[e] = kNegInf;
-                    }
-                    res = L::pack(f);
-                    L::unpack(res, f);  // the log-sum-exp is that of the stored values
+                if (temp || k != ALL) {
+                    finish(v, k, f);
                 } else {
-                    res = val[u];
-                }
-                sum.add(f, L::top(L::max2(L::max2(res.x, res.y), L::max2(res.z, res.w))));
-            }
-            if (!in_place || changed) {
-                if (vec_out) {
-                    __stcs(reinterpret_cast<uint4*>(out + t0), res);
-                } else {
-                    const T* e = reinterpret_cast<const T*>(&res);
-#pragma unroll
-                    for (int q = 0; q < E; ++q) out[t0 + q] = e[q];
+                    sum.add(f, L::top(L::max2(L::max2(val[u].x, val[u].y), L::max2(val[u].z, val[u].w))));
+                    if (!in_place) store(v, val[u]);
                 }
             }
+            for (; late; late &= late - 1) {
+                const int v = vb + (__ffs(late) - 1) * kProcThreads;
+                finish_marked(v, __ldcs(xv + v));
+            }
+        }
+        if (pens || hots) {
+            __syncthreads();
+            const int listed = min(s_listed, kProcListed);
+            for (int i = tid; i < listed; i += kProcThreads) finish_marked(s_list[i], s_vec[i]);
         }
     }
 
@@ -994,8 +1050,6 @@ cudaError_t launch_scan(const SelectParams& p, cudaStream_t stream) {
 }
 
 }  // namespace
-
-size_t process_piece_bytes(int dtype) { return static_cast<size_t>(kProcThreads / 32) * 1024 * (dtype == BSP_LOGITS_FP32 ? 4 : 2); }
 
 cudaError_t launch_process(int dtype, const ProcessParams& p, int cluster, size_t smem, cudaStream_t stream) {
     switch (dtype) {

@@ -181,16 +181,17 @@ bsp_status bsp_process_logits(const bsp_plan_t* plan, const void* logits, int32_
     // so that all SMs take part, as far as a slice keeps a vector per thread, and a long row until a CTA's
     // bitmaps fit.
     int cluster = 1;
-    while (cluster < 8 && static_cast<int64_t>(p.rows) * cluster * 2 <= 2 * plan->num_sms &&
-           static_cast<int64_t>(vocab) * es / (2 * cluster) >= 8192)
+    const int64_t row_bytes = static_cast<int64_t>(vocab) * es;
+    while (cluster < 8 && static_cast<int64_t>(p.rows) * cluster * 2 <= 2 * plan->num_sms && row_bytes / (2 * cluster) >= 8192)
+        cluster *= 2;
+    while (cluster < 8 && static_cast<int64_t>(p.rows) * cluster < 16 * plan->num_sms && row_bytes / (2 * cluster) >= 32768)
         cluster *= 2;
     size_t smem = 0;
     for (;; cluster *= 2) {
         p.bitmap_words = static_cast<int>(((ceil_div(vocab, cluster) + 48) / 32 + 2 + 3) / 4 * 4);
-        // three bitmaps, the table, and for masked rows a piece of the output per warp
-        smem = static_cast<size_t>(p.bitmap_words) * 12 + static_cast<size_t>(p.hash_slots) * kProcessSlotBytes +
-               (p.mask.bits ? process_piece_bytes(logits_dtype) : 0);
-        if (smem <= kMaxSmem - 2048) break;
+        // three bitmaps and the table
+        smem = static_cast<size_t>(p.bitmap_words) * 12 + static_cast<size_t>(p.hash_slots) * kProcessSlotBytes;
+        if (smem <= kMaxSmem - 18432) break;  // (beside the kernel's own lists)
         if (cluster == 8) return BSP_ERR_UNSUPPORTED;
     }
     return launched(launch_process(logits_dtype, p, cluster, smem, static_cast<cudaStream_t>(stream)));
