@@ -235,6 +235,7 @@ struct AdvanceParams {
 cudaError_t launch_advance(const AdvanceParams& p, cudaStream_t stream);
 
 struct WeightsParams {
+    const void* q;
     const int32_t* req;
     const int32_t* pages;
     const int32_t* plan_hdr;
@@ -249,6 +250,7 @@ struct WeightsParams {
     float scale_log2, lse_mul;
 };
 constexpr int kWeightsBarBytes = 512;
+constexpr int kWeightsTableBytes = (8 * 128 + 4 * 128) * 4;  // -lse and partial sums
 cudaError_t launch_weights(int head_dim, bool bf16, bool fp8, const CUtensorMap& tq, const CUtensorMap& tk,
                            const WeightsParams& p, int ctas, size_t smem, cudaStream_t stream);
 

@@ -322,14 +322,16 @@ bsp_status key_weights_impl(const bsp_plan_t* plan, const void* q, const void* k
     p.mma_n = static_cast<int>(ceil_div(p.block_rows * G, 16) * 16);
     p.strided = rows > p.block_rows;
     const size_t q_bytes = static_cast<size_t>(D) * 2 * p.mma_n, k_bytes = static_cast<size_t>(D) * 2 * 128;
-    const size_t fixed = 1024 + 512 * 4 + 512 * 4 + kWeightsBarBytes + (static_cast<size_t>(plan->batch) + 1) * 4;
+    const size_t fixed = 1024 + kWeightsTableBytes + kWeightsBarBytes + (static_cast<size_t>(plan->batch) + 1) * 4;
     const size_t room = kMaxSmem - fixed;
-    p.q_slots = 2 * q_bytes + 2 * k_bytes <= room ? 2 : 1;
+    // a second Q slot hides the change of (request, kv head), a deeper K ring the latency of every tile
+    p.q_slots = 2 * q_bytes + 5 * k_bytes <= room ? 2 : 1;
     p.k_slots = static_cast<int>(std::min<size_t>(8, (room - p.q_slots * q_bytes) / k_bytes));
     if (p.k_slots < 1) return BSP_ERR_UNSUPPORTED;
     p.req = section(plan, plan->off_req);
     p.pages = section(plan, plan->off_pages);
     p.plan_hdr = image_header(plan);
+    p.q = q;
     p.lse = lse;
     p.weights = weights;
     p.stride = weights_stride;

@@ -10,10 +10,15 @@
 // at head_dim 256). A CTA takes a contiguous run of items when one block holds all rows of a (b, g), so that Q
 // stays in shared memory from one tile to the next, and every gridDim-th item otherwise.
 //
-// Warps: 0 loads K tiles (TMA boxes of a page, or 64 rows of one) and Q blocks; 1 issues tcgen05.mma into two
-// TMEM accumulators by turns; 2 stages the blocks' -lse; 4-11 sum, warps 4-7 the even and 8-11 the odd
-// 32-column chunks; 12-15 (E4M3 pools) widen the K tiles to the q dtype. Bounds, at 192 rows per (b, g) and
-// head_dim 128: K from HBM once, and one exp2 per (row, key, head) pair.
+// Warps: 0 loads K tiles (TMA boxes of a page, or 64 rows of one), 2 the Q blocks; 1 issues tcgen05.mma into four
+// TMEM accumulators of 128 columns, or two of 256; 4-19 sum: four sets of four warps (one per lane quadrant);
+// 20-23 (E4M3 pools) widen the K tiles to the q dtype. Up to 128 rows, the sets take items by turns; above, two
+// sets take the halves of an item's columns and two the next one's, and the second half's sums pass through
+// shared memory. (Halves as products of their own would read K twice from shared memory: 227 us.) An item costs a warp some 200 instructions of its own at latencies that the sets hide from one
+// another: all warps on one tile, with the columns dealt among them, took twice as long (12 warps: 237 us
+// on the shape below).
+// Bounds, at 192 rows per (b, g) and head_dim 128: K from HBM once, 0.7 us a tile and SM; the products, 0.5 us; one
+// exp2 per (row, key, head) pair, 0.4 us.
 // Every wait is bounded (1 s without progress); on expiry the CTA flags BSP_DEVFLAG_TIMEOUT, drains its own
 // copies and MMAs, frees TMEM and exits.
 #include <cuda.h>
@@ -31,6 +36,9 @@ namespace bsp {
 namespace {
 
 constexpr int TK = 128;                             // keys per tile (MMA M)
+constexpr int kSets = 4;                            // sets of four summing warps
+constexpr int kSumWarps = 4 * kSets;
+constexpr int kSetCols = 128;                       // TMEM columns of an accumulator
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint64_t kDrainWaitNs = 200000000ull;
 constexpr uint32_t FULL = 0xffffffffu;
@@ -38,14 +46,15 @@ constexpr uint32_t FULL = 0xffffffffu;
 struct Bars {
     uint64_t k_full[8], k_ready[8], k_empty[8];
     uint64_t q_full[2], q_empty[2];
-    uint64_t lse_full[2], lse_empty[2];
-    uint64_t acc_full[2], acc_empty[2];
-    uint64_t part_full[4];
+    uint64_t lse_full[kSets];   // a set's -lse of a new block
+    uint64_t acc_full[kSets], acc_empty[kSets];
+    uint64_t part_full[2][2];   // the second half's sums of an item of the pair of sets, in either place
     uint64_t drain;
     uint32_t tmem_base;
     int abort_flag;
 };
 static_assert(sizeof(Bars) <= kWeightsBarBytes, "barrier area");
+
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -64,81 +73,117 @@ __device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, f
         : "f"(a0), "f"(a1), "f"(b), "f"(c0), "f"(c1));
 }
 
-// The items of a CTA in order. Every role walks the same sequence.
+// The items of a CTA in order: all of them, or from the `from`-th on every `every`-th. A request's record is read
+// once, and an item that follows its predecessor costs no division.
 struct Walk {
-    const WeightsParams& p;
+    const WeightsParams* pp;
     const int* cum;       // [batch + 1] key tiles of the requests before b
-    long long at, end, step;
-    int b = 0, last_b = -1, last_g = -1;
-    bool last_single = false;
-    // the current item
+    long long at, end;
+    int every;
+    bool near;            // neighbouring items
+    int b = -1, last_b = -1, last_g = -1;
+    int nt = 0;           // key tiles of request b
+    // the current item: kv head, key tile; its request's keys, pages, first row, rows, blocks of rows; the blocks
+    // it takes are rb .. nrb - 1
     int g = 0, kt = 0, P = 0, page_off = 0, row0 = 0, seen = 0, cbase = 0, rb = 0, nrb = 0;
     bool causal = false, new_q = false;
 
-    __device__ __forceinline__ Walk(const WeightsParams& p_, const int* cum_) : p(p_), cum(cum_) {
+    __device__ __forceinline__ Walk(const WeightsParams& p, const int* cum_, int from = 0, int every_ = 1) : pp(&p), cum(cum_), every(every_) {
         const long long total = static_cast<long long>(cum[p.batch]) * p.Hkv;
-        if (p.strided) {
-            at = blockIdx.x;
-            end = total;
-            step = gridDim.x;
-        } else {
-            at = total * blockIdx.x / gridDim.x;
+        near = !p.strided;
+        if (near) {
+            at = total * blockIdx.x / gridDim.x + from;
             end = total * (blockIdx.x + 1) / gridDim.x;
-            step = 1;
-        }
-        if (at < end) {
-            int lo = 0, hi = p.batch - 1;  // the last request whose tiles begin at or before the item
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (static_cast<long long>(cum[mid]) * p.Hkv <= at) lo = mid; else hi = mid - 1;
-            }
-            b = lo;
+        } else {
+            at = blockIdx.x + static_cast<long long>(from) * gridDim.x;
+            end = total;
         }
     }
     __device__ __forceinline__ bool more() const { return at < end; }
-    // reads the item at `at`; its query-row blocks are rb .. nrb - 1
+    __device__ __forceinline__ void next() { at += near ? every : static_cast<long long>(every) * gridDim.x; }
     __device__ __forceinline__ void open() {
-        while (static_cast<long long>(cum[b + 1]) * p.Hkv <= at) ++b;
-        const int nt = cum[b + 1] - cum[b];
-        const int rem = static_cast<int>(at - static_cast<long long>(cum[b]) * p.Hkv);
-        g = rem / nt;
-        kt = rem - g * nt;
-        const int32_t* r = p.req + static_cast<long long>(b) * kReqFields;
+        if (b >= 0 && near) {
+            kt += every;
+            while (kt >= nt) {
+                kt -= nt;
+                if (++g == pp->Hkv) {
+                    g = 0;
+                    int to = b + 1;
+                    while (cum[to + 1] == cum[to]) ++to;  // (there is one: the item exists)
+                    read(to);
+                }
+            }
+        } else {
+            int lo = 0, hi = pp->batch - 1;  // the last request whose tiles begin at or before the item
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (static_cast<long long>(cum[mid]) * pp->Hkv <= at) lo = mid; else hi = mid - 1;
+            }
+            if (lo != b) read(lo);
+            const int rem = static_cast<int>(at - static_cast<long long>(cum[b]) * pp->Hkv);
+            g = rem / nt;
+            kt = rem - g * nt;
+        }
+        rb = causal ? max(0, kt * TK - cbase) / pp->block_rows : 0;
+        new_q = nrb != 1 || b != last_b || g != last_g;
+        last_b = nrb == 1 ? b : -1;
+        last_g = g;
+    }
+
+private:
+    __device__ __forceinline__ void read(int to) {
+        b = to;
+        nt = cum[b + 1] - cum[b];
+        const int32_t* r = pp->req + static_cast<long long>(b) * kReqFields;
         P = __ldg(r + kReqPrefix);
         page_off = __ldg(r + kReqPageOff);
         const int rows = __ldg(r + kReqRows), c = __ldg(r + kReqCausal);
-        seen = p.window > 0 ? min(p.window, rows) : rows;
+        seen = pp->window > 0 ? min(pp->window, rows) : rows;
         row0 = __ldg(r + kReqRowOff) + rows - seen;
         causal = c >= 0;
         cbase = c + rows - seen;  // causal: row i of the seen ones sees keys 0 .. cbase + i
-        nrb = (seen + p.block_rows - 1) / p.block_rows;
-        rb = causal ? max(0, kt * TK - cbase) / p.block_rows : 0;
-        new_q = !(nrb == 1 && last_single && b == last_b && g == last_g);
-        last_b = b;
-        last_g = g;
-        last_single = nrb == 1;
+        nrb = (seen + pp->block_rows - 1) / pp->block_rows;
     }
-    __device__ __forceinline__ void next() { at += step; }
 };
 
+// A place in a ring of n slots and the parity of its present round. A consumer waits for `parity`, a producer for
+// the other one (which a fresh barrier counts as passed).
+struct Ring {
+    int n, slot = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ explicit Ring(int n_) : n(n_) {}
+    __device__ __forceinline__ void next() {
+        if (++slot == n) {
+            slot = 0;
+            parity ^= 1;
+        }
+    }
+};
+
+__host__ __device__ constexpr int weights_threads(bool fp8) { return 32 * (4 + kSumWarps + (fp8 ? 4 : 0)); }
+
 template <int D, bool BF16, bool FP8>
-__global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
+__global__ void __launch_bounds__(weights_threads(FP8), 1)
 key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const WeightsParams p) {
     constexpr int NC = D / 64;
     constexpr int K_BYTES = TK * D * 2;
-    constexpr int THREADS = FP8 ? 512 : 384;
+    constexpr int THREADS = weights_threads(FP8);
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int NS = p.mma_n;                         // rows of a Q block as the MMA sees it
     const int q_bytes = NC * NS * 128;
     const int NQ = p.q_slots, KST = p.k_slots;
-    auto q_buf = [&](int i) { return smem + (i % NQ) * q_bytes; };
-    auto k_buf = [&](int i) { return smem + NQ * q_bytes + (i % KST) * K_BYTES; };
+    const bool halves = NS > kSetCols;              // a block's columns go to two sets
+    const int NU = halves ? (NS / 2 + 31) / 32 * 32 : NS;  // columns of the first
+    const int accs = halves ? 2 : kSets;            // accumulators
+    const int acc_cols = 4 * kSetCols / accs;
+    auto q_buf = [&](int slot) { return smem + slot * q_bytes; };
+    auto k_buf = [&](int slot) { return smem + NQ * q_bytes + slot * K_BYTES; };
     uint8_t* rest = smem + NQ * q_bytes + KST * K_BYTES;
-    float* s_nlse = reinterpret_cast<float*>(rest);                 // [2][256]
-    float* s_part = s_nlse + 512;                                   // [4][128]
-    Bars* bars = reinterpret_cast<Bars*>(s_part + 512);
+    float* s_nlse = reinterpret_cast<float*>(rest);                 // [kSets][2][128]: -lse of the present block and the next
+    float* s_part = s_nlse + kSets * 2 * kSetCols;                  // [2][2][128]: of each pair of sets, two items
+    Bars* bars = reinterpret_cast<Bars*>(s_part + 2 * 2 * TK);
     int* s_cum = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + kWeightsBarBytes);  // [batch + 1]
     volatile int* abort_flag = &bars->abort_flag;
 
@@ -155,13 +200,15 @@ key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->q_full[i], 1);
-            mbar_init(&bars->q_empty[i], 1);
-            mbar_init(&bars->lse_full[i], 1);
-            mbar_init(&bars->lse_empty[i], 8);
-            mbar_init(&bars->acc_full[i], 1);
-            mbar_init(&bars->acc_empty[i], 8);
+            mbar_init(&bars->q_empty[i], 1);  // the block's last product completed
+            mbar_init(&bars->part_full[0][i], 4);
+            mbar_init(&bars->part_full[1][i], 4);
         }
-        for (int i = 0; i < 4; ++i) mbar_init(&bars->part_full[i], 4);
+        for (int i = 0; i < kSets; ++i) {
+            mbar_init(&bars->lse_full[i], 4);
+            mbar_init(&bars->acc_full[i], 1);
+            mbar_init(&bars->acc_empty[i], p.mma_n > kSetCols ? 8 : 4);
+        }
         mbar_init(&bars->drain, 1);
         bars->abort_flag = 0;
         fence_mbar_init();
@@ -199,46 +246,55 @@ key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     if (warp == 0) {
         // ================= loads
         const int BR = min(ps, 64);
-        int kn = 0, qn = 0;
+        Ring k(KST);
         bool ok = true;
-        for (Walk w(p, s_cum); w.more() && ok; w.next(), ++kn) {
+        Walk w(p, s_cum);
+        // lane ch: the page of the tile's chunk ch (at most 16 chunks), fetched an item ahead
+        auto page_of = [&](const Walk& at) -> int {
+            const int key = at.kt * TK + lane * BR;
+            return lane < TK / BR && key < at.P ? __ldg(p.pages + at.page_off + (key >> p.ps_log2)) : 0;
+        };
+        int page_next = 0;
+        if (w.more()) {
             w.open();
+            page_next = page_of(w);
+        }
+        while (w.more() && ok) {
+            const int pages = page_next;
+            Walk ahead = w;
+            ahead.next();
+            if (ahead.more()) {
+                ahead.open();
+                page_next = page_of(ahead);
+            }
             // K of the item
-            if (kn >= KST) ok = __all_sync(FULL, mbar_wait(&bars->k_empty[kn % KST], ((kn / KST) - 1) & 1, abort_flag, kWaitNs));
+            ok = __all_sync(FULL, mbar_wait(&bars->k_empty[k.slot], k.parity ^ 1, abort_flag, kWaitNs));
             if (!ok) break;
             const int key0 = w.kt * TK;
             const int valid = min(TK, w.P - key0);
             const int nchunks = (valid + BR - 1) / BR;
-            uint64_t* full = &bars->k_full[kn % KST];
+            uint64_t* full = &bars->k_full[k.slot];
+            uint8_t* tile = k_buf(k.slot);
             if (lane == 0) mbar_arrive_expect_tx(full, nchunks * BR * D * (FP8 ? 1 : 2));
             __syncwarp();
             constexpr int NB = FP8 ? 1 : NC;  // boxes of a chunk: column halves (E4M3: whole rows)
-            for (int bx = lane; bx < nchunks * NB; bx += 32) {
-                const int ch = bx / NB, c = bx - ch * NB;
-                const int key = key0 + ch * BR;
-                int page = __ldg(p.pages + w.page_off + (key >> p.ps_log2));
+            for (int b0 = 0; b0 < nchunks * NB; b0 += 32) {
+                const int bx = b0 + lane, ch = min(bx / NB, nchunks - 1), c = bx % NB;
+                int page = __shfl_sync(FULL, pages, ch);
+                if (bx >= nchunks * NB) continue;
                 if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) {
                     atomicOr(p.status, BSP_DEVFLAG_PAGE_INDEX);
                     page = 0;
                 }
-                const int row = ((page * p.Hkv + w.g) << p.ps_log2) + (key & (ps - 1));
+                const int row = ((page * p.Hkv + w.g) << p.ps_log2) + ((key0 + ch * BR) & (ps - 1));
                 if constexpr (FP8)
-                    tma_load_2d(k_buf(kn) + TK * D + ch * BR * D, &tm_k, full, 0, row);
+                    tma_load_2d(tile + TK * D + ch * BR * D, &tm_k, full, 0, row);
                 else
-                    tma_load_2d(k_buf(kn) + c * TK * 128 + ch * BR * 128, &tm_k, full, c * 64, row);
+                    tma_load_2d(tile + c * TK * 128 + ch * BR * 128, &tm_k, full, c * 64, row);
             }
             __syncwarp();
-            for (int rb = w.rb; rb < w.nrb && w.new_q; ++rb, ++qn) {
-                if (qn >= NQ) ok = __all_sync(FULL, mbar_wait(&bars->q_empty[qn % NQ], ((qn / NQ) - 1) & 1, abort_flag, kWaitNs));
-                if (!ok) break;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&bars->q_full[qn % NQ], NC * p.block_rows * p.G * 128);
-                    for (int c = 0; c < NC; ++c)
-                        tma_load_3d(q_buf(qn) + c * NS * 128, &tm_q, &bars->q_full[qn % NQ], c * 64, w.g * p.G,
-                                    w.row0 + rb * p.block_rows);
-                }
-                __syncwarp();
-            }
+            w = ahead;
+            k.next();
         }
         if (!ok) {
             if (lane == 0) {
@@ -247,43 +303,50 @@ key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             // drain: this CTA's own copies land before it exits
             const uint64_t t0 = globaltimer_ns();
-            for (int j = max(0, kn - KST); j <= kn; ++j)
-                while (!mbar_try_wait(&bars->k_full[j % KST], (j / KST) & 1) && globaltimer_ns() - t0 < kDrainWaitNs) {
-                }
-            for (int j = max(0, qn - NQ); j <= qn; ++j)
-                while (!mbar_try_wait(&bars->q_full[j % NQ], (j / NQ) & 1) && globaltimer_ns() - t0 < kDrainWaitNs) {
+            // (the round before in the slots from this one on, this round in the others)
+            for (int j = 0; j < KST; ++j)
+                while (!mbar_try_wait(&bars->k_full[j], j < k.slot ? k.parity : k.parity ^ 1) && globaltimer_ns() - t0 < kDrainWaitNs) {
                 }
         }
     } else if (warp == 1) {
         // ================= products
         if (lane == 0) {
             const uint32_t idesc = idesc_f16(TK, NS, BF16, false);
-            int kn = 0, qn = -1, step = 0;
+            const uint64_t k_desc0 = sdesc_sw128(smem_u32(k_buf(0)), 16, 1024), q_desc0 = sdesc_sw128(smem_u32(q_buf(0)), 16, 1024);
+            Ring k(KST), q(NQ);
+            uint64_t q_desc = q_desc0;
+            Ring acc(accs);
+            uint32_t parities = 0;  // of the accumulators
+            int q_slot = -1;        // the present block's
             bool ok = true;
-            for (Walk w(p, s_cum); w.more() && ok; w.next(), ++kn) {
+            for (Walk w(p, s_cum); w.more() && ok; w.next(), k.next()) {
                 w.open();
-                ok = mbar_wait(FP8 ? &bars->k_ready[kn % KST] : &bars->k_full[kn % KST], (kn / KST) & 1, abort_flag, kWaitNs);
+                ok = mbar_wait(FP8 ? &bars->k_ready[k.slot] : &bars->k_full[k.slot], k.parity, abort_flag, kWaitNs);
                 if (!ok) break;
-                const uint32_t k_addr = smem_u32(k_buf(kn));
-                for (int rb = w.rb; rb < w.nrb; ++rb, ++step) {
+                const uint64_t k_desc = k_desc0 + static_cast<uint32_t>(k.slot * (K_BYTES >> 4));
+                for (int rb = w.rb; rb < w.nrb && ok; ++rb) {
                     if (w.new_q) {
-                        ++qn;
-                        ok = mbar_wait(&bars->q_full[qn % NQ], (qn / NQ) & 1, abort_flag, kWaitNs);
+                        if (q_slot >= 0) mma_commit(&bars->q_empty[q_slot]);
+                        ok = mbar_wait(&bars->q_full[q.slot], q.parity, abort_flag, kWaitNs);
                         if (!ok) break;
+                        q_slot = q.slot;
+                        q_desc = q_desc0 + static_cast<uint32_t>(q.slot * (q_bytes >> 4));
+                        q.next();
                     }
-                    const int a = step & 1;
-                    if (step >= 2) ok = mbar_wait(&bars->acc_empty[a], ((step >> 1) - 1) & 1, abort_flag, kWaitNs);
+                    // (the blocks of an item take its accumulator one after another)
+                    const int a = acc.slot;
+                    ok = mbar_wait(&bars->acc_empty[a], ((parities >> a) & 1u) ^ 1u, abort_flag, kWaitNs);
                     if (!ok) break;
+                    parities ^= 1u << a;
                     tc_fence_after();
-                    const uint32_t q_addr = smem_u32(q_buf(qn));
+                    // (a k-step of 16 elements is 32 bytes on, a column region TK or NS rows of 128 bytes)
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint64_t ad = sdesc_sw128(k_addr + (kk >> 2) * (TK * 128) + (kk & 3) * 32, 16, 1024);
-                        const uint64_t bd = sdesc_sw128(q_addr + (kk >> 2) * (NS * 128) + (kk & 3) * 32, 16, 1024);
-                        mma_f16(tmem + a * 256, ad, bd, idesc, kk > 0 ? 1u : 0u);
-                    }
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        mma_f16(tmem + a * acc_cols, k_desc + ((kk >> 2) * (TK * 8) + (kk & 3) * 2),
+                                q_desc + static_cast<uint32_t>((kk >> 2) * (NS * 8) + (kk & 3) * 2), idesc, kk > 0 ? 1u : 0u);
                     mma_commit(&bars->acc_full[a]);
                 }
+                acc.next();
             }
             if (!ok) {
                 *abort_flag = 1;
@@ -296,81 +359,97 @@ key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
         }
     } else if (warp == 2) {
-        // ================= -lse of each Q block, in base 2; -inf for rows without one
-        int qn = 0;
+        // ================= the Q blocks
+        Ring q(NQ);
         bool ok = true;
         for (Walk w(p, s_cum); w.more() && ok; w.next()) {
             w.open();
-            for (int rb = w.rb; rb < w.nrb && w.new_q; ++rb, ++qn) {
+            for (int rb = w.rb; rb < w.nrb && w.new_q; ++rb, q.next()) {
                 const int i0 = rb * p.block_rows;
-                const int n = min(p.block_rows, w.seen - i0) * p.G;
-                float v[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int c = lane + 32 * j;
-                    v[j] = -INFINITY;
-                    if (c < n) {
-                        const int i = c / p.G;
-                        const float l = __ldg(p.lse + static_cast<long long>(w.row0 + i0 + i) * p.Hq + w.g * p.G + (c - i * p.G));
-                        v[j] = l == -INFINITY ? -INFINITY : -l * p.lse_mul;
-                    }
+                // the block on its way to L2: its shared-memory slot may be free only shortly before it is needed
+                const int line = p.G * D * 2 / 128;  // 128-byte lines of a row's heads
+                const uint8_t* rows = static_cast<const uint8_t*>(p.q) + (static_cast<long long>(w.row0 + i0) * p.Hq + w.g * p.G) * (D * 2);
+                for (int j = lane; j < min(p.block_rows, w.seen - i0) * line; j += 32) {
+                    const int i = j / line;
+                    prefetch_l2(rows + static_cast<long long>(i) * p.Hq * (D * 2) + (j - i * line) * 128);
                 }
-                if (qn >= 2) ok = __all_sync(FULL, mbar_wait(&bars->lse_empty[qn & 1], ((qn >> 1) - 1) & 1, abort_flag, kWaitNs));
+                ok = __all_sync(FULL, mbar_wait(&bars->q_empty[q.slot], q.parity ^ 1, abort_flag, kWaitNs));
                 if (!ok) break;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) s_nlse[(qn & 1) * 256 + lane + 32 * j] = v[j];
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&bars->q_full[q.slot], NC * p.block_rows * p.G * 128);
+                    for (int c = 0; c < NC; ++c)
+                        tma_load_3d(q_buf(q.slot) + c * NS * 128, &tm_q, &bars->q_full[q.slot], c * 64, w.g * p.G, w.row0 + i0);
+                }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->lse_full[qn & 1]);
             }
         }
-        if (!ok && lane == 0) {
-            *abort_flag = 1;
-            atomicOr(p.status, BSP_DEVFLAG_TIMEOUT);
+        if (!ok) {
+            if (lane == 0) {
+                *abort_flag = 1;
+                atomicOr(p.status, BSP_DEVFLAG_TIMEOUT);
+            }
+            const uint64_t t0 = globaltimer_ns();
+            for (int j = 0; j < NQ; ++j)
+                while (!mbar_try_wait(&bars->q_full[j], j < q.slot ? q.parity : q.parity ^ 1) && globaltimer_ns() - t0 < kDrainWaitNs) {
+                }
         }
-    } else if (warp >= 4 && warp < 12) {
+    } else if (warp >= 4 && warp < 4 + kSumWarps) {
         // ================= sums: thread <-> key <-> TMEM lane
-        const int quad = warp & 3, odd = warp >= 8 ? 1 : 0;
+        const int quad = warp & 3, set = (warp - 4) >> 2;
         const int key_lane = quad * 32 + lane;
-        const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16);
         const float c2 = p.scale_log2;
-        int kn = 0, qn = -1, step = 0;
+        const int every = halves ? 2 : 4, half = halves ? set & 1 : 0, pair = set >> 1;
+        const int col0 = half * NU;                       // the set's first column of a block
+        const int slot = halves ? pair : set;             // its accumulator
+        const uint32_t acc = tmem + slot * acc_cols + col0 + (static_cast<uint32_t>(quad * 32) << 16);
+        float* nlse = s_nlse + set * 2 * kSetCols;        // of the present block: by turns in either half
+        int k_slot = slot % KST;
+        uint32_t acc_parity = 0, lse_parity = 0;
+        Ring part(2);                                     // places of the second half's sums
         bool ok = true;
-        for (Walk w(p, s_cum); w.more() && ok; w.next(), ++kn) {
+        for (Walk w(p, s_cum, slot, every); w.more() && ok; w.next()) {
             w.open();
             const int key = w.kt * TK + key_lane;
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int rb = w.rb; rb < w.nrb; ++rb, ++step) {
-                const int a = step & 1;
-                if (w.new_q) {
-                    // the block before is done with: its products are complete and its -lse read
-                    if (qn >= 0 && lane == 0) {
-                        mbar_arrive(&bars->lse_empty[qn & 1]);
-                        if (warp == 4) mbar_arrive(&bars->q_empty[qn % NQ]);
-                    }
-                    ++qn;
-                    ok = mbar_wait(&bars->lse_full[qn & 1], (qn >> 1) & 1, abort_flag, kWaitNs);
-                    ok = __all_sync(FULL, ok);
-                    if (!ok) break;
-                }
-                ok = mbar_wait(&bars->acc_full[a], (step >> 1) & 1, abort_flag, kWaitNs);
-                ok = __all_sync(FULL, ok);
-                if (!ok) break;
-                tc_fence_after();
-                if (warp == 4 && lane == 0 && rb == w.nrb - 1) mbar_arrive(&bars->k_empty[kn % KST]);
+            for (int rb = w.rb; rb < w.nrb; ++rb) {
                 const int i0 = rb * p.block_rows;
-                const int n = min(p.block_rows, w.seen - i0) * p.G;
+                const int n = min(p.block_rows, w.seen - i0) * p.G - col0;  // the block's columns for this set
+                if (w.new_q) {
+                    // -lse of the set's columns in base 2, a column per thread; -inf for rows without one. The other
+                    // half of the buffer is still read by warps that are a block behind, but no further: they
+                    // have arrived for the present block.
+                    nlse = s_nlse + set * 2 * kSetCols + (lse_parity ? 0 : kSetCols);
+                    float v = -INFINITY;
+                    if (key_lane < min(n, NU)) {
+                        const int i = (col0 + key_lane) / p.G;
+                        const float l = __ldg(p.lse + static_cast<long long>(w.row0 + i0 + i) * p.Hq + w.g * p.G + (col0 + key_lane - i * p.G));
+                        v = l == -INFINITY ? -INFINITY : -l * p.lse_mul;
+                    }
+                    nlse[key_lane] = v;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->lse_full[set]);
+                    ok = __all_sync(FULL, mbar_wait(&bars->lse_full[set], lse_parity, abort_flag, kWaitNs));
+                    if (!ok) break;
+                    lse_parity ^= 1;
+                }
+                ok = __all_sync(FULL, mbar_wait(&bars->acc_full[slot], acc_parity, abort_flag, kWaitNs));
+                if (!ok) break;
+                acc_parity ^= 1;
+                tc_fence_after();
+                // the K tile has been read when its last product is complete
+                if (quad == 0 && lane == 0 && half == 0 && rb == w.nrb - 1) mbar_arrive(&bars->k_empty[k_slot]);
+                const int cols = min(n, NU);
                 // columns below cmin are rows that do not see this thread's key
-                const int cmin = w.causal ? max(0, key - w.cbase - i0) * p.G : 0;
+                const int cmin = w.causal ? max(0, key - w.cbase - i0) * p.G - col0 : 0;
                 const bool all_see = !w.causal || w.kt * TK + TK - 1 <= w.cbase + i0;
-                const float* nl = s_nlse + (qn & 1) * 256;
-                for (int c0 = odd * 32; c0 < n; c0 += 64) {
+                for (int c0 = 0; c0 < cols; c0 += 32) {
                     uint32_t s[32];
-                    tmem_ld32(lane_base + a * 256 + c0, s);
+                    tmem_ld32(acc + c0, s);
                     tmem_wait_ld();
-                    if (all_see && c0 + 32 <= n) {
+                    if (all_see && c0 + 32 <= cols) {
 #pragma unroll
                         for (int c = 0; c < 32; c += 4) {
-                            const float4 l = *reinterpret_cast<const float4*>(nl + c0 + c);
+                            const float4 l = *reinterpret_cast<const float4*>(nlse + c0 + c);
                             float e0, e1, e2, e3;
                             fma2(e0, e1, __uint_as_float(s[c]), __uint_as_float(s[c + 1]), c2, l.x, l.y);
                             fma2(e2, e3, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]), c2, l.z, l.w);
@@ -380,46 +459,52 @@ key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     } else {
 #pragma unroll
                         for (int c = 0; c < 32; ++c) {
-                            const float e = ex2(fmaf(__uint_as_float(s[c]), c2, nl[c0 + c]));
-                            sum[c & 3] += (c0 + c < n && c0 + c >= cmin) ? e : 0.f;
+                            const float e = ex2(fmaf(__uint_as_float(s[c]), c2, nlse[c0 + c]));
+                            sum[c & 3] += (c0 + c < cols && c0 + c >= cmin) ? e : 0.f;
                         }
                     }
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->acc_empty[a]);
+                if (lane == 0) mbar_arrive(&bars->acc_empty[slot]);
             }
             if (!ok) break;
-            const float mine = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            // The odd chunks' sums pass through shared memory, in four slots by turns: item kn + 4 is summed
-            // only once both halves have left the accumulator of item kn + 2, so its slot has been read.
-            if (odd) {
-                s_part[(kn & 3) * 128 + key_lane] = mine;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->part_full[kn & 3]);
-            } else {
-                ok = mbar_wait(&bars->part_full[kn & 3], (kn >> 2) & 1, abort_flag, kWaitNs);
-                ok = __all_sync(FULL, ok);
-                if (!ok) break;
-                if (key < w.P) {
-                    float* out = p.weights + (static_cast<long long>(w.b) * p.Hkv + w.g) * p.stride + key;
-                    const float v = mine + s_part[(kn & 3) * 128 + key_lane];
-                    *out = p.accumulate ? *out + v : v;
+            k_slot += every;
+            while (k_slot >= KST) k_slot -= KST;
+            float v = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            if (halves) {
+                // The second half's sums, in two places by turns with a barrier each: the second half's set is at
+                // most one item ahead, since the accumulator of the item after waits for both sets.
+                float* place = s_part + (2 * pair + part.slot) * TK + key_lane;
+                uint64_t* full = &bars->part_full[pair][part.slot];
+                if (half) {
+                    *place = v;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full);
+                } else {
+                    ok = __all_sync(FULL, mbar_wait(full, part.parity, abort_flag, kWaitNs));
+                    if (!ok) break;
+                    v += *place;
                 }
+                part.next();
+            }
+            if (!half && key < w.P) {
+                float* out = p.weights + (static_cast<long long>(w.b) * p.Hkv + w.g) * p.stride + key;
+                *out = p.accumulate ? *out + v : v;
             }
         }
         if (!ok && lane == 0) {
             *abort_flag = 1;
             atomicOr(p.status, BSP_DEVFLAG_TIMEOUT);
         }
-    } else if (FP8 && warp >= 12) {
+    } else if (FP8 && warp >= 4 + kSumWarps) {
         // ================= E4M3 tiles widened to the q dtype in their slots
         if constexpr (FP8) {
-            int kn = 0;
+            Ring k(KST);
             bool ok = true;
-            for (Walk w(p, s_cum); w.more(); w.next(), ++kn) {
+            for (Walk w(p, s_cum); w.more(); w.next(), k.next()) {
                 w.open();
-                ok = mbar_wait(&bars->k_full[kn % KST], (kn / KST) & 1, abort_flag, kWaitNs);
+                ok = mbar_wait(&bars->k_full[k.slot], k.parity, abort_flag, kWaitNs);
                 // the four warps go on, or leave, together
                 uint32_t all;
                 asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
@@ -427,10 +512,10 @@ key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                              : "=r"(all) : "r"(ok ? 1u : 0u) : "memory");
                 ok = all != 0;
                 if (!ok) break;
-                widen_e4m3_tile<D, TK, BF16, 128>(k_buf(kn), min(TK, w.P - w.kt * TK), tid - 384, 1);
+                widen_e4m3_tile<D, TK, BF16, 128>(k_buf(k.slot), min(TK, w.P - w.kt * TK), tid - 32 * (4 + kSumWarps), 1);
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->k_ready[kn % KST]);
+                if (lane == 0) mbar_arrive(&bars->k_ready[k.slot]);
             }
             if (!ok && lane == 0) {
                 *abort_flag = 1;
@@ -452,7 +537,7 @@ cudaError_t launch_t(const CUtensorMap& tq, const CUtensorMap& tk, const Weights
     cudaError_t e = cudaFuncSetAttribute(key_weights_kernel<D, BF16, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    key_weights_kernel<D, BF16, FP8><<<ctas, FP8 ? 512 : 384, smem, stream>>>(tq, tk, p);
+    key_weights_kernel<D, BF16, FP8><<<ctas, weights_threads(FP8), smem, stream>>>(tq, tk, p);
     return cudaGetLastError();
 }
 

@@ -321,3 +321,35 @@ def test_beam_advance_flags_bad_parents_and_refuses_short_tables():
         bsp.beam_advance(plan, chosen, chosen, tokens=tok[:, :2].contiguous())
     with pytest.raises(bsp.BspError):
         bsp.beam_advance(plan, chosen, chosen, torch.zeros((1, 3, 2), dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.parametrize("W,G,D,dtype,lens", [(96, 2, 128, "bf16", (1200, 1900)), (30, 2, 128, "fp16", (1000, 1600)),
+                                              (40, 5, 64, "bf16", (900, 2100)), (64, 4, 256, "bf16", (500, 900))])
+def test_key_weights_many_tiles_per_sm(W, G, D, dtype, lens):
+    """Dozens of key tiles for every SM, so that rings and accumulators go round many times, against fp64 products."""
+    rng = np.random.default_rng(W)
+    n = rng.integers(lens[0], lens[1], 40).astype(np.int32)
+    Hkv = 8
+    c = Cache(W, n, Hkv * G, Hkv, D, 32, dtype)
+    plan = c.decode_plan(W)
+    q = c.rows(40 * W)
+    lse = torch.empty((40 * W, Hkv * G), device="cuda")
+    want, size = [], 0.0
+    for b in range(40):
+        pages = torch.from_numpy(c.table[b, :-(-n[b] // 32)].astype(np.int64)).cuda()
+        k = c.k[pages].double().permute(1, 0, 2, 3).reshape(Hkv, -1, D)[:, :n[b]]
+        qb = q[b * W:(b + 1) * W].double().view(W, Hkv, G, D).permute(1, 2, 0, 3).reshape(Hkv, G * W, D)
+        s = qb @ k.transpose(1, 2) / math.sqrt(D)
+        ls = torch.logsumexp(s, -1).float()
+        lse[b * W:(b + 1) * W] = ls.view(Hkv, G, W).permute(2, 0, 1).reshape(W, Hkv * G)
+        want.append(torch.exp(s - ls.double()[..., None]).sum(1))
+        size = max(size, float(qb.norm(dim=-1).max() * k.norm(dim=-1).max()) / math.sqrt(D))
+    for rep in range(3):
+        got = torch.full((40, Hkv, int(n.max())), -7.0, device="cuda")
+        bsp.key_weights(plan, q, c.k, lse, 1 / math.sqrt(D), got)
+        assert bsp.read_device_status(plan) == (0, 0)
+        for b in range(40):
+            # as check_weights: the product's D 2^-24 of |q||k|, exp2, its argument, lse, the sum
+            tol = want[b] * (D * 2.0 ** -24 * size + 2.0 ** -22 + 2.0 ** -22 * (size + 20) + W * G * 2.0 ** -24) + 1e-30
+            assert ((got[b, :, :n[b]].double() - want[b]).abs() <= tol).all()
+            assert (got[b, :, n[b]:] == -7.0).all()
