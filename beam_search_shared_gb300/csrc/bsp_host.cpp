@@ -351,7 +351,8 @@ bsp_status plan_build_core(const bsp_geometry* geo, int32_t batch, int32_t beam_
         }
     }
     const bool alt = layout == 1;
-    const int group = alt ? nrb : 1;
+    // (more row blocks than SMs: no such neighbours, each block dealt by itself)
+    const int group = alt && nrb <= num_sms ? nrb : 1;
     if (!pf) urows = wblk;
     auto nrb_of = [&](int b) -> int { return pf ? static_cast<int>(ceil_div(rows[b], urows)) : nrb; };
     std::vector<int64_t> tiles(batch);
