@@ -478,6 +478,10 @@ def decode_attn_noalloc(geo: Geometry, batch, beam_width, prefix_len, tail_len, 
 LOGITS_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
+def _address(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
 def _table(name: str, t: torch.Tensor, dtype, shape, exact_last: bool = True):
     """Checks a table's type and shape (None: any extent) and that its rows are contiguous and evenly spaced;
     returns the row stride in elements."""
@@ -589,7 +593,7 @@ def process_logits(plan_: Plan, logits: torch.Tensor, params: LogitsParams, out:
         _table("lse", lse, torch.float32, (rows,))
     _check("bsp_process_logits", load().bsp_process_logits(
         ctypes.byref(plan_), logits.data_ptr(), LOGITS_DTYPES[logits.dtype], stride, logits.shape[1],
-        ctypes.byref(params.c), out.data_ptr(), out_stride, _dptr(lse), _stream(stream)))
+        ctypes.byref(params.c), out.data_ptr(), out_stride, _address(lse), _stream(stream)))
 
 
 def beam_select_workspace(batch: int, beam_width: int, vocab: int, num_candidates: int, device="cuda") -> torch.Tensor:
@@ -657,9 +661,9 @@ def beam_advance(plan_: Plan, parents: torch.Tensor, chosen: torch.Tensor,
     if token_len is not None:
         _table("token_len", token_len, i32, (rows,))
     _check("bsp_beam_advance", load().bsp_beam_advance(
-        ctypes.byref(plan_), parents.data_ptr(), chosen.data_ptr(), stride, _dptr(cache_indirection),
-        _dptr(cache_indirection_out), max_seq, _dptr(tokens), _dptr(tokens_out), token_stride, token_cols,
-        _dptr(token_len), _stream(stream)))
+        ctypes.byref(plan_), parents.data_ptr(), chosen.data_ptr(), stride, _address(cache_indirection),
+        _address(cache_indirection_out), max_seq, _address(tokens), _address(tokens_out), token_stride, token_cols,
+        _address(token_len), _stream(stream)))
 
 
 def _key_table(plan_: Plan, name: str, t: torch.Tensor, dtype):
@@ -711,6 +715,6 @@ def evict_prefix(plan_: Plan, weights: torch.Tensor, keep_len: torch.Tensor, sin
         if t is not None and _key_table(plan_, name, t, dt) != out_stride:
             raise ValueError(f"{name} must have the row stride of kept")
     _check("bsp_evict_prefix", load().bsp_evict_prefix(
-        ctypes.byref(plan_), weights.data_ptr(), stride, _dptr(positions), keep_len.data_ptr(), int(sinks), int(recent),
-        k_pool.data_ptr(), v_pool.data_ptr(), kept.data_ptr(), _dptr(weights_out), _dptr(positions_out), out_stride,
+        ctypes.byref(plan_), weights.data_ptr(), stride, _address(positions), keep_len.data_ptr(), int(sinks), int(recent),
+        k_pool.data_ptr(), v_pool.data_ptr(), kept.data_ptr(), _address(weights_out), _address(positions_out), out_stride,
         _stream(stream)))

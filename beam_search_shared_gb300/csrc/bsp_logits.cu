@@ -312,14 +312,14 @@ __global__ void __launch_bounds__(kProcThreads, 4) process_logits_kernel(const P
     const bool vec_out = ((reinterpret_cast<uintptr_t>(out + head)) & 15) == 0;
     const uint4* xv = reinterpret_cast<const uint4*>(x + head);
 
-    uint32_t* bm_pen = smem;
-    uint32_t* bm_hot = bm_pen + p.bitmap_words;
-    uint32_t* bm_mask = bm_hot + p.bitmap_words;
-    HashSlot* table = reinterpret_cast<HashSlot*>(bm_mask + p.bitmap_words);
-    const uint32_t hmask = p.hash_slots - 1;
-    const int words = (hi - base + 31) >> 5;
     const bool counts = p.frequency || p.presence;
     const bool pens = p.repetition && (p.prompt_tokens || p.tokens), hots = p.hash_slots > 0;
+    uint32_t* bm_pen = smem;
+    uint32_t* bm_hot = smem + p.hot_at;
+    uint32_t* bm_mask = smem + p.mask_at;
+    HashSlot* table = reinterpret_cast<HashSlot*>(smem + p.table_at);
+    const uint32_t hmask = p.hash_slots - 1;
+    const int words = (hi - base + 31) >> 5;
 
     uint4 val[U];
     if (!p.mask.bits) {
@@ -625,8 +625,7 @@ __global__ void __launch_bounds__(kProcThreads, 4) process_logits_kernel(const P
 
 template <int DT>
 cudaError_t launch_process_t(const ProcessParams& p, int cluster, size_t smem, cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(process_logits_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(process_logits_kernel<DT>), smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(p.rows) * cluster);
@@ -1045,7 +1044,10 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const SelectP
 
 template <int DT>
 cudaError_t launch_scan(const SelectParams& p, cudaStream_t stream) {
-    beam_scan_kernel<DT><<<p.ctas, kSelThreads, static_cast<size_t>(p.cap) * 8, stream>>>(p);
+    const size_t smem = static_cast<size_t>(p.cap) * 8;
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(beam_scan_kernel<DT>), smem);
+    if (e != cudaSuccess) return e;
+    beam_scan_kernel<DT><<<p.ctas, kSelThreads, smem, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -1073,10 +1075,8 @@ cudaError_t launch_select(int dtype, const SelectParams& p, int most_lists, cuda
                                                : launch_scan<BSP_LOGITS_FP32>(p, stream);
     if (e != cudaSuccess) return e;
     const size_t smem = static_cast<size_t>(most_lists) * p.K * 8;
-    if (smem > 32 * 1024) {
-        e = cudaFuncSetAttribute(beam_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        if (e != cudaSuccess) return e;
-    }
+    e = allow_smem(reinterpret_cast<const void*>(beam_merge_kernel), smem);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(p.batch);
     cfg.blockDim = dim3(kMergeThreads);

@@ -177,22 +177,23 @@ bsp_status bsp_process_logits(const bsp_plan_t* plan, const void* logits, int32_
     if (named > BSP_MAX_LISTED) return BSP_ERR_UNSUPPORTED;
     p.hash_slots = named ? std::max(4, 1 << ilog2(static_cast<int>(2 * named))) : 0;
 
-    // One cluster per row. Many rows fill the SMs with one CTA each; fewer rows are cut into up to 8 slices
-    // so that all SMs take part, as far as a slice keeps a vector per thread, and a long row until a CTA's
-    // bitmaps fit.
     int cluster = 1;
     const int64_t row_bytes = static_cast<int64_t>(vocab) * es;
-    while (cluster < 8 && static_cast<int64_t>(p.rows) * cluster * 2 <= 2 * plan->num_sms && row_bytes / (2 * cluster) >= 8192)
-        cluster *= 2;
-    while (cluster < 8 && static_cast<int64_t>(p.rows) * cluster < 16 * plan->num_sms && row_bytes / (2 * cluster) >= 32768)
+    while (cluster < 8 && static_cast<int64_t>(p.rows) * cluster * 2 <= 4 * plan->num_sms && row_bytes / (2 * cluster) >= 4096)
         cluster *= 2;
     size_t smem = 0;
     for (;; cluster *= 2) {
-        p.bitmap_words = static_cast<int>(((ceil_div(vocab, cluster) + 48) / 32 + 2 + 3) / 4 * 4);
-        // three bitmaps and the table
-        smem = static_cast<size_t>(p.bitmap_words) * 12 + static_cast<size_t>(p.hash_slots) * kProcessSlotBytes;
-        if (smem <= kMaxSmem - 18432) break;  // (beside the kernel's own lists)
-        if (cluster == 8) return BSP_ERR_UNSUPPORTED;
+        // bitmaps of a slice: penalised tokens, tokens in the table, allowed tokens; each as far as it is needed
+        const int words = static_cast<int>(((ceil_div(vocab, cluster) + 48) / 32 + 2 + 3) / 4 * 4);
+        p.hot_at = q.repetition_penalty && (p.prompt_tokens || p.tokens) ? words : 0;
+        p.mask_at = p.hot_at + (p.hash_slots ? words : 0);
+        p.table_at = p.mask_at + (p.mask.bits ? words : 0);
+        smem = static_cast<size_t>(p.table_at) * 4 + static_cast<size_t>(p.hash_slots) * kProcessSlotBytes;
+        if (smem <= 40 * 1024) break;
+        if (cluster == 8) {
+            if (smem > kMaxSmem - 18432) return BSP_ERR_UNSUPPORTED;
+            break;
+        }
     }
     return launched(launch_process(logits_dtype, p, cluster, smem, static_cast<cudaStream_t>(stream)));
 }
@@ -325,7 +326,7 @@ bsp_status key_weights_impl(const bsp_plan_t* plan, const void* q, const void* k
     const size_t fixed = 1024 + kWeightsTableBytes + kWeightsBarBytes + (static_cast<size_t>(plan->batch) + 1) * 4;
     const size_t room = kMaxSmem - fixed;
     // a second Q slot hides the change of (request, kv head), a deeper K ring the latency of every tile
-    p.q_slots = 2 * q_bytes + 5 * k_bytes <= room ? 2 : 1;
+    p.q_slots = 2 * q_bytes + 3 * k_bytes <= room ? 2 : 1;
     p.k_slots = static_cast<int>(std::min<size_t>(8, (room - p.q_slots * q_bytes) / k_bytes));
     if (p.k_slots < 1) return BSP_ERR_UNSUPPORTED;
     p.req = section(plan, plan->off_req);

@@ -12,13 +12,16 @@
 //
 // Warps: 0 loads K tiles (TMA boxes of a page, or 64 rows of one), 2 the Q blocks; 1 issues tcgen05.mma into four
 // TMEM accumulators of 128 columns, or two of 256; 4-19 sum: four sets of four warps (one per lane quadrant);
-// 20-23 (E4M3 pools) widen the K tiles to the q dtype. Up to 128 rows, the sets take items by turns; above, two
-// sets take the halves of an item's columns and two the next one's, and the second half's sums pass through
-// shared memory. (Halves as products of their own would read K twice from shared memory: 227 us.) An item costs a warp some 200 instructions of its own at latencies that the sets hide from one
-// another: all warps on one tile, with the columns dealt among them, took twice as long (12 warps: 237 us
-// on the shape below).
-// Bounds, at 192 rows per (b, g) and head_dim 128: K from HBM once, 0.7 us a tile and SM; the products, 0.5 us; one
-// exp2 per (row, key, head) pair, 0.4 us.
+// 20-23 (E4M3 pools) widen the K tiles to the q dtype; 3 fills up the first warpgroup. Up to 128 rows, the sets
+// take items by turns; above, two sets take the halves of an item's columns and two the next one's, and the
+// second half's sums pass through shared memory. An item costs a summing warp some 200 instructions of its own,
+// at latencies that the sets hide from one another.
+//
+// Measured at batch 128, 96 beams, 16/8 heads, D = 128, bf16, 2800-3200 keys (192 rows per (b, g); K is 0.79 GB
+// and q, lse and the weights 0.06 GB): 166 us, 5.1 TB/s, 0.75 of what a copy reaches. The same kernel without the
+// sums takes 157 us, with all warps on one tile and the columns dealt among them 237 us at the best warp
+// count, with the halves as products of their own (K read twice from shared memory) 227 us. Per tile and SM:
+// K from HBM 0.7 us, the products 0.5 us, one exp2 per (row, key, head) pair 0.4 us; K bounds it.
 // Every wait is bounded (1 s without progress); on expiry the CTA flags BSP_DEVFLAG_TIMEOUT, drains its own
 // copies and MMAs, frees TMEM and exits.
 #include <cuda.h>

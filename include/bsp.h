@@ -566,10 +566,11 @@ BSP_API bsp_status bsp_decode_attn_noalloc(const bsp_geometry* geo, int32_t batc
  * They follow the conventions above: host-checkable errors return before any launch; nothing is allocated or
  * synchronised; indices in device memory are checked by the kernels. Their logits, scores, lists and tables
  * need the alignment of their element only (q, the pools and workspaces: 16 bytes), and every pointer must be
- * memory of the current device (or managed memory). They may be captured into a CUDA graph: the lengths are
- * read from the staged plan, so a replay follows later plans of the same batch and beam width (decode plans);
- * a replay that finds a plan of another shape, or lengths past the tables it was captured with, leaves what
- * it would write and sets BSP_DEVFLAG_GRAPH.
+ * memory of the current device (or managed memory). They may be captured into a CUDA graph. bsp_process_logits
+ * and bsp_beam_select take only the batch, the beam width and the status word of the plan, at the call. The others
+ * read the lengths from the staged plan, so that a replay follows later plans of the same batch and beam width
+ * (decode plans); a replay that finds a plan of another shape, or lengths past the tables it was captured
+ * with, leaves what it would write and sets BSP_DEVFLAG_GRAPH.
  */
 
 enum { BSP_LOGITS_BF16 = 0, BSP_LOGITS_FP16 = 1, BSP_LOGITS_FP32 = 2 };
@@ -626,7 +627,8 @@ typedef struct bsp_logits_params {
  * values: -inf for a row without a finite one, +inf with +inf in the row, NaN with a NaN.
  *   logits, out     [batch * beam_width] rows of vocab elements, logits_stride / out_stride elements apart
  *                   (>= vocab). out may be logits itself (same stride): only vectors that change are written
- *                   then; any other overlap is BSP_ERR_INVALID_ARG
+ *                   then; any other overlap of the two address ranges (first row's start to last row's end) is
+ *                   BSP_ERR_INVALID_ARG
  * A tensor-parallel or padded head's columns past vocab are neither read nor written.
  */
 BSP_API bsp_status bsp_process_logits(const bsp_plan_t* plan, const void* logits, int32_t logits_dtype,

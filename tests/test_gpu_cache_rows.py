@@ -261,6 +261,16 @@ def test_evict_prefill_plan():
     run_evict(c, plan, torch.rand((3, 2, 120), generator=c.gen).cuda(), [60, 10, 5], 1, 4, lens=[120, 0, 33])
 
 
+@pytest.mark.parametrize("P,stride,keep", [(47000, 47000, 20000), (52001, 52001, 52000), (120000, 120000, 3),
+                                           (60000, 1 << 19, 30011)])
+def test_evict_long_prompts(P, stride, keep):
+    """Prompts whose keys' order does not fit beside the bitmap, and rows of the tables as long as any may be."""
+    c = Cache(P, [P], 1, 1, 64, 64, "bf16")
+    plan = c.decode_plan(1)
+    w = torch.rand((1, 1, stride), generator=c.gen).cuda()
+    run_evict(c, plan, w, [keep], 4, 100)
+
+
 def test_evict_refuses_tails_and_bad_arguments():
     c = Cache(14, [100], 2, 2, 64, 16, "bf16")
     w = torch.rand((1, 2, 100), generator=c.gen).cuda()
