@@ -14,7 +14,7 @@ constexpr int kAdvThreads = 512;
 // One CTA per request. The tail columns of cache_indirection and of the generated tokens are gathered by
 // parent through shared memory, `cols` columns of both at a time: everything a round overwrites has been
 // read before, so the outputs may be the inputs. A few KB per request: the launch and two dependent loads
-// bound it.
+// bound it (one request of 4 beams 2.5 us, 128 requests of 96 beams 3.4 us, of which an empty launch is about 2).
 __global__ void __launch_bounds__(kAdvThreads) beam_advance_kernel(const AdvanceParams p) {
     extern __shared__ int32_t s_buf[];  // [2][cols][W]
     const int b = blockIdx.x, tid = threadIdx.x, W = p.W;

@@ -37,6 +37,8 @@ __device__ __forceinline__ int nth_bit(uint32_t m, int n) {
 // or behind keep and targets before it, so the order of the copies does not matter; outputs that are the
 // inputs are written once all CTAs of the cluster have read them.
 // Bound by the scattered rows' traffic, 2 x (K, V) x row bytes each; few heads: by the passes over the keys.
+// Measured, 8 kv heads, D = 128, 16 bits: batch 128, about 3000 rows cut to 1024: 161 us, 4.7 TB/s, 0.69 of what a
+// copy reaches (choosing in one kernel and moving in another: 246 us); one request of 10000 rows cut to 2048: 18.4 us.
 template <int NT>
 __global__ void __launch_bounds__(NT, 1024 / NT) evict_kernel(const EvictParams p) {
     extern __shared__ uint32_t s_dyn[];  // [3][words]: kept bits, movers and holes before the word; then the orders
@@ -262,7 +264,9 @@ cudaError_t launch_evict(EvictParams p, int longest, int num_sms, cudaStream_t s
     p.cached_keys = static_cast<int>(static_cast<size_t>(longest) * 4 <= room ? longest : room / 4);
     const size_t smem = bitmap + static_cast<size_t>(p.cached_keys) * 4;
     // Many (request, kv head) pairs: small CTAs, so that some choose while others move rows. Few: clusters of
-    // large ones, for the passes over the keys and for the copies.
+    // large ones, for the passes over the keys and for the copies. 3000 rows cut to 1024, small and large CTAs:
+    // 240 pairs 60 and 53 us, 304 pairs 65 and 59, 384 pairs 73 and 80, 1024 pairs 160 and 193 (600 rows cut to
+    // 300: 384 pairs 26 and 35). Above 10000 rows large ones stay ahead (512 pairs 337 and 311), by less.
     const long long heads = static_cast<long long>(p.batch) * p.Hkv;
     p.cluster = 1;
     if (heads > 2ll * num_sms) return launch_t<256>(p, smem, stream);

@@ -218,8 +218,9 @@ struct SelectParams {
     int segments;  // scanning units of a row
     int cap;       // keys of a scanning CTA's buffer
 };
-int select_unit_elems(int dtype);
+int select_unit_elems(int dtype, bool masked);
 int select_unit_warps();
+int select_sm_ctas(bool masked);
 int select_buffer(int K);
 cudaError_t launch_select(int dtype, const SelectParams& p, int most_lists, cudaStream_t stream);
 
@@ -253,7 +254,7 @@ struct WeightsParams {
     int batch, plan_w, plan_kind, Hq, Hkv, G, ps_log2, num_pages, max_keys, window, accumulate;
     int block_rows;  // beams (prompt tokens) of a Q block
     int mma_n;       // its rows for the MMA: block_rows * G rounded up to 16
-    int q_slots, k_slots, strided;
+    int q_slots, k_slots;
     float scale_log2, lse_mul;
 };
 constexpr int kWeightsBarBytes = 512;

@@ -272,10 +272,17 @@ __device__ __forceinline__ void store_at_rank(const void* p, uint32_t rank, floa
 
 // One cluster per row, each CTA a slice of the vocabulary. Tokens that the lists name are marked in two
 // bitmaps of the slice (penalised; in the table of counts and biases), so that a 16-byte vector without a
-// marked token costs two shared-memory words; a vector whose tokens the grammar rejects is not read at all.
+// marked token costs two shared-memory words; a vector whose tokens the grammar rejects is not read at all, and
+// where no 32 tokens have more than 8 allowed ones only those are read, one by one.
 // The lists, their lengths and the mask are fetched together, and with no mask the first logits before them:
-// a row is short beside their latencies, which several CTAs per SM hide from one another. Bound by the
-// logits' traffic, and by the exponentials' instructions where nothing is masked.
+// a row is short beside their latencies, which the four CTAs of an SM hide from one another.
+//
+// Bound by the logits' traffic, and then by the exponentials' instructions. Measured: 64 x 30 rows of 128000
+// bf16 (0.98 GB), lists and temperature, 222 us, 4.4 TB/s, 0.65 of what a copy reaches; without lists and
+// temperature 165 us, 0.88. (Five CTAs per SM at fewer registers 257 us, CTAs of 128 threads 271.)
+// Sparse masks: 128 x 96 rows of 32000 fp16 with 1 / 3 / 6 / 12 % allowed take 220 / 271 / 307 / 393 us by their
+// bits and 347 / 341 / 337 / 331 by vectors; 64 x 30 rows of 128000 bf16 166 / 205 / 213 / 235 and
+// 197 / 204 / 205 / 204. Eight of 32 are reached somewhere in a row at about 6 %.
 template <int DT>
 __global__ void __launch_bounds__(kProcThreads, 4) process_logits_kernel(const ProcessParams p) {
     using L = Logit<DT>;
@@ -349,7 +356,7 @@ __global__ void __launch_bounds__(kProcThreads, 4) process_logits_kernel(const P
         for (int i = tid; i < p.hash_slots; i += kProcThreads) table[i] = HashSlot{0u, 0u, ~0u};
     }
     if (tid == 0) s_listed = 0;
-    bool dense = !mrow;  // some 32 tokens of the slice have more than 8 allowed ones
+    bool dense = !mrow;  // or: some 32 tokens of the slice have more than 8 allowed ones
     if (mrow)
         for (int i = tid; i < words; i += kProcThreads) {
             const uint32_t m = mask_bits(mrow, (p.vocab + 31) >> 5, base + 32 * i);
@@ -646,7 +653,17 @@ cudaError_t launch_process_t(const ProcessParams& p, int cluster, size_t smem, c
 
 constexpr int kSelThreads = 256;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelU = 8;       // vectors per lane and unit
+// Vectors per lane and unit, and CTAs per SM at the registers that takes. Without masks eight in flight and 128
+// registers (built for three or four CTAs the loop spills). With masks much of a unit is the wait for the mask, then
+// for the tokens it leaves: more warps on smaller units (128 x 96 rows of 32000 bf16, K = 192, 1 / 3 / 12 % allowed:
+// 4 CTAs 191 / 208 / 263 us, 3 200 / 211 / 266, 2 252 / 264 / 327; eight vectors and 2 CTAs 250 / 267 / 480).
+template <bool MASKED>
+constexpr int kSelVectors = MASKED ? 4 : 8;
+template <bool MASKED>
+constexpr int kSelCtas = MASKED ? 4 : 2;
+// Allowed ones of any 32 tokens up to which they are read one by one (the rows above, 1 / 3 / 12 / 25 / 50 %: always
+// one by one 190 / 207 / 259 / 306 / 377 us, always vectors 293 / 298 / 296 / 297 / 292).
+constexpr int kByBits = 8;
 constexpr int kSelRounds = 4;  // units per warp of the sample that sets the first floor
 
 // Candidates as 64-bit keys: the score's order in the high half, the flat index (beam * vocab + token)
@@ -668,12 +685,15 @@ __device__ __forceinline__ uint64_t candidate_key(float score, uint32_t flat) {
 // of the best K, a share K / n of the sample's do, and the floor is the sample's vector maximum some four
 // deviations further down. It lets through a few times K candidates in all. If fewer than K come through, the
 // CTA scans its part of the request once more under the sample's K-th maximum, which is a sure bound.
-// Bound by reading the logits.
-template <int DT>
-__global__ void __launch_bounds__(kSelThreads, 2) beam_scan_kernel(const SelectParams p) {
+// Bound by reading the logits, and by the candidates' way through the buffer: 64 x 30 rows of 128000 bf16, K = 60,
+// 128 us, 3.8 TB/s, 0.56 of what a copy reaches; 128 x 96 rows of 32000, K = 192, 189 us (154 and 98 us with a
+// floor that no logit reaches, which is the scan alone). A run of units per warp in place of every eighth one
+// took 239 us for the latter, rings of bulk copies in shared memory 190-198 us.
+template <int DT, bool MASKED>
+__global__ void __launch_bounds__(kSelThreads, kSelCtas<MASKED>) beam_scan_kernel(const SelectParams p) {
     using L = Logit<DT>;
     using T = typename L::T;
-    constexpr int E = L::E, U = kSelU;
+    constexpr int E = L::E, U = kSelVectors<MASKED>;
     constexpr uint32_t ALL = (1u << E) - 1;
     extern __shared__ uint64_t s_buf[];  // [p.cap], cap >= the sample's keys (4 per thread) and > K
     __shared__ TopkScratch<kSelThreads> s_top;
@@ -721,7 +741,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) beam_scan_kernel(const SelectP
             x = cum > kNegInf ? static_cast<const T*>(p.x) + static_cast<long long>(r) * p.x_stride : nullptr;
             head = min(lead_elems<E>(x), p.vocab);
             nv = (p.vocab - head) / E;
-            mrow = mask_row(p.mask, r, p.status, flag);
+            if constexpr (MASKED) mrow = mask_row(p.mask, r, p.status, flag);
             set_reach();
         };
         auto score = [&](float v) { return __fadd_rn(__fsub_rn(v, lse), cum); };
@@ -769,21 +789,29 @@ __global__ void __launch_bounds__(kSelThreads, 2) beam_scan_kernel(const SelectP
                 ok = ok && key > floor_key;
             }
         };
-        // the lane's vectors of the unit that begins at vector v0, those with an allowed token; their tokens that
-        // count, E bits each
-        auto load = [&](int v0, uint4 (&val)[U]) -> uint64_t {
+        // lane i: which of tokens 32 i .. 32 i + 31 of the unit that begins at vector v0 are allowed
+        auto allowed = [&](int v0) -> uint32_t {
+            static_assert(!MASKED || U * E <= 32, "a word of the mask per lane");
+            const int t = head + v0 * E + 32 * lane, left = lane < U * E ? head + nv * E - t : 0;
+            if (left <= 0) return 0u;
+            return (mrow ? mask_bits(mrow, mwords, t) : ~0u) & (left < 32 ? (1u << left) - 1 : ~0u);
+        };
+        // the lane's vectors of the unit, those with an allowed token; their tokens that count, E bits each
+        auto load = [&](int v0, uint32_t word, uint4 (&val)[U]) -> uint64_t {
             const uint4* xv = reinterpret_cast<const uint4*>(x + head) + v0 + lane;
             uint64_t keep = 0;
-            if (!mrow && v0 + 32 * U <= nv) {
+            if (!MASKED && v0 + 32 * U <= nv) {
 #pragma unroll
                 for (int k = 0; k < U; ++k) val[k] = __ldcs(xv + 32 * k);
                 keep = E * U == 64 ? ~0ull : (1ull << (E * U & 63)) - 1;
             } else {
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
-                    const int v = v0 + lane + 32 * k;
-                    uint32_t m = v < nv ? ALL : 0u;
-                    if (m && mrow) m &= mask_bits(mrow, mwords, head + v * E);
+                    uint32_t m;
+                    if constexpr (MASKED)
+                        m = (__shfl_sync(~0u, word, lane * E / 32 + E * k) >> (lane * E & 31)) & ALL;
+                    else
+                        m = v0 + lane + 32 * k < nv ? ALL : 0u;
                     if (m) val[k] = __ldcs(xv + 32 * k);
                     keep |= static_cast<uint64_t>(m) << (E * k);
                 }
@@ -809,7 +837,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) beam_scan_kernel(const SelectP
                 if (!x) continue;
                 const int v0 = (u - w * nseg) * (32 * U);
                 uint4 val[U];
-                const uint64_t keep = load(v0, val);
+                const uint64_t keep = load(v0, MASKED ? allowed(v0) : 0u, val);
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
                     const uint32_t m = static_cast<uint32_t>(keep >> (E * k)) & ALL;
@@ -869,38 +897,37 @@ __global__ void __launch_bounds__(kSelThreads, 2) beam_scan_kernel(const SelectP
             if (!x) continue;
             const int v0 = seg * (32 * U);
             uint64_t pend = 0;  // the lane's elements that reach the floor
+            float first = 0.f;  // the first one's logit: most units that have any hold one
+            uint32_t word = 0;
             bool by_bits = false;
-            if (mrow) {
-                // a word of the mask per lane and 32 * 32 tokens; few allowed: those are read one by one
-                constexpr int N = U * E < 32 ? 1 : U * E / 32;
-                uint32_t bits[N];
-                int n = 0;
-#pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    const int t = head + v0 * E + 32 * (32 * j + lane), left = (U * E < 32 && lane >= U * E ? 0 : head + nv * E - t);
-                    bits[j] = left > 0 ? mask_bits(mrow, mwords, t) & (left < 32 ? (1u << left) - 1 : ~0u) : 0u;
-                    n = max(n, __popc(bits[j]));
-                }
-                n = __reduce_max_sync(~0u, n);
-                by_bits = n <= 8;
+            if constexpr (MASKED) {
+                // few allowed: those are read one by one
+                word = allowed(v0);
+                by_bits = __reduce_max_sync(~0u, __popc(word)) <= kByBits;
                 if (by_bits) {
+                    constexpr int R = 4;  // a lane's tokens in flight together
+                    while (__any_sync(~0u, word != 0)) {
+                        float v[R];
+                        int t[R];
 #pragma unroll
-                    for (int j = 0; j < N; ++j) {
-                        while (__any_sync(~0u, bits[j] != 0)) {
-                            const int t = head + v0 * E + 32 * (32 * j + lane) + (bits[j] ? __ffs(bits[j]) - 1 : 0);
-                            const float v = bits[j] ? L::get(x[t]) : kNegInf;
-                            const bool ok = bits[j] && v >= reach;
-                            bits[j] &= bits[j] - 1;
-                            if (__any_sync(~0u, ok)) put(ok, score(v), t);
+                        for (int q = 0; q < R; ++q) {
+                            t[q] = word ? head + v0 * E + 32 * lane + __ffs(word) - 1 : -1;
+                            v[q] = word ? L::get(x[t[q]]) : kNegInf;
+                            word &= word - 1;
+                        }
+#pragma unroll
+                        for (int q = 0; q < R; ++q) {
+                            const bool ok = t[q] >= 0 && v[q] >= reach;
+                            if (__any_sync(~0u, ok)) put(ok, score(v[q]), t[q]);
                         }
                     }
                 }
             }
             if (!by_bits) {
                 uint4 val[U];
-                const uint64_t keep = load(v0, val);
+                const uint64_t keep = load(v0, word, val);
                 bool hit = true;
-                if (!mrow && v0 + 32 * U <= nv) {  // all vectors there: one maximum
+                if (!MASKED && v0 + 32 * U <= nv) {  // all vectors there: one maximum
                     uint4 m = val[0];
 #pragma unroll
                     for (int k = 1; k < U; ++k) {
@@ -922,16 +949,24 @@ __global__ void __launch_bounds__(kSelThreads, 2) beam_scan_kernel(const SelectP
                         uint32_t got = 0;
 #pragma unroll
                         for (int e = 0; e < E; ++e) got |= f[e] >= reach ? 1u << e : 0u;
-                        if (some) pend |= static_cast<uint64_t>(got & m) << (E * k);
+                        if (some && (got & m)) {
+                            if (!pend) {
+                                const int e0 = __ffs(got & m) - 1;
+                                first = f[0];
+#pragma unroll
+                                for (int e = 1; e < E; ++e) first = e == e0 ? f[e] : first;
+                            }
+                            pend |= static_cast<uint64_t>(got & m) << (E * k);
+                        }
                     }
                 }
             }
-            while (__any_sync(~0u, pend != 0)) {
+            for (bool again = false; __any_sync(~0u, pend != 0); again = true) {
                 const bool ok = pend != 0;
                 const int bit = ok ? __ffsll(static_cast<long long>(pend)) - 1 : 0;
                 pend &= pend - 1;
                 const int t = head + E * (v0 + lane + 32 * (bit / E)) + bit % E;
-                const float v = ok ? L::get(x[t]) : kNegInf;
+                const float v = ok && again ? L::get(x[t]) : first;
                 put(ok, score(v), t);
             }
             // the ragged ends of a row: with its first and its last unit
@@ -1042,13 +1077,17 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const SelectP
     }
 }
 
+template <int DT, bool MASKED>
+cudaError_t launch_scan_t(const SelectParams& p, cudaStream_t stream) {
+    const size_t smem = static_cast<size_t>(p.cap) * 8;
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(beam_scan_kernel<DT, MASKED>), smem);
+    if (e != cudaSuccess) return e;
+    beam_scan_kernel<DT, MASKED><<<p.ctas, kSelThreads, smem, stream>>>(p);
+    return cudaGetLastError();
+}
 template <int DT>
 cudaError_t launch_scan(const SelectParams& p, cudaStream_t stream) {
-    const size_t smem = static_cast<size_t>(p.cap) * 8;
-    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(beam_scan_kernel<DT>), smem);
-    if (e != cudaSuccess) return e;
-    beam_scan_kernel<DT><<<p.ctas, kSelThreads, smem, stream>>>(p);
-    return cudaGetLastError();
+    return p.mask.bits ? launch_scan_t<DT, true>(p, stream) : launch_scan_t<DT, false>(p, stream);
 }
 
 }  // namespace
@@ -1061,9 +1100,10 @@ cudaError_t launch_process(int dtype, const ProcessParams& p, int cluster, size_
     }
 }
 
-// Logits of a scanning unit, and the least buffer of a CTA.
-int select_unit_elems(int dtype) { return 32 * kSelU * (dtype == BSP_LOGITS_FP32 ? 4 : 8); }
+// Logits of a scanning unit, warps of a CTA, CTAs resident on an SM, and the least buffer of a CTA.
+int select_unit_elems(int dtype, bool masked) { return 32 * (masked ? kSelVectors<true> : kSelVectors<false>) * (dtype == BSP_LOGITS_FP32 ? 4 : 8); }
 int select_unit_warps() { return kSelWarps; }
+int select_sm_ctas(bool masked) { return masked ? kSelCtas<true> : kSelCtas<false>; }
 int select_buffer(int K) {
     const int sample = 4 * kSelThreads;
     return K + 256 > sample ? K + 256 : sample;

@@ -67,21 +67,20 @@ bsp_status check_mask(const bsp_token_mask* m, int32_t vocab, TokenMask* out) {
 }
 
 constexpr size_t kMaxSmem = 227 * 1024;
-constexpr int64_t kMergeKeys = 16384;  // candidates one merging CTA holds (128 KB)
-constexpr int64_t kSelectCtas = 2;     // scanning CTAs per SM that are resident at once
+constexpr int64_t kMergeKeys = 16384;  // candidates one merging CTA holds (128 KB of its shared memory)
 
 // How a selection is cut: units of a row, scanning CTAs, and the most CTAs that meet one request.
 struct SelectSplit {
     int segments, ctas, lists;
 };
-SelectSplit select_split(int batch, int W, int vocab, int K, int dtype, int sms) {
+SelectSplit select_split(int batch, int W, int vocab, int K, int dtype, bool masked, int sms) {
     SelectSplit s;
-    s.segments = static_cast<int>(ceil_div(vocab, select_unit_elems(dtype)));
+    s.segments = static_cast<int>(ceil_div(vocab, select_unit_elems(dtype, masked)));
     const int64_t units = static_cast<int64_t>(W) * s.segments * batch;
     // a unit for each warp at least; a request's lists fit its merging CTA (an even cut of n CTAs over the
     // batch gives a request at most ceil(n / batch) + 1 of them)
     const int64_t merge = std::max<int64_t>(1, kMergeKeys / K - 1) * batch;
-    s.ctas = static_cast<int>(std::max<int64_t>(1, std::min({ceil_div(units, select_unit_warps()), kSelectCtas * sms, merge})));
+    s.ctas = static_cast<int>(std::max<int64_t>(1, std::min({ceil_div(units, select_unit_warps()), static_cast<int64_t>(select_sm_ctas(masked)) * sms, merge})));
     s.lists = static_cast<int>(ceil_div(s.ctas, std::max(1, batch)) + 1);
     return s;
 }
@@ -177,6 +176,11 @@ bsp_status bsp_process_logits(const bsp_plan_t* plan, const void* logits, int32_
     if (named > BSP_MAX_LISTED) return BSP_ERR_UNSUPPORTED;
     p.hash_slots = named ? std::max(4, 1 << ilog2(static_cast<int>(2 * named))) : 0;
 
+    // A cluster per row, its CTAs slices of the vocabulary. Few rows are cut while the CTAs are all resident at
+    // once (four per SM) and a slice keeps 4 KB: 4 rows of 256 KB 55 us whole, 31 / 18 / 12 in 2 / 4 / 8; 240 rows
+    // of 64 KB 16.7 whole, 14.9 / 19.5 in 2 / 4. Rows beyond that stay whole (960 rows of 256 KB 121, in two 126;
+    // 1920 of 64 KB 78 and 90), unless the bitmaps of a slice would leave fewer than four CTAs to an SM
+    // (3840 rows of 512 KB: 1028 whole, 751 in two, 814 in four).
     int cluster = 1;
     const int64_t row_bytes = static_cast<int64_t>(vocab) * es;
     while (cluster < 8 && static_cast<int64_t>(p.rows) * cluster * 2 <= 4 * plan->num_sms && row_bytes / (2 * cluster) >= 4096)
@@ -189,9 +193,9 @@ bsp_status bsp_process_logits(const bsp_plan_t* plan, const void* logits, int32_
         p.mask_at = p.hot_at + (p.hash_slots ? words : 0);
         p.table_at = p.mask_at + (p.mask.bits ? words : 0);
         smem = static_cast<size_t>(p.table_at) * 4 + static_cast<size_t>(p.hash_slots) * kProcessSlotBytes;
-        if (smem <= 40 * 1024) break;
+        if (smem <= 40 * 1024) break;  // (with the kernel's own 16 KB, four times in an SM)
         if (cluster == 8) {
-            if (smem > kMaxSmem - 18432) return BSP_ERR_UNSUPPORTED;
+            if (smem > kMaxSmem - 16 * 1024) return BSP_ERR_UNSUPPORTED;
             break;
         }
     }
@@ -202,8 +206,8 @@ bsp_status bsp_beam_select_workspace_size(int32_t batch, int32_t beam_width, int
                                           size_t* device_bytes) {
     if (!device_bytes || batch < 0 || beam_width < 1 || vocab < 1 || num_candidates < 1) return BSP_ERR_INVALID_ARG;
     if (vocab > BSP_MAX_VOCAB || num_candidates > BSP_MAX_CANDIDATES) return BSP_ERR_UNSUPPORTED;
-    // the most lists any logits type and SM count up to 1024 give
-    const SelectSplit s = select_split(std::max(batch, 1), beam_width, vocab, num_candidates, BSP_LOGITS_FP32, 1024);
+    // the most lists that any logits type, masks or none, and SM counts up to 512 give
+    const SelectSplit s = select_split(std::max(batch, 1), beam_width, vocab, num_candidates, BSP_LOGITS_FP32, true, 512);
     const int64_t lists = static_cast<int64_t>(s.ctas) + batch;
     *device_bytes = static_cast<size_t>(lists) * (static_cast<size_t>(num_candidates) + 2) * 8;
     return BSP_OK;
@@ -229,7 +233,7 @@ bsp_status bsp_beam_select(const bsp_plan_t* plan, const void* logits, int32_t l
     if (st != BSP_OK) return st;
     int sms = 0;
     if (!device_sms(&sms)) return BSP_ERR_CUDA;
-    const SelectSplit s = select_split(plan->batch, plan->beam_width, vocab, num_candidates, logits_dtype, std::min(sms, 1024));
+    const SelectSplit s = select_split(plan->batch, plan->beam_width, vocab, num_candidates, logits_dtype, p.mask.bits != nullptr, std::min(sms, 512));
     if (static_cast<int64_t>(plan->beam_width) * s.segments > (int64_t(1) << 30)) return BSP_ERR_UNSUPPORTED;
     const int64_t lists = static_cast<int64_t>(s.ctas) + plan->batch;
     if (static_cast<size_t>(lists) * (static_cast<size_t>(num_candidates) + 2) * 8 > workspace_bytes) return BSP_ERR_CAPACITY;
@@ -321,11 +325,12 @@ bsp_status key_weights_impl(const bsp_plan_t* plan, const void* q, const void* k
                                      : plan->total_rows;
     p.block_rows = std::min(rows, nmax / G);
     p.mma_n = static_cast<int>(ceil_div(p.block_rows * G, 16) * 16);
-    p.strided = rows > p.block_rows;
     const size_t q_bytes = static_cast<size_t>(D) * 2 * p.mma_n, k_bytes = static_cast<size_t>(D) * 2 * 128;
     const size_t fixed = 1024 + kWeightsTableBytes + kWeightsBarBytes + (static_cast<size_t>(plan->batch) + 1) * 4;
     const size_t room = kMaxSmem - fixed;
-    // a second Q slot hides the change of (request, kv head), a deeper K ring the latency of every tile
+    // A second Q slot hides the change of (request, kv head), a deeper K ring the latency of every tile: two slots
+    // where three K slots remain (30 beams, D = 128: group 2, 500 keys, 20.8 us and 23.0 with one; group 4, 2000
+    // keys, 55 and 58). With fewer the K ring is worth more (D = 256, group 4: one K slot left, 142 and 100).
     p.q_slots = 2 * q_bytes + 3 * k_bytes <= room ? 2 : 1;
     p.k_slots = static_cast<int>(std::min<size_t>(8, (room - p.q_slots * q_bytes) / k_bytes));
     if (p.k_slots < 1) return BSP_ERR_UNSUPPORTED;

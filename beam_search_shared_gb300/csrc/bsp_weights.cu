@@ -7,8 +7,9 @@
 // reduction across threads, no atomics, the same order on every run.
 //
 // Work item = (b, g, 128 keys). Its K tile is loaded once; the query rows pass in blocks of at most 256 (128
-// at head_dim 256). A CTA takes a contiguous run of items when one block holds all rows of a (b, g), so that Q
-// stays in shared memory from one tile to the next, and every gridDim-th item otherwise.
+// at head_dim 256). A CTA takes a contiguous run of items: where one block holds all rows of a (b, g), Q stays in
+// shared memory from one tile to the next, else its blocks in L2 (32 requests of 96 beams, group 4, D = 128, 2000
+// keys, two blocks: 100 us, and 115 with every gridDim-th item to a CTA).
 //
 // Warps: 0 loads K tiles (TMA boxes of a page, or 64 rows of one), 2 the Q blocks; 1 issues tcgen05.mma into four
 // TMEM accumulators of 128 columns, or two of 256; 4-19 sum: four sets of four warps (one per lane quadrant);
@@ -18,7 +19,7 @@
 // at latencies that the sets hide from one another.
 //
 // Measured at batch 128, 96 beams, 16/8 heads, D = 128, bf16, 2800-3200 keys (192 rows per (b, g); K is 0.79 GB
-// and q, lse and the weights 0.06 GB): 166 us, 5.1 TB/s, 0.75 of what a copy reaches. The same kernel without the
+// and q, lse and the weights 0.06 GB): 165 us, 5.1 TB/s, 0.75 of what a copy reaches. The same kernel without the
 // sums takes 157 us, with all warps on one tile and the columns dealt among them 237 us at the best warp
 // count, with the halves as products of their own (K read twice from shared memory) 227 us. Per tile and SM:
 // K from HBM 0.7 us, the products 0.5 us, one exp2 per (row, key, head) pair 0.4 us; K bounds it.
@@ -83,7 +84,6 @@ struct Walk {
     const int* cum;       // [batch + 1] key tiles of the requests before b
     long long at, end;
     int every;
-    bool near;            // neighbouring items
     int b = -1, last_b = -1, last_g = -1;
     int nt = 0;           // key tiles of request b
     // the current item: kv head, key tile; its request's keys, pages, first row, rows, blocks of rows; the blocks
@@ -93,19 +93,13 @@ struct Walk {
 
     __device__ __forceinline__ Walk(const WeightsParams& p, const int* cum_, int from = 0, int every_ = 1) : pp(&p), cum(cum_), every(every_) {
         const long long total = static_cast<long long>(cum[p.batch]) * p.Hkv;
-        near = !p.strided;
-        if (near) {
-            at = total * blockIdx.x / gridDim.x + from;
-            end = total * (blockIdx.x + 1) / gridDim.x;
-        } else {
-            at = blockIdx.x + static_cast<long long>(from) * gridDim.x;
-            end = total;
-        }
+        at = total * blockIdx.x / gridDim.x + from;
+        end = total * (blockIdx.x + 1) / gridDim.x;
     }
     __device__ __forceinline__ bool more() const { return at < end; }
-    __device__ __forceinline__ void next() { at += near ? every : static_cast<long long>(every) * gridDim.x; }
+    __device__ __forceinline__ void next() { at += every; }
     __device__ __forceinline__ void open() {
-        if (b >= 0 && near) {
+        if (b >= 0) {
             kt += every;
             while (kt >= nt) {
                 kt -= nt;
