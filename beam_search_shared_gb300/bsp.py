@@ -655,8 +655,8 @@ def beam_advance(plan_: Plan, parents: torch.Tensor, chosen: torch.Tensor,
     if tokens is not None:
         tokens_out = tokens if tokens_out is None else tokens_out
         token_cols = tokens.shape[-1]
-        token_stride = _table("tokens", tokens, i32, (rows, None))
-        if _table("tokens_out", tokens_out, i32, tuple(tokens.shape)) != token_stride:
+        token_stride = _table("tokens", tokens, i32, (rows, token_cols))
+        if _table("tokens_out", tokens_out, i32, (rows, token_cols)) != token_stride:
             raise ValueError("tokens and tokens_out must have the same row stride")
     if token_len is not None:
         _table("token_len", token_len, i32, (rows,))

@@ -673,7 +673,7 @@ __device__ __forceinline__ uint64_t candidate_key(float score, uint32_t flat) {
     return (static_cast<uint64_t>(float_order(score)) << 32) | static_cast<uint32_t>(~flat);
 }
 
-// The best K of each request in one pass over the logits. The units of all requests (32 * kSelU vectors of a
+// The best K of each request in one pass over the logits. The units of all requests (32 * kSelVectors vectors of a
 // row) are one sequence, cut evenly among the CTAs, whatever the batch; a CTA that crosses into another
 // request leaves its list and begins anew. Inside a CTA the warps scan on their own. A unit costs a packed
 // maximum over the lane's vectors and one comparison with the logit below which the row cannot reach the
@@ -686,7 +686,7 @@ __device__ __forceinline__ uint64_t candidate_key(float score, uint32_t flat) {
 // deviations further down. It lets through a few times K candidates in all. If fewer than K come through, the
 // CTA scans its part of the request once more under the sample's K-th maximum, which is a sure bound.
 // Bound by reading the logits, and by the candidates' way through the buffer: 64 x 30 rows of 128000 bf16, K = 60,
-// 128 us, 3.8 TB/s, 0.56 of what a copy reaches; 128 x 96 rows of 32000, K = 192, 189 us (154 and 98 us with a
+// 128 us, 3.8 TB/s, 0.56 of what a copy reaches; 128 x 96 rows of 32000, K = 192, 189 us (98 and 154 us with a
 // floor that no logit reaches, which is the scan alone). A run of units per warp in place of every eighth one
 // took 239 us for the latter, rings of bulk copies in shared memory 190-198 us.
 template <int DT, bool MASKED>
