@@ -38,6 +38,9 @@ bool optional_ptr(const void* p, size_t align) { return !p || device_ptr(p, alig
 
 int logits_bytes(int dtype) { return dtype == BSP_LOGITS_FP32 ? 4 : 2; }
 
+// The plan's workspace is on the current device, where the kernel is going to read it.
+bool plan_here(const bsp_plan_t* plan) { return device_ptr(plan->ws_device, 16); }
+
 int32_t* status_word(const bsp_plan_t* plan) { return static_cast<int32_t*>(plan->ws_device); }
 const int32_t* image_header(const bsp_plan_t* plan) {
     return reinterpret_cast<const int32_t*>(static_cast<const uint8_t*>(plan->ws_device) + kStatusBytes);
@@ -112,6 +115,7 @@ bsp_status bsp_process_logits(const bsp_plan_t* plan, const void* logits, int32_
     ProcessParams p{};
     p.rows = plan->total_rows;
     if (p.rows == 0) return BSP_OK;
+    if (!plan_here(plan)) return BSP_ERR_INVALID_ARG;
     if (!device_ptr(logits, es) || !device_ptr(out, es) || !optional_ptr(lse, 4)) return BSP_ERR_INVALID_ARG;
     if (out == logits && out_stride != logits_stride) return BSP_ERR_INVALID_ARG;
     if (out != logits) {
@@ -224,6 +228,7 @@ bsp_status bsp_beam_select(const bsp_plan_t* plan, const void* logits, int32_t l
     if (static_cast<int64_t>(plan->beam_width) * vocab > (int64_t(1) << 32) - 1) return BSP_ERR_UNSUPPORTED;
     if (plan->batch > 65535) return BSP_ERR_UNSUPPORTED;
     if (plan->total_rows == 0) return BSP_OK;
+    if (!plan_here(plan)) return BSP_ERR_INVALID_ARG;
     const int es = logits_bytes(logits_dtype);
     if (!device_ptr(logits, es) || !device_ptr(lse, 4) || !device_ptr(cum_scores, 4) || !device_ptr(scores, 4) ||
         !device_ptr(parents, 4) || !device_ptr(tokens, 4) || !device_ptr(workspace, 16))
@@ -269,6 +274,7 @@ bsp_status bsp_beam_advance(const bsp_plan_t* plan, const int32_t* parents, cons
         return BSP_ERR_INVALID_ARG;
     if (plan->beam_width > BSP_MAX_ADVANCE_BEAMS) return BSP_ERR_UNSUPPORTED;
     if (plan->total_rows == 0) return BSP_OK;
+    if (!plan_here(plan)) return BSP_ERR_INVALID_ARG;
     if (!device_ptr(parents, 4) || !device_ptr(chosen, 4) || !optional_ptr(ci_in, 4) || !optional_ptr(ci_out, 4) ||
         !optional_ptr(tokens_in, 4) || !optional_ptr(tokens_out, 4) || !optional_ptr(token_len, 4))
         return BSP_ERR_INVALID_ARG;
@@ -313,6 +319,7 @@ bsp_status key_weights_impl(const bsp_plan_t* plan, const void* q, const void* k
     if (weights_stride < plan->max_prefix_len) return BSP_ERR_INVALID_ARG;
     if (plan->batch > BSP_MAX_WEIGHTS_BATCH) return BSP_ERR_UNSUPPORTED;
     if (plan->total_rows == 0) return BSP_OK;
+    if (!plan_here(plan)) return BSP_ERR_INVALID_ARG;
     if (!device_ptr(q, 16) || !device_ptr(k_pool, 16) || !device_ptr(lse, 4) || !device_ptr(weights, 4))
         return BSP_ERR_INVALID_ARG;
     const int D = geo.head_dim, Hq = geo.num_q_heads, Hkv = geo.num_kv_heads, G = Hq / Hkv, ps = geo.page_size;
@@ -400,6 +407,7 @@ bsp_status bsp_evict_prefix(const bsp_plan_t* plan, const float* weights, int64_
     if (weights_stride < plan->max_prefix_len || out_stride < plan->max_prefix_len) return BSP_ERR_INVALID_ARG;
     if (plan->max_prefix_len > BSP_MAX_EVICT_ROWS || plan->batch > 65535) return BSP_ERR_UNSUPPORTED;
     if (plan->total_rows == 0) return BSP_OK;
+    if (!plan_here(plan)) return BSP_ERR_INVALID_ARG;
     if (!device_ptr(weights, 4) || !optional_ptr(positions, 4) || !device_ptr(keep_len, 4) || !device_ptr(k_pool, 16) ||
         !device_ptr(v_pool, 16) || !device_ptr(kept, 4) || !optional_ptr(weights_out, 4) || !optional_ptr(positions_out, 4))
         return BSP_ERR_INVALID_ARG;

@@ -565,8 +565,8 @@ BSP_API bsp_status bsp_decode_attn_noalloc(const bsp_geometry* geo, int32_t batc
  * These calls take the plan of the step for its batch, beam width, lengths, prompt pages and status word.
  * They follow the conventions above: host-checkable errors return before any launch; nothing is allocated or
  * synchronised; indices in device memory are checked by the kernels. Their logits, scores, lists and tables
- * need the alignment of their element only (q, the pools and workspaces: 16 bytes), and every pointer must be
- * memory of the current device (or managed memory). They may be captured into a CUDA graph. bsp_process_logits
+ * need the alignment of their element only (q, the pools and workspaces: 16 bytes), and every pointer, the plan's
+ * workspace too, must be memory of the current device (or managed memory). They may be captured into a CUDA graph. bsp_process_logits
  * and bsp_beam_select take only the batch, the beam width and the status word of the plan, at the call. The others
  * read the lengths from the staged plan, so that a replay follows later plans of the same batch and beam width
  * (decode plans); a replay that finds a plan of another shape, or lengths past the tables it was captured
@@ -711,7 +711,7 @@ BSP_API bsp_status bsp_key_weights_fp8(const bsp_plan_t* plan, const void* q, co
  * weights.
  *   plan           a decode plan without tail rows (they would follow the old length: BSP_ERR_INVALID_ARG) or
  *                  a prefill plan (a request without prompt rows is left as it is), whose requests share no
- *                  page with one another
+ *                  page with one another and hold none twice
  *   positions      device int32 [batch][num_kv_heads][weights_stride]: the slots' logical positions, or NULL:
  *                  the slot numbers (a cache that nothing was evicted from)
  *   keep_len       device int32 [batch]
