@@ -1054,26 +1054,27 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const SelectP
     }
     __syncthreads();
     int n = s_count;
-    if (n > p.K) {
+    if (n > p.K && n > kTopkRanked) {
         topk_compact<kMergeThreads>(s_buf, n, p.K, 0, s_top);
         n = p.K;
     }
-    // rank = number of larger keys (distinct keys, K <= 512): the output place
-    for (int i = tid; i < p.K; i += kMergeThreads) {
-        const long long o = static_cast<long long>(b) * p.K;
-        if (i < n) {
-            const uint64_t key = s_buf[i];
-            int place = 0;
-            for (int j = 0; j < n; ++j) place += s_buf[j] > key;
-            const uint32_t flat = ~static_cast<uint32_t>(key);
-            p.scores[o + place] = order_float(static_cast<uint32_t>(key >> 32));
-            p.parents[o + place] = static_cast<int32_t>(flat / static_cast<uint32_t>(p.vocab));
-            p.tokens[o + place] = static_cast<int32_t>(flat % static_cast<uint32_t>(p.vocab));
-        } else {
-            p.scores[o + i] = kNegInf;
-            p.parents[o + i] = -1;
-            p.tokens[o + i] = -1;
-        }
+    // rank = number of larger keys (distinct keys): the output place
+    const long long o = static_cast<long long>(b) * p.K;
+    for (int i = tid; i < n; i += kMergeThreads) {
+        const uint64_t key = s_buf[i];
+        int place = 0;
+#pragma unroll 8
+        for (int j = 0; j < n; ++j) place += s_buf[j] > key;
+        if (place >= p.K) continue;
+        const uint32_t flat = ~static_cast<uint32_t>(key);
+        p.scores[o + place] = order_float(static_cast<uint32_t>(key >> 32));
+        p.parents[o + place] = static_cast<int32_t>(flat / static_cast<uint32_t>(p.vocab));
+        p.tokens[o + place] = static_cast<int32_t>(flat % static_cast<uint32_t>(p.vocab));
+    }
+    for (int i = n + tid; i < p.K; i += kMergeThreads) {
+        p.scores[o + i] = kNegInf;
+        p.parents[o + i] = -1;
+        p.tokens[o + i] = -1;
     }
 }
 

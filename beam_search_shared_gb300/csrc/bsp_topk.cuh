@@ -16,6 +16,10 @@ __device__ __forceinline__ float order_float(uint32_t k) {
 }
 
 constexpr int kTopkBins = 1024;  // 32 x 32, so that two warp scans find a bin
+// Up to so many keys are ranked against one another at once, without the histogram (a selection of K = 8 over 4 x 50257
+// logits: up to 64, 128, 256 keys 11.6, 11.0, 11.6 us, never 14.0; K = 192 over 96 x 32000, 128 requests, masked: 212,
+// 212, 217 and 212).
+constexpr int kTopkRanked = 128;
 
 template <int NT>
 struct TopkScratch {
@@ -55,6 +59,22 @@ template <int NT, typename Key>
 __device__ uint64_t topk_threshold(int n, int K, int slack, TopkScratch<NT>& s, Key key) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int NW = NT / 32;
+    static_assert(kTopkRanked <= NT, "the keys ranked at once");
+    if (n <= kTopkRanked) {
+        if (tid < n) s.list[tid] = key(tid);
+        __syncthreads();
+        if (tid < n) {
+            const uint64_t k = s.list[tid];
+            int larger = 0;
+#pragma unroll 8
+            for (int j = 0; j < n; ++j) larger += s.list[j] > k;
+            if (larger == K - 1) s.range_lo = k;  // (no absent one: at least K keys are larger than those)
+        }
+        __syncthreads();
+        const uint64_t t = s.range_lo;
+        __syncthreads();
+        return t;
+    }
     uint64_t lo = ~0ull, hi = 0;
     for (int i = tid; i < n; i += NT) {
         const uint64_t k = key(i);

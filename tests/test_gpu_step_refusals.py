@@ -1,6 +1,4 @@
 """Calls around a step whose memory is not where the kernels could read it: refused before any launch."""
-import ctypes
-
 import numpy as np
 import pytest
 import torch
@@ -9,7 +7,7 @@ from beam_search_shared_gb300 import bsp
 
 pytestmark = pytest.mark.gpu
 
-INVALID = 1
+INVALID, STALE = 1, 5
 
 
 def state():
@@ -51,8 +49,8 @@ def test_memory_of_the_host_is_refused(name):
     moved = bsp.Plan.from_buffer_copy(plan)
     host = torch.zeros(4096, dtype=torch.uint8).pin_memory()
     moved.ws_device = host.data_ptr()
-    with pytest.raises(bsp.BspError) as e:
+    with pytest.raises(bsp.BspError) as e:  # not the workspace that the plan was staged in
         call(moved, t)
-    assert e.value.status == INVALID
+    assert e.value.status == STALE
     call(plan, t)
     assert bsp.read_device_status(plan) == (0, 0)
