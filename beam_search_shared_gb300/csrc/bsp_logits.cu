@@ -664,7 +664,7 @@ constexpr int kSelCtas = MASKED ? 4 : 2;
 // Allowed ones of any 32 tokens up to which they are read one by one (the rows above, 1 / 3 / 12 / 25 / 50 %: always
 // one by one 190 / 207 / 259 / 306 / 377 us, always vectors 293 / 298 / 296 / 297 / 292).
 constexpr int kByBits = 8;
-constexpr int kSelRounds = 4;  // units per warp of the sample that sets the first floor
+constexpr int kSelRounds = 4;  // most units per warp of the sample that sets the first floor
 
 // Candidates as 64-bit keys: the score's order in the high half, the flat index (beam * vocab + token)
 // complemented in the low half, so that the larger key is the better candidate and equal scores go by the
@@ -683,7 +683,7 @@ __device__ __forceinline__ uint64_t candidate_key(float score, uint32_t flat) {
 //
 // The first floor is guessed from a sample of units spread over the CTA's: if K of n vectors hold a candidate
 // of the best K, a share K / n of the sample's do, and the floor is the sample's vector maximum some four
-// deviations further down. It lets through a few times K candidates in all. If fewer than K come through, the
+// deviations further down. (The sample spreads over the rows: beams differ in their scores.) It lets through a few times K candidates in all. If fewer than K come through, the
 // CTA scans its part of the request once more under the sample's K-th maximum, which is a sure bound.
 // Bound by reading the logits, and by the candidates' way through the buffer: 64 x 30 rows of 128000 bf16, K = 60,
 // 128 us, 3.8 TB/s, 0.56 of what a copy reaches; 128 x 96 rows of 32000, K = 192, 189 us (98 and 154 us with a
@@ -819,20 +819,18 @@ __global__ void __launch_bounds__(kSelThreads, kSelCtas<MASKED>) beam_scan_kerne
             return keep;
         };
 
-        // ---- the first floor: from each of 32 units spread over the run (round q takes unit
-        // (2 (8 q + warp) + 1) / 64 of the way), or in a shorter run from each warp's first unit
+        // ---- the first floor: from up to four units per warp, spread over the run
         {
             const int units = u_end - u_begin;
-            const bool spread = units >= kSelRounds * kSelWarps;
-            const float mean = static_cast<float>(p.K) * min(units, spread ? kSelRounds * kSelWarps : kSelWarps) / units;
+            const int rounds = max(1, min(kSelRounds, units / kSelWarps)), probes = min(units, rounds * kSelWarps);
+            const float mean = static_cast<float>(p.K) * probes / units;
             const int rank = sure ? p.K : min(p.K, static_cast<int>(mean + 4.f * sqrtf(mean)) + 4);
             uint64_t best[4] = {0, 0, 0, 0};  // the lane's best candidates: of a round, or of a quarter of the unit
 #pragma unroll
             for (int q = 0; q < kSelRounds; ++q) {
-                if (!spread && (q > 0 || warp >= units)) break;
-                const int u = u_begin + (spread ? static_cast<int>(static_cast<long long>(units) * (2 * (q * kSelWarps + warp) + 1) /
-                                                                   (2 * kSelRounds * kSelWarps))
-                                                : warp);
+                const int probe = q * kSelWarps + warp;
+                if (q >= rounds || probe >= probes) break;
+                const int u = u_begin + static_cast<int>(static_cast<long long>(units) * (2 * probe + 1) / (2 * probes));
                 open_row(u / nseg, false);
                 if (!x) continue;
                 const int v0 = (u - w * nseg) * (32 * U);
@@ -853,7 +851,7 @@ __global__ void __launch_bounds__(kSelThreads, kSelCtas<MASKED>) beam_scan_kerne
                         }
                     const float sc = score(top);
                     const uint64_t key = sc > kNegInf ? key_of(sc, head + E * (v0 + lane + 32 * k) + e0) : 0;
-                    const int slot = spread ? q : k / (U / 4);
+                    const int slot = rounds > 1 ? q : k / (U / 4);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         if (i == slot && key > best[i]) best[i] = key;

@@ -79,12 +79,22 @@ struct SelectSplit {
 SelectSplit select_split(int batch, int W, int vocab, int K, int dtype, bool masked, int sms) {
     SelectSplit s;
     s.segments = static_cast<int>(ceil_div(vocab, select_unit_elems(dtype, masked)));
-    const int64_t units = static_cast<int64_t>(W) * s.segments * batch;
-    // a unit for each warp at least; a request's lists fit its merging CTA (an even cut of n CTAs over the
-    // batch gives a request at most ceil(n / batch) + 1 of them)
-    const int64_t merge = std::max<int64_t>(1, kMergeKeys / K - 1) * batch;
-    s.ctas = static_cast<int>(std::max<int64_t>(1, std::min({ceil_div(units, select_unit_warps()), static_cast<int64_t>(select_sm_ctas(masked)) * sms, merge})));
-    s.lists = static_cast<int>(ceil_div(s.ctas, std::max(1, batch)) + 1);
+    const int64_t requests = std::max(1, batch), warps = select_unit_warps();
+    const int64_t u = static_cast<int64_t>(W) * s.segments;  // units of a request
+    const int64_t most = static_cast<int64_t>(select_sm_ctas(masked)) * sms;
+    // a request's lists fit its merging CTA (an even cut of n CTAs over the batch gives a request at most
+    // ceil(n / requests) + 1 of them)
+    const int64_t room = std::max<int64_t>(1, kMergeKeys / K - 1);
+    // Few units: n CTAs for a request take about 3 us for each of a warp's ceil(u / 8n) units and 0.8 ns for each of
+    // the merge's n K keys, which is least near n^2 = 468 u / K; then as few as do with the same units per warp, and no
+    // CTA between two requests (1 x 30 rows of 128000, K = 60: 237 CTAs of 8 units 30.5 us, 118 of 16 25.5, 86 of 22
+    // 30.1, 59 of 32 27.3; 8 x 30 of 32000: 30 a request 23, 38 a request 29.5). Many, from 8 a warp on: all that are
+    // resident, on an even cut of the whole batch.
+    const int64_t best = static_cast<int64_t>(std::sqrt(468.0 * static_cast<double>(u) / K)) + 1;
+    const int64_t n = std::max<int64_t>(1, std::min({best, room, most / requests, ceil_div(u, warps)}));
+    const int64_t each = ceil_div(u, warps * n);  // units of a warp
+    s.ctas = static_cast<int>(each < 8 ? requests * ceil_div(u, warps * each) : std::min(most, room * requests));
+    s.lists = static_cast<int>(ceil_div(s.ctas, requests) + 1);
     return s;
 }
 
@@ -210,9 +220,13 @@ bsp_status bsp_beam_select_workspace_size(int32_t batch, int32_t beam_width, int
                                           size_t* device_bytes) {
     if (!device_bytes || batch < 0 || beam_width < 1 || vocab < 1 || num_candidates < 1) return BSP_ERR_INVALID_ARG;
     if (vocab > BSP_MAX_VOCAB || num_candidates > BSP_MAX_CANDIDATES) return BSP_ERR_UNSUPPORTED;
-    // the most lists that any logits type, masks or none, and SM counts up to 512 give
-    const SelectSplit s = select_split(std::max(batch, 1), beam_width, vocab, num_candidates, BSP_LOGITS_FP32, true, 512);
-    const int64_t lists = static_cast<int64_t>(s.ctas) + batch;
+    // No cut has more CTAs than one per request, or than are resident (up to 512 SMs), fit the merge and have a unit
+    // for every warp: of the smallest units, fp32 under masks.
+    const int64_t requests = std::max(1, batch), warps = select_unit_warps();
+    const int64_t u = static_cast<int64_t>(beam_width) * ceil_div(vocab, select_unit_elems(BSP_LOGITS_FP32, true));
+    const int64_t room = std::max<int64_t>(1, kMergeKeys / num_candidates - 1);
+    const int64_t ctas = std::max(requests, std::min({int64_t(select_sm_ctas(true)) * 512, room * requests, requests * ceil_div(u, warps)}));
+    const int64_t lists = ctas + batch;
     *device_bytes = static_cast<size_t>(lists) * (static_cast<size_t>(num_candidates) + 2) * 8;
     return BSP_OK;
 }
