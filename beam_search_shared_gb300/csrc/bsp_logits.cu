@@ -223,7 +223,7 @@ struct RowSum {
 // ---------------------------------------------------------------- process
 
 constexpr int kProcThreads = 256;
-constexpr int kProcListed = 768;  // marked vectors of a slice put aside
+constexpr int kProcListed = 96;  // marked vectors a warp puts aside
 
 struct HashSlot {
     uint32_t token;  // token + 1; 0: empty
@@ -278,8 +278,9 @@ __device__ __forceinline__ void store_at_rank(const void* p, uint32_t rank, floa
 // a row is short beside their latencies, which the four CTAs of an SM hide from one another.
 //
 // Bound by the logits' traffic, and then by the exponentials' instructions. Measured: 64 x 30 rows of 128000
-// bf16 (0.98 GB), lists and temperature, 222 us, 4.4 TB/s, 0.65 of what a copy reaches; without lists and
-// temperature 165 us, 0.88. (Five CTAs per SM at fewer registers 257 us, CTAs of 128 threads 271.)
+// bf16 (0.98 GB), lists and temperature, 235 us, 4.2 TB/s, 0.61 of what a copy reaches; without lists and
+// temperature 168 us, 0.86. (Five CTAs per SM at fewer registers 257 us, CTAs of 128 threads 271. One list of marked
+// vectors for the CTA, filled by an atomic counter, 229 us, but then the order of the sums differs from run to run.)
 // Sparse masks: 128 x 96 rows of 32000 fp16 with 1 / 3 / 6 / 12 % allowed take 220 / 271 / 307 / 393 us by their
 // bits and 347 / 341 / 337 / 331 by vectors; 64 x 30 rows of 128000 bf16 166 / 205 / 213 / 235 and
 // 197 / 204 / 205 / 204. Eight of 32 are reached somewhere in a row at about 6 %.
@@ -293,9 +294,9 @@ __global__ void __launch_bounds__(kProcThreads, 4) process_logits_kernel(const P
     extern __shared__ uint32_t smem[];
     __shared__ Running s_part[kProcThreads / 32];
     __shared__ float s_m[16], s_s[16];
-    __shared__ uint4 s_vec[kProcListed];  // marked vectors put aside, and their numbers
-    __shared__ int s_list[kProcListed];
-    __shared__ int s_listed;
+    __shared__ uint4 s_vec[kProcThreads / 32 * kProcListed];  // marked vectors put aside, and their numbers
+    __shared__ int s_list[kProcThreads / 32 * kProcListed];
+    __shared__ int s_listed[kProcThreads / 32];
 
     const int tid = threadIdx.x;
     const int rank = static_cast<int>(cluster_rank()), ranks = static_cast<int>(cluster_size());
@@ -355,7 +356,6 @@ __global__ void __launch_bounds__(kProcThreads, 4) process_logits_kernel(const P
         for (int i = tid; i < words; i += kProcThreads) bm_hot[i] = 0;
         for (int i = tid; i < p.hash_slots; i += kProcThreads) table[i] = HashSlot{0u, 0u, ~0u};
     }
-    if (tid == 0) s_listed = 0;
     bool dense = !mrow;  // or: some 32 tokens of the slice have more than 8 allowed ones
     if (mrow)
         for (int i = tid; i < words; i += kProcThreads) {
@@ -543,10 +543,13 @@ __global__ void __launch_bounds__(kProcThreads, 4) process_logits_kernel(const P
         finish(v, k, f);
     };
     if (dense) {
-        // all vectors of the slice but those with a marked token: these are listed, as far as the list goes, so
-        // that afterwards a warp has one for each lane
+        // all vectors of the slice but those with a marked token: each warp lists its own, as far as the list goes,
+        // so that afterwards all threads have one each; places in the order of the vectors, hence sums in the same
+        // order on every run
+        const int lane = tid & 31, warp = tid >> 5;
+        int listed = 0;
         bool loaded = !p.mask.bits;  // the first vectors are there
-        for (int vb = v0 + tid; vb < v1; vb += U * kProcThreads) {
+        for (int vb = v0 + tid; vb - lane < v1; vb += U * kProcThreads) {
             uint32_t keep = 0;  // E bits per vector
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -557,24 +560,35 @@ __global__ void __launch_bounds__(kProcThreads, 4) process_logits_kernel(const P
                 keep |= k << (E * u);
             }
             loaded = false;
-            uint32_t late = 0;
+            uint32_t late = 0, aside = 0;
+            if (pens || hots) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int v = vb + u * kProcThreads;
+                    const uint32_t k = (keep >> (E * u)) & ALL;
+                    const bool marked = k && (marked_bits(head + v * E - base) & k);
+                    const uint32_t who = __ballot_sync(~0u, marked);
+                    if (marked) {
+                        const int at = listed + __popc(who & ((1u << lane) - 1));
+                        aside |= 1u << u;
+                        if (at < kProcListed) {
+                            s_list[warp * kProcListed + at] = v;
+                            s_vec[warp * kProcListed + at] = val[u];
+                        } else {
+                            late |= 1u << u;
+                        }
+                    }
+                    listed += __popc(who);
+                }
+            }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int v = vb + u * kProcThreads;
                 if (v >= v1) break;
+                if ((aside >> u) & 1u) continue;
                 const uint32_t k = (keep >> (E * u)) & ALL;
                 if (!k) {
                     store(v, make_uint4(L::kNegInfPair, L::kNegInfPair, L::kNegInfPair, L::kNegInfPair));
-                    continue;
-                }
-                if ((pens || hots) && (marked_bits(head + v * E - base) & k)) {
-                    const int at = atomicAdd(&s_listed, 1);
-                    if (at < kProcListed) {
-                        s_list[at] = v;
-                        s_vec[at] = val[u];
-                    } else {
-                        late |= 1u << u;
-                    }
                     continue;
                 }
                 float f[E];
@@ -592,9 +606,14 @@ __global__ void __launch_bounds__(kProcThreads, 4) process_logits_kernel(const P
             }
         }
         if (pens || hots) {
+            if (lane == 0) s_listed[warp] = min(listed, kProcListed);
             __syncthreads();
-            const int listed = min(s_listed, kProcListed);
-            for (int i = tid; i < listed; i += kProcThreads) finish_marked(s_list[i], s_vec[i]);
+            for (int i = tid;; i += kProcThreads) {
+                int w = 0, j = i;  // the j-th of warp w
+                while (w < kProcThreads / 32 && j >= s_listed[w]) j -= s_listed[w++];
+                if (w == kProcThreads / 32) break;
+                finish_marked(s_list[w * kProcListed + j], s_vec[w * kProcListed + j]);
+            }
         }
     }
 
