@@ -700,14 +700,15 @@ __device__ __forceinline__ uint64_t candidate_key(float score, uint32_t flat) {
 // lane's next one at a time. When that is full the warps meet, cut it to the best K and raise the floor to the
 // K-th. Rows with a sparse mask are read by its bits.
 //
-// The first floor is guessed from a sample of units spread over the CTA's: if K of n vectors hold a candidate
-// of the best K, a share K / n of the sample's do, and the floor is the sample's vector maximum some four
-// deviations further down. (The sample spreads over the rows: beams differ in their scores.) It lets through a few times K candidates in all. If fewer than K come through, the
-// CTA scans its part of the request once more under the sample's K-th maximum, which is a sure bound.
+// The first floor is guessed from a sample of units spread over the CTA's, hence over its rows, for beams differ in
+// their scores: if K of n vectors hold a candidate of the best K, a share K / n of the sample's do, and the floor is
+// the sample's vector maximum some four deviations further down. It lets through a few times K candidates in all. If
+// fewer than K come through, the CTA scans its part of the request once more under the sample's K-th maximum, which is
+// a sure bound.
 // Bound by reading the logits, and by the candidates' way through the buffer: 64 x 30 rows of 128000 bf16, K = 60,
-// 128 us, 3.8 TB/s, 0.56 of what a copy reaches; 128 x 96 rows of 32000, K = 192, 189 us (98 and 154 us with a
-// floor that no logit reaches, which is the scan alone). A run of units per warp in place of every eighth one
-// took 239 us for the latter, rings of bulk copies in shared memory 190-198 us.
+// 129 us, 3.8 TB/s, 0.56 of what a copy reaches; 128 x 96 rows of 32000, K = 192, 190 us (98 and 154 us with a floor
+// that no logit reaches, which is the scan alone). A run of units per warp in place of every eighth one took 239 us for
+// the latter, rings of bulk copies in shared memory 190-198 us.
 template <int DT, bool MASKED>
 __global__ void __launch_bounds__(kSelThreads, kSelCtas<MASKED>) beam_scan_kernel(const SelectParams p) {
     using L = Logit<DT>;
