@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_kernel(const EvictParams 
     extern __shared__ uint32_t s_dyn[];  // [3][words]: kept bits, movers and holes before the word; then the orders
     __shared__ TopkScratch<NT> s_top;
     __shared__ int s_warp[2][32];
-    __shared__ int s_max;
+    __shared__ int s_last, s_fixed;  // the last position held; protected slots
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = p.cluster;
     const long long head = blockIdx.x / C;
@@ -67,15 +67,18 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_kernel(const EvictParams 
 
     // ---- the keys: protected slots above all weights, NaN below them, equal weights by the lower slot
     int last = P - 1;  // the last position held
+    if (tid == 0) {
+        s_last = INT32_MIN;
+        s_fixed = 0;
+    }
+    __syncthreads();
     if (pos) {
-        if (tid == 0) s_max = INT32_MIN;
-        __syncthreads();
         int m = INT32_MIN;
         for (int i = tid; i < P; i += NT) m = max(m, __ldcg(pos + i));
         m = __reduce_max_sync(~0u, m);
-        if (lane == 0) atomicMax(&s_max, m);
+        if (lane == 0) atomicMax(&s_last, m);
         __syncthreads();
-        last = s_max;
+        last = s_last;
     }
     const long long recent0 = static_cast<long long>(last) + 1 - p.recent;
     auto order = [&](int i) -> uint32_t {
@@ -90,8 +93,6 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_kernel(const EvictParams 
     uint32_t* s_ord = s_dyn + 3 * words;
     const bool cached = P <= p.cached_keys;
     int fixed = 0;  // protected slots
-    if (tid == 0) s_max = 0;
-    __syncthreads();
 #pragma unroll 4
     for (int i = tid; i < P; i += NT) {
         const uint32_t o = order(i);
@@ -99,9 +100,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_kernel(const EvictParams 
         fixed += o == ~0u;
     }
     fixed = __reduce_add_sync(~0u, fixed);
-    if (lane == 0) atomicAdd(&s_max, fixed);
+    if (lane == 0) atomicAdd(&s_fixed, fixed);
     __syncthreads();
-    fixed = s_max;
+    fixed = s_fixed;
     auto key = [&](int i) -> uint64_t {
         return (static_cast<uint64_t>(cached ? s_ord[i] : order(i)) << 32) | static_cast<uint32_t>(~i);
     };
