@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_kernel(const EvictParams 
     const long long head = blockIdx.x / C;
     const int rank = blockIdx.x % C;
     const int b = static_cast<int>(head / p.Hkv), h = static_cast<int>(head - static_cast<long long>(b) * p.Hkv);
-    if (!plan_matches(p.plan_hdr, p.batch, p.plan_w, p.plan_kind)) {
+    if (!plan_matches(p.plan_hdr, p.shape)) {
         if (tid == 0 && blockIdx.x == 0) atomicOr(p.status, BSP_DEVFLAG_GRAPH);
         return;
     }

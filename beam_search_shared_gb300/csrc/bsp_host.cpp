@@ -687,14 +687,20 @@ bsp_status plan_build_core(const bsp_geometry* geo, int32_t batch, int32_t beam_
     if (!image || image_bytes < need) return BSP_ERR_CAPACITY;
     uint8_t* img = static_cast<uint8_t*>(image);
     std::memset(img, 0, kImageHeaderBytes);
-    // header: [2] batch, [3] units, [4] beam width, [5] SM count, [6] kind, [7] tail bound (what a
-    // replayed graph checks against its capture)
-    reinterpret_cast<int32_t*>(img)[2] = batch;
-    reinterpret_cast<int32_t*>(img)[3] = static_cast<int32_t>(units.size());
-    reinterpret_cast<int32_t*>(img)[4] = part_w;
-    reinterpret_cast<int32_t*>(img)[5] = num_sms;
-    reinterpret_cast<int32_t*>(img)[6] = pf ? 1 : 0;
-    reinterpret_cast<int32_t*>(img)[7] = max_tail;
+    // header: what a replayed graph checks against its capture
+    int32_t* hdr = reinterpret_cast<int32_t*>(img);
+    hdr[kHdrBatch] = batch;
+    hdr[kHdrUnits] = static_cast<int32_t>(units.size());
+    hdr[kHdrWidth] = part_w;
+    hdr[kHdrSms] = num_sms;
+    hdr[kHdrKind] = pf ? 1 : 0;
+    hdr[kHdrMaxTail] = max_tail;
+    hdr[kHdrRows] = static_cast<int32_t>(total_rows);
+    hdr[kHdrPages] = static_cast<int32_t>(off_pages);
+    hdr[kHdrQHeads] = geo->num_q_heads;
+    hdr[kHdrKvHeads] = geo->num_kv_heads;
+    hdr[kHdrPageSize] = geo->page_size;
+    hdr[kHdrHeadDim] = geo->head_dim;
     int32_t* req = reinterpret_cast<int32_t*>(img + off_req);
     for (int b = 0; b < batch; ++b) {
         int32_t* r = req + static_cast<size_t>(b) * kReqFields;

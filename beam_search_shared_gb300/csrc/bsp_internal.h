@@ -20,7 +20,11 @@ constexpr size_t kStatusBytes = 256;
 constexpr size_t kAlign = 256;
 
 // Plan image (int32 fields, offsets relative to the image start).
-constexpr int kImageHeaderBytes = 64;  // u64 generation, i32 batch, i32 num_units, ...
+constexpr int kImageHeaderBytes = 64;  // u64 generation, then int32 fields:
+// kHdrRows: query rows of the plan; kHdrPages: bytes from the image's start to the page table; the heads, page
+// size and head_dim the plan was made for.
+enum HeaderField { kHdrBatch = 2, kHdrUnits = 3, kHdrWidth = 4, kHdrSms = 5, kHdrKind = 6, kHdrMaxTail = 7, kHdrRows = 8,
+                   kHdrPages = 9, kHdrQHeads = 10, kHdrKvHeads = 11, kHdrPageSize = 12, kHdrHeadDim = 13 };
 // Per-request record.
 // kReqFused: the prompt kernel finishes the request (one prompt partial state, and every unit's tail keys
 // fit the prompt kernel's tail tiles); the tail kernel skips it.
@@ -155,11 +159,30 @@ cudaError_t launch_wide(int head_dim, bool bf16, int ctas, const CUtensorMap& tq
                         const CUtensorMap& tv, const PrefixParams& p, cudaStream_t stream, bool fp8 = false);
 // ---------------------------------------------------------------- the operators around a step (bsp_step.cpp)
 
-// Whether the plan staged now has the shape a launch was made for: a launch replayed from a CUDA graph reads
-// the lengths of the latest plan. hdr: the image header ([2] batch, [4] beam width, [6] kind).
+// The plan a launch was made for, as far as what the launch fixes (addresses in the image, tensor maps, sizes of its
+// other tensors) depends on it.
+struct PlanShape {
+    int32_t gen[2];  // of a prefill plan
+    int32_t batch, w, kind, rows, pages_at, q_heads, kv_heads, page_size, head_dim;
+};
+
+// Whether the plan staged now is one the launch may follow: a launch replayed from a CUDA graph reads the lengths and
+// pages of the latest plan. hdr: its image's header.
 #ifdef __CUDACC__
+// For the requests' records alone, which stand at the same place in every image.
 __device__ __forceinline__ bool plan_matches(const int32_t* hdr, int batch, int w, int kind) {
-    return __ldg(hdr + 2) == batch && __ldg(hdr + 4) == w && __ldg(hdr + 6) == kind;
+    return __ldg(hdr + kHdrBatch) == batch && __ldg(hdr + kHdrWidth) == w && __ldg(hdr + kHdrKind) == kind;
+}
+// For the page table, q and lse too. A decode plan's image has one layout for its batch, beam width and geometry. A
+// prefill plan's is packed and its rows are the prompts' tokens: only the very plan of the launch will do.
+__device__ __forceinline__ bool plan_matches(const int32_t* hdr, const PlanShape& s) {
+    const int4* h = reinterpret_cast<const int4*>(hdr);
+    const int4 a = __ldg(h), b = __ldg(h + 1), c = __ldg(h + 2), d = __ldg(h + 3);
+    static_assert(kHdrBatch == 2 && kHdrWidth == 4 && kHdrKind == 6 && kHdrRows == 8 && kHdrPages == 9 && kHdrQHeads == 10 &&
+                      kHdrKvHeads == 11 && kHdrPageSize == 12 && kHdrHeadDim == 13, "the fields read as vectors");
+    return a.z == s.batch && b.x == s.w && b.z == s.kind && c.x == s.rows && c.y == s.pages_at && c.z == s.q_heads &&
+           c.w == s.kv_heads && d.x == s.page_size && d.y == s.head_dim &&
+           (s.kind == 0 || (a.x == s.gen[0] && a.y == s.gen[1]));
 }
 #endif
 
@@ -251,7 +274,8 @@ struct WeightsParams {
     float* weights;
     long long stride;
     int32_t* status;
-    int batch, plan_w, plan_kind, Hq, Hkv, G, ps_log2, num_pages, max_keys, window, accumulate;
+    PlanShape shape;
+    int batch, Hq, Hkv, G, ps_log2, num_pages, max_keys, window, accumulate;
     int block_rows;  // beams (prompt tokens) of a Q block
     int mma_n;       // its rows for the MMA: block_rows * G rounded up to 16
     int q_slots, k_slots;
@@ -276,7 +300,8 @@ struct EvictParams {
     int32_t* positions_out;
     long long stride, out_stride;
     int32_t* status;
-    int batch, plan_w, plan_kind, Hkv, ps_log2, row_bytes, max_keys, sinks, recent;
+    PlanShape shape;
+    int batch, Hkv, ps_log2, row_bytes, max_keys, sinks, recent;
     int cached_keys, cluster;  // set by launch_evict
 };
 // longest: the plan's longest prompt

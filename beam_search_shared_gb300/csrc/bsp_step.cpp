@@ -48,6 +48,14 @@ const int32_t* image_header(const bsp_plan_t* plan) {
 const int32_t* section(const bsp_plan_t* plan, uint64_t off) {
     return reinterpret_cast<const int32_t*>(static_cast<const uint8_t*>(plan->ws_device) + off);
 }
+// What the staged image's header says of this plan.
+PlanShape plan_shape(const bsp_plan_t* plan) {
+    const bsp_geometry& geo = plan->geo;
+    return PlanShape{{static_cast<int32_t>(plan->generation), static_cast<int32_t>(plan->generation >> 32)},
+                     plan->batch, plan->beam_width, plan->kind, plan->total_rows,
+                     static_cast<int32_t>(plan->off_pages - kStatusBytes), geo.num_q_heads, geo.num_kv_heads,
+                     geo.page_size, geo.head_dim};
+}
 
 // The decode plan, logits type, vocabulary and row stride that the logits' calls share.
 bsp_status check_logits(const bsp_plan_t* plan, int32_t dtype, int32_t vocab, int64_t stride) {
@@ -364,8 +372,7 @@ bsp_status key_weights_impl(const bsp_plan_t* plan, const void* q, const void* k
     p.stride = weights_stride;
     p.status = status_word(plan);
     p.batch = plan->batch;
-    p.plan_w = plan->beam_width;
-    p.plan_kind = plan->kind;
+    p.shape = plan_shape(plan);
     p.Hq = Hq;
     p.Hkv = Hkv;
     p.G = G;
@@ -444,8 +451,7 @@ bsp_status bsp_evict_prefix(const bsp_plan_t* plan, const float* weights, int64_
     p.out_stride = out_stride;
     p.status = status_word(plan);
     p.batch = plan->batch;
-    p.plan_w = plan->beam_width;
-    p.plan_kind = plan->kind;
+    p.shape = plan_shape(plan);
     p.Hkv = geo.num_kv_heads;
     p.ps_log2 = ilog2(geo.page_size);
     p.row_bytes = geo.head_dim * (geo.kv_dtype == BSP_KV_DTYPE_E4M3 ? 1 : 2);

@@ -185,7 +185,7 @@ key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     volatile int* abort_flag = &bars->abort_flag;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (!plan_matches(p.plan_hdr, p.batch, p.plan_w, p.plan_kind)) {
+    if (!plan_matches(p.plan_hdr, p.shape)) {
         if (tid == 0 && blockIdx.x == 0) atomicOr(p.status, BSP_DEVFLAG_GRAPH);
         return;
     }

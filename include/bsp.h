@@ -568,9 +568,10 @@ BSP_API bsp_status bsp_decode_attn_noalloc(const bsp_geometry* geo, int32_t batc
  * need the alignment of their element only (q, the pools and workspaces: 16 bytes), and every pointer, the plan's
  * workspace too, must be memory of the current device (or managed memory). They may be captured into a CUDA graph. bsp_process_logits
  * and bsp_beam_select take only the batch, the beam width and the status word of the plan, at the call. The others
- * read the lengths from the staged plan, so that a replay follows later plans of the same batch and beam width
- * (decode plans); a replay that finds a plan of another shape, or lengths past the tables it was captured
- * with, leaves what it would write and sets BSP_DEVFLAG_GRAPH.
+ * read the lengths from the staged plan, so that a replay follows later decode plans of the same batch, beam width and
+ * (bsp_key_weights, bsp_evict_prefix) geometry; a replay that finds any other plan, after a capture on a prefill
+ * plan any but that very one, or lengths past the tables it was captured with, leaves what it would write and sets
+ * BSP_DEVFLAG_GRAPH.
  */
 
 enum { BSP_LOGITS_BF16 = 0, BSP_LOGITS_FP16 = 1, BSP_LOGITS_FP32 = 2 };
