@@ -195,10 +195,15 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_kernel(const EvictParams 
             if (p.positions_out) p.positions_out[head * p.out_stride + i] = pos ? __ldcg(pos + from) : from;
         }
         long long src = 0, dst = 0;  // byte offsets of the rows in either pool
-        const bool moves = from != i;
+        bool moves = from != i;
         if (moves) {
-            src = (((static_cast<long long>(__ldg(pages + (from >> p.ps_log2))) * p.Hkv + h) << p.ps_log2) + (from & ps_mask)) * p.row_bytes;
-            dst = (((static_cast<long long>(__ldg(pages + (i >> p.ps_log2))) * p.Hkv + h) << p.ps_log2) + (i & ps_mask)) * p.row_bytes;
+            const int here = __ldg(pages + (from >> p.ps_log2)), there = __ldg(pages + (i >> p.ps_log2));
+            if (max(static_cast<unsigned>(here), static_cast<unsigned>(there)) >= static_cast<unsigned>(p.num_pages)) {
+                atomicOr(p.status, BSP_DEVFLAG_PAGE_INDEX);  // a replayed plan whose pools are larger: the row stays
+                moves = false;
+            }
+            src = (((static_cast<long long>(here) * p.Hkv + h) << p.ps_log2) + (from & ps_mask)) * p.row_bytes;
+            dst = (((static_cast<long long>(there) * p.Hkv + h) << p.ps_log2) + (i & ps_mask)) * p.row_bytes;
         }
         // lane k takes over the k-th slot that moves
         const uint32_t todo = __ballot_sync(~0u, moves);

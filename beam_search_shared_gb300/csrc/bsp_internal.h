@@ -301,7 +301,7 @@ struct EvictParams {
     long long stride, out_stride;
     int32_t* status;
     PlanShape shape;
-    int batch, Hkv, ps_log2, row_bytes, max_keys, sinks, recent;
+    int batch, Hkv, num_pages, ps_log2, row_bytes, max_keys, sinks, recent;
     int cached_keys, cluster;  // set by launch_evict
 };
 // longest: the plan's longest prompt

@@ -453,6 +453,7 @@ bsp_status bsp_evict_prefix(const bsp_plan_t* plan, const float* weights, int64_
     p.batch = plan->batch;
     p.shape = plan_shape(plan);
     p.Hkv = geo.num_kv_heads;
+    p.num_pages = geo.num_pages;
     p.ps_log2 = ilog2(geo.page_size);
     p.row_bytes = geo.head_dim * (geo.kv_dtype == BSP_KV_DTYPE_E4M3 ? 1 : 2);
     // lengths of a replayed plan are checked against this, the tables' room

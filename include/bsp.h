@@ -720,7 +720,8 @@ BSP_API bsp_status bsp_key_weights_fp8(const bsp_plan_t* plan, const void* q, co
  *                  was in slot kept[i]
  *   weights_out, positions_out   NULL, or [batch][num_kv_heads][out_stride]: the kept slots' weights and
  *                  positions (each may be its input when the strides agree)
- * Entries of the outputs from `keep` on stay as they were. weights_stride, out_stride >= the longest prompt.
+ * Entries of the outputs from `keep` on stay as they were. weights_stride, out_stride >= the longest prompt. A replay
+ * that finds a page id past the pools it was captured with does not copy that row and sets BSP_DEVFLAG_PAGE_INDEX.
  */
 BSP_API bsp_status bsp_evict_prefix(const bsp_plan_t* plan, const float* weights, int64_t weights_stride,
                                     const int32_t* positions, const int32_t* keep_len, int32_t sinks, int32_t recent,

@@ -224,3 +224,47 @@ def test_captured_bookkeeping_past_its_tables():
     before = [t.clone() for t in (ci, tok, n)]
     graph.replay()
     assert bsp.read_device_status(p) == REFUSED and same(before, (ci, tok, n))
+
+
+def test_replays_under_page_ids_past_the_captured_pools():
+    """A later plan of larger pools: rows on pages that the captured ones lack are neither read nor written, and flagged.
+    (The pools here have twice the pages the capture was told of.)"""
+    c = Cache(most=640)
+    n = c.pages
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    shape = (2 * n, c.Hkv, c.ps, c.D)
+    c.k, c.v = (torch.randn(shape, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    plan = c.decode([300, 500])
+    evict = capture(lambda: c.evict(plan))
+    weigh = capture(lambda: c.weigh(plan))
+    good = c.table.copy()
+    c.keep.fill_(200)
+    for odd in (1, 2):  # every second page of request 1 out of the capture's range, or all of them
+        c.table = good.copy()
+        c.table[1, ::3 - odd] += n
+        geo = bsp.geometry(4, c.Hkv, c.D, c.ps, 2 * n, "bf16")
+        plan = c.ws.plan(geo, c.B, c.W, np.array([300, 500], np.int32), np.zeros(2, np.int32), c.table)
+        bsp.key_weights(plan, c.q[:6], c.k, c.lse[:6], 0.125, c.sums)
+        want = c.sums.clone()
+        c.sums.fill_(-7.0)
+        weigh.replay()
+        assert bsp.read_device_status(plan) == (3, bsp.DEVFLAG_PAGE_INDEX)
+        assert torch.equal(c.sums[0], want[0])
+        on_known = torch.from_numpy(c.table[1, np.arange(500) // c.ps] < n).cuda()
+        assert torch.equal(c.sums[1][:, :500][:, on_known], want[1][:, :500][:, on_known])
+        before = c.state()
+        evict.replay()
+        assert bsp.read_device_status(plan) == (3, bsp.DEVFLAG_PAGE_INDEX)
+        w = c.w.cpu().numpy()
+        for b, rows in enumerate((300, 500)):
+            for h in range(c.Hkv):
+                src = steps.evict(w[b, h, :rows], 200, 2, 5)
+                assert np.array_equal(c.kept[b, h, :200].cpu().numpy(), src)
+                to, of = c.table[b, np.arange(200) // c.ps], c.table[b, src // c.ps]
+                moved = (to < n) & (of < n)
+                src = torch.from_numpy(np.where(moved, src, np.arange(200))).cuda()
+                pages = torch.from_numpy(c.table[b].astype(np.int64)).cuda()
+                i = torch.arange(200, device="cuda")
+                for new, old in ((c.k, before[0]), (c.v, before[1])):
+                    assert torch.equal(new[pages[i // c.ps], h, i % c.ps], old[pages[src // c.ps], h, src % c.ps])
+        assert torch.equal(c.k[n:], before[0][n:]) and torch.equal(c.v[n:], before[1][n:])
