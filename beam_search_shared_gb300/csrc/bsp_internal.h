@@ -283,6 +283,9 @@ struct WeightsParams {
 };
 constexpr int kWeightsBarBytes = 512;
 constexpr int kWeightsTableBytes = (8 * 128 + 4 * 128) * 4;  // -lse and partial sums
+// Before the tensor maps: their encoder needs a current context, and on a host thread that has made no CUDA call yet
+// the kernel's attribute is the first call to make one so.
+cudaError_t prepare_weights(int head_dim, bool bf16, bool fp8, size_t smem);
 cudaError_t launch_weights(int head_dim, bool bf16, bool fp8, const CUtensorMap& tq, const CUtensorMap& tk,
                            const WeightsParams& p, int ctas, size_t smem, cudaStream_t stream);
 

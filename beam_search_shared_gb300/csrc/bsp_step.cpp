@@ -384,6 +384,10 @@ bsp_status key_weights_impl(const bsp_plan_t* plan, const void* q, const void* k
     const float log2e = 1.4426950408889634f;
     p.scale_log2 = softmax_scale * k_scale * log2e;
     p.lse_mul = (flags & BSP_FLAG_LSE_BASE2) ? 1.f : log2e;
+    const size_t smem = fixed + p.q_slots * q_bytes + p.k_slots * k_bytes;
+    const bool bf16 = geo.dtype == BSP_DTYPE_BF16;
+    st = launched(prepare_weights(D, bf16, fp8, smem));
+    if (st != BSP_OK) return st;
     CUtensorMap tq, tk;
     cuuint64_t qdims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hq), static_cast<cuuint64_t>(plan->total_rows)};
     cuuint64_t qstr[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(Hq) * D * 2};
@@ -393,9 +397,7 @@ bsp_status key_weights_impl(const bsp_plan_t* plan, const void* q, const void* k
     cuuint32_t kbox[2] = {static_cast<cuuint32_t>(fp8 ? D : 64), static_cast<cuuint32_t>(std::min(ps, 64))};
     if (!encode_map(&tq, geo.dtype, 3, q, qdims, qstr, qbox) || !encode_map(&tk, geo.dtype, 2, k_pool, kdims, kstr, kbox, fp8))
         return BSP_ERR_CUDA;
-    const size_t smem = fixed + p.q_slots * q_bytes + p.k_slots * k_bytes;
-    st = launched(launch_weights(D, geo.dtype == BSP_DTYPE_BF16, fp8, tq, tk, p, plan->num_sms, smem,
-                                 static_cast<cudaStream_t>(stream)));
+    st = launched(launch_weights(D, bf16, fp8, tq, tk, p, plan->num_sms, smem, static_cast<cudaStream_t>(stream)));
     if (st != BSP_OK) return st;
     return (flags & BSP_FLAG_CHECK) ? bsp_read_device_status(plan, stream, 1, nullptr) : BSP_OK;
 }

@@ -528,32 +528,34 @@ key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     }
 }
 
-template <int D, bool BF16, bool FP8>
-cudaError_t launch_t(const CUtensorMap& tq, const CUtensorMap& tk, const WeightsParams& p, int ctas, size_t smem,
-                     cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(key_weights_kernel<D, BF16, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-    key_weights_kernel<D, BF16, FP8><<<ctas, weights_threads(FP8), smem, stream>>>(tq, tk, p);
-    return cudaGetLastError();
+using Kernel = void (*)(CUtensorMap, CUtensorMap, WeightsParams);
+template <int D>
+Kernel kernel_of(bool bf16) {
+    return bf16 ? key_weights_kernel<D, true, false> : key_weights_kernel<D, false, false>;
+}
+template <int D>
+Kernel kernel_of_fp8(bool bf16) {
+    return bf16 ? key_weights_kernel<D, true, true> : key_weights_kernel<D, false, true>;
+}
+Kernel kernel_of(int head_dim, bool bf16, bool fp8) {
+    if (fp8) return head_dim == 64 ? kernel_of_fp8<64>(bf16) : head_dim == 128 ? kernel_of_fp8<128>(bf16) : nullptr;
+    return head_dim == 64 ? kernel_of<64>(bf16) : head_dim == 128 ? kernel_of<128>(bf16) : kernel_of<256>(bf16);
 }
 
 }  // namespace
 
+cudaError_t prepare_weights(int head_dim, bool bf16, bool fp8, size_t smem) {
+    const Kernel kernel = kernel_of(head_dim, bf16, fp8);
+    if (!kernel) return cudaErrorInvalidValue;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+}
+
 cudaError_t launch_weights(int head_dim, bool bf16, bool fp8, const CUtensorMap& tq, const CUtensorMap& tk,
                            const WeightsParams& p, int ctas, size_t smem, cudaStream_t stream) {
-    if (fp8) {
-        if (head_dim == 64)
-            return bf16 ? launch_t<64, true, true>(tq, tk, p, ctas, smem, stream) : launch_t<64, false, true>(tq, tk, p, ctas, smem, stream);
-        if (head_dim == 128)
-            return bf16 ? launch_t<128, true, true>(tq, tk, p, ctas, smem, stream) : launch_t<128, false, true>(tq, tk, p, ctas, smem, stream);
-        return cudaErrorInvalidValue;
-    }
-    if (head_dim == 64)
-        return bf16 ? launch_t<64, true, false>(tq, tk, p, ctas, smem, stream) : launch_t<64, false, false>(tq, tk, p, ctas, smem, stream);
-    if (head_dim == 128)
-        return bf16 ? launch_t<128, true, false>(tq, tk, p, ctas, smem, stream) : launch_t<128, false, false>(tq, tk, p, ctas, smem, stream);
-    return bf16 ? launch_t<256, true, false>(tq, tk, p, ctas, smem, stream) : launch_t<256, false, false>(tq, tk, p, ctas, smem, stream);
+    const Kernel kernel = kernel_of(head_dim, bf16, fp8);
+    if (!kernel) return cudaErrorInvalidValue;
+    kernel<<<ctas, weights_threads(fp8), smem, stream>>>(tq, tk, p);
+    return cudaGetLastError();
 }
 
 }  // namespace bsp
