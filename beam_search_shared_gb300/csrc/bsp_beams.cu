@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kAdvThreads) beam_advance_kernel(const Advance
 
 cudaError_t launch_advance(const AdvanceParams& p, cudaStream_t stream) {
     const size_t smem = static_cast<size_t>(2) * p.cols * p.W * 4;
-    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(beam_advance_kernel), smem);
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(beam_advance_kernel), smem, kAdvanceSmem);
     if (e != cudaSuccess) return e;
     beam_advance_kernel<<<p.batch, kAdvThreads, smem, stream>>>(p);
     return cudaGetLastError();

@@ -240,9 +240,12 @@ __global__ void __launch_bounds__(NT, 1024 / NT) evict_kernel(const EvictParams 
     }
 }
 
+constexpr size_t kStatic = 14 * 1024;  // the kernel's other shared memory
+static_assert(sizeof(TopkScratch<1024>) + 1024 <= kStatic, "shared memory of the narrowing");
+
 template <int NT>
 cudaError_t launch_t(const EvictParams& p, size_t smem, cudaStream_t stream) {
-    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(evict_kernel<NT>), smem);
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(evict_kernel<NT>), smem, kMaxSmem - kStatic);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(p.batch) * p.Hkv * p.cluster);
@@ -264,9 +267,7 @@ cudaError_t launch_t(const EvictParams& p, size_t smem, cudaStream_t stream) {
 cudaError_t launch_evict(EvictParams p, int longest, int num_sms, cudaStream_t stream) {
     // the orders of the longest prompt in shared memory beside the bitmap, as far as they fit
     const size_t bitmap = static_cast<size_t>((p.max_keys + 31) >> 5) * 12;
-    constexpr size_t kStatic = 14 * 1024;  // the kernel's other shared memory
-    static_assert(sizeof(TopkScratch<1024>) + 1024 <= kStatic, "shared memory of the narrowing");
-    const size_t room = 227 * 1024 - kStatic - bitmap;
+    const size_t room = kMaxSmem - kStatic - bitmap;
     p.cached_keys = static_cast<int>(static_cast<size_t>(longest) * 4 <= room ? longest : room / 4);
     const size_t smem = bitmap + static_cast<size_t>(p.cached_keys) * 4;
     // Many (request, kv head) pairs: small CTAs, so that some choose while others move rows. Few: clusters of

@@ -186,11 +186,16 @@ __device__ __forceinline__ bool plan_matches(const int32_t* hdr, const PlanShape
 }
 #endif
 
+constexpr size_t kMaxSmem = 227 * 1024;  // shared memory of a CTA, static and dynamic
+
 // Lets a kernel of at most 16 KB of static shared memory have `smem` bytes of dynamic; within the 48 KB that every
-// kernel has, the call is saved (0.5 us of a launch's host time).
-inline cudaError_t allow_smem(const void* kernel, size_t smem) {
+// kernel has, the call is saved (0.5 us of a launch's host time). The limit belongs to the function, not to the launch:
+// it is set to `most`, the most that any call of the kernel asks for, so that threads whose calls differ in size set the
+// same value and none lowers it between another's setting and launch.
+inline cudaError_t allow_smem(const void* kernel, size_t smem, size_t most) {
     if (smem <= 32 * 1024) return cudaSuccess;
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (smem > most) return cudaErrorInvalidValue;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
 }
 
 struct TokenMask {
@@ -221,6 +226,7 @@ struct ProcessParams {
     int hash_slots;    // slots of the table of counts and biases (a power of two), 0: none
 };
 constexpr int kProcessSlotBytes = 12;
+constexpr size_t kProcessSmem = kMaxSmem - 16 * 1024;  // dynamic, beside the kernel's own
 cudaError_t launch_process(int dtype, const ProcessParams& p, int cluster, size_t smem, cudaStream_t stream);
 
 struct SelectParams {
@@ -241,6 +247,7 @@ struct SelectParams {
     int segments;  // scanning units of a row
     int cap;       // keys of a scanning CTA's buffer
 };
+constexpr int64_t kMergeKeys = 16384;  // candidates one merging CTA holds (128 KB of its shared memory)
 int select_unit_elems(int dtype, bool masked);
 int select_unit_warps();
 int select_sm_ctas(bool masked);
@@ -263,6 +270,7 @@ struct AdvanceParams {
     int batch, W, max_seq, tok_cols;
     int cols;  // tail columns of both tables staged at a time
 };
+constexpr size_t kAdvanceSmem = 160 * 1024;
 cudaError_t launch_advance(const AdvanceParams& p, cudaStream_t stream);
 
 struct WeightsParams {
@@ -285,7 +293,7 @@ constexpr int kWeightsBarBytes = 512;
 constexpr int kWeightsTableBytes = (8 * 128 + 4 * 128) * 4;  // -lse and partial sums
 // Before the tensor maps: their encoder needs a current context, and on a host thread that has made no CUDA call yet
 // the kernel's attribute is the first call to make one so.
-cudaError_t prepare_weights(int head_dim, bool bf16, bool fp8, size_t smem);
+cudaError_t prepare_weights(int head_dim, bool bf16, bool fp8);
 cudaError_t launch_weights(int head_dim, bool bf16, bool fp8, const CUtensorMap& tq, const CUtensorMap& tk,
                            const WeightsParams& p, int ctas, size_t smem, cudaStream_t stream);
 

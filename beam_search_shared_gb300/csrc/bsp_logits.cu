@@ -651,7 +651,7 @@ __global__ void __launch_bounds__(kProcThreads, 4) process_logits_kernel(const P
 
 template <int DT>
 cudaError_t launch_process_t(const ProcessParams& p, int cluster, size_t smem, cudaStream_t stream) {
-    cudaError_t e = allow_smem(reinterpret_cast<const void*>(process_logits_kernel<DT>), smem);
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(process_logits_kernel<DT>), smem, kProcessSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(p.rows) * cluster);
@@ -1098,9 +1098,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const SelectP
 
 template <int DT, bool MASKED>
 cudaError_t launch_scan_t(const SelectParams& p, cudaStream_t stream) {
-    const size_t smem = static_cast<size_t>(p.cap) * 8;
-    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(beam_scan_kernel<DT, MASKED>), smem);
-    if (e != cudaSuccess) return e;
+    const size_t smem = static_cast<size_t>(p.cap) * 8;  // at most 8 KB
     beam_scan_kernel<DT, MASKED><<<p.ctas, kSelThreads, smem, stream>>>(p);
     return cudaGetLastError();
 }
@@ -1134,7 +1132,7 @@ cudaError_t launch_select(int dtype, const SelectParams& p, int most_lists, cuda
                                                : launch_scan<BSP_LOGITS_FP32>(p, stream);
     if (e != cudaSuccess) return e;
     const size_t smem = static_cast<size_t>(most_lists) * p.K * 8;
-    e = allow_smem(reinterpret_cast<const void*>(beam_merge_kernel), smem);
+    e = allow_smem(reinterpret_cast<const void*>(beam_merge_kernel), smem, kMergeKeys * 8);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(p.batch);

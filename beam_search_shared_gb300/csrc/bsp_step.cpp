@@ -77,9 +77,6 @@ bsp_status check_mask(const bsp_token_mask* m, int32_t vocab, TokenMask* out) {
     return BSP_OK;
 }
 
-constexpr size_t kMaxSmem = 227 * 1024;
-constexpr int64_t kMergeKeys = 16384;  // candidates one merging CTA holds (128 KB of its shared memory)
-
 // How a selection is cut: units of a row, scanning CTAs, and the most CTAs that meet one request.
 struct SelectSplit {
     int segments, ctas, lists;
@@ -217,7 +214,7 @@ bsp_status bsp_process_logits(const bsp_plan_t* plan, const void* logits, int32_
         smem = static_cast<size_t>(p.table_at) * 4 + static_cast<size_t>(p.hash_slots) * kProcessSlotBytes;
         if (smem <= 40 * 1024) break;  // (with the kernel's own 16 KB, four times in an SM)
         if (cluster == 8) {
-            if (smem > kMaxSmem - 16 * 1024) return BSP_ERR_UNSUPPORTED;
+            if (smem > kProcessSmem) return BSP_ERR_UNSUPPORTED;
             break;
         }
     }
@@ -319,7 +316,7 @@ bsp_status bsp_beam_advance(const bsp_plan_t* plan, const int32_t* parents, cons
     p.max_seq = max_seq;
     p.tok_stride = token_stride;
     p.tok_cols = token_cols;
-    p.cols = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(BSP_MAX_TAIL, (160 * 1024) / (8 * int64_t(plan->beam_width)))));
+    p.cols = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(BSP_MAX_TAIL, int64_t(kAdvanceSmem) / (8 * int64_t(plan->beam_width)))));
     return launched(launch_advance(p, static_cast<cudaStream_t>(stream)));
 }
 
@@ -386,7 +383,7 @@ bsp_status key_weights_impl(const bsp_plan_t* plan, const void* q, const void* k
     p.lse_mul = (flags & BSP_FLAG_LSE_BASE2) ? 1.f : log2e;
     const size_t smem = fixed + p.q_slots * q_bytes + p.k_slots * k_bytes;
     const bool bf16 = geo.dtype == BSP_DTYPE_BF16;
-    st = launched(prepare_weights(D, bf16, fp8, smem));
+    st = launched(prepare_weights(D, bf16, fp8));
     if (st != BSP_OK) return st;
     CUtensorMap tq, tk;
     cuuint64_t qdims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hq), static_cast<cuuint64_t>(plan->total_rows)};

@@ -544,10 +544,10 @@ Kernel kernel_of(int head_dim, bool bf16, bool fp8) {
 
 }  // namespace
 
-cudaError_t prepare_weights(int head_dim, bool bf16, bool fp8, size_t smem) {
+cudaError_t prepare_weights(int head_dim, bool bf16, bool fp8) {
     const Kernel kernel = kernel_of(head_dim, bf16, fp8);
     if (!kernel) return cudaErrorInvalidValue;
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxSmem));
 }
 
 cudaError_t launch_weights(int head_dim, bool bf16, bool fp8, const CUtensorMap& tq, const CUtensorMap& tk,
