@@ -911,7 +911,7 @@ __global__ void __launch_bounds__(kSelThreads, kSelCtas<MASKED>) beam_scan_kerne
                 ++to_w;
             }
             if (to_w != w) open_row(to_w, lane == 0 && seg < kSelWarps);
-            if (s_full) meet(false);
+            if (__any_sync(~0u, s_full)) meet(false);  // (the lanes' reads may differ: the warp goes together)
             if (!x) continue;
             const int v0 = seg * (32 * U);
             uint64_t pend = 0;  // the lane's elements that reach the floor
