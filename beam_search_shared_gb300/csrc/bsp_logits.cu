@@ -234,7 +234,8 @@ static_assert(sizeof(HashSlot) == kProcessSlotBytes, "table slot");
 
 __device__ __forceinline__ uint32_t hash_of(uint32_t token, uint32_t mask) { return (token * 0x9E3779B1u >> 15) & mask; }
 
-// The table's slot of a token, claimed if it is new. The table has at least twice as many slots as tokens.
+// The table's slot of a token, claimed if it is new. The table has at least twice as many slots as tokens, or beside the
+// largest vocabularies as many.
 __device__ __forceinline__ HashSlot* hash_claim(HashSlot* table, uint32_t mask, uint32_t token) {
     uint32_t h = hash_of(token, mask);
     for (uint32_t probe = 0; probe <= mask; ++probe, h = (h + 1) & mask) {

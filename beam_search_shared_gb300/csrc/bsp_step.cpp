@@ -214,7 +214,15 @@ bsp_status bsp_process_logits(const bsp_plan_t* plan, const void* logits, int32_
         smem = static_cast<size_t>(p.table_at) * 4 + static_cast<size_t>(p.hash_slots) * kProcessSlotBytes;
         if (smem <= 40 * 1024) break;  // (with the kernel's own 16 KB, four times in an SM)
         if (cluster == 8) {
-            if (smem > kProcessSmem) return BSP_ERR_UNSUPPORTED;
+            if (smem > kProcessSmem) {
+                // More than 4096 named tokens beside the bitmaps of a large vocabulary: a table that they may fill, with
+                // longer walks to a slot (V = 2^21, all 8192 in one slice).
+                p.hash_slots = 1 << ilog2(static_cast<int>(named));
+                smem = static_cast<size_t>(p.table_at) * 4 + static_cast<size_t>(p.hash_slots) * kProcessSlotBytes;
+                static_assert(3 * ((BSP_MAX_VOCAB / 8 + 48) / 32 + 8) * 4 + BSP_MAX_LISTED * kProcessSlotBytes <= kProcessSmem &&
+                                  (BSP_MAX_LISTED & (BSP_MAX_LISTED - 1)) == 0,
+                              "the largest vocabulary with the longest lists");
+            }
             break;
         }
     }
