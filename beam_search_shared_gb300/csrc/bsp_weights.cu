@@ -43,6 +43,7 @@ constexpr int TK = 128;                             // keys per tile (MMA M)
 constexpr int kSets = 4;                            // sets of four summing warps
 constexpr int kSumWarps = 4 * kSets;
 constexpr int kSetCols = 128;                       // TMEM columns of an accumulator
+constexpr int kLse = kSetCols + 4;                  // words of a block's -lse
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint64_t kDrainWaitNs = 200000000ull;
 constexpr uint32_t FULL = 0xffffffffu;
@@ -178,8 +179,9 @@ key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     auto q_buf = [&](int slot) { return smem + slot * q_bytes; };
     auto k_buf = [&](int slot) { return smem + NQ * q_bytes + slot * K_BYTES; };
     uint8_t* rest = smem + NQ * q_bytes + KST * K_BYTES;
-    float* s_nlse = reinterpret_cast<float*>(rest);                 // [kSets][2][128]: -lse of the present block and the next
-    float* s_part = s_nlse + kSets * 2 * kSetCols;                  // [2][2][128]: of each pair of sets, two items
+    // [kSets][2][128 + 4]: -lse of the present block and the next, and which columns' rows add nothing, 32 a word
+    float* s_nlse = reinterpret_cast<float*>(rest);
+    float* s_part = s_nlse + kSets * 2 * kLse;                  // [2][2][128]: of each pair of sets, two items
     Bars* bars = reinterpret_cast<Bars*>(s_part + 2 * 2 * TK);
     int* s_cum = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + kWeightsBarBytes);  // [batch + 1]
     volatile int* abort_flag = &bars->abort_flag;
@@ -399,7 +401,7 @@ key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const int col0 = half * NU;                       // the set's first column of a block
         const int slot = halves ? pair : set;             // its accumulator
         const uint32_t acc = tmem + slot * acc_cols + col0 + (static_cast<uint32_t>(quad * 32) << 16);
-        float* nlse = s_nlse + set * 2 * kSetCols;        // of the present block: by turns in either half
+        float* nlse = s_nlse + set * 2 * kLse;            // of the present block: by turns in either half
         int k_slot = slot % KST;
         uint32_t acc_parity = 0, lse_parity = 0;
         Ring part(2);                                     // places of the second half's sums
@@ -415,20 +417,30 @@ key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     // -lse of the set's columns in base 2, a column per thread; -inf for rows without one. The other
                     // half of the buffer is still read by warps that are a block behind, but no further: they
                     // have arrived for the present block.
-                    nlse = s_nlse + set * 2 * kSetCols + (lse_parity ? 0 : kSetCols);
+                    nlse = s_nlse + set * 2 * kLse + (lse_parity ? 0 : kLse);
                     float v = -INFINITY;
+                    bool adds = true;
                     if (key_lane < min(n, NU)) {
                         const int i = (col0 + key_lane) / p.G;
                         const float l = __ldg(p.lse + static_cast<long long>(w.row0 + i0 + i) * p.Hq + w.g * p.G + (col0 + key_lane - i * p.G));
-                        v = l == -INFINITY ? -INFINITY : -l * p.lse_mul;
+                        adds = l != -INFINITY;
+                        if (adds) v = -l * p.lse_mul;
                     }
                     nlse[key_lane] = v;
+                    const uint32_t out = __ballot_sync(FULL, !adds);
+                    if (lane == 0) reinterpret_cast<uint32_t*>(nlse + kSetCols)[quad] = out;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars->lse_full[set]);
                     ok = __all_sync(FULL, mbar_wait(&bars->lse_full[set], lse_parity, abort_flag, kWaitNs));
                     if (!ok) break;
                     lse_parity ^= 1;
                 }
+                // A row with lse -inf adds nothing, whatever its q holds: a product that is not finite would make a NaN of
+                // its 0, so from the first 32 columns with such a row on they are left out one by one. (Looked up for
+                // every item: kept in a register over the items of a block 1 us more, a look at each 32 columns 5 us. At the
+                // size above 176 us a call from the host, and 175 without the case.)
+                const uint4 out4 = *reinterpret_cast<const uint4*>(nlse + kSetCols);
+                const int first = out4.x ? 0 : out4.y ? 32 : out4.z ? 64 : out4.w ? 96 : 128;
                 ok = __all_sync(FULL, mbar_wait(&bars->acc_full[slot], acc_parity, abort_flag, kWaitNs));
                 if (!ok) break;
                 acc_parity ^= 1;
@@ -438,12 +450,13 @@ key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const int cols = min(n, NU);
                 // columns below cmin are rows that do not see this thread's key
                 const int cmin = w.causal ? max(0, key - w.cbase - i0) * p.G - col0 : 0;
-                const bool all_see = !w.causal || w.kt * TK + TK - 1 <= w.cbase + i0;
+                // up to here: columns of the block whose rows all see the tile's keys and have a log-sum-exp
+                const int full = !w.causal || w.kt * TK + TK - 1 <= w.cbase + i0 ? min(cols, first) : 0;
                 for (int c0 = 0; c0 < cols; c0 += 32) {
                     uint32_t s[32];
                     tmem_ld32(acc + c0, s);
                     tmem_wait_ld();
-                    if (all_see && c0 + 32 <= cols) {
+                    if (c0 + 32 <= full) {
 #pragma unroll
                         for (int c = 0; c < 32; c += 4) {
                             const float4 l = *reinterpret_cast<const float4*>(nlse + c0 + c);
@@ -454,10 +467,11 @@ key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             add2_acc(sum[2], sum[3], ex2(e2), ex2(e3));
                         }
                     } else {
+                        const uint32_t out = __float_as_uint(nlse[kSetCols + (c0 >> 5)]);
 #pragma unroll
                         for (int c = 0; c < 32; ++c) {
                             const float e = ex2(fmaf(__uint_as_float(s[c]), c2, nlse[c0 + c]));
-                            sum[c & 3] += (c0 + c < cols && c0 + c >= cmin) ? e : 0.f;
+                            sum[c & 3] += (c0 + c < cols && c0 + c >= cmin && !((out >> c) & 1u)) ? e : 0.f;
                         }
                     }
                 }
