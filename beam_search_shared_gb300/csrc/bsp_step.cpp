@@ -253,7 +253,7 @@ bsp_status bsp_beam_select(const bsp_plan_t* plan, const void* logits, int32_t l
     if (num_candidates < 1 || cum_stride < plan->beam_width) return BSP_ERR_INVALID_ARG;
     if (num_candidates > BSP_MAX_CANDIDATES) return BSP_ERR_UNSUPPORTED;
     if (static_cast<int64_t>(plan->beam_width) * vocab > (int64_t(1) << 32) - 1) return BSP_ERR_UNSUPPORTED;
-    if (plan->batch > 65535) return BSP_ERR_UNSUPPORTED;
+    if (plan->batch > BSP_MAX_STEP_BATCH) return BSP_ERR_UNSUPPORTED;
     if (plan->total_rows == 0) return BSP_OK;
     if (!plan_here(plan)) return BSP_ERR_INVALID_ARG;
     const int es = logits_bytes(logits_dtype);
@@ -433,7 +433,7 @@ bsp_status bsp_evict_prefix(const bsp_plan_t* plan, const float* weights, int64_
     if (sinks < 0 || recent < 0) return BSP_ERR_INVALID_ARG;
     if (plan->max_tail_len > 0) return BSP_ERR_INVALID_ARG;  // tail rows follow the prompt: evict before there are any
     if (weights_stride < plan->max_prefix_len || out_stride < plan->max_prefix_len) return BSP_ERR_INVALID_ARG;
-    if (plan->max_prefix_len > BSP_MAX_EVICT_ROWS || plan->batch > 65535) return BSP_ERR_UNSUPPORTED;
+    if (plan->max_prefix_len > BSP_MAX_EVICT_ROWS || plan->batch > BSP_MAX_STEP_BATCH) return BSP_ERR_UNSUPPORTED;
     if (plan->total_rows == 0) return BSP_OK;
     if (!plan_here(plan)) return BSP_ERR_INVALID_ARG;
     if (!device_ptr(weights, 4) || !optional_ptr(positions, 4) || !device_ptr(keep_len, 4) || !device_ptr(k_pool, 16) ||

@@ -566,8 +566,9 @@ BSP_API bsp_status bsp_decode_attn_noalloc(const bsp_geometry* geo, int32_t batc
  * They follow the conventions above: host-checkable errors return before any launch; nothing is allocated or
  * synchronised; indices in device memory are checked by the kernels. Their logits, scores, lists and tables
  * need the alignment of their element only (q, the pools and workspaces: 16 bytes), and every pointer, the plan's
- * workspace too, must be memory of the current device (or managed memory). They may be captured into a CUDA graph. bsp_process_logits
- * and bsp_beam_select take only the batch, the beam width and the status word of the plan, at the call. The others
+ * workspace too, must be memory of the current device (or managed memory). They may be captured into a CUDA graph
+ * (without BSP_FLAG_CHECK, which synchronises). bsp_process_logits and bsp_beam_select take only the batch, the beam
+ * width and the status word of the plan, at the call. The others
  * read the lengths from the staged plan, so that a replay follows later decode plans of the same batch, beam width and
  * (bsp_key_weights, bsp_evict_prefix) geometry; a replay that finds any other plan, after a capture on a prefill
  * plan any but that very one, or lengths past the tables it was captured with, leaves what it would write and sets
@@ -580,6 +581,7 @@ enum { BSP_LOGITS_BF16 = 0, BSP_LOGITS_FP16 = 1, BSP_LOGITS_FP32 = 2 };
 #define BSP_MAX_LISTED 8192          /* token_cols (with frequency or presence penalties) + bias_cols */
 #define BSP_MAX_CANDIDATES 512       /* continuations per request of bsp_beam_select */
 #define BSP_MAX_ADVANCE_BEAMS 16384
+#define BSP_MAX_STEP_BATCH 65535     /* requests of bsp_beam_select and bsp_evict_prefix */
 #define BSP_MAX_WEIGHTS_BATCH 4096
 #define BSP_MAX_EVICT_ROWS (1 << 19) /* prompt rows per request of bsp_evict_prefix */
 
@@ -610,7 +612,7 @@ typedef struct bsp_logits_params {
     const float* repetition_penalty; /* [batch], > 0 */
     const float* frequency_penalty;  /* [batch] */
     const float* presence_penalty;   /* [batch] */
-    const float* temperature;        /* [batch], > 0 */
+    const float* temperature;        /* [batch], > 0 and large enough for a finite reciprocal (from 2^-127 on) */
     bsp_token_mask mask;
     int32_t prompt_cols, token_cols, bias_cols; /* columns of the lists */
     int32_t reserved;               /* 0 */

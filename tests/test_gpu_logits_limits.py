@@ -56,3 +56,44 @@ def test_long_lists_over_large_vocabularies(V, bias, made, scattered, masked):
         # the sum of V positive terms in some V / 512 additions a thread and a slice's eighth, as in the other tests
         ref = steps.log_sum_exp(got[r])
         assert abs(float(lse[r]) - ref) <= 2.0 ** -22 + 64 * 2.0 ** -22 + (V / 512 + 40) * 2.0 ** -24 + 3 * 2.0 ** -24 * (abs(ref) + 20)
+
+
+def small_step(B, W):
+    geo = bsp.geometry(2, 1, 64, 32, 1, "bf16")
+    ws = bsp.Workspace(geo, B, W, 1)
+    return ws, ws.plan(geo, B, W, np.zeros(B, np.int32), np.zeros(B, np.int32), np.zeros((B, 1), np.int32))
+
+
+def test_one_listed_token_too_many():
+    ws, plan = small_step(1, 1)
+    x = torch.zeros((1, 100), device="cuda")
+    i32 = torch.int32
+    bias = dict(bias_tokens=torch.zeros((1, 8000), dtype=i32, device="cuda"), bias_values=torch.ones((1, 8000), device="cuda"))
+    made = lambda n: dict(tokens=torch.ones((1, n), dtype=i32, device="cuda"), token_len=torch.full((1,), n, dtype=i32, device="cuda"))  # noqa: E731
+    rep, pen = dict(repetition_penalty=torch.ones(1, device="cuda")), dict(presence_penalty=torch.full((1,), 0.5, device="cuda"))
+    out = torch.empty_like(x)
+    bsp.process_logits(plan, x, bsp.LogitsParams(**bias, **made(192), **pen), out)
+    assert out[0, 0] == 1.0 and out[0, 1] == -0.5 and (out[0, 2:] == 0).all()
+    with pytest.raises(bsp.BspError) as e:
+        bsp.process_logits(plan, x, bsp.LogitsParams(**bias, **made(193), **pen), out)
+    assert e.value.status == 2
+    # histories that only the repetition penalty reads are no part of the limit
+    bsp.process_logits(plan, x, bsp.LogitsParams(**bias, **made(5000), **rep), out)
+    assert out[0, 0] == 1.0 and (out[0, 1:] == 0).all()
+
+
+def test_extreme_temperatures():
+    """From 2^-127, whose reciprocal is finite (a denormal), to 2^126: powers of two scale exactly."""
+    ws, plan = small_step(3, 1)
+    k = torch.arange(-50, 50, device="cuda").float()
+    x = torch.stack([k * 2.0 ** -130, k, k * 2.0 ** 100])
+    temperature = torch.tensor([2.0 ** -127, 0.25, 2.0 ** 126], device="cuda")
+    out, lse = torch.empty_like(x), torch.empty(3, device="cuda")
+    bsp.process_logits(plan, x, bsp.LogitsParams(temperature=temperature), out, lse)
+    want = torch.stack([k / 8, k * 4, k * 2.0 ** -26])
+    assert torch.equal(out, want)
+    # the other tests' bound: exponentials and their arguments, a few additions, and three roundings of the size of the
+    # result (-m log2(e) as one fp32 number: 2^-24 |m|; the last sum: half a step of the result, 2^-17 alone where the
+    # result is 196; the logarithm): 3 x 2^-24 (|result| + 20)
+    ref = torch.logsumexp(want.double(), -1)
+    assert ((lse - ref).abs() <= 2.0 ** -22 + 64 * 2.0 ** -22 + 41 * 2.0 ** -24 + 3 * 2.0 ** -24 * (ref.abs() + 20)).all()
