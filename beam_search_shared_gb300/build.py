@@ -15,7 +15,7 @@ SOURCES = ["bsp_host.cpp", "bsp_append.cu", "bsp_rope.cu", "bsp_tail.cu", "bsp_p
            "bsp_step.cpp", "bsp_logits.cu", "bsp_beams.cu", "bsp_weights.cu", "bsp_evict.cu"]
 # built without fast-math: their stored results are single IEEE operations in a fixed order
 EXACT_MATH = {"bsp_logits.cu", "bsp_beams.cu", "bsp_weights.cu", "bsp_evict.cu"}
-HEADERS = ["bsp_internal.h", "bsp_ptx.cuh", "bsp_prompt.cuh", "bsp_topk.cuh", "bsp_write.h"]
+HEADERS = ["bsp_internal.h", "bsp_step.h", "bsp_ptx.cuh", "bsp_prompt.cuh", "bsp_topk.cuh", "bsp_write.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -4,7 +4,7 @@
 #include <cstdint>
 
 #include "../../include/bsp.h"
-#include "bsp_internal.h"
+#include "bsp_step.h"
 
 namespace bsp {
 namespace {

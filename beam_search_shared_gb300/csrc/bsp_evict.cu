@@ -7,7 +7,7 @@
 #include <cstdint>
 
 #include "../../include/bsp.h"
-#include "bsp_internal.h"
+#include "bsp_step.h"
 #include "bsp_topk.cuh"
 
 namespace bsp {

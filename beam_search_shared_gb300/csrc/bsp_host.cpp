@@ -17,6 +17,7 @@
 
 #include "../../include/bsp.h"
 #include "bsp_internal.h"
+#include "bsp_step.h"
 #include "bsp_write.h"
 
 namespace {

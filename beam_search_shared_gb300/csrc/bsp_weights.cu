@@ -32,7 +32,7 @@
 #include <cstdint>
 
 #include "../../include/bsp.h"
-#include "bsp_internal.h"
+#include "bsp_step.h"
 #include "bsp_prompt.cuh"
 #include "bsp_ptx.cuh"
 
