@@ -149,8 +149,8 @@ struct WeightsParams {
     int q_slots, k_slots;
     float scale_log2, lse_mul;
 };
-constexpr int kWeightsBarBytes = 384;
-constexpr int kWeightsTableBytes = (8 * 132 + 4 * 128) * 4;  // -lse and partial sums
+constexpr int kWeightsBarBytes = 512;
+constexpr int kWeightsTableBytes = (8 * 128 + 4 * 128) * 4;  // -lse and partial sums
 // Before the tensor maps: their encoder needs a current context, and on a host thread that has made no CUDA call yet
 // the kernel's attribute is the first call to make one so.
 cudaError_t prepare_weights(int head_dim, bool bf16, bool fp8);

@@ -43,14 +43,13 @@ constexpr int TK = 128;                             // keys per tile (MMA M)
 constexpr int kSets = 4;                            // sets of four summing warps
 constexpr int kSumWarps = 4 * kSets;
 constexpr int kSetCols = 128;                       // TMEM columns of an accumulator
-constexpr int kLse = kSetCols + 4;                  // words of a block's -lse
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr uint64_t kDrainWaitNs = 200000000ull;
 constexpr uint32_t FULL = 0xffffffffu;
 
 struct Bars {
     uint64_t k_full[8], k_ready[8], k_empty[8];
-    uint64_t q_full[2], q_empty[2];
+    uint64_t q_full[2], q_clean[2], q_empty[2];
     uint64_t lse_full[kSets];   // a set's -lse of a new block
     uint64_t acc_full[kSets], acc_empty[kSets];
     uint64_t part_full[2][2];   // the second half's sums of an item of the pair of sets, in either place
@@ -65,6 +64,10 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// a load that stays where it is written, before the waits that follow
+__device__ __forceinline__ void ld_early(float& d, const float* p) {
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(d) : "l"(p));
 }
 // (d0, d1) = (a0, a1) * b + (c0, c1)
 __device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b, float c0, float c1) {
@@ -179,9 +182,8 @@ key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     auto q_buf = [&](int slot) { return smem + slot * q_bytes; };
     auto k_buf = [&](int slot) { return smem + NQ * q_bytes + slot * K_BYTES; };
     uint8_t* rest = smem + NQ * q_bytes + KST * K_BYTES;
-    // [kSets][2][128 + 4]: -lse of the present block and the next, and which columns' rows add nothing, 32 a word
-    float* s_nlse = reinterpret_cast<float*>(rest);
-    float* s_part = s_nlse + kSets * 2 * kLse;                  // [2][2][128]: of each pair of sets, two items
+    float* s_nlse = reinterpret_cast<float*>(rest);                 // [kSets][2][128]: -lse of the present block and the next
+    float* s_part = s_nlse + kSets * 2 * kSetCols;                  // [2][2][128]: of each pair of sets, two items
     Bars* bars = reinterpret_cast<Bars*>(s_part + 2 * 2 * TK);
     int* s_cum = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + kWeightsBarBytes);  // [batch + 1]
     volatile int* abort_flag = &bars->abort_flag;
@@ -199,6 +201,7 @@ key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->q_full[i], 1);
+            mbar_init(&bars->q_clean[i], 1);  // its rows without a log-sum-exp are 0
             mbar_init(&bars->q_empty[i], 1);  // the block's last product completed
             mbar_init(&bars->part_full[0][i], 4);
             mbar_init(&bars->part_full[1][i], 4);
@@ -326,7 +329,8 @@ key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 for (int rb = w.rb; rb < w.nrb && ok; ++rb) {
                     if (w.new_q) {
                         if (q_slot >= 0) mma_commit(&bars->q_empty[q_slot]);
-                        ok = mbar_wait(&bars->q_full[q.slot], q.parity, abort_flag, kWaitNs);
+                        ok = mbar_wait(&bars->q_full[q.slot], q.parity, abort_flag, kWaitNs) &&
+                             mbar_wait(&bars->q_clean[q.slot], q.parity, abort_flag, kWaitNs);
                         if (!ok) break;
                         q_slot = q.slot;
                         q_desc = q_desc0 + static_cast<uint32_t>(q.slot * (q_bytes >> 4));
@@ -359,17 +363,38 @@ key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
     } else if (warp == 2) {
         // ================= the Q blocks
+        // A row with lse -inf (padding) adds nothing whatever its q holds: exp2 of a finite product less infinity is 0,
+        // of a NaN or an infinite one it is a NaN. So such rows' q is cleared where it lies, between its load and the
+        // products: 1 % of the kernel (E4M3 pools 2.5 %, the smallest calls 0.6 us), 3 to 6 % where a third of the rows
+        // are such. (Leaving their columns out of the sums: 1 to 10 %, and 85 %. A warp of its own for the clearing: up to
+        // 5 %.) lse is fetched before the wait for the slot, so that the look costs the block no time.
+        const int line = p.G * D * 2 / 128;  // 128-byte lines of a row's heads
+        // j / line and c / G as products: exact for the at most 512 lines and 256 rows of a block
+        const int line_mul = 65536 / line + 1, g_mul = 65536 / p.G + 1;
+        int at[8];  // where lse of the block's rows lane + 32 j stands, of at most 256
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int c = lane + 32 * j, i = (c * g_mul) >> 16;
+            at[j] = i * p.Hq + (c - i * p.G);
+        }
         Ring q(NQ);
         bool ok = true;
         for (Walk w(p, s_cum); w.more() && ok; w.next()) {
             w.open();
             for (int rb = w.rb; rb < w.nrb && w.new_q; ++rb, q.next()) {
                 const int i0 = rb * p.block_rows;
+                const int rows_here = min(p.block_rows, w.seen - i0), n = rows_here * p.G;
+                const float* lse = p.lse + static_cast<long long>(w.row0 + i0) * p.Hq + w.g * p.G;
+                float l[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    l[j] = 0.f;
+                    if (lane + 32 * j < n) ld_early(l[j], lse + at[j]);
+                }
                 // the block on its way to L2: its shared-memory slot may be free only shortly before it is needed
-                const int line = p.G * D * 2 / 128;  // 128-byte lines of a row's heads
                 const uint8_t* rows = static_cast<const uint8_t*>(p.q) + (static_cast<long long>(w.row0 + i0) * p.Hq + w.g * p.G) * (D * 2);
-                for (int j = lane; j < min(p.block_rows, w.seen - i0) * line; j += 32) {
-                    const int i = j / line;
+                for (int j = lane; j < rows_here * line; j += 32) {
+                    const int i = (j * line_mul) >> 16;
                     prefetch_l2(rows + static_cast<long long>(i) * p.Hq * (D * 2) + (j - i * line) * 128);
                 }
                 ok = __all_sync(FULL, mbar_wait(&bars->q_empty[q.slot], q.parity ^ 1, abort_flag, kWaitNs));
@@ -380,6 +405,26 @@ key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         tma_load_3d(q_buf(q.slot) + c * NS * 128, &tm_q, &bars->q_full[q.slot], c * 64, w.g * p.G, w.row0 + i0);
                 }
                 __syncwarp();
+                uint32_t none = 0;  // bit j: row lane + 32 j has no log-sum-exp
+#pragma unroll
+                for (int j = 0; j < 8; ++j) none |= l[j] == -INFINITY ? 1u << j : 0u;
+                if (__any_sync(FULL, none != 0)) {
+                    ok = __all_sync(FULL, mbar_wait(&bars->q_full[q.slot], q.parity, abort_flag, kWaitNs));
+                    if (!ok) {
+                        q.next();  // (this slot's copy is under way: it is drained with the round's)
+                        break;
+                    }
+                    for (; none; none &= none - 1) {
+                        // (a row is 128 bytes in each column region, whatever the order of their 16-byte chunks)
+                        uint8_t* row = q_buf(q.slot) + (lane + 32 * (__ffs(none) - 1)) * 128;
+                        for (int c = 0; c < NC; ++c)
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) reinterpret_cast<uint4*>(row + c * NS * 128)[k] = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                if (lane == 0) mbar_arrive(&bars->q_clean[q.slot]);
             }
         }
         if (!ok) {
@@ -401,7 +446,7 @@ key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const int col0 = half * NU;                       // the set's first column of a block
         const int slot = halves ? pair : set;             // its accumulator
         const uint32_t acc = tmem + slot * acc_cols + col0 + (static_cast<uint32_t>(quad * 32) << 16);
-        float* nlse = s_nlse + set * 2 * kLse;            // of the present block: by turns in either half
+        float* nlse = s_nlse + set * 2 * kSetCols;        // of the present block: by turns in either half
         int k_slot = slot % KST;
         uint32_t acc_parity = 0, lse_parity = 0;
         Ring part(2);                                     // places of the second half's sums
@@ -417,30 +462,20 @@ key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     // -lse of the set's columns in base 2, a column per thread; -inf for rows without one. The other
                     // half of the buffer is still read by warps that are a block behind, but no further: they
                     // have arrived for the present block.
-                    nlse = s_nlse + set * 2 * kLse + (lse_parity ? 0 : kLse);
+                    nlse = s_nlse + set * 2 * kSetCols + (lse_parity ? 0 : kSetCols);
                     float v = -INFINITY;
-                    bool adds = true;
                     if (key_lane < min(n, NU)) {
                         const int i = (col0 + key_lane) / p.G;
                         const float l = __ldg(p.lse + static_cast<long long>(w.row0 + i0 + i) * p.Hq + w.g * p.G + (col0 + key_lane - i * p.G));
-                        adds = l != -INFINITY;
-                        if (adds) v = -l * p.lse_mul;
+                        v = l == -INFINITY ? -INFINITY : -l * p.lse_mul;
                     }
                     nlse[key_lane] = v;
-                    const uint32_t out = __ballot_sync(FULL, !adds);
-                    if (lane == 0) reinterpret_cast<uint32_t*>(nlse + kSetCols)[quad] = out;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars->lse_full[set]);
                     ok = __all_sync(FULL, mbar_wait(&bars->lse_full[set], lse_parity, abort_flag, kWaitNs));
                     if (!ok) break;
                     lse_parity ^= 1;
                 }
-                // A row with lse -inf adds nothing, whatever its q holds: a product that is not finite would make a NaN of
-                // its 0, so from the first 32 columns with such a row on they are left out one by one. (Looked up for
-                // every item: kept in a register over the items of a block 1 us more, a look at each 32 columns 5 us. At the
-                // size above 176 us a call from the host, and 175 without the case.)
-                const uint4 out4 = *reinterpret_cast<const uint4*>(nlse + kSetCols);
-                const int first = out4.x ? 0 : out4.y ? 32 : out4.z ? 64 : out4.w ? 96 : 128;
                 ok = __all_sync(FULL, mbar_wait(&bars->acc_full[slot], acc_parity, abort_flag, kWaitNs));
                 if (!ok) break;
                 acc_parity ^= 1;
@@ -450,13 +485,12 @@ key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const int cols = min(n, NU);
                 // columns below cmin are rows that do not see this thread's key
                 const int cmin = w.causal ? max(0, key - w.cbase - i0) * p.G - col0 : 0;
-                // up to here: columns of the block whose rows all see the tile's keys and have a log-sum-exp
-                const int full = !w.causal || w.kt * TK + TK - 1 <= w.cbase + i0 ? min(cols, first) : 0;
+                const bool all_see = !w.causal || w.kt * TK + TK - 1 <= w.cbase + i0;
                 for (int c0 = 0; c0 < cols; c0 += 32) {
                     uint32_t s[32];
                     tmem_ld32(acc + c0, s);
                     tmem_wait_ld();
-                    if (c0 + 32 <= full) {
+                    if (all_see && c0 + 32 <= cols) {
 #pragma unroll
                         for (int c = 0; c < 32; c += 4) {
                             const float4 l = *reinterpret_cast<const float4*>(nlse + c0 + c);
@@ -467,11 +501,10 @@ key_weights_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             add2_acc(sum[2], sum[3], ex2(e2), ex2(e3));
                         }
                     } else {
-                        const uint32_t out = __float_as_uint(nlse[kSetCols + (c0 >> 5)]);
 #pragma unroll
                         for (int c = 0; c < 32; ++c) {
                             const float e = ex2(fmaf(__uint_as_float(s[c]), c2, nlse[c0 + c]));
-                            sum[c & 3] += (c0 + c < cols && c0 + c >= cmin && !((out >> c) & 1u)) ? e : 0.f;
+                            sum[c & 3] += (c0 + c < cols && c0 + c >= cmin) ? e : 0.f;
                         }
                     }
                 }

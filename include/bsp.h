@@ -687,7 +687,7 @@ BSP_API bsp_status bsp_beam_advance(const bsp_plan_t* plan, const int32_t* paren
  * key j of its prompt (a decode plan: j < P_b; a prefill plan: j < cached + prompt rows),
  *   weights[b][g][j] = sum over rows r of b and query heads h of g of exp(softmax_scale * q[r][h] . k[j] - lse[r][h])
  * with lse from the attention of the same rows (bsp_decode_attn: the whole sequence's, tail included; base 2
- * with BSP_FLAG_LSE_BASE2). A row with lse -inf adds nothing, whatever its q holds (padding). A causal prefill's row adds to the keys it sees.
+ * with BSP_FLAG_LSE_BASE2). A row with lse -inf adds nothing, whatever its q holds (padding; over finite keys). A causal prefill's row adds to the keys it sees.
  *   window        a prefill plan: only the last `window` prompt rows of each request are summed (0: all);
  *                 a decode plan: 0
  *   flags         BSP_FLAG_LSE_BASE2, BSP_FLAG_CHECK, BSP_FLAG_ACCUMULATE (add to weights)
