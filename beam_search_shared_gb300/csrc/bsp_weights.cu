@@ -23,6 +23,8 @@
 // sums takes 157 us, with all warps on one tile and the columns dealt among them 237 us at the best warp
 // count, with the halves as products of their own (K read twice from shared memory) 227 us. Per tile and SM:
 // K from HBM 0.7 us, the products 0.5 us, one exp2 per (row, key, head) pair 0.4 us; K bounds it.
+// A weight is good to some 2^-21: the hardware's exp2 is off by 2^-22, its argument, whose -lse log2(e) is one fp32 number
+// so that a packed FMA does the whole, by 2^-23 of lse (itself fp32, off by as much), the fp32 product by less.
 // Every wait is bounded (1 s without progress); on expiry the CTA flags BSP_DEVFLAG_TIMEOUT, drains its own
 // copies and MMAs, frees TMEM and exits.
 #include <cuda.h>
