@@ -678,14 +678,20 @@ def _rows_ok(plan_: Plan, q: torch.Tensor, lse: torch.Tensor):
         raise ValueError(f"lse must be contiguous fp32 [{plan_.total_rows}, {plan_.geo.num_q_heads}]")
 
 
-def _pool_ok(plan_: Plan, name: str, t: torch.Tensor):
-    """A pool of the plan's geometry: its element type, all of its pages, contiguous (the calls go by its address)."""
+_POOL_TYPES = {(KV_DTYPE_SAME, 0): (torch.bfloat16,), (KV_DTYPE_SAME, 1): (torch.float16,),
+               (KV_DTYPE_E4M3, 0): (torch.uint8, torch.float8_e4m3fn), (KV_DTYPE_E4M3, 1): (torch.uint8, torch.float8_e4m3fn)}
+
+
+def _pools_ok(plan_: Plan, *pools: torch.Tensor):
+    """Pools of the plan's geometry: its element type, all of its pages, contiguous (the calls go by their addresses)."""
     g = plan_.geo
-    row = (g.num_kv_heads, g.page_size, g.head_dim)
-    types = (torch.uint8, torch.float8_e4m3fn) if g.kv_dtype == KV_DTYPE_E4M3 else (torch.bfloat16 if g.dtype == 0 else torch.float16,)
-    if (t.dtype not in types or not t.is_contiguous() or t.numel() < g.num_pages * row[0] * row[1] * row[2] or
-            (t.dim() == 4 and tuple(t.shape[1:]) != row)):
-        raise ValueError(f"{name} must be contiguous {types[0]} [{g.num_pages}, {row[0]}, {row[1]}, {row[2]}], not {t.dtype} {tuple(t.shape)}")
+    heads, slots, dim, types = g.num_kv_heads, g.page_size, g.head_dim, _POOL_TYPES[g.kv_dtype, g.dtype]
+    shape = (g.num_pages, heads, slots, dim)
+    for t in pools:
+        if t.dtype in types and t.is_contiguous() and (t.shape == shape or (  # (the usual case first)
+                t.numel() >= shape[0] * heads * slots * dim and (t.dim() != 4 or t.shape[1:] == shape[1:]))):
+            continue
+        raise ValueError(f"a pool must be contiguous {types[0]} {list(shape)}, not {t.dtype} {list(t.shape)}")
 
 
 def key_weights(plan_: Plan, q: torch.Tensor, k_pool: torch.Tensor, lse: torch.Tensor, softmax_scale: float,
@@ -693,7 +699,7 @@ def key_weights(plan_: Plan, q: torch.Tensor, k_pool: torch.Tensor, lse: torch.T
     """bsp_key_weights: the attention weight each prompt key received from the plan's query rows, into weights
     fp32 [batch, num_kv_heads, >= longest prompt] (flags FLAG_ACCUMULATE: added to it)."""
     _rows_ok(plan_, q, lse)
-    _pool_ok(plan_, "k_pool", k_pool)
+    _pools_ok(plan_, k_pool)
     stride = _key_table(plan_, "weights", weights, torch.float32)
     _check("bsp_key_weights", load().bsp_key_weights(
         ctypes.byref(plan_), q.data_ptr(), k_pool.data_ptr(), lse.data_ptr(), float(softmax_scale), int(window),
@@ -704,7 +710,7 @@ def key_weights_fp8(plan_: Plan, q: torch.Tensor, k_pool: torch.Tensor, lse: tor
                     k_scale: float, weights: torch.Tensor, window: int = 0, flags: int = 0, stream=None):
     """bsp_key_weights_fp8: key_weights over a uint8 E4M3 pool (key = code x k_scale)."""
     _rows_ok(plan_, q, lse)
-    _pool_ok(plan_, "k_pool", k_pool)
+    _pools_ok(plan_, k_pool)
     stride = _key_table(plan_, "weights", weights, torch.float32)
     _check("bsp_key_weights_fp8", load().bsp_key_weights_fp8(
         ctypes.byref(plan_), q.data_ptr(), k_pool.data_ptr(), lse.data_ptr(), float(softmax_scale), float(k_scale),
@@ -721,8 +727,7 @@ def evict_prefix(plan_: Plan, weights: torch.Tensor, keep_len: torch.Tensor, sin
     stride = _key_table(plan_, "weights", weights, torch.float32)
     out_stride = _key_table(plan_, "kept", kept, i32)
     _table("keep_len", keep_len, i32, (plan_.batch,))
-    _pool_ok(plan_, "k_pool", k_pool)
-    _pool_ok(plan_, "v_pool", v_pool)
+    _pools_ok(plan_, k_pool, v_pool)
     if positions is not None and _key_table(plan_, "positions", positions, i32) != stride:
         raise ValueError("positions must have the row stride of weights")
     for name, t, dt in (("weights_out", weights_out, torch.float32), ("positions_out", positions_out, i32)):
