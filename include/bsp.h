@@ -568,11 +568,10 @@ BSP_API bsp_status bsp_decode_attn_noalloc(const bsp_geometry* geo, int32_t batc
  * need the alignment of their element only (q, the pools and workspaces: 16 bytes), and every pointer, the plan's
  * workspace too, must be memory of the current device (or managed memory). They may be captured into a CUDA graph
  * (without BSP_FLAG_CHECK, which synchronises). bsp_process_logits and bsp_beam_select take only the batch, the beam
- * width and the status word of the plan, at the call. The others
- * read the lengths from the staged plan, so that a replay follows later decode plans of the same batch, beam width and
- * (bsp_key_weights, bsp_evict_prefix) geometry; a replay that finds any other plan, after a capture on a prefill
- * plan any but that very one, or lengths past the tables it was captured with, leaves what it would write and sets
- * BSP_DEVFLAG_GRAPH.
+ * width and the status word of the plan, at the call. The others read the lengths from the staged plan, so that a replay
+ * follows later decode plans of the same batch, beam width and (bsp_key_weights, bsp_evict_prefix) geometry; a replay
+ * that finds any other plan, after a capture on a prefill plan any but that very one, or lengths past the tables it was
+ * captured with, leaves what it would write and sets BSP_DEVFLAG_GRAPH.
  */
 
 enum { BSP_LOGITS_BF16 = 0, BSP_LOGITS_FP16 = 1, BSP_LOGITS_FP32 = 2 };
@@ -687,7 +686,8 @@ BSP_API bsp_status bsp_beam_advance(const bsp_plan_t* plan, const int32_t* paren
  * key j of its prompt (a decode plan: j < P_b; a prefill plan: j < cached + prompt rows),
  *   weights[b][g][j] = sum over rows r of b and query heads h of g of exp(softmax_scale * q[r][h] . k[j] - lse[r][h])
  * with lse from the attention of the same rows (bsp_decode_attn: the whole sequence's, tail included; base 2
- * with BSP_FLAG_LSE_BASE2). A row with lse -inf adds nothing, whatever its q holds (padding; over finite keys). A causal prefill's row adds to the keys it sees.
+ * with BSP_FLAG_LSE_BASE2). A row with lse -inf adds nothing, whatever its q holds (padding; over finite keys). A
+ * causal prefill's row adds to the keys it sees.
  *   window        a prefill plan: only the last `window` prompt rows of each request are summed (0: all);
  *                 a decode plan: 0
  *   flags         BSP_FLAG_LSE_BASE2, BSP_FLAG_CHECK, BSP_FLAG_ACCUMULATE (add to weights)

@@ -42,3 +42,38 @@ def test_weights_eviction_and_bookkeeping_repeat(B, W, Hq, Hkv, D, most, positio
         first = got if first is None else first
         assert all(torch.equal(a, b) for a, b in zip(got, first))
     assert bsp.read_device_status(plan) == (0, 0)
+
+
+def test_weights_beside_the_attention_of_another_step():
+    """Both hold tensor memory: on two streams at once each gives what it gives alone."""
+    def make(seed, B, W, P, Hq, Hkv, D):
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        wide = -(-P // 32)
+        geo = bsp.geometry(Hq, Hkv, D, 32, B * wide, "bf16")
+        ws = bsp.Workspace(geo, B, W, wide)
+        plan = ws.plan(geo, B, W, np.full(B, P, np.int32), np.zeros(B, np.int32), np.arange(B * wide, dtype=np.int32).reshape(B, wide))
+        k, v = (torch.randn((B * wide, Hkv, 32, D), generator=gen, device="cuda").bfloat16() for _ in range(2))
+        q = torch.randn((B * W, Hq, D), generator=gen, device="cuda").bfloat16()
+        out = torch.empty_like(q), torch.empty((B * W, Hq), device="cuda"), torch.zeros((B, Hkv, P), device="cuda")
+        attend = lambda s: bsp.decode_attn(plan, q, k, v, None, None, D ** -0.5, out[0], out[1], stream=s)  # noqa: E731
+        weigh = lambda s: bsp.key_weights(plan, q, k, out[1], D ** -0.5, out[2], stream=s)  # noqa: E731
+        return ws, plan, attend, weigh, out
+
+    steps_ = [make(1, 16, 30, 900, 16, 8, 128), make(2, 8, 96, 1200, 8, 4, 64)]
+    want = []
+    for _, _, attend, weigh, out in steps_:
+        attend(None)
+        weigh(None)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in out])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    (_, _, attend_a, weigh_a, _), (_, _, attend_b, weigh_b, _) = steps_
+    for _ in range(100):
+        attend_a(streams[0])
+        weigh_b(streams[1])
+        weigh_a(streams[0])
+        attend_b(streams[1])
+    torch.cuda.synchronize()
+    for (_, plan, _, _, out), w in zip(steps_, want):
+        assert bsp.read_device_status(plan) == (0, 0)
+        assert all(torch.equal(a, b) for a, b in zip(out, w))
