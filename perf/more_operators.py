@@ -286,6 +286,7 @@ def prepare(case, seed):
         geo = bsp.geometry(q_heads, kv, dim, page, total, case["dtype"])
         s["ws"] = bsp.Workspace(geo, batch, beam, prompt.shape[1])
         s["plan"] = s["ws"].plan(geo, batch, beam, lens, tails, prompt)
+        s["fork_ws"] = bsp.fork_workspace(batch, case["forks"])
     return s
 
 
@@ -317,7 +318,7 @@ def _prepare_compact(case, s, gen, rs, bsp):
         geo = bsp.geometry(kv, kv, dim, page, pages, case["dtype"])
         s["ws"] = bsp.Workspace(geo, 1, 1, 1)
         s["plan"] = s["ws"].plan(geo, 1, 1, [1], [0], np.zeros((1, 1), np.int32))
-        s["moves"] = bsp.page_moves(pages)
+        s["moves"] = bsp.PageMoves(pages)
     return s
 
 
@@ -521,7 +522,7 @@ def run(s):
                                    s["indirection"], s["scale"], s["o"], s["lse"])
         return s["o"], s["lse"]
     if op == "fork":
-        bsp.fork_tables(s["plan"], s["forks"], s["refs"], s["refs_out"], s["pages_out"])
+        bsp.fork_tables(s["plan"], s["forks"], s["refs"], s["refs_out"], s["pages_out"], s["fork_ws"])
         bsp.fork_rows(s["plan"], s["forks"], s["pages_out"], s["beam_pages"], s["indirection"], s["k_pool"], s["v_pool"])
         return s["refs_out"], s["pages_out"], s["k_pool"], s["v_pool"]
     bsp.free_pages(s["plan"], s["finished"], s["refs"], s["refs_freed"])
