@@ -31,6 +31,7 @@ DEVFLAG_PAGE_INDEX = 1
 DEVFLAG_TIMEOUT = 2
 DEVFLAG_POSITION = 4
 DEVFLAG_GRAPH = 8
+DEVFLAG_PAGES = 16
 
 
 class NativeLibraryError(RuntimeError):
@@ -88,7 +89,10 @@ EXPORTS = ["bsp_status_string", "bsp_bucket_rows", "bsp_workspace_size", "bsp_pl
            "bsp_plan_prefill_build", "bsp_plan_prefill", "bsp_prefill_attn", "bsp_rope_cos_sin",
            "bsp_rope_append_kv", "bsp_append_kv_fp8", "bsp_rope_append_kv_fp8", "bsp_plan_update_tails",
            "bsp_decode_attn_fp8", "bsp_process_logits", "bsp_beam_select_workspace_size", "bsp_beam_select",
-           "bsp_beam_advance", "bsp_key_weights", "bsp_key_weights_fp8", "bsp_evict_prefix"]
+           "bsp_beam_advance", "bsp_key_weights", "bsp_key_weights_fp8", "bsp_evict_prefix",
+           "bsp_decode_attn_fp8_blocks", "bsp_append_kv_fp8_blocks", "bsp_norm_rope_append_kv",
+           "bsp_norm_rope_append_kv_fp8", "bsp_rope_cos_sin_scaled", "bsp_fork_workspace_size", "bsp_fork_tables",
+           "bsp_fork_rows", "bsp_free_pages", "bsp_compact_tables", "bsp_copy_pages"]
 NOALLOC_SCRATCH_MIB = 32
 
 
@@ -166,6 +170,29 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
     lib.bsp_key_weights_fp8.argtypes = [P(Plan), vp, vp, vp, f32, f32, i32, i32, vp, i64, vp]
     lib.bsp_evict_prefix.restype = i32
     lib.bsp_evict_prefix.argtypes = [P(Plan), vp, i64, vp, vp, i32, i32, vp, vp, vp, vp, vp, i64, vp]
+    lib.bsp_rope_cos_sin_scaled.restype = i32
+    lib.bsp_rope_cos_sin_scaled.argtypes = [i32, i32, ctypes.c_double, P(_RopeScaling), vp, vp]
+    head = [P(Plan), P(_QkNorm), P(RopeConfig), vp, vp, i64, vp, i64, vp, vp, i64]
+    for fn, args in (("bsp_norm_rope_append_kv", [vp, i32, vp, vp, vp, vp]),
+                     ("bsp_norm_rope_append_kv_fp8", [f32, f32, vp, i32, vp, vp, vp, vp]),
+                     ("bsp_append_kv_fp8_blocks", [vp, i32, vp, vp, P(_BlockScales), vp, vp])):
+        getattr(lib, fn).restype = i32
+        getattr(lib, fn).argtypes = head + args
+    lib.bsp_fork_workspace_size.restype = i32
+    lib.bsp_fork_workspace_size.argtypes = [i32, i32, P(sz)]
+    lib.bsp_fork_tables.restype = i32
+    lib.bsp_fork_tables.argtypes = [P(Plan), vp, i64, i32, vp, vp, vp, i64, i32, vp, sz, vp]
+    lib.bsp_fork_rows.restype = i32
+    lib.bsp_fork_rows.argtypes = [P(Plan), vp, i64, i32, vp, i64, i32, vp, i32, vp, i32, vp, vp, P(_BlockScales), vp]
+    lib.bsp_free_pages.restype = i32
+    lib.bsp_free_pages.argtypes = [P(Plan), vp, i64, i32, i32, vp, vp, vp]
+    lib.bsp_compact_tables.restype = i32
+    lib.bsp_compact_tables.argtypes = [P(Plan), vp, vp, vp, vp, vp, vp, vp, i64, i32, i32, vp]
+    lib.bsp_copy_pages.restype = i32
+    lib.bsp_copy_pages.argtypes = [P(Plan), vp, vp, i32, vp, vp, P(_BlockScales), vp]
+    lib.bsp_decode_attn_fp8_blocks.restype = i32
+    lib.bsp_decode_attn_fp8_blocks.argtypes = [P(Plan), vp, vp, vp, P(_BlockScales), vp, i32, vp, i32, f32, i32, vp, vp,
+                                               vp, vp]
     _lib = lib
     return lib
 
@@ -356,15 +383,41 @@ def append_kv_fp8(plan_: Plan, k_new: torch.Tensor, v_new: torch.Tensor, out_cac
         _dptr(out_cache_loc), n, _dptr(k_pool), _dptr(v_pool), _events(events, 2), _stream(stream)))
 
 
+class _RopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("original_positions", ctypes.c_int32), ("factor", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double), ("amplitude", ctypes.c_double)]
+
+
+class RopeScaling:
+    """Frequencies of a model stretched beyond its trained length (bsp_rope_scaling). kind: "linear", "base", "bands" or
+    "ramp"; bands and ramp go by original_positions and the turns low < high; amplitude multiplies cos and sin."""
+
+    KINDS = {"linear": 1, "base": 2, "bands": 3, "ramp": 4}
+
+    def __init__(self, kind: str, factor: float, original_positions: int = 0, low: float = 0.0, high: float = 0.0,
+                 amplitude: float = 1.0):
+        if kind not in self.KINDS:
+            raise ValueError(f"kind {kind!r} is none of {sorted(self.KINDS)}")
+        self.kind = kind
+        self.c = _RopeScaling(self.KINDS[kind], int(original_positions), float(factor), float(low), float(high),
+                              float(amplitude))
+
+
 class Rope:
-    """A RoPE table (device fp32 [max_position][rotary_dim], filled by bsp_rope_cos_sin) and its layout."""
+    """A RoPE table (device fp32 [max_position][rotary_dim], filled by bsp_rope_cos_sin, with ``scaling`` by
+    bsp_rope_cos_sin_scaled) and its layout."""
 
     def __init__(self, max_position: int, rotary_dim: int, base: float, interleaved: bool = False, device="cuda",
-                 stream=None):
+                 stream=None, scaling: Optional[RopeScaling] = None):
         self.cos_sin = torch.empty((int(max_position), int(rotary_dim)), dtype=torch.float32, device=device)
         self.base = float(base)
-        _check("bsp_rope_cos_sin", load().bsp_rope_cos_sin(int(max_position), int(rotary_dim), self.base,
-                                                            _dptr(self.cos_sin), _stream(stream)))
+        if scaling is None:
+            _check("bsp_rope_cos_sin", load().bsp_rope_cos_sin(int(max_position), int(rotary_dim), self.base,
+                                                                _dptr(self.cos_sin), _stream(stream)))
+        else:
+            _check("bsp_rope_cos_sin_scaled", load().bsp_rope_cos_sin_scaled(
+                int(max_position), int(rotary_dim), self.base, ctypes.byref(scaling.c), _dptr(self.cos_sin),
+                _stream(stream)))
         self.config = RopeConfig(self.cos_sin.data_ptr(), int(max_position), int(rotary_dim), 1 if interleaved else 0, 0)
 
     @property
@@ -452,6 +505,179 @@ def decode_attn_fp8(plan_: Plan, q: torch.Tensor, k_pool: torch.Tensor, v_pool: 
         ctypes.byref(plan_), _dptr(q), _dptr(k_pool), _dptr(v_pool), _dptr(beam_pages), bps,
         _dptr(cache_indirection), max_seq, float(softmax_scale), float(k_scale), float(v_scale), int(flags),
         _dptr(o), _dptr(lse), ev, _stream(stream)))
+
+
+class _BlockScales(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("block", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class BlockScales:
+    """Scales of E4M3 pools, one for each block of ``block`` slots of a (page, kv head): exponent bytes E of 2^(E - 127)
+    in uint8 tables k and v [num_pages, num_kv_heads, page_size // block] (made zeroed, or the given ones)."""
+
+    def __init__(self, geo: Geometry, block: int, k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None,
+                 device="cuda"):
+        self.block = int(block)
+        if self.block < 1 or geo.page_size % self.block:
+            raise ValueError(f"blocks of {block} slots in pages of {geo.page_size}")
+        self.shape = (geo.num_pages, geo.num_kv_heads, geo.page_size // self.block)
+        new = lambda: torch.zeros(self.shape, dtype=torch.uint8, device=device)  # noqa: E731
+        self.k, self.v = new() if k is None else k, new() if v is None else v
+        for name, t in (("k", self.k), ("v", self.v)):
+            if t.dtype is not torch.uint8 or tuple(t.shape) != self.shape or not t.is_contiguous():
+                raise ValueError(f"the {name} scales must be contiguous uint8 {list(self.shape)}, not {t.dtype} {list(t.shape)}")
+        self.c = _BlockScales(self.k.data_ptr(), self.v.data_ptr(), self.block, 0)
+
+    def _of(self, plan_: Plan):
+        """For a call on the plan's pools: its tables must be theirs."""
+        g = plan_.geo
+        if self.shape != (g.num_pages, g.num_kv_heads, g.page_size // self.block):
+            raise ValueError(f"scales {list(self.shape)} in blocks of {self.block} for pools of {g.num_pages} pages, "
+                             f"{g.num_kv_heads} heads, {g.page_size} slots")
+        return ctypes.byref(self.c)
+
+
+def decode_attn_fp8_blocks(plan_: Plan, q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
+                           scales: BlockScales, beam_pages: Optional[torch.Tensor],
+                           cache_indirection: Optional[torch.Tensor], softmax_scale: float, o: torch.Tensor,
+                           lse: torch.Tensor, flags: int = 0, events=None, stream=None):
+    """bsp_decode_attn_fp8_blocks: decode attention over uint8 E4M3 pools with block scales; writes o [R,Hq,D] in
+    the q dtype and lse [R,Hq] (fp32)."""
+    bps = int(beam_pages.shape[-1]) if beam_pages is not None else 0
+    max_seq = int(cache_indirection.shape[-1]) if cache_indirection is not None else 0
+    _pools_ok(plan_, k_pool, v_pool)
+    _check("bsp_decode_attn_fp8_blocks", load().bsp_decode_attn_fp8_blocks(
+        ctypes.byref(plan_), _dptr(q), _dptr(k_pool), _dptr(v_pool), scales._of(plan_), _dptr(beam_pages), bps,
+        _dptr(cache_indirection), max_seq, float(softmax_scale), int(flags), _dptr(o), _dptr(lse), _events(events, 3),
+        _stream(stream)))
+
+
+# ---------------------------------------------------------------- appends of normalised rows
+
+class _QkNorm(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("weight_offset", ctypes.c_float), ("weight_fp32", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class QkNorm:
+    """The RMS norm of queries and keys per head: q_weight, k_weight [head_dim], both in the geometry's dtype or both
+    fp32 (None: ones), eps, and what is added to the weights (1 for weights stored as their distance from one)."""
+
+    def __init__(self, q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 weight_offset: float = 0.0):
+        given = [w for w in (q_weight, k_weight) if w is not None]
+        if any(w.dim() != 1 or not w.is_contiguous() or w.dtype != given[0].dtype or w.shape != given[0].shape for w in given):
+            raise ValueError("q_weight and k_weight must be contiguous vectors of one type and length")
+        self.dtype = given[0].dtype if given else None
+        self.dim = given[0].shape[0] if given else None
+        if self.dtype not in (None, torch.float32, torch.bfloat16, torch.float16):
+            raise ValueError(f"weights are {self.dtype}")
+        self.c = _QkNorm(_address(q_weight), _address(k_weight), float(eps), float(weight_offset),
+                         int(self.dtype is torch.float32), 0)
+        self._keep = (q_weight, k_weight)
+
+    def _of(self, plan_: Plan):
+        g = plan_.geo
+        if self.dim not in (None, g.head_dim) or self.dtype not in (None, torch.float32, _ELEMENT[g.dtype]):
+            raise ValueError(f"norm weights {self.dtype} [{self.dim}] for heads of {g.head_dim} {_ELEMENT[g.dtype]}")
+        return ctypes.byref(self.c)
+
+
+_ELEMENT = (torch.bfloat16, torch.float16)
+
+
+def _token_rows(name: str, t: torch.Tensor, dtype, n: int, width: int) -> int:
+    """Rows of tokens [n, width] or [n, heads, dim], contiguous in a token; their stride in elements."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} is {t.dtype}, not {dtype}")
+    if not n:
+        return width + 7 & ~7
+    shape, step = t.shape, t.stride()
+    if len(shape) == 2:
+        fits, packed = shape[1] == width, width == 1 or step[1] == 1
+    else:
+        fits = len(shape) == 3 and shape[1] * shape[2] == width
+        packed = fits and step[2] == 1 and (shape[1] == 1 or step[1] == shape[2])
+    if not fits or shape[0] < n:
+        raise ValueError(f"{name} has shape {tuple(shape)}, not [{n}, {width}]")
+    if not packed:
+        raise ValueError(f"the rows of {name} are not contiguous")
+    return step[0] if n > 1 else width + 7 & ~7
+
+
+def _norm_append_args(plan_: Plan, norm, rope, positions, q, q_out, k_new, v_new, out_cache_loc):
+    """The arguments that the appends of normalised rows have in common, checked: (.., n) as the library takes them."""
+    g = plan_.geo
+    dt = _ELEMENT[g.dtype]
+    n = out_cache_loc.numel()
+    row = g.num_kv_heads * g.head_dim
+    stride = _token_rows("k_new", k_new, dt, n, row)
+    if _token_rows("v_new", v_new, dt, n, row) != stride:
+        raise ValueError("k_new and v_new must have the same row stride")
+    if out_cache_loc.dtype is not torch.int32 or not out_cache_loc.is_contiguous():
+        raise ValueError("out_cache_loc must be contiguous int32")
+    q_stride = out_stride = 0
+    if q is not None:
+        q_out = q if q_out is None else q_out
+        q_stride = _token_rows("q", q, dt, n, g.num_q_heads * g.head_dim)
+        out_stride = q_stride if q_out is q else _token_rows("q_out", q_out, dt, n, g.num_q_heads * g.head_dim)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if rope is not None:
+        if positions is None or positions.dtype is not torch.int32 or positions.numel() < n or not positions.is_contiguous():
+            raise ValueError(f"positions must be contiguous int32 [{n}]")
+    return (ctypes.byref(plan_), None if norm is None else norm._of(plan_),
+            None if rope is None else ctypes.byref(rope.config), None if rope is None else positions.data_ptr(),
+            _address(q), q_stride, _address(q_out), out_stride, k_new.data_ptr(), v_new.data_ptr(), stride), n
+
+
+def norm_rope_append_kv(plan_: Plan, norm: QkNorm, rope: Optional[Rope], positions: Optional[torch.Tensor],
+                        q: Optional[torch.Tensor], k_new: torch.Tensor, v_new: torch.Tensor, out_cache_loc: torch.Tensor,
+                        k_pool: torch.Tensor, v_pool: torch.Tensor, q_out: Optional[torch.Tensor] = None, events=None,
+                        stream=None):
+    """bsp_norm_rope_append_kv: K rows normalised per head, rotated (rope None: not) and written to their slots, V rows
+    written, query rows normalised and rotated into q_out (None: in place). q, k_new, v_new: [n, heads * head_dim] or
+    [n, heads, head_dim], tokens any stride apart (column slices of one projection's output)."""
+    args, n = _norm_append_args(plan_, norm, rope, positions, q, q_out, k_new, v_new, out_cache_loc)
+    _pools_ok(plan_, k_pool, v_pool)
+    _check("bsp_norm_rope_append_kv", load().bsp_norm_rope_append_kv(
+        *args, out_cache_loc.data_ptr(), n, k_pool.data_ptr(), v_pool.data_ptr(), _events(events, 2), _stream(stream)))
+
+
+def _pools8_ok(plan_: Plan, *pools: torch.Tensor):
+    """E4M3 pools of the plan's geometry, whatever its kv_dtype."""
+    g = plan_.geo
+    shape = (g.num_pages, g.num_kv_heads, g.page_size, g.head_dim)
+    for t in pools:
+        if t.dtype not in (torch.uint8, torch.float8_e4m3fn) or tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"a pool must be contiguous uint8 {list(shape)}, not {t.dtype} {list(t.shape)}")
+
+
+def norm_rope_append_kv_fp8(plan_: Plan, norm: QkNorm, rope: Optional[Rope], positions: Optional[torch.Tensor],
+                            q: Optional[torch.Tensor], k_new: torch.Tensor, v_new: torch.Tensor,
+                            out_cache_loc: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor, k_mul: float = 1.0,
+                            v_mul: float = 1.0, q_out: Optional[torch.Tensor] = None, events=None, stream=None):
+    """bsp_norm_rope_append_kv_fp8: norm_rope_append_kv into uint8 (E4M3) pools with one multiplier per tensor."""
+    args, n = _norm_append_args(plan_, norm, rope, positions, q, q_out, k_new, v_new, out_cache_loc)
+    _pools8_ok(plan_, k_pool, v_pool)
+    _check("bsp_norm_rope_append_kv_fp8", load().bsp_norm_rope_append_kv_fp8(
+        *args, float(k_mul), float(v_mul), out_cache_loc.data_ptr(), n, k_pool.data_ptr(), v_pool.data_ptr(),
+        _events(events, 2), _stream(stream)))
+
+
+def append_kv_fp8_blocks(plan_: Plan, k_new: torch.Tensor, v_new: torch.Tensor, out_cache_loc: torch.Tensor,
+                         k_pool: torch.Tensor, v_pool: torch.Tensor, scales: BlockScales, norm: Optional[QkNorm] = None,
+                         rope: Optional[Rope] = None, positions: Optional[torch.Tensor] = None,
+                         q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None, events=None,
+                         stream=None):
+    """bsp_append_kv_fp8_blocks: K rows (normalised with norm, rotated with rope) and V rows into uint8 (E4M3) pools with
+    block scales, query rows into q_out (None: in place). Tokens whose slots are in one block stand next to one another
+    in ascending order of their slots."""
+    args, n = _norm_append_args(plan_, norm, rope, positions, q, q_out, k_new, v_new, out_cache_loc)
+    _pools8_ok(plan_, k_pool, v_pool)
+    _check("bsp_append_kv_fp8_blocks", load().bsp_append_kv_fp8_blocks(
+        *args, out_cache_loc.data_ptr(), n, k_pool.data_ptr(), v_pool.data_ptr(), scales._of(plan_), _events(events, 2),
+        _stream(stream)))
 
 
 def decode_attn_noalloc(geo: Geometry, batch, beam_width, prefix_len, tail_len, prefix_pages, max_tail,
@@ -737,3 +963,107 @@ def evict_prefix(plan_: Plan, weights: torch.Tensor, keep_len: torch.Tensor, sin
         ctypes.byref(plan_), weights.data_ptr(), stride, _address(positions), keep_len.data_ptr(), int(sinks), int(recent),
         k_pool.data_ptr(), v_pool.data_ptr(), kept.data_ptr(), _address(weights_out), _address(positions_out), out_stride,
         _stream(stream)))
+
+
+# ---------------------------------------------------------------- pages of the cache
+
+def fork_workspace(batch: int, num_forks: int, device="cuda") -> torch.Tensor:
+    """Device workspace of ``fork_tables`` (bsp_fork_workspace_size bytes)."""
+    n = ctypes.c_size_t()
+    _check("bsp_fork_workspace_size", load().bsp_fork_workspace_size(int(batch), int(num_forks), ctypes.byref(n)))
+    return torch.empty(max(16, n.value), dtype=torch.uint8, device=device)
+
+
+def _counts(plan_: Plan, *refs: torch.Tensor):
+    for t in refs:
+        _table("refs", t, torch.int32, (plan_.geo.num_pages,))
+
+
+def fork_tables(plan_: Plan, beams: torch.Tensor, refs: torch.Tensor, refs_out: torch.Tensor, pages_out: torch.Tensor,
+                workspace: torch.Tensor, stream=None):
+    """bsp_fork_tables: tables of the beams (int32 [batch, num_forks], -1: none) that go on as sequences of their own:
+    full prompt pages shared, fresh ones for the rest, in pages_out int32 [batch * num_forks, columns]. refs, refs_out:
+    int32 [num_pages], the counts before and after (may be one tensor)."""
+    i32 = torch.int32
+    forks = beams.shape[-1]
+    stride = _table("beams", beams, i32, (plan_.batch, forks))
+    _counts(plan_, refs, refs_out)
+    out_stride = _table("pages_out", pages_out, i32, (plan_.batch * forks, None))
+    _check("bsp_fork_tables", load().bsp_fork_tables(
+        ctypes.byref(plan_), beams.data_ptr(), stride, forks, refs.data_ptr(), refs_out.data_ptr(), pages_out.data_ptr(),
+        out_stride, pages_out.shape[1], workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _stream(stream)))
+
+
+def fork_rows(plan_: Plan, beams: torch.Tensor, pages_out: torch.Tensor, beam_pages: Optional[torch.Tensor],
+              cache_indirection: Optional[torch.Tensor], k_pool: torch.Tensor, v_pool: torch.Tensor,
+              scales: Optional[BlockScales] = None, stream=None):
+    """bsp_fork_rows: the prompt's last rows and the beams' tail rows into the fresh pages of ``fork_tables``."""
+    i32 = torch.int32
+    forks = beams.shape[-1]
+    stride = _table("beams", beams, i32, (plan_.batch, forks))
+    out_stride = _table("pages_out", pages_out, i32, (plan_.batch * forks, None))
+    cols = max_seq = 0
+    if beam_pages is not None:
+        cols = _table("beam_pages", beam_pages, i32, (plan_.total_rows, None))
+        if cache_indirection is not None:
+            max_seq = cache_indirection.shape[-1]
+            if _table("cache_indirection", cache_indirection, i32, (plan_.batch, plan_.beam_width, max_seq)) != max_seq:
+                raise ValueError("cache_indirection must be contiguous")
+    _pools_ok(plan_, k_pool, v_pool)
+    _check("bsp_fork_rows", load().bsp_fork_rows(
+        ctypes.byref(plan_), beams.data_ptr(), stride, forks, pages_out.data_ptr(), out_stride, pages_out.shape[1],
+        _address(beam_pages), cols, _address(cache_indirection), max_seq, k_pool.data_ptr(), v_pool.data_ptr(),
+        None if scales is None else scales._of(plan_), _stream(stream)))
+
+
+def free_pages(plan_: Plan, tables: torch.Tensor, refs: torch.Tensor, refs_out: torch.Tensor, stream=None):
+    """bsp_free_pages: one reference less for every page in tables (int32 [rows, columns], -1: none)."""
+    stride = _table("tables", tables, torch.int32, (None, None))
+    _counts(plan_, refs, refs_out)
+    _check("bsp_free_pages", load().bsp_free_pages(
+        ctypes.byref(plan_), tables.data_ptr(), stride, tables.shape[0], tables.shape[1], refs.data_ptr(),
+        refs_out.data_ptr(), _stream(stream)))
+
+
+class PageMoves:
+    """Buffers of a compaction: pairs int32 [num_pages // 2, 2] (from, to), count int32 [2] (pairs, live pages), remap
+    int32 [num_pages]; or with ``pairs`` and ``count`` given, a list of copies of the caller's."""
+
+    def __init__(self, num_pages: int, device="cuda", pairs: Optional[torch.Tensor] = None,
+                 count: Optional[torch.Tensor] = None):
+        i32 = torch.int32
+        self.pairs = torch.empty((num_pages // 2, 2), dtype=i32, device=device) if pairs is None else pairs
+        self.count = torch.zeros(2, dtype=i32, device=device) if count is None else count
+        self.remap = torch.empty(num_pages, dtype=i32, device=device) if pairs is None else None
+        if _table("pairs", self.pairs, i32, (None, 2)) != 2:
+            raise ValueError("pairs must be contiguous")
+        _table("count", self.count, i32, (None,))
+
+
+def compact_tables(plan_: Plan, refs: torch.Tensor, refs_out: torch.Tensor, moves: PageMoves,
+                   tables: Optional[torch.Tensor] = None, tables_out: Optional[torch.Tensor] = None, stream=None):
+    """bsp_compact_tables: the live pages' new places, the lowest ids, into ``moves``, refs_out and tables_out (None: in
+    place). tables: int32 [rows, columns], every live sequence's pages (-1: none)."""
+    _counts(plan_, refs, refs_out)
+    if moves.remap is None or moves.remap.shape[0] != plan_.geo.num_pages:
+        raise ValueError(f"moves are not made for {plan_.geo.num_pages} pages")
+    stride = rows = cols = 0
+    if tables is not None:
+        tables_out = tables if tables_out is None else tables_out
+        rows, cols = tables.shape
+        stride = _table("tables", tables, torch.int32, (rows, cols))
+        if _table("tables_out", tables_out, torch.int32, (rows, cols)) != stride:
+            raise ValueError("tables and tables_out must have the same row stride")
+    _check("bsp_compact_tables", load().bsp_compact_tables(
+        ctypes.byref(plan_), refs.data_ptr(), refs_out.data_ptr(), moves.pairs.data_ptr(), moves.count.data_ptr(),
+        moves.remap.data_ptr(), _address(tables), _address(tables_out), stride, rows, cols, _stream(stream)))
+
+
+def copy_pages(plan_: Plan, moves: PageMoves, k_pool: torch.Tensor, v_pool: torch.Tensor,
+               scales: Optional[BlockScales] = None, stream=None):
+    """bsp_copy_pages: the first count[0] pairs of ``moves``, whole pages of both pools (and their scales)."""
+    _pools_ok(plan_, k_pool, v_pool)
+    _check("bsp_copy_pages", load().bsp_copy_pages(
+        ctypes.byref(plan_), moves.pairs.data_ptr(), moves.count.data_ptr(), moves.pairs.shape[0], k_pool.data_ptr(),
+        v_pool.data_ptr(), None if scales is None else scales._of(plan_), _stream(stream)))

@@ -11,11 +11,11 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libbsp.so")
-SOURCES = ["bsp_host.cpp", "bsp_append.cu", "bsp_rope.cu", "bsp_tail.cu", "bsp_prefix.cu", "bsp_wide.cu", "bsp_alt.cu", "bsp_noalloc.cu",
-           "bsp_step.cpp", "bsp_logits.cu", "bsp_beams.cu", "bsp_weights.cu", "bsp_evict.cu"]
+SOURCES = ["bsp_host.cpp", "bsp_append.cu", "bsp_rope.cu", "bsp_norm.cu", "bsp_tail.cu", "bsp_prefix.cu", "bsp_wide.cu", "bsp_alt.cu", "bsp_noalloc.cu",
+           "bsp_cache.cpp", "bsp_step.cpp", "bsp_logits.cu", "bsp_beams.cu", "bsp_weights.cu", "bsp_evict.cu", "bsp_pages.cu"]
 # built without fast-math: their stored results are single IEEE operations in a fixed order
-EXACT_MATH = {"bsp_logits.cu", "bsp_beams.cu", "bsp_weights.cu", "bsp_evict.cu"}
-HEADERS = ["bsp_internal.h", "bsp_step.h", "bsp_ptx.cuh", "bsp_prompt.cuh", "bsp_topk.cuh", "bsp_write.h"]
+EXACT_MATH = {"bsp_norm.cu", "bsp_logits.cu", "bsp_beams.cu", "bsp_weights.cu", "bsp_evict.cu"}
+HEADERS = ["bsp_internal.h", "bsp_step.h", "bsp_check.h", "bsp_pages.h", "bsp_ptx.cuh", "bsp_prompt.cuh", "bsp_topk.cuh", "bsp_write.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -150,6 +150,9 @@ bool encode_map(CUtensorMap* m, int dtype, int rank, const void* base, const cuu
 
 namespace {
 
+}  // namespace
+
+namespace bsp {
 // Records a timing event; under stream capture it becomes an external event-record node.
 bool record_event(void* const* events, int i, cudaStream_t s) {
     if (!events) return true;
@@ -159,8 +162,7 @@ bool record_event(void* const* events, int i, cudaStream_t s) {
     if (cs == cudaStreamCaptureStatusActive) return cudaEventRecordWithFlags(ev, s, cudaEventRecordExternal) == cudaSuccess;
     return cudaEventRecord(ev, s) == cudaSuccess;
 }
-
-}  // namespace
+}  // namespace bsp
 
 extern "C" {
 
@@ -1105,6 +1107,7 @@ bsp_status bsp_read_device_status(const bsp_plan_t* plan, void* stream, int32_t 
     if (flags_out) *flags_out = flags;
     if (flags & (BSP_DEVFLAG_PAGE_INDEX | BSP_DEVFLAG_POSITION)) return BSP_ERR_PAGE_INDEX;
     if (flags & BSP_DEVFLAG_GRAPH) return BSP_ERR_STALE_PLAN;
+    if (flags & BSP_DEVFLAG_PAGES) return BSP_ERR_CAPACITY;
     if (flags & BSP_DEVFLAG_TIMEOUT) return BSP_ERR_DEVICE_TIMEOUT;
     return BSP_OK;
 }
@@ -1112,6 +1115,15 @@ bsp_status bsp_read_device_status(const bsp_plan_t* plan, void* stream, int32_t 
 }  // extern "C"
 
 namespace bsp {
+bsp_status check_block_scales(const bsp_block_scales* scales, int page_size, bool tables) {
+    if (!scales || scales->reserved != 0) return BSP_ERR_INVALID_ARG;
+    const int n = scales->block;
+    if (n < 1 || (n & (n - 1))) return BSP_ERR_INVALID_ARG;
+    if (n > BSP_MAX_SCALE_BLOCK || n > page_size) return BSP_ERR_UNSUPPORTED;
+    if (tables && (!device_ptr_ok(scales->k) || !device_ptr_ok(scales->v))) return BSP_ERR_INVALID_ARG;
+    return BSP_OK;
+}
+
 // Host-checkable arguments of the attention launches of `plan` (prefill == false: a decode plan, else a
 // prefill plan). Nothing is enqueued.
 bsp_status attn_check_args(const bsp_plan_t* plan, const void* q, const void* k_pool, const void* v_pool,
@@ -1147,7 +1159,8 @@ bsp_status attn_check_args(const bsp_plan_t* plan, const void* q, const void* k_
 bsp_status attn_launches(const bsp_plan_t* plan, uint8_t* ws, const void* q, const void* k_pool, const void* v_pool,
                          const int32_t* beam_pages, int32_t beam_pages_stride, const int32_t* cache_indirection,
                          int32_t max_seq, float softmax_scale, int32_t flags, void* o, float* lse,
-                         void* const* events, cudaStream_t s, bool prefill, float k_scale, float v_scale) {
+                         void* const* events, cudaStream_t s, bool prefill, float k_scale, float v_scale,
+                         const bsp_block_scales* scales) {
     const bool graph = (flags & BSP_FLAG_GRAPH) != 0;
     const bsp_geometry& geo = plan->geo;
     const int64_t R = plan->total_rows;
@@ -1158,14 +1171,15 @@ bsp_status attn_launches(const bsp_plan_t* plan, uint8_t* ws, const void* q, con
     const bool alt = plan->layout == 1, wide = plan->layout == 2;
     const bool fp8 = geo.kv_dtype == BSP_KV_DTYPE_E4M3;  // the planner gave such a plan layout 1 or 2
     if (fp8 && !alt && !wide) return BSP_ERR_INVALID_ARG;
+    const PoolKind pools = !fp8 ? kPool16 : scales ? kPoolBlocks : kPoolE4m3;
 
     // everything that is not a launch (attributes, tensor maps, parameters) comes before the
     // first timing event
     const bool prefix = graph || plan->num_units > 0;
-    if (prefix && (alt ? prepare_alt(D, bf16, fp8) : wide ? prepare_wide(D, bf16, fp8) : prepare_prefix(D, bf16)) !=
+    if (prefix && (alt ? prepare_alt(D, bf16, pools) : wide ? prepare_wide(D, bf16, pools) : prepare_prefix(D, bf16)) !=
                       cudaSuccess)
         return BSP_ERR_CUDA;
-    if (prepare_tail(D, bf16, graph ? plan->max_tail : plan->max_tail_len, Hq, fp8) != cudaSuccess) return BSP_ERR_CUDA;
+    if (prepare_tail(D, bf16, graph ? plan->max_tail : plan->max_tail_len, Hq, pools) != cudaSuccess) return BSP_ERR_CUDA;
     CUtensorMap tq, tk, tv;
     PrefixParams pp{};
     if (prefix) {
@@ -1222,6 +1236,11 @@ bsp_status attn_launches(const bsp_plan_t* plan, uint8_t* ws, const void* q, con
         }
         pp.scale_log2 = softmax_scale * k_scale * log2e;
         pp.v_scale = v_scale;
+        if (scales) {
+            pp.k_exp = scales->k;
+            pp.v_exp = scales->v;
+            pp.block_log2 = ilog2(scales->block);
+        }
     }
     TailParams tp{};
     tp.q = q;
@@ -1247,6 +1266,11 @@ bsp_status attn_launches(const bsp_plan_t* plan, uint8_t* ws, const void* q, con
     tp.scale_log2 = softmax_scale * k_scale * log2e;
     tp.lse_base2 = (flags & BSP_FLAG_LSE_BASE2) ? 1 : 0;
     tp.v_scale = v_scale;
+    if (scales) {
+        tp.k_exp = scales->k;
+        tp.v_exp = scales->v;
+        tp.block_log2 = ilog2(scales->block);
+    }
     if (graph) {
         tp.graph_hdr = reinterpret_cast<const int32_t*>(ws + kStatusBytes);
         tp.graph_max_tail = plan->max_tail;
@@ -1256,15 +1280,15 @@ bsp_status attn_launches(const bsp_plan_t* plan, uint8_t* ws, const void* q, con
     if (!record(0)) return BSP_ERR_CUDA;
     if (prefix) {
         const int ctas = graph ? plan->num_sms : plan->prefix_ctas;
-        const cudaError_t e = alt    ? launch_alt(D, bf16, ctas, tq, tk, tv, pp, s, fp8)
-                              : wide ? launch_wide(D, bf16, ctas, tq, tk, tv, pp, s, fp8)
+        const cudaError_t e = alt    ? launch_alt(D, bf16, ctas, tq, tk, tv, pp, s, pools)
+                              : wide ? launch_wide(D, bf16, ctas, tq, tk, tv, pp, s, pools)
                                    : launch_prefix(D, bf16, ctas, tq, tk, tv, pp, s);
         if (e != cudaSuccess) return BSP_ERR_CUDA;
     }
     if (!record(1)) return BSP_ERR_CUDA;
     // without timing events between them, the tail kernel overlaps the end of the prompt kernel
     if ((graph || plan->tail_requests > 0) &&
-        launch_tail(D, bf16, graph ? plan->max_tail : plan->max_tail_len, tp, prefix && events == nullptr, s, fp8) !=
+        launch_tail(D, bf16, graph ? plan->max_tail : plan->max_tail_len, tp, prefix && events == nullptr, s, pools) !=
             cudaSuccess)
         return BSP_ERR_CUDA;
     if (!record(2)) return BSP_ERR_CUDA;
@@ -1278,7 +1302,8 @@ namespace {
 bsp_status attn_impl(const bsp_plan_t* plan, const void* q, const void* k_pool, const void* v_pool,
                      const int32_t* beam_pages, int32_t beam_pages_stride, const int32_t* cache_indirection,
                      int32_t max_seq, float softmax_scale, int32_t flags, void* o, float* lse, void* const* events,
-                     void* stream, bool prefill, bool fp8 = false, float k_scale = 1.f, float v_scale = 1.f) {
+                     void* stream, bool prefill, bool fp8 = false, float k_scale = 1.f, float v_scale = 1.f,
+                     const bsp_block_scales* scales = nullptr) {
     bsp_status st = check_plan(plan);
     if (st != BSP_OK) return st;
     st = attn_check_args(plan, q, k_pool, v_pool, beam_pages, beam_pages_stride, cache_indirection, max_seq,
@@ -1287,7 +1312,7 @@ bsp_status attn_impl(const bsp_plan_t* plan, const void* q, const void* k_pool, 
     if (plan->total_rows == 0) return BSP_OK;
     st = attn_launches(plan, static_cast<uint8_t*>(plan->ws_device), q, k_pool, v_pool, beam_pages, beam_pages_stride,
                        cache_indirection, max_seq, softmax_scale, flags, o, lse, events,
-                       static_cast<cudaStream_t>(stream), prefill, k_scale, v_scale);
+                       static_cast<cudaStream_t>(stream), prefill, k_scale, v_scale, scales);
     if (st != BSP_OK) return st;
     if (flags & BSP_FLAG_CHECK) return bsp_read_device_status(plan, stream, 1, nullptr);
     return BSP_OK;
@@ -1311,6 +1336,19 @@ bsp_status bsp_decode_attn_fp8(const bsp_plan_t* plan, const void* q, const void
                                void* const* events, void* stream) {
     return attn_impl(plan, q, k_pool, v_pool, beam_pages, beam_pages_stride, cache_indirection, max_seq,
                      softmax_scale, flags, o, lse, events, stream, false, true, k_scale, v_scale);
+}
+
+bsp_status bsp_decode_attn_fp8_blocks(const bsp_plan_t* plan, const void* q, const void* k_pool, const void* v_pool,
+                                      const bsp_block_scales* scales, const int32_t* beam_pages,
+                                      int32_t beam_pages_stride, const int32_t* cache_indirection, int32_t max_seq,
+                                      float softmax_scale, int32_t flags, void* o, float* lse, void* const* events,
+                                      void* stream) {
+    bsp_status st = check_plan(plan);
+    if (st != BSP_OK) return st;
+    st = check_block_scales(scales, plan->geo.page_size, plan->total_rows > 0);
+    if (st != BSP_OK) return st;
+    return attn_impl(plan, q, k_pool, v_pool, beam_pages, beam_pages_stride, cache_indirection, max_seq,
+                     softmax_scale, flags, o, lse, events, stream, false, true, 1.f, 1.f, scales);
 }
 
 bsp_status bsp_prefill_attn(const bsp_plan_t* plan, const void* q, const void* k_pool, const void* v_pool,

@@ -93,6 +93,10 @@ struct PrefixParams {
     int bq;            // > 0: half-row softmax, bq beams of the block per TMEM lane quadrant (prefix_quad_beams)
     int num_units;     // units in the list
     float v_scale;     // E4M3 pools: the values' per-tensor scale, applied to O (1 for 16-bit pools)
+    // E4M3 pools with block scales (else null): exponent bytes of 2^block_log2 rows of a (page, kv head) each
+    const uint8_t* k_exp;
+    const uint8_t* v_exp;
+    int block_log2;
     // graph mode (else null): the staged plan's header, checked at the start against the launch
     // (batch, beam width, one CTA per SM of the plan, a decode plan)
     const int32_t* graph_hdr;
@@ -116,6 +120,9 @@ struct TailParams {
     float scale_log2;
     int lse_base2;
     float v_scale;     // E4M3 pools: the values' per-tensor scale, applied to the tail's O (1 otherwise)
+    const uint8_t* k_exp;  // E4M3 pools with block scales (else null), as above
+    const uint8_t* v_exp;
+    int block_log2;
     // graph mode (else null): the staged plan's header, checked against the launch (batch, beam width,
     // a decode plan, a tail bound within the one the launch was made for)
     const int32_t* graph_hdr;
@@ -138,21 +145,24 @@ cudaError_t launch_prefix(int head_dim, bool bf16, int ctas, const CUtensorMap& 
 // Kernel attributes (shared-memory size and split) are set by the prepare_* calls, once before
 // the launches, so that timing events recorded around a launch bracket the launch alone.
 cudaError_t prepare_prefix(int head_dim, bool bf16);
-cudaError_t prepare_tail(int head_dim, bool bf16, int max_tail_len, int num_q_heads, bool fp8 = false);
+// What a kernel's pools hold: elements of q's dtype, E4M3 bytes with one scale per tensor, or E4M3 bytes with block
+// scales.
+enum PoolKind { kPool16 = 0, kPoolE4m3 = 1, kPoolBlocks = 2 };
+cudaError_t prepare_tail(int head_dim, bool bf16, int max_tail_len, int num_q_heads, PoolKind pools = kPool16);
 // after_prefix: the prompt kernel was the last launch on `stream`; the tail kernel is then a
 // programmatic dependent launch of it (it starts on SMs the prompt kernel has left, resolves and
 // prefetches its tail rows, and waits for the prompt kernel's partials before merging).
 cudaError_t launch_tail(int head_dim, bool bf16, int max_tail_len, const TailParams& p, bool after_prefix,
-                        cudaStream_t stream, bool fp8 = false);
-// The alternating-tile prompt kernel (p.Wblk = beams per row block, p.bq = beams per quadrant). fp8: E4M3
-// pools (tk, tv map one-byte elements without swizzle, boxes of min(page, 64) rows x head_dim bytes).
-cudaError_t prepare_alt(int head_dim, bool bf16, bool fp8 = false);
+                        cudaStream_t stream, PoolKind pools = kPool16);
+// The alternating-tile prompt kernel (p.Wblk = beams per row block, p.bq = beams per quadrant). E4M3 pools:
+// tk, tv map one-byte elements without swizzle, boxes of min(page, 64) rows x head_dim bytes.
+cudaError_t prepare_alt(int head_dim, bool bf16, PoolKind pools = kPool16);
 cudaError_t launch_alt(int head_dim, bool bf16, int ctas, const CUtensorMap& tq, const CUtensorMap& tk,
-                       const CUtensorMap& tv, const PrefixParams& p, cudaStream_t stream, bool fp8 = false);
-// The wide-layout prompt kernel (p.Wblk = beams per block, p.bq = beams per quadrant); fp8 as above.
-cudaError_t prepare_wide(int head_dim, bool bf16, bool fp8 = false);
+                       const CUtensorMap& tv, const PrefixParams& p, cudaStream_t stream, PoolKind pools = kPool16);
+// The wide-layout prompt kernel (p.Wblk = beams per block, p.bq = beams per quadrant); pools as above.
+cudaError_t prepare_wide(int head_dim, bool bf16, PoolKind pools = kPool16);
 cudaError_t launch_wide(int head_dim, bool bf16, int ctas, const CUtensorMap& tq, const CUtensorMap& tk,
-                        const CUtensorMap& tv, const PrefixParams& p, cudaStream_t stream, bool fp8 = false);
+                        const CUtensorMap& tv, const PrefixParams& p, cudaStream_t stream, PoolKind pools = kPool16);
 cudaError_t prepare_append();
 cudaError_t launch_append(const AppendParams& p, cudaStream_t stream);
 
@@ -160,15 +170,21 @@ cudaError_t launch_append(const AppendParams& p, cudaStream_t stream);
 // (the caller's workspace, or the fixed scratch of the no-allocation entry point). attn_check_args
 // checks what the host can check and enqueues nothing; attn_launches enqueues the launches.
 // fp8: the caller is the E4M3 entry point (the plan's pools must then be E4M3, and 16-bit otherwise);
-// k_scale and v_scale are the E4M3 pools' per-tensor scales (1 for 16-bit pools).
+// k_scale and v_scale are the E4M3 pools' per-tensor scales (1 for 16-bit pools). scales: null, or the E4M3
+// pools' block scales.
 bsp_status attn_check_args(const bsp_plan_t* plan, const void* q, const void* k_pool, const void* v_pool,
                            const int32_t* beam_pages, int32_t beam_pages_stride, const int32_t* cache_indirection,
                            int32_t max_seq, float softmax_scale, int32_t flags, void* o, float* lse, bool prefill,
                            bool fp8 = false, float k_scale = 1.f, float v_scale = 1.f);
+// The block scales of E4M3 pools as far as the host can check them: the block size, and the tables' addresses
+// (`tables`: a call that reads them).
+bsp_status check_block_scales(const bsp_block_scales* scales, int page_size, bool tables);
+bool record_event(void* const* events, int i, cudaStream_t s);
 bsp_status attn_launches(const bsp_plan_t* plan, uint8_t* ws, const void* q, const void* k_pool, const void* v_pool,
                          const int32_t* beam_pages, int32_t beam_pages_stride, const int32_t* cache_indirection,
                          int32_t max_seq, float softmax_scale, int32_t flags, void* o, float* lse,
-                         void* const* events, cudaStream_t s, bool prefill, float k_scale = 1.f, float v_scale = 1.f);
+                         void* const* events, cudaStream_t s, bool prefill, float k_scale = 1.f, float v_scale = 1.f,
+                         const bsp_block_scales* scales = nullptr);
 // A decode plan with the packed layout (sections and partial states sized by the plan's own units and
 // splits), for a caller that never replays it from a CUDA graph.
 bsp_status plan_build_packed(const bsp_geometry* geo, int32_t batch, int32_t beam_width, const int32_t* prefix_len,

@@ -79,12 +79,116 @@ __device__ __forceinline__ uint32_t e4m3x2_to_16(uint32_t two) {
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(t), "r"(0x77807780u));  // 2^112 in both halves
     return r;
 }
+
+// The factor, in both halves of a word, that scaled_e4m3x2 takes for a block's exponent byte E (scale 2^(E - 127)).
+// bfloat16: 2^112 * 2^(E - 127), one exponent field of E + 112 (E up to 142, a scale of 2^15), so that the scale costs no
+// multiplication of its own. binary16: 2^(E - 127) for exponents in [-15, 7], with which every product is a number of
+// the type: |code| <= 448 * 2^7 < 2^16, and the smallest step of a code, 2^-9, gives a multiple of 2^-24.
+template <bool BF16>
+__device__ __forceinline__ uint32_t block_factor(uint32_t e) {
+    uint32_t f;
+    if constexpr (BF16) {
+        f = (min(e, 142u) + 112u) << 7;
+    } else {
+        const uint32_t c = min(max(e, 112u), 134u);
+        f = c == 112u ? 0x0200u : (c - 112u) << 10;  // 2^-15 is half of the smallest normal number
+    }
+    return f | (f << 16);
+}
+// The same scale in fp32 (0 for a block that nothing was written to).
+template <bool BF16>
+__device__ __forceinline__ float block_scale(uint32_t e) {
+    return __uint_as_float((BF16 ? min(e, 142u) : min(max(e, 112u), 134u)) << 23);
+}
+// e4m3x2_to_16 times a block's scale, exact where the product is a number of the type (bfloat16: all but the
+// smallest scales' products below 2^-133).
+template <bool BF16>
+__device__ __forceinline__ uint32_t scaled_e4m3x2(uint32_t two, uint32_t factor) {
+    uint32_t h, r;
+    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h) : "r"(two));
+    if constexpr (BF16) {
+        const uint32_t t = ((h & 0x7fff7fffu) >> 3) | (h & 0x80008000u);
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(t), "r"(factor));
+    } else {
+        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(factor));
+    }
+    return r;
+}
 // 8 E4M3 codes (bytes in order) -> one 16-byte chunk of 8 16-bit values
 template <bool BF16>
 __device__ __forceinline__ uint4 e4m3x8_to_16(uint2 in) {
     return make_uint4(e4m3x2_to_16<BF16>(in.x & 0xffffu), e4m3x2_to_16<BF16>(in.x >> 16),
                       e4m3x2_to_16<BF16>(in.y & 0xffffu), e4m3x2_to_16<BF16>(in.y >> 16));
 }
+
+// The same with a block's scale (BLK).
+template <bool BF16, bool BLK>
+__device__ __forceinline__ uint4 widen_e4m3x8(uint2 in, uint32_t factor) {
+    if constexpr (BLK)
+        return make_uint4(scaled_e4m3x2<BF16>(in.x & 0xffffu, factor), scaled_e4m3x2<BF16>(in.x >> 16, factor),
+                          scaled_e4m3x2<BF16>(in.y & 0xffffu, factor), scaled_e4m3x2<BF16>(in.y >> 16, factor));
+    else
+        return e4m3x8_to_16<BF16>(in);
+}
+
+// The prompt tiles of a CTA's units in order, one ahead of the tile that is widened, so that the exponent bytes of the
+// next tile's rows (a page id, then a byte: two loads from L2 or farther) arrive while this one waits for its codes.
+// Run by the NT threads of a widening stream. Each holds the factors of TK / NT of the tile's rows: the LPR lanes that
+// widen rows r0 + RS i hold row r0 + RS (j + LPR e) on lane j, and a row's factor comes from its lane by a shuffle.
+template <int D, int TK, bool BF16, int NT>
+struct BlockFactors {
+    static constexpr int LPR = D / 16;       // lanes of a row
+    static constexpr int RS = NT / LPR;      // rows one pass of the threads covers
+    static constexpr int NE = TK / NT;       // rows whose factor a thread holds
+    int k, t, tiles, key0, key_end, page_off, g;
+    uint32_t f[NE];
+
+    __device__ __forceinline__ void unit(const PrefixParams& p, int u_begin, int nunits) {
+        for (tiles = 0; k < nunits; ++k) {
+            const UnitInfo ui = load_unit(p, u_begin + k);
+            tiles = prompt_tiles<TK>(ui);
+            if (tiles <= 0) continue;
+            t = 0;
+            key0 = ui.key_begin;
+            key_end = ui.key_end;
+            page_off = ui.page_off;
+            g = ui.g;
+            return;
+        }
+    }
+    __device__ __forceinline__ void fetch(const PrefixParams& p, const uint8_t* exps, int nunits, int gtid) {
+#pragma unroll
+        for (int e = 0; e < NE; ++e) {
+            const int key = key0 + gtid / LPR + RS * ((gtid & (LPR - 1)) + LPR * e);
+            uint32_t x = 0;
+            if (k < nunits && key < key_end) {
+                const int page = __ldg(p.pages + page_off + (key >> p.ps_log2));
+                if (static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages)) {
+                    const long long row = ((static_cast<long long>(page) * p.Hkv + g) << p.ps_log2) + (key & ((1 << p.ps_log2) - 1));
+                    x = __ldg(exps + (row >> p.block_log2));
+                }
+            }
+            f[e] = x;
+        }
+    }
+    __device__ __forceinline__ void begin(const PrefixParams& p, const uint8_t* exps, int u_begin, int nunits, int gtid) {
+        k = 0;
+        unit(p, u_begin, nunits);
+        fetch(p, exps, nunits, gtid);
+    }
+    // the factors of the tile at hand into now[], and the next tile's bytes on their way
+    __device__ __forceinline__ void next(const PrefixParams& p, const uint8_t* exps, int u_begin, int nunits, int gtid,
+                                         uint32_t (&now)[NE]) {
+#pragma unroll
+        for (int e = 0; e < NE; ++e) now[e] = block_factor<BF16>(f[e]);
+        key0 += TK;
+        if (++t >= tiles && k < nunits) {
+            ++k;
+            unit(p, u_begin, nunits);
+        }
+        fetch(p, exps, nunits, gtid);
+    }
+};
 
 // Byte offset of 16-byte chunk kc (8 elements) of key row r in a 16-bit K or V tile of TK rows laid out
 // as a TMA box with 128-byte swizzle: column half kc / 8, then row r, then chunk (kc % 8) ^ (r % 8).
@@ -103,8 +207,17 @@ __device__ __forceinline__ uint32_t sw128_chunk(int kc, int r) {
 //  - D = 64: the 16-bit row r covers E4M3 rows 2r - TK and 2r - TK + 1, so all threads read the whole
 //    tile into registers before any of them writes.
 // The caller fences the writes for the tensor core and synchronises the NT threads afterwards.
-template <int D, int TK, bool BF16, int NT = 64>
-__device__ __forceinline__ void widen_e4m3_tile(uint8_t* slot, int valid, int gtid, int bar) {
+// BLK: each row is widened with its block's scale, of the factors that the threads hold (BlockFactors).
+template <int D, int TK, bool BF16, int NT = 64, bool BLK = false>
+__device__ __forceinline__ void widen_e4m3_tile(uint8_t* slot, int valid, int gtid, int bar,
+                                                const uint32_t (&factor)[TK / NT] = {}) {
+    // the factor of the thread's i-th row, from the lane that holds it (every lane takes part)
+    auto of_row = [&](int i) -> uint32_t {
+        if constexpr (!BLK) return 0u;
+        constexpr int LPR = D / 16;
+        const uint32_t held = TK / NT > 1 && i >= LPR ? factor[TK / NT - 1] : factor[0];
+        return __shfl_sync(0xffffffffu, held, (gtid & 31 & ~(LPR - 1)) | (i & (LPR - 1)));
+    };
     static_assert(D == 64 || D == 128, "E4M3 tiles at head_dim 64 and 128");
     static_assert(NT == 64 || NT == 128, "64 or 128 threads");
     const uint8_t* src = slot + TK * D;
@@ -125,9 +238,10 @@ __device__ __forceinline__ void widen_e4m3_tile(uint8_t* slot, int valid, int gt
             for (int u = 0; u < 4; ++u) {
                 const int r = r0 + RS * (i0 + u);
                 uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+                const uint32_t fac = of_row(i0 + u);
                 if (r < valid) {
-                    lo = e4m3x8_to_16<BF16>(make_uint2(in[u].x, in[u].y));
-                    hi = e4m3x8_to_16<BF16>(make_uint2(in[u].z, in[u].w));
+                    lo = widen_e4m3x8<BF16, BLK>(make_uint2(in[u].x, in[u].y), fac);
+                    hi = widen_e4m3x8<BF16, BLK>(make_uint2(in[u].z, in[u].w), fac);
                 }
                 *reinterpret_cast<uint4*>(slot + sw128_chunk<TK>(2 * j, r)) = lo;
                 *reinterpret_cast<uint4*>(slot + sw128_chunk<TK>(2 * j + 1, r)) = hi;
@@ -149,9 +263,10 @@ __device__ __forceinline__ void widen_e4m3_tile(uint8_t* slot, int valid, int gt
         for (int i = 0; i < TK / RS; ++i) {
             const int r = r0 + RS * i;
             uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+            const uint32_t fac = of_row(i);
             if (r < valid) {
-                lo = e4m3x8_to_16<BF16>(make_uint2(in[i].x, in[i].y));
-                hi = e4m3x8_to_16<BF16>(make_uint2(in[i].z, in[i].w));
+                lo = widen_e4m3x8<BF16, BLK>(make_uint2(in[i].x, in[i].y), fac);
+                hi = widen_e4m3x8<BF16, BLK>(make_uint2(in[i].z, in[i].w), fac);
             }
             *reinterpret_cast<uint4*>(slot + sw128_chunk<TK>(2 * j, r)) = lo;
             *reinterpret_cast<uint4*>(slot + sw128_chunk<TK>(2 * j + 1, r)) = hi;

@@ -9,53 +9,14 @@
 #include <cstdint>
 
 #include "../../include/bsp.h"
+#include "bsp_check.h"
 #include "bsp_step.h"
 
 namespace {
 
 using namespace bsp;
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-int ilog2(int x) {
-    int l = 0;
-    while ((1 << l) < x) ++l;
-    return l;
-}
-
-// Device (or managed) memory of the current device, aligned to `align` bytes.
-bool device_ptr(const void* p, size_t align) {
-    if (!p || (reinterpret_cast<uintptr_t>(p) & (align - 1))) return false;
-    cudaPointerAttributes a;
-    if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
-        cudaGetLastError();
-        return false;
-    }
-    if (a.type == cudaMemoryTypeManaged) return true;
-    int dev = 0;
-    return a.type == cudaMemoryTypeDevice && cudaGetDevice(&dev) == cudaSuccess && a.device == dev;
-}
-bool optional_ptr(const void* p, size_t align) { return !p || device_ptr(p, align); }
-
 int logits_bytes(int dtype) { return dtype == BSP_LOGITS_FP32 ? 4 : 2; }
-
-// The plan's workspace is on the current device, where the kernel is going to read it.
-bool plan_here(const bsp_plan_t* plan) { return device_ptr(plan->ws_device, 16); }
-
-int32_t* status_word(const bsp_plan_t* plan) { return static_cast<int32_t*>(plan->ws_device); }
-const int32_t* image_header(const bsp_plan_t* plan) {
-    return reinterpret_cast<const int32_t*>(static_cast<const uint8_t*>(plan->ws_device) + kStatusBytes);
-}
-const int32_t* section(const bsp_plan_t* plan, uint64_t off) {
-    return reinterpret_cast<const int32_t*>(static_cast<const uint8_t*>(plan->ws_device) + off);
-}
-// What the staged image's header says of this plan.
-PlanShape plan_shape(const bsp_plan_t* plan) {
-    const bsp_geometry& geo = plan->geo;
-    return PlanShape{{static_cast<int32_t>(plan->generation), static_cast<int32_t>(plan->generation >> 32)},
-                     plan->batch, plan->beam_width, plan->kind, plan->total_rows,
-                     static_cast<int32_t>(plan->off_pages - kStatusBytes), geo.num_q_heads, geo.num_kv_heads,
-                     geo.page_size, geo.head_dim};
-}
 
 // The decode plan, logits type, vocabulary and row stride that the logits' calls share.
 bsp_status check_logits(const bsp_plan_t* plan, int32_t dtype, int32_t vocab, int64_t stride) {
@@ -107,12 +68,6 @@ bool device_sms(int* sms) {
     int dev = 0;
     return cudaGetDevice(&dev) == cudaSuccess &&
            cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
-}
-
-bsp_status launched(cudaError_t e) {
-    if (e == cudaSuccess) return BSP_OK;
-    cudaGetLastError();
-    return BSP_ERR_CUDA;
 }
 
 }  // namespace

@@ -90,10 +90,11 @@ constexpr int kTailThreads = 128;
 // MAXP: head passes whose tail state is held in registers across the wait for the prompt kernel
 // (passes = Hq / (4 warps x heads per warp pass), rounded up to 1, 2 or 4; more passes are done
 // in groups of MAXP).
-// FP8: E4M3 pools (a lane reads 8 one-byte codes of a row instead of 8 16-bit elements; the keys'
+// POOL: E4M3 pools (a lane reads 8 one-byte codes of a row instead of 8 16-bit elements; the keys'
 // scale is folded into scale_log2, the values' scale into the tail's share of O).
-template <int D, bool BF16, int MAXT, int MAXP, bool FP8>
+template <int D, bool BF16, int MAXT, int MAXP, PoolKind POOL>
 __global__ void __launch_bounds__(kTailThreads) tail_merge_kernel(TailParams p) {
+    constexpr bool FP8 = POOL != kPool16, BLK = POOL == kPoolBlocks;
     constexpr int LPR = D / 8;       // lanes per K/V row
     constexpr int HPW = 32 / LPR;    // heads per warp pass
     constexpr int NW = kTailThreads / 32;
@@ -164,11 +165,13 @@ __global__ void __launch_bounds__(kTailThreads) tail_merge_kernel(TailParams p) 
             // a lane's 8 elements of a K or V row: 16 bytes, or 8 E4M3 codes (the upper half unused)
             uint4 kraw[MAXT], vraw[MAXT];
             bool ok[MAXT];
+            float kscale[MAXT], vscale[MAXT];  // the rows' block scales (E4M3 pools that have them)
 #pragma unroll
             for (int t = 0; t < MAXT; ++t) {
                 const long long off = t < T ? s_off[t] : -1;
                 ok[t] = active && off >= 0;
                 kraw[t] = vraw[t] = make_uint4(0, 0, 0, 0);
+                kscale[t] = vscale[t] = 1.f;
                 if (ok[t]) {
                     const long long e = off + g * head_stride;  // element offset
                     if constexpr (FP8) {
@@ -176,6 +179,11 @@ __global__ void __launch_bounds__(kTailThreads) tail_merge_kernel(TailParams p) 
                         const uint2 vv = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.v_pool) + e) + li);
                         kraw[t] = make_uint4(kk.x, kk.y, 0, 0);
                         vraw[t] = make_uint4(vv.x, vv.y, 0, 0);
+                        if constexpr (BLK) {
+                            const long long x = e / D >> p.block_log2;
+                            kscale[t] = block_scale<BF16>(__ldg(p.k_exp + x));
+                            vscale[t] = block_scale<BF16>(__ldg(p.v_exp + x));
+                        }
                     } else {
                         kraw[t] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.k_pool) + e) + li);
                         vraw[t] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.v_pool) + e) + li);
@@ -198,6 +206,7 @@ __global__ void __launch_bounds__(kTailThreads) tail_merge_kernel(TailParams p) 
                     for (int e = 0; e < 8; ++e) dot = fmaf(q[e], kf[e], dot);
 #pragma unroll
                     for (int off = LPR / 2; off >= 1; off >>= 1) dot += __shfl_xor_sync(FULL, dot, off);
+                    if constexpr (BLK) dot *= kscale[t];
                     if (ok[t]) sc[t] = dot * p.scale_log2;
                     m = fmaxf(m, sc[t]);
                 }
@@ -214,7 +223,7 @@ __global__ void __launch_bounds__(kTailThreads) tail_merge_kernel(TailParams p) 
                     if constexpr (FP8) unpack8_e4m3(make_uint2(vraw[t].x, vraw[t].y), vf);
                     else unpack8<BF16>(vraw[t], vf);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) acc[pi][e] = fmaf(e_s, vf[e], acc[pi][e]);
+                    for (int e = 0; e < 8; ++e) acc[pi][e] = fmaf(BLK ? e_s * vscale[t] : e_s, vf[e], acc[pi][e]);
                     l += e_s;
                 }
             }
@@ -335,7 +344,7 @@ __global__ void __launch_bounds__(kTailThreads) tail_merge_kernel(TailParams p) 
     }
 }
 
-template <int D, bool BF16, int MAXT, int MAXP, bool FP8>
+template <int D, bool BF16, int MAXT, int MAXP, PoolKind POOL>
 static cudaError_t launch_tail_k(const TailParams& p, bool after_prefix, int pass_ctas, cudaStream_t stream) {
     const long long rows = static_cast<long long>(p.B) * p.W;
     cudaLaunchConfig_t cfg = {};
@@ -348,7 +357,7 @@ static cudaError_t launch_tail_k(const TailParams& p, bool after_prefix, int pas
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = after_prefix ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, tail_merge_kernel<D, BF16, MAXT, MAXP, FP8>, p);
+    return cudaLaunchKernelEx(&cfg, tail_merge_kernel<D, BF16, MAXT, MAXP, POOL>, p);
 }
 
 // head passes of a 128-thread CTA: Hq / (4 warps x heads per warp pass)
@@ -371,80 +380,83 @@ static int device_sms() {
     return cache[dev];
 }
 
-template <int D, bool BF16, int MAXT, bool FP8>
+template <int D, bool BF16, int MAXT, PoolKind POOL>
 static cudaError_t launch_tail_p(const TailParams& p, bool after_prefix, cudaStream_t stream) {
     const int passes = tail_passes<D>(p.Hq);
     const long long rows = static_cast<long long>(p.B) * p.W;
     // fewer rows than SMs: one CTA per (row, head pass), so a row's heads merge in parallel
-    if (passes > 1 && rows < device_sms()) return launch_tail_k<D, BF16, MAXT, 1, FP8>(p, after_prefix, passes, stream);
-    if (passes <= 1) return launch_tail_k<D, BF16, MAXT, 1, FP8>(p, after_prefix, 1, stream);
-    if (passes <= 2) return launch_tail_k<D, BF16, MAXT, 2, FP8>(p, after_prefix, 1, stream);
-    return launch_tail_k<D, BF16, MAXT, 4, FP8>(p, after_prefix, 1, stream);
+    if (passes > 1 && rows < device_sms()) return launch_tail_k<D, BF16, MAXT, 1, POOL>(p, after_prefix, passes, stream);
+    if (passes <= 1) return launch_tail_k<D, BF16, MAXT, 1, POOL>(p, after_prefix, 1, stream);
+    if (passes <= 2) return launch_tail_k<D, BF16, MAXT, 2, POOL>(p, after_prefix, 1, stream);
+    return launch_tail_k<D, BF16, MAXT, 4, POOL>(p, after_prefix, 1, stream);
 }
 
-template <int D, bool BF16, bool FP8>
+template <int D, bool BF16, PoolKind POOL>
 static cudaError_t launch_tail_t(const TailParams& p, int max_tail_len, bool after_prefix, cudaStream_t stream) {
     const long long rows = static_cast<long long>(p.B) * p.W;
     if (rows == 0) return cudaSuccess;
-    if (max_tail_len <= 2) return launch_tail_p<D, BF16, 2, FP8>(p, after_prefix, stream);
-    if (max_tail_len <= 4) return launch_tail_p<D, BF16, 4, FP8>(p, after_prefix, stream);
-    return launch_tail_p<D, BF16, 8, FP8>(p, after_prefix, stream);
+    if (max_tail_len <= 2) return launch_tail_p<D, BF16, 2, POOL>(p, after_prefix, stream);
+    if (max_tail_len <= 4) return launch_tail_p<D, BF16, 4, POOL>(p, after_prefix, stream);
+    return launch_tail_p<D, BF16, 8, POOL>(p, after_prefix, stream);
 }
 
 // the same L1/shared split as the prompt kernel, so SMs are not reconfigured between the
 // kernels of a step
-template <int D, bool BF16, int MAXT, bool FP8>
+template <int D, bool BF16, int MAXT, PoolKind POOL>
 static cudaError_t prepare_tail_p(int Hq) {
     const cudaFuncAttribute a = cudaFuncAttributePreferredSharedMemoryCarveout;
     const int passes = tail_passes<D>(Hq);
     // the one-pass variant also serves steps with fewer rows than SMs
     const cudaError_t e =
-        cudaFuncSetAttribute(tail_merge_kernel<D, BF16, MAXT, 1, FP8>, a, cudaSharedmemCarveoutMaxShared);
+        cudaFuncSetAttribute(tail_merge_kernel<D, BF16, MAXT, 1, POOL>, a, cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess || passes <= 1) return e;
-    if (passes <= 2) return cudaFuncSetAttribute(tail_merge_kernel<D, BF16, MAXT, 2, FP8>, a, cudaSharedmemCarveoutMaxShared);
-    return cudaFuncSetAttribute(tail_merge_kernel<D, BF16, MAXT, 4, FP8>, a, cudaSharedmemCarveoutMaxShared);
+    if (passes <= 2) return cudaFuncSetAttribute(tail_merge_kernel<D, BF16, MAXT, 2, POOL>, a, cudaSharedmemCarveoutMaxShared);
+    return cudaFuncSetAttribute(tail_merge_kernel<D, BF16, MAXT, 4, POOL>, a, cudaSharedmemCarveoutMaxShared);
 }
 
-template <int D, bool BF16, bool FP8>
+template <int D, bool BF16, PoolKind POOL>
 static cudaError_t prepare_tail_t(int max_tail_len, int Hq) {
-    if (max_tail_len <= 2) return prepare_tail_p<D, BF16, 2, FP8>(Hq);
-    if (max_tail_len <= 4) return prepare_tail_p<D, BF16, 4, FP8>(Hq);
-    return prepare_tail_p<D, BF16, 8, FP8>(Hq);
+    if (max_tail_len <= 2) return prepare_tail_p<D, BF16, 2, POOL>(Hq);
+    if (max_tail_len <= 4) return prepare_tail_p<D, BF16, 4, POOL>(Hq);
+    return prepare_tail_p<D, BF16, 8, POOL>(Hq);
 }
 
-template <int D, bool FP8>
+template <int D, PoolKind POOL>
 static cudaError_t prepare_tail_d(bool bf16, int max_tail_len, int Hq) {
-    return bf16 ? prepare_tail_t<D, true, FP8>(max_tail_len, Hq) : prepare_tail_t<D, false, FP8>(max_tail_len, Hq);
+    return bf16 ? prepare_tail_t<D, true, POOL>(max_tail_len, Hq) : prepare_tail_t<D, false, POOL>(max_tail_len, Hq);
 }
 
-template <int D, bool FP8>
+template <int D, PoolKind POOL>
 static cudaError_t launch_tail_d(bool bf16, int max_tail_len, const TailParams& p, bool after_prefix,
                                  cudaStream_t stream) {
-    return bf16 ? launch_tail_t<D, true, FP8>(p, max_tail_len, after_prefix, stream)
-                : launch_tail_t<D, false, FP8>(p, max_tail_len, after_prefix, stream);
+    return bf16 ? launch_tail_t<D, true, POOL>(p, max_tail_len, after_prefix, stream)
+                : launch_tail_t<D, false, POOL>(p, max_tail_len, after_prefix, stream);
 }
 
 // E4M3 pools at head_dim 64 and 128 only
-cudaError_t prepare_tail(int head_dim, bool bf16, int max_tail_len, int num_q_heads, bool fp8) {
-    switch (head_dim) {
-        case 64: return fp8 ? prepare_tail_d<64, true>(bf16, max_tail_len, num_q_heads)
-                            : prepare_tail_d<64, false>(bf16, max_tail_len, num_q_heads);
-        case 128: return fp8 ? prepare_tail_d<128, true>(bf16, max_tail_len, num_q_heads)
-                             : prepare_tail_d<128, false>(bf16, max_tail_len, num_q_heads);
-        case 256: return fp8 ? cudaErrorInvalidValue : prepare_tail_d<256, false>(bf16, max_tail_len, num_q_heads);
+cudaError_t prepare_tail(int head_dim, bool bf16, int max_tail_len, int num_q_heads, PoolKind pools) {
+    switch (head_dim + pools) {
+        case 64 + kPool16: return prepare_tail_d<64, kPool16>(bf16, max_tail_len, num_q_heads);
+        case 64 + kPoolE4m3: return prepare_tail_d<64, kPoolE4m3>(bf16, max_tail_len, num_q_heads);
+        case 64 + kPoolBlocks: return prepare_tail_d<64, kPoolBlocks>(bf16, max_tail_len, num_q_heads);
+        case 128 + kPool16: return prepare_tail_d<128, kPool16>(bf16, max_tail_len, num_q_heads);
+        case 128 + kPoolE4m3: return prepare_tail_d<128, kPoolE4m3>(bf16, max_tail_len, num_q_heads);
+        case 128 + kPoolBlocks: return prepare_tail_d<128, kPoolBlocks>(bf16, max_tail_len, num_q_heads);
+        case 256 + kPool16: return prepare_tail_d<256, kPool16>(bf16, max_tail_len, num_q_heads);
         default: return cudaErrorInvalidValue;
     }
 }
 
 cudaError_t launch_tail(int head_dim, bool bf16, int max_tail_len, const TailParams& p, bool after_prefix,
-                        cudaStream_t stream, bool fp8) {
-    switch (head_dim) {
-        case 64: return fp8 ? launch_tail_d<64, true>(bf16, max_tail_len, p, after_prefix, stream)
-                            : launch_tail_d<64, false>(bf16, max_tail_len, p, after_prefix, stream);
-        case 128: return fp8 ? launch_tail_d<128, true>(bf16, max_tail_len, p, after_prefix, stream)
-                             : launch_tail_d<128, false>(bf16, max_tail_len, p, after_prefix, stream);
-        case 256: return fp8 ? cudaErrorInvalidValue
-                             : launch_tail_d<256, false>(bf16, max_tail_len, p, after_prefix, stream);
+                        cudaStream_t stream, PoolKind pools) {
+    switch (head_dim + pools) {
+        case 64 + kPool16: return launch_tail_d<64, kPool16>(bf16, max_tail_len, p, after_prefix, stream);
+        case 64 + kPoolE4m3: return launch_tail_d<64, kPoolE4m3>(bf16, max_tail_len, p, after_prefix, stream);
+        case 64 + kPoolBlocks: return launch_tail_d<64, kPoolBlocks>(bf16, max_tail_len, p, after_prefix, stream);
+        case 128 + kPool16: return launch_tail_d<128, kPool16>(bf16, max_tail_len, p, after_prefix, stream);
+        case 128 + kPoolE4m3: return launch_tail_d<128, kPoolE4m3>(bf16, max_tail_len, p, after_prefix, stream);
+        case 128 + kPoolBlocks: return launch_tail_d<128, kPoolBlocks>(bf16, max_tail_len, p, after_prefix, stream);
+        case 256 + kPool16: return launch_tail_d<256, kPool16>(bf16, max_tail_len, p, after_prefix, stream);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -181,11 +181,12 @@ __device__ __forceinline__ bool gather_sync_and(bool ok) {
 
 }  // namespace
 
-template <int D, bool BF16, bool FP8>
-__global__ void __launch_bounds__(FP8 ? 640 : 384, 1)
+template <int D, bool BF16, int POOL>
+__global__ void __launch_bounds__(POOL != kPool16 ? 640 : 384, 1)
 prefix_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const PrefixParams p) {
     using C = WideCfg<D>;
+    constexpr bool FP8 = POOL != kPool16, BLK = POOL == kPoolBlocks;
     constexpr int TK = C::TK, NC = C::NC, KST = C::KST, VST = C::VST;
     constexpr unsigned FULL = 0xffffffffu;
     extern __shared__ uint8_t smem_raw[];
@@ -521,6 +522,10 @@ prefix_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                 prefetch_l2(k_pool + static_cast<long long>(r) * (D * EB) + off);
                                 prefetch_l2(v_pool + static_cast<long long>(r) * (D * EB) + off);
                             }
+                            if constexpr (BLK) {
+                                prefetch_l2(p.k_exp + (r >> p.block_log2));
+                                prefetch_l2(p.v_exp + (r >> p.block_log2));
+                            }
                         }
                         res[n][h] = r;
                     }
@@ -563,8 +568,13 @@ prefix_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             if constexpr (FP8) {
                                 uint4 kw = make_uint4(0, 0, 0, 0), vw = kw;  // absent keys are zero rows
                                 if (r >= 0) {
-                                    kw = e4m3x8_to_16<BF16>(__ldg(reinterpret_cast<const uint2*>(k_pool + e)));
-                                    vw = e4m3x8_to_16<BF16>(__ldg(reinterpret_cast<const uint2*>(v_pool + e)));
+                                    uint32_t kfac = 0, vfac = 0;
+                                    if constexpr (BLK) {
+                                        kfac = block_factor<BF16>(__ldg(p.k_exp + (r >> p.block_log2)));
+                                        vfac = block_factor<BF16>(__ldg(p.v_exp + (r >> p.block_log2)));
+                                    }
+                                    kw = widen_e4m3x8<BF16, BLK>(__ldg(reinterpret_cast<const uint2*>(k_pool + e)), kfac);
+                                    vw = widen_e4m3x8<BF16, BLK>(__ldg(reinterpret_cast<const uint2*>(v_pool + e)), vfac);
                                 }
                                 *reinterpret_cast<uint4*>(kt + off) = kw;
                                 *reinterpret_cast<uint4*>(vt + off) = vw;
@@ -603,6 +613,10 @@ prefix_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const int bar = 2 + tensor;                 // named barrier of the stream's threads
                 bool ok = true;
                 int gt = 0;
+                const uint8_t* exps = tensor == 0 ? p.k_exp : p.v_exp;
+                BlockFactors<D, TK, BF16, C::CONV_THREADS> ahead;
+                uint32_t factor[TK / C::CONV_THREADS] = {};
+                if constexpr (BLK) ahead.begin(p, exps, u_begin, nunits, stid);
                 for (int k = 0; k < nunits && ok; ++k) {
                     const UnitInfo cur = load_unit(p, u_begin + k);
                     const int ptiles = prompt_tiles<TK>(cur);
@@ -612,13 +626,15 @@ prefix_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                         // hands the slots over; nothing to widen): so each parity wait names the phase it means
                         uint64_t* full8 = tensor == 0 ? &bars->k8_full[gt % KST] : &bars->v8_full[gt % VST];
                         const uint32_t ph = tensor == 0 ? (gt / KST) & 1 : (gt / VST) & 1;
+                        if constexpr (BLK)
+                            if (t < ptiles) ahead.next(p, exps, u_begin, nunits, stid, factor);
                         ok = mbar_wait(full8, ph, abort_flag, kWideWaitNs);
                         ok = __all_sync(FULL, ok);
                         ok = named_sync_and(bar, C::CONV_THREADS, ok);
                         if (!ok || t >= ptiles) continue;
                         const int valid = min(TK, cur.key_end - (cur.key_begin + t * TK));
-                        widen_e4m3_tile<D, TK, BF16, C::CONV_THREADS>(tensor == 0 ? k_tile(gt) : v_tile(gt), valid,
-                                                                      stid, bar);
+                        widen_e4m3_tile<D, TK, BF16, C::CONV_THREADS, BLK>(tensor == 0 ? k_tile(gt) : v_tile(gt),
+                                                                           valid, stid, bar, factor);
                         fence_proxy_async_smem();
                         ok = named_sync_and(bar, C::CONV_THREADS, ok);
                         if (ok && stid == 0)
@@ -923,67 +939,78 @@ prefix_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     }
 }
 
-template <int D, bool BF16, bool FP8>
+template <int D, bool BF16, PoolKind POOL>
 static cudaError_t prepare_wide_k() {
     using C = WideCfg<D>;
     static_assert(sizeof(WideBarriers) <= 512, "barrier block");
-    if constexpr (FP8) {
+    if constexpr (POOL != kPool16) {
         // the register split (setmaxnreg) draws on the launch's registers: a build that runs the kernel at
         // another per-thread count would leave the softmax warps waiting for registers, so it is refused
         static const cudaError_t regs = [] {
             cudaFuncAttributes fa{};
-            const cudaError_t r = cudaFuncGetAttributes(&fa, prefix_wide_kernel<D, BF16, FP8>);
+            const cudaError_t r = cudaFuncGetAttributes(&fa, prefix_wide_kernel<D, BF16, POOL>);
             if (r != cudaSuccess) return r;
             return fa.numRegs == C::REGS_LAUNCH_E4M3 ? cudaSuccess : cudaErrorInvalidConfiguration;
         }();
         if (regs != cudaSuccess) return regs;
     }
     cudaError_t e =
-        cudaFuncSetAttribute(prefix_wide_kernel<D, BF16, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        cudaFuncSetAttribute(prefix_wide_kernel<D, BF16, POOL>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(prefix_wide_kernel<D, BF16, FP8>, cudaFuncAttributePreferredSharedMemoryCarveout,
+    return cudaFuncSetAttribute(prefix_wide_kernel<D, BF16, POOL>, cudaFuncAttributePreferredSharedMemoryCarveout,
                                 cudaSharedmemCarveoutMaxShared);
 }
 
-template <int D, bool FP8>
-static cudaError_t prepare_wide_d(bool bf16) {
-    return bf16 ? prepare_wide_k<D, true, FP8>() : prepare_wide_k<D, false, FP8>();
+template <int D>
+static cudaError_t prepare_wide_d(bool bf16, PoolKind pools) {
+    switch (pools) {
+        case kPool16: return bf16 ? prepare_wide_k<D, true, kPool16>() : prepare_wide_k<D, false, kPool16>();
+        case kPoolE4m3: return bf16 ? prepare_wide_k<D, true, kPoolE4m3>() : prepare_wide_k<D, false, kPoolE4m3>();
+        default: return bf16 ? prepare_wide_k<D, true, kPoolBlocks>() : prepare_wide_k<D, false, kPoolBlocks>();
+    }
 }
 
-cudaError_t prepare_wide(int head_dim, bool bf16, bool fp8) {
+cudaError_t prepare_wide(int head_dim, bool bf16, PoolKind pools) {
     switch (head_dim) {
-        case 64: return fp8 ? prepare_wide_d<64, true>(bf16) : prepare_wide_d<64, false>(bf16);
-        case 128: return fp8 ? prepare_wide_d<128, true>(bf16) : prepare_wide_d<128, false>(bf16);
+        case 64: return prepare_wide_d<64>(bf16, pools);
+        case 128: return prepare_wide_d<128>(bf16, pools);
         default: return cudaErrorInvalidValue;
     }
 }
 
-template <int D, bool BF16, bool FP8>
+template <int D, bool BF16, PoolKind POOL>
 static void launch_wide_k(int ctas, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                           const PrefixParams& p, cudaStream_t stream) {
-    constexpr int threads = FP8 ? WideCfg<D>::THREADS_E4M3 : WideCfg<D>::THREADS;
-    prefix_wide_kernel<D, BF16, FP8><<<ctas, threads, WideCfg<D>::SMEM, stream>>>(tq, tk, tv, p);
+    constexpr int threads = POOL != kPool16 ? WideCfg<D>::THREADS_E4M3 : WideCfg<D>::THREADS;
+    prefix_wide_kernel<D, BF16, POOL><<<ctas, threads, WideCfg<D>::SMEM, stream>>>(tq, tk, tv, p);
 }
 
 template <int D>
-static void launch_wide_d(bool bf16, bool fp8, int ctas, const CUtensorMap& tq, const CUtensorMap& tk,
-                          const CUtensorMap& tv, const PrefixParams& p, cudaStream_t stream) {
-    if (bf16) {
-        if (fp8) launch_wide_k<D, true, true>(ctas, tq, tk, tv, p, stream);
-        else launch_wide_k<D, true, false>(ctas, tq, tk, tv, p, stream);
-    } else {
-        if (fp8) launch_wide_k<D, false, true>(ctas, tq, tk, tv, p, stream);
-        else launch_wide_k<D, false, false>(ctas, tq, tk, tv, p, stream);
+static void launch_wide_d(bool bf16, PoolKind pools, int ctas, const CUtensorMap& tq, const CUtensorMap& tk,
+                         const CUtensorMap& tv, const PrefixParams& p, cudaStream_t stream) {
+    switch (pools) {
+        case kPool16:
+            if (bf16) launch_wide_k<D, true, kPool16>(ctas, tq, tk, tv, p, stream);
+            else launch_wide_k<D, false, kPool16>(ctas, tq, tk, tv, p, stream);
+            break;
+        case kPoolE4m3:
+            if (bf16) launch_wide_k<D, true, kPoolE4m3>(ctas, tq, tk, tv, p, stream);
+            else launch_wide_k<D, false, kPoolE4m3>(ctas, tq, tk, tv, p, stream);
+            break;
+        case kPoolBlocks:
+            if (bf16) launch_wide_k<D, true, kPoolBlocks>(ctas, tq, tk, tv, p, stream);
+            else launch_wide_k<D, false, kPoolBlocks>(ctas, tq, tk, tv, p, stream);
+            break;
     }
 }
 
 cudaError_t launch_wide(int head_dim, bool bf16, int ctas, const CUtensorMap& tq, const CUtensorMap& tk,
-                        const CUtensorMap& tv, const PrefixParams& p, cudaStream_t stream, bool fp8) {
+                        const CUtensorMap& tv, const PrefixParams& p, cudaStream_t stream, PoolKind pools) {
     if (ctas == 0 || p.num_units == 0) return cudaSuccess;
     if (p.bq <= 0 || p.bq * p.G > 32) return cudaErrorInvalidValue;
     switch (head_dim) {
-        case 64: launch_wide_d<64>(bf16, fp8, ctas, tq, tk, tv, p, stream); break;
-        case 128: launch_wide_d<128>(bf16, fp8, ctas, tq, tk, tv, p, stream); break;
+        case 64: launch_wide_d<64>(bf16, pools, ctas, tq, tk, tv, p, stream); break;
+        case 128: launch_wide_d<128>(bf16, pools, ctas, tq, tk, tv, p, stream); break;
         default: return cudaErrorInvalidValue;
     }
     return cudaGetLastError();

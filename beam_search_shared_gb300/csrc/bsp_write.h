@@ -5,6 +5,8 @@
 
 #include <cstdint>
 
+#include "../../include/bsp.h"
+
 namespace bsp {
 
 // RoPE on the paged append (bsp_rope.cu).
@@ -45,5 +47,49 @@ struct AppendFp8Params {
 cudaError_t launch_append_fp8(int src, const AppendFp8Params& p, cudaStream_t stream);
 cudaError_t prepare_append_fp8(int src);
 
+// Normalised and rotated appends (bsp_norm.cu): what K and query rows go through, and the query rows.
+struct NormRope {
+    const int32_t* loc;
+    const int32_t* pos;        // with cos_sin
+    const float* cos_sin;      // [max_pos][rot], or null: no rotation
+    const void* q;             // may be null: no query rows
+    void* q_out;
+    int64_t q_stride, q_out_stride;  // elements
+    const void* q_weight;      // may be null: ones
+    const void* k_weight;
+    float eps, weight_offset;
+    int norm, weight_fp32;
+    int n, Hq, rot, interleaved, max_pos;
+};
+struct NormAppendParams {
+    NormRope a;
+    const void* k_new;
+    const void* v_new;
+    int64_t src_stride;
+    void* k_pool;
+    void* v_pool;
+    int32_t* status;
+    int Hkv, ps_log2, num_pages;
+    float k_mul, v_mul;        // E4M3 pools
+};
+// fp8: the pools are E4M3 bytes with one multiplier per tensor, else the q dtype
+cudaError_t launch_norm_append(int head_dim, bool bf16, bool fp8, const NormAppendParams& p, cudaStream_t stream);
+struct BlockAppendParams {
+    NormRope a;
+    const void* k_new;
+    const void* v_new;
+    int64_t src_stride;
+    uint8_t* k_pool;
+    uint8_t* v_pool;
+    uint8_t* k_exp;            // exponent bytes of the blocks
+    uint8_t* v_exp;
+    int32_t* status;
+    int Hkv, ps_log2, num_pages, block_log2;
+    int exp_lo, exp_hi;        // exponent bytes that a write chooses from
+    unsigned kv_ctas;          // set by launch_block_append
+};
+cudaError_t launch_block_append(int head_dim, bool bf16, const BlockAppendParams& p, cudaStream_t stream);
+cudaError_t launch_rope_scaled(int max_pos, int rot, double base, const bsp_rope_scaling& sc, float* cos_sin,
+                               cudaStream_t stream);
 
 }  // namespace bsp

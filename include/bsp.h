@@ -101,6 +101,7 @@ enum {
 #define BSP_DEVFLAG_PAGE_INDEX 1
 #define BSP_DEVFLAG_TIMEOUT 2
 #define BSP_DEVFLAG_POSITION 4  /* a RoPE position outside [0, max_position) (bsp_rope_append_kv) */
+#define BSP_DEVFLAG_PAGES 16    /* bsp_fork_tables: not enough free pages for every row; reported as BSP_ERR_CAPACITY */
 #define BSP_DEVFLAG_GRAPH 8     /* a replayed graph-mode launch found a plan of another shape (nothing
                                    written); reported as BSP_ERR_STALE_PLAN */
 
@@ -392,6 +393,66 @@ BSP_API bsp_status bsp_rope_append_kv_fp8(const bsp_plan_t* plan, const bsp_rope
                                           void* const* events, void* stream);
 
 /*
+ * Rotary tables of a model stretched beyond the length it was trained for: bsp_rope_cos_sin with scaled frequencies,
+ * theta_j = base^(-2j / rotary_dim) before, and both halves of the table times `amplitude`. fp64 on the device, each
+ * value rounded once. Kinds:
+ *   BSP_ROPE_LINEAR  theta_j / factor (position interpolation)
+ *   BSP_ROPE_BASE    a base of base * factor^(rotary_dim / (rotary_dim - 2)); rotary_dim > 2
+ *   BSP_ROPE_BANDS   by the turns t_j = original_positions * theta_j / (2 pi) that a pair makes over the trained length:
+ *                    theta_j * ((1 - s) / factor + s), s = clamp((t_j - low) / (high - low), 0, 1)
+ *   BSP_ROPE_RAMP    by the pair's index (Peng et al., YaRN, section 3.2): theta_j / factor * s + theta_j * (1 - s),
+ *                    s = clamp((j - lo) / max(hi - lo, 0.001), 0, 1) with i(t) = rotary_dim * ln(original_positions /
+ *                    (2 pi t)) / (2 ln base), lo = max(floor(i(high)), 0), hi = min(ceil(i(low)), rotary_dim - 1)
+ * factor > 0, amplitude > 0 finite; BANDS and RAMP: original_positions > 0 and 0 < low < high, finite (not read
+ * otherwise). Errors as bsp_rope_cos_sin. (No counterpart on the pages the method comes from.)
+ */
+enum { BSP_ROPE_LINEAR = 1, BSP_ROPE_BASE = 2, BSP_ROPE_BANDS = 3, BSP_ROPE_RAMP = 4 };
+typedef struct bsp_rope_scaling {
+    int32_t kind;                /* BSP_ROPE_* */
+    int32_t original_positions;
+    double factor;
+    double low, high;            /* turns */
+    double amplitude;            /* 1: plain cos and sin */
+} bsp_rope_scaling;
+BSP_API bsp_status bsp_rope_cos_sin_scaled(int32_t max_position, int32_t rotary_dim, double base,
+                                           const bsp_rope_scaling* scaling, float* cos_sin, void* stream);
+
+/*
+ * The append of a layer that normalises its queries and keys per head, one launch: every K row and query row x of
+ * head_dim elements becomes
+ *   y = x / sqrt(mean(x^2) + eps) * (w + weight_offset)
+ * in fp32, is rotated by its token's position as in bsp_rope_append_kv (rope NULL: not), and is rounded once; K goes to
+ * the pool, the query row to q_out. V rows are copied bit for bit (E4M3 pools: quantised as in bsp_append_kv_fp8).
+ *   norm            weights and eps; q_weight, k_weight device [head_dim], 16-byte aligned, in the geometry's dtype or
+ *                   fp32 (weight_fp32 = 1), or NULL: ones (weight_offset is then not added); eps >= 0, finite
+ *   q, q_row_stride NULL, or device [n] rows of num_q_heads * head_dim elements q_row_stride apart
+ *   q_out, q_out_stride  where the query rows go (with q): q itself with its stride, or memory that overlaps none of the
+ *                   call's inputs (BSP_ERR_INVALID_ARG); rows of decode_attn's q when q_out_stride = num_q_heads * head_dim
+ *   positions       device int32 [n]; NULL without rope
+ *   other arguments, skipped tokens and errors: as bsp_rope_append_kv (events too)
+ * The _fp8 form writes E4M3 pools with one multiplier per tensor. (No counterpart on the pages the method comes from.)
+ */
+typedef struct bsp_qk_norm {
+    const void* q_weight;
+    const void* k_weight;
+    float eps;
+    float weight_offset;   /* 0, or 1 for weights stored as their distance from one */
+    int32_t weight_fp32;
+    int32_t reserved;      /* 0 */
+} bsp_qk_norm;
+BSP_API bsp_status bsp_norm_rope_append_kv(const bsp_plan_t* plan, const bsp_qk_norm* norm, const bsp_rope_config* rope,
+                                           const int32_t* positions, const void* q, int64_t q_row_stride, void* q_out,
+                                           int64_t q_out_stride, const void* k_new, const void* v_new,
+                                           int64_t src_row_stride, const int32_t* out_cache_loc, int32_t n, void* k_pool,
+                                           void* v_pool, void* const* events, void* stream);
+BSP_API bsp_status bsp_norm_rope_append_kv_fp8(const bsp_plan_t* plan, const bsp_qk_norm* norm,
+                                               const bsp_rope_config* rope, const int32_t* positions, const void* q,
+                                               int64_t q_row_stride, void* q_out, int64_t q_out_stride,
+                                               const void* k_new, const void* v_new, int64_t src_row_stride, float k_mul,
+                                               float v_mul, const int32_t* out_cache_loc, int32_t n, void* k_pool,
+                                               void* v_pool, void* const* events, void* stream);
+
+/*
  * Cascade decode attention (TensorRT-LLM PR #21738, description, "Solution"):
  * for every row r = b*W + w and query head h,
  *   O[r][h] = softmax(scale * q K^T) V over the beam's logical sequence:
@@ -444,6 +505,57 @@ BSP_API bsp_status bsp_decode_attn_fp8(const bsp_plan_t* plan, const void* q, co
                                const int32_t* cache_indirection, int32_t max_seq, float softmax_scale,
                                float k_scale, float v_scale, int32_t flags, void* o, float* lse,
                                void* const* events, void* stream);
+
+/*
+ * E4M3 pools with block scales: each block of `block` consecutive slots of a (page, kv head) has a scale of its own
+ * for K and for V, a power of two kept as its exponent byte E: element x of the block stands for
+ * e4m3(x) * 2^(E - 127). E = 0 means that nothing has been written to the block (its codes are read as 0). An 8-bit
+ * float loses nothing by a power of two, so the scale only places its range; it can be changed without rounding the
+ * codes again (but for those that leave the range below), and the product is exact in 16 bits: bf16 takes exponents
+ * E - 127 up to 15, fp16 those in [-15, 7]; larger ones (fp16: smaller ones too) are read as the nearest of these.
+ * (These entry points have no counterpart on the pages the method comes from.)
+ */
+#define BSP_MAX_SCALE_BLOCK 32
+typedef struct bsp_block_scales {
+    uint8_t* k;        /* device [num_pages][num_kv_heads][page_size / block], 16-byte aligned; zeroed once */
+    uint8_t* v;        /* the same for V */
+    int32_t block;     /* slots of a block: a power of two, at most the page size and BSP_MAX_SCALE_BLOCK */
+    int32_t reserved;  /* 0 */
+} bsp_block_scales;
+
+/*
+ * The append into such pools, one launch: K rows (normalised with norm, rotated with rope; each may be NULL) and V rows
+ * of the geometry's dtype become codes and scales, query rows go to q_out as in bsp_norm_rope_append_kv. The tokens of
+ * a call whose slots are in one block form a run and must stand next to one another in ascending order of their slots,
+ * as a prompt's or a beam's do; otherwise, and where a skipped token (which is flagged) parts a run, the codes and scale
+ * that the block ends up with are unspecified. With top the largest finite or infinite magnitude of the run's rows (of one head, of K or of V):
+ *  - E is the smallest exponent byte with top <= 448 * 2^(E - 127), within 27 .. 142 (fp16: 112 .. 134): for all but
+ *    the largest values nothing saturates; 0 if top is 0;
+ *  - a run that begins at the block's first slot starts the block anew with E. Another keeps the rows before it: the
+ *    block's exponent becomes the larger of E and its own, and if it grew, the codes of the slots before the run are
+ *    brought to it (times a power of two, rounded to nearest even). So a page that is taken from another sequence and
+ *    not written from a block's first slot on has its exponents cleared, or copied with its rows, first;
+ *  - x is stored as the E4M3 value nearest to x * 2^(127 - E), ties to even, saturated to +-448; a NaN as a NaN code.
+ * The plan may have either kv_dtype and any head_dim. Other arguments and errors as bsp_norm_rope_append_kv.
+ */
+BSP_API bsp_status bsp_append_kv_fp8_blocks(const bsp_plan_t* plan, const bsp_qk_norm* norm, const bsp_rope_config* rope,
+                                            const int32_t* positions, const void* q, int64_t q_row_stride, void* q_out,
+                                            int64_t q_out_stride, const void* k_new, const void* v_new,
+                                            int64_t src_row_stride, const int32_t* out_cache_loc, int32_t n, void* k_pool,
+                                            void* v_pool, const bsp_block_scales* scales, void* const* events,
+                                            void* stream);
+
+/*
+ * bsp_decode_attn over E4M3 pools with block scales (the plan's geometry has kv_dtype = BSP_KV_DTYPE_E4M3 and head_dim
+ * 64 or 128): bsp_decode_attn over the keys and values that the codes and scales stand for, prompt and tail alike. The
+ * kernels are those of bsp_decode_attn_fp8; a tile's codes are widened together with their scales, exactly, so the
+ * scales cost one byte read per row and no product of their own. Other arguments, flags, events and errors as there.
+ */
+BSP_API bsp_status bsp_decode_attn_fp8_blocks(const bsp_plan_t* plan, const void* q, const void* k_pool,
+                                              const void* v_pool, const bsp_block_scales* scales,
+                                              const int32_t* beam_pages, int32_t beam_pages_stride,
+                                              const int32_t* cache_indirection, int32_t max_seq, float softmax_scale,
+                                              int32_t flags, void* o, float* lse, void* const* events, void* stream);
 
 /*
  * Prefill over the cached prefix (TensorRT-Model-Connect PR #2202, "prefill and
@@ -729,6 +841,90 @@ BSP_API bsp_status bsp_evict_prefix(const bsp_plan_t* plan, const float* weights
                                     const int32_t* positions, const int32_t* keep_len, int32_t sinks, int32_t recent,
                                     void* k_pool, void* v_pool, int32_t* kept, float* weights_out,
                                     int32_t* positions_out, int64_t out_stride, void* stream);
+
+/* ------------------------------------------------------------------------------------------------------
+ * Pages of the cache. (These entry points have no counterpart on the pages the method comes from.)
+ *
+ * What is known of a pool's pages is one count per page, device int32 refs[num_pages]: how many sequences hold it. A
+ * page with a count of 0 is free. The calls take the plan for its geometry (num_pages, the page's heads, slots and
+ * element type) and status word, and follow the conventions of the operators around a step; the tables' calls run once
+ * for all layers, the rows' calls once per layer. Counts and tables need the alignment of their element. Where a call has
+ * refs_in and refs_out, or tables_in and tables_out, the second may be the first (no other overlap). Free pages are
+ * taken lowest id first and live pages keep their order, so repeated calls agree.
+ */
+
+#define BSP_MAX_PAGES (1 << 28)      /* pages of a pool, for these calls */
+#define BSP_MAX_FORK_ROWS (1 << 20)  /* batch * num_forks of bsp_fork_tables and bsp_fork_rows */
+
+/*
+ * Beams that go on as sequences of their own. Row i = b * num_forks + j is the fork of beam w = beams[b][j] of request
+ * b, with the L = P_b + T_b positions of the plan (a decode plan): its table is the full prompt pages, shared (the first
+ * floor(P_b / page_size) of the plan's; each gains a reference per row), and then fresh pages up to
+ * ceil(L / page_size) in all, the lowest free ones in the order of the rows, with a count of 1.
+ * bsp_fork_rows writes what belongs there.
+ *   beams          device int32 [batch] rows, beams_stride (>= num_forks) apart: beams in [0, beam_width), or -1: none
+ *                  (others are taken as -1 and flagged as BSP_DEVFLAG_PAGE_INDEX). A beam may be forked several times
+ *   refs_in, refs_out  the counts before and after
+ *   pages_out      device int32 [batch * num_forks] rows of pages_out_cols (>= ceil(max L / page_size)) entries,
+ *                  pages_out_stride apart: the first ceil(L / page_size) are written, the others stay as they were
+ *   workspace      4-byte aligned device memory of bsp_fork_workspace_size bytes, contents not kept; calls whose GPU
+ *                  work overlaps (two graphs too) need one each
+ * A row without a beam gets -1 entries and no pages. When the free pages do not suffice, the rows from the first that
+ * finds too few on get -1 entries and hold nothing, and BSP_DEVFLAG_PAGES is set (a row that needs no fresh page is
+ * served all the same).
+ */
+BSP_API bsp_status bsp_fork_workspace_size(int32_t batch, int32_t num_forks, size_t* device_bytes);
+BSP_API bsp_status bsp_fork_tables(const bsp_plan_t* plan, const int32_t* beams, int64_t beams_stride, int32_t num_forks,
+                                   const int32_t* refs_in, int32_t* refs_out, int32_t* pages_out,
+                                   int64_t pages_out_stride, int32_t pages_out_cols, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+/*
+ * The rows of the forks' fresh pages, K and V: positions from floor(P_b / page_size) * page_size to P_b - 1 out of the
+ * plan's prompt page, the tail's out of beam_pages[b * W + cache_indirection[b][w][pos]], as bsp_decode_attn reads them.
+ * Rows whose table holds -1 are left out. The fresh pages' other slots keep what they held.
+ *   beam_pages, cache_indirection  as bsp_decode_attn (both may be NULL for a plan without tails)
+ *   scales         NULL, or the block scales of E4M3 pools: a block takes the largest exponent among those of the blocks
+ *                  that its rows come from, rows of a smaller one are brought to it (times a power of two, rounded to
+ *                  nearest even), and blocks without rows are cleared
+ */
+BSP_API bsp_status bsp_fork_rows(const bsp_plan_t* plan, const int32_t* beams, int64_t beams_stride, int32_t num_forks,
+                                 const int32_t* pages_out, int64_t pages_out_stride, int32_t pages_out_cols,
+                                 const int32_t* beam_pages, int32_t beam_pages_stride,
+                                 const int32_t* cache_indirection, int32_t max_seq, void* k_pool, void* v_pool,
+                                 const bsp_block_scales* scales, void* stream);
+
+/*
+ * References given back: refs_out[p] = refs_in[p] less the number of times that page p stands in the tables. -1 entries
+ * are passed over; an entry outside the pool, and one more reference given back than there are (the count stays 0),
+ * set BSP_DEVFLAG_PAGE_INDEX.
+ *   tables   device int32 [rows] rows of cols entries, stride (>= cols) apart
+ */
+BSP_API bsp_status bsp_free_pages(const bsp_plan_t* plan, const int32_t* tables, int64_t stride, int32_t rows,
+                                  int32_t cols, const int32_t* refs_in, int32_t* refs_out, void* stream);
+
+/*
+ * Compaction: with L pages live, the i-th live page whose id is at least L takes the place of the i-th free page below
+ * L, so that afterwards the pages 0 .. L - 1 are the live ones and the rest of the pool is free.
+ *   pairs    device int32 [num_pages / 2][2] out: (from, to) of the pages that move, in ascending order
+ *   count    device int32 [2] out: the number of pairs, and L
+ *   remap    device int32 [num_pages] out: where each page is now
+ *   tables_in, tables_out  device int32 [rows] rows of cols entries, stride apart: every live sequence's table, with the
+ *            new ids in tables_out (-1 entries, and others outside the pool, which are flagged, as they are); NULL with
+ *            rows = 0 (remap then serves to update what else names pages)
+ * bsp_copy_pages moves the rows of each layer.
+ */
+BSP_API bsp_status bsp_compact_tables(const bsp_plan_t* plan, const int32_t* refs_in, int32_t* refs_out, int32_t* pairs,
+                                      int32_t* count, int32_t* remap, const int32_t* tables_in, int32_t* tables_out,
+                                      int64_t stride, int32_t rows, int32_t cols, void* stream);
+
+/*
+ * Whole pages copied, K and V (and their exponents with `scales`): page pairs[i][1] becomes a copy of pairs[i][0], for
+ * i < min(count[0], max_pairs). No page is both a source and a target, or a target twice. A pair of -1 is passed over;
+ * others outside the pool are skipped and flagged as BSP_DEVFLAG_PAGE_INDEX.
+ *   pairs, count   device int32 [max_pairs][2], [1] (of bsp_compact_tables, or the caller's own)
+ */
+BSP_API bsp_status bsp_copy_pages(const bsp_plan_t* plan, const int32_t* pairs, const int32_t* count, int32_t max_pairs,
+                                  void* k_pool, void* v_pool, const bsp_block_scales* scales, void* stream);
 
 #ifdef __cplusplus
 }
