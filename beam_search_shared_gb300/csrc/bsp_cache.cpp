@@ -110,7 +110,7 @@ bsp_status norm_append_impl(const bsp_plan_t* plan, const bsp_qk_norm* norm, con
     p.v_mul = v_mul;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (!record_event(events, 0, s)) return BSP_ERR_CUDA;
-    st = launched(launch_norm_append(geo.head_dim, geo.dtype == BSP_DTYPE_BF16, fp8, p, s));
+    st = launched(launch_norm_append(geo.head_dim, geo.dtype == BSP_DTYPE_BF16, fp8 ? kPoolE4m3 : kPool16, false, p, plan->num_sms, s));
     if (st != BSP_OK) return st;
     return record_event(events, 1, s) ? BSP_OK : BSP_ERR_CUDA;
 }
@@ -163,7 +163,7 @@ bsp_status bsp_append_kv_fp8_blocks(const bsp_plan_t* plan, const bsp_qk_norm* n
     const bsp_geometry& geo = plan->geo;
     st = check_block_scales(scales, geo.page_size, n > 0);
     if (st != BSP_OK) return st;
-    BlockAppendParams p{};
+    NormAppendParams p{};
     st = check_norm_append(plan, norm, rope, positions, q, q_row_stride, q_out, q_out_stride, k_new, v_new, src_row_stride,
                            out_cache_loc, n, k_pool, v_pool, &p.a);
     if (st != BSP_OK || p.a.n == 0) return st;
@@ -172,8 +172,8 @@ bsp_status bsp_append_kv_fp8_blocks(const bsp_plan_t* plan, const bsp_qk_norm* n
     p.k_new = k_new;
     p.v_new = v_new;
     p.src_stride = src_row_stride;
-    p.k_pool = static_cast<uint8_t*>(k_pool);
-    p.v_pool = static_cast<uint8_t*>(v_pool);
+    p.k_pool = k_pool;
+    p.v_pool = v_pool;
     p.k_exp = scales->k;
     p.v_exp = scales->v;
     p.status = status_word(plan);
@@ -185,7 +185,7 @@ bsp_status bsp_append_kv_fp8_blocks(const bsp_plan_t* plan, const bsp_qk_norm* n
     p.exp_hi = bf16 ? 142 : 134;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (!record_event(events, 0, s)) return BSP_ERR_CUDA;
-    st = launched(launch_block_append(geo.head_dim, bf16, p, s));
+    st = launched(launch_norm_append(geo.head_dim, bf16, kPoolBlocks, plan->kind == 1, p, plan->num_sms, s));
     if (st != BSP_OK) return st;
     return record_event(events, 1, s) ? BSP_OK : BSP_ERR_CUDA;
 }

@@ -1,6 +1,6 @@
 // Appends of normalised and rotated rows: per-head RMS norm of keys and queries, the rotary rotation, and the write
-// into 16-bit pools or E4M3 pools with one scale per tensor (norm_append_kernel) or with block scales
-// (block_append_kernel), one launch each.
+// into 16-bit pools or E4M3 pools with one scale per tensor or per block of slots, in one launch; and the tables of
+// stretched rotations.
 //
 // A head row x of D elements becomes y = x / sqrt(mean(x^2) + eps) * (w + offset), in fp32, then its first rot dims
 // turn by the position's angles (bsp_rope.cu has the rotation), and the result is rounded once, into the pools' type.
@@ -11,6 +11,7 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "../../include/bsp.h"
@@ -21,29 +22,58 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 
+// Pairs of fp32, one instruction for both: the arithmetic of the rows is what bounds the larger steps.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pair(float x, float y) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 halves(f2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 x, f2 y) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 x, f2 y) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 x, f2 y, f2 z) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+
+// 8 elements of a row as 4 pairs
 template <bool BF16>
-__device__ __forceinline__ void unpack8(const uint4& x, float (&f)[8]) {
+__device__ __forceinline__ void unpack8(const uint4& x, f2 (&f)[4]) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         float2 v;
-        if constexpr (BF16) v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+        if constexpr (BF16) v = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
         else v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        f[2 * i] = v.x;
-        f[2 * i + 1] = v.y;
+        f[i] = pair(v.x, v.y);
     }
 }
 
 template <bool BF16>
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+__device__ __forceinline__ uint4 pack8(const f2 (&f)[4]) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+        const float2 v = halves(f[i]);
         if constexpr (BF16) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
             w[i] = *reinterpret_cast<const uint32_t*>(&h);
         } else {
-            const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+            const __half2 h = __floats2half2_rn(v.x, v.y);
             w[i] = *reinterpret_cast<const uint32_t*>(&h);
         }
     }
@@ -51,299 +81,491 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 }
 
 // 8 values times a factor, each product rounded to fp32, then to the nearest E4M3 (ties to even, saturating)
-__device__ __forceinline__ uint2 quant8(const float (&f)[8], float mul) {
-    uint32_t w[2];
+__device__ __forceinline__ uint2 quant8(const f2 (&f)[4], float mul) {
+    const f2 m = pair(mul, mul);
+    uint32_t q[4];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const float2 a = make_float2(__fmul_rn(f[4 * e], mul), __fmul_rn(f[4 * e + 1], mul));
-        const float2 b = make_float2(__fmul_rn(f[4 * e + 2], mul), __fmul_rn(f[4 * e + 3], mul));
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3);
-        w[e] = (lo & 0xffffu) | (hi << 16);
-    }
-    return make_uint2(w[0], w[1]);
+    for (int e = 0; e < 4; ++e) q[e] = __nv_cvt_float2_to_fp8x2(halves(mul2(f[e], m)), __NV_SATFINITE, __NV_E4M3);
+    return make_uint2(__byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410));
 }
 
 // Chunk c (8 elements) of a norm's weights, in fp32 and with the offset added; weights NULL: ones.
 template <bool BF16>
-__device__ __forceinline__ void load_weight(const NormRope& a, const void* weight, int c, float (&w)[8]) {
+__device__ __forceinline__ void load_weight(const NormRope& a, const void* weight, int c, f2 (&w)[4]) {
     if (!weight) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = 1.f;
+        for (int e = 0; e < 4; ++e) w[e] = pair(1.f, 1.f);
         return;
     }
     if (a.weight_fp32) {
         const float4 lo = __ldg(static_cast<const float4*>(weight) + 2 * c), hi = __ldg(static_cast<const float4*>(weight) + 2 * c + 1);
-        w[0] = lo.x, w[1] = lo.y, w[2] = lo.z, w[3] = lo.w, w[4] = hi.x, w[5] = hi.y, w[6] = hi.z, w[7] = hi.w;
+        w[0] = pair(lo.x, lo.y), w[1] = pair(lo.z, lo.w), w[2] = pair(hi.x, hi.y), w[3] = pair(hi.z, hi.w);
     } else {
         unpack8<BF16>(__ldg(static_cast<const uint4*>(weight) + c), w);
     }
+    const f2 o = pair(a.weight_offset, a.weight_offset);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] += a.weight_offset;
+    for (int e = 0; e < 4; ++e) w[e] = add2(w[e], o);
 }
 
-// The lane's 8 elements f of a head row, chunk c of its D / 8, normalised (NORM and `on`) and rotated by table row t
-// (`on` and t not null). Every lane of the warp takes part, rows of different kinds beside one another.
+// How a lane's 8 elements x of a head row become y = r * (x A + z B): r the row's 1 / sqrt(mean + eps), z the partners'
+// elements in the rotation; A and B hold the norm's weights and the position's cos and sin, so that they are worked
+// out once for all rows of a kind at a position.
+struct Mix {
+    f2 A[4], B[4];
+};
 template <int D, bool BF16>
-__device__ __forceinline__ void norm_rotate(const NormRope& a, const void* weight, bool on, const float* t, int lane,
-                                            float (&f)[8]) {
-    constexpr int CPR = D / 8;
-    const int c = lane & (CPR - 1);
-    if (a.norm) {
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(f[e], f[e], ss);
-#pragma unroll
-        for (int o = CPR / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
-        if (on) {
-            const float r = 1.f / sqrtf(fmaf(ss, 1.f / D, a.eps));
-            float w[8];
-            load_weight<BF16>(a, weight, c, w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = f[e] * r * w[e];
-        }
-    }
+__device__ __forceinline__ void load_mix(const NormRope& a, const void* weight, int pos, int lane, Mix& m) {
+    const int c = lane & (D / 8 - 1);
+    load_weight<BF16>(a, weight, c, m.A);
     if (!a.cos_sin) return;  // (uniform)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m.B[e] = 0ull;
+    if (8 * c >= a.rot) return;
     const int half = a.rot >> 1;
-    const bool turned = on && t != nullptr && 8 * c < a.rot;
-    if (!a.interleaved) {
-        const int hc = a.rot >> 4;  // the partner chunk is hc away
-        const bool first = c < hc;
-        const int src = lane - c + (8 * c < a.rot ? (first ? c + hc : c - hc) : c);
-        float z[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) z[e] = __shfl_sync(kFull, f[e], src);
-        if (turned) {
-            const int j0 = 8 * (first ? c : c - hc);
-            const float4 c0 = __ldg(reinterpret_cast<const float4*>(t + j0)), c1 = __ldg(reinterpret_cast<const float4*>(t + j0 + 4));
-            const float4 s0 = __ldg(reinterpret_cast<const float4*>(t + half + j0)), s1 = __ldg(reinterpret_cast<const float4*>(t + half + j0 + 4));
-            const float cs[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-            const float sn[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-            const float sign = first ? -1.f : 1.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = __fmaf_rn(f[e], cs[e], sign * __fmul_rn(z[e], sn[e]));
-        }
-    } else if (turned) {
-        const float4 c4 = __ldg(reinterpret_cast<const float4*>(t + 4 * c)), s4 = __ldg(reinterpret_cast<const float4*>(t + half + 4 * c));
-        const float cs[4] = {c4.x, c4.y, c4.z, c4.w}, sn[4] = {s4.x, s4.y, s4.z, s4.w};
+    const float* row = a.cos_sin + static_cast<long long>(pos) * a.rot;
+    if (a.interleaved) {
+        const float4 x = __ldg(reinterpret_cast<const float4*>(row + 4 * c)), y = __ldg(reinterpret_cast<const float4*>(row + half + 4 * c));
+        const float cs[4] = {x.x, x.y, x.z, x.w}, sn[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const float x = f[2 * e], y = f[2 * e + 1];
-            f[2 * e] = __fmaf_rn(x, cs[e], -__fmul_rn(y, sn[e]));
-            f[2 * e + 1] = __fmaf_rn(y, cs[e], __fmul_rn(x, sn[e]));
+            const float2 w = halves(m.A[e]);
+            m.B[e] = mul2(pair(-w.y, w.x), pair(sn[e], sn[e]));
+            m.A[e] = mul2(m.A[e], pair(cs[e], cs[e]));
         }
+    } else {
+        const int hc = a.rot >> 4;  // the partner chunk is hc away
+        const int pc = c < hc ? c + hc : c - hc, j = 8 * min(c, pc);
+        const float4 c0 = __ldg(reinterpret_cast<const float4*>(row + j)), c1 = __ldg(reinterpret_cast<const float4*>(row + j + 4));
+        const float4 s0 = __ldg(reinterpret_cast<const float4*>(row + half + j)), s1 = __ldg(reinterpret_cast<const float4*>(row + half + j + 4));
+        const float sign = c < hc ? -1.f : 1.f;  // x cos - z sin in the first half, x cos + z sin in the second
+        const f2 sg = pair(sign, sign);
+        load_weight<BF16>(a, weight, pc, m.B);
+        m.A[0] = mul2(m.A[0], pair(c0.x, c0.y)), m.A[1] = mul2(m.A[1], pair(c0.z, c0.w));
+        m.A[2] = mul2(m.A[2], pair(c1.x, c1.y)), m.A[3] = mul2(m.A[3], pair(c1.z, c1.w));
+        m.B[0] = mul2(mul2(m.B[0], sg), pair(s0.x, s0.y)), m.B[1] = mul2(mul2(m.B[1], sg), pair(s0.z, s0.w));
+        m.B[2] = mul2(mul2(m.B[2], sg), pair(s1.x, s1.y)), m.B[3] = mul2(mul2(m.B[3], sg), pair(s1.z, s1.w));
     }
 }
 
-__device__ __forceinline__ const float* table_row(const NormRope& a, int pos) {
-    return a.cos_sin ? a.cos_sin + static_cast<long long>(pos) * a.rot : nullptr;
+// The lane's 8 elements of a head row (raw: as read), normalised and rotated. Every lane of the warp takes part.
+template <int D, bool BF16>
+__device__ __forceinline__ void norm_rotate(const NormRope& a, const Mix& m, int lane, const uint4& raw, f2 (&f)[4]) {
+    constexpr int CPR = D / 8;
+    const int c = lane & (CPR - 1);
+    f2 x[4];
+    unpack8<BF16>(raw, x);
+    float r = 1.f;
+    if (a.norm) {  // (uniform)
+        f2 s2 = mul2(x[0], x[0]);
+#pragma unroll
+        for (int e = 1; e < 4; ++e) s2 = fma2(x[e], x[e], s2);
+        const float2 s = halves(s2);
+        float ss = s.x + s.y;
+#pragma unroll
+        for (int o = CPR / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
+        r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+    }
+    const f2 rr = pair(r, r);
+    if (!a.cos_sin) {  // (uniform)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = mul2(mul2(x[e], rr), m.A[e]);
+        return;
+    }
+    f2 z[4];
+    const bool turned = 8 * c < a.rot;
+    if (a.interleaved) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 v = halves(x[e]);
+            z[e] = turned ? pair(v.y, v.x) : 0ull;
+        }
+    } else {
+        const int hc = a.rot >> 4;
+        const int src = lane - c + (turned ? (c < hc ? c + hc : c - hc) : c);
+        uint4 w;
+        w.x = __shfl_sync(kFull, raw.x, src);
+        w.y = __shfl_sync(kFull, raw.y, src);
+        w.z = __shfl_sync(kFull, raw.z, src);
+        w.w = __shfl_sync(kFull, raw.w, src);
+        unpack8<BF16>(turned ? w : make_uint4(0, 0, 0, 0), z);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = mul2(rr, fma2(x[e], m.A[e], mul2(z[e], m.B[e])));
 }
 
 // A token's slot (-1: the token is skipped) and position; what is wrong with it is flagged where `tell`.
-__device__ __forceinline__ int token_slot(const NormRope& a, int i, int ps_log2, int num_pages, int32_t* status, bool tell, int* pos) {
+__device__ __forceinline__ int token_slot(const NormAppendParams& p, int i, bool tell, int* pos) {
+    const NormRope& a = p.a;
     const int loc = __ldg(a.loc + i);
     *pos = a.cos_sin ? __ldg(a.pos + i) : 0;
     const bool pos_ok = !a.cos_sin || (*pos >= 0 && *pos < a.max_pos);
-    if (pos_ok && loc >= 0 && loc < static_cast<long long>(num_pages) << ps_log2) return loc;
-    if (tell) atomicOr(status, pos_ok ? BSP_DEVFLAG_PAGE_INDEX : BSP_DEVFLAG_POSITION);
+    if (pos_ok && loc >= 0 && loc < static_cast<long long>(p.num_pages) << p.ps_log2) return loc;
+    if (tell) atomicOr(p.status, pos_ok ? BSP_DEVFLAG_PAGE_INDEX : BSP_DEVFLAG_POSITION);
     return -1;
 }
 
-// A lane's share of the tokens' query rows: row `r` of n * Hq.
-template <int D, bool BF16>
-__device__ __forceinline__ void query_row(const NormRope& a, long long r, int lane, int ps_log2, int num_pages, int32_t* status) {
+// A slot's row of a kv head in the pools.
+__device__ __forceinline__ long long pool_row(const NormAppendParams& p, int slot, int h) {
+    return ((static_cast<long long>(slot >> p.ps_log2) * p.Hkv + h) << p.ps_log2) + (slot & ((1 << p.ps_log2) - 1));
+}
+
+// The exponent byte of a block whose new rows' largest magnitude has the bits `top` and whose own byte is `old` (0:
+// starts anew): the smallest E with top <= 448 * 2^(E - 127), 448 = 1.75 * 2^8, within the written range.
+__device__ __forceinline__ int block_exponent(const NormAppendParams& p, uint32_t top, int old) {
+    int e = 0;
+    if (top) e = min(max(static_cast<int>(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u), p.exp_lo), p.exp_hi);
+    return max(e, old);
+}
+__device__ __forceinline__ float code_factor(int e) {  // 2^(127 - E)
+    return e == 0 ? 0.f : __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+}
+
+// The `off` leading rows of a block (from `row` on, D codes each) brought from exponent old to e, by one row's lanes.
+template <int D>
+__device__ __forceinline__ void raise_rows(uint8_t* row, int off, int old, int e, int c) {
     constexpr int CPR = D / 8;
-    const int c = lane & (CPR - 1);
-    const bool live = r < static_cast<long long>(a.n) * a.Hq;
-    const int i = live ? static_cast<int>(r / a.Hq) : 0;
-    const int h = live ? static_cast<int>(r - static_cast<long long>(i) * a.Hq) : 0;
-    uint4 x = make_uint4(0, 0, 0, 0);
-    int pos = 0, slot = -1;
-    if (live) {
-        x = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + i * a.q_stride + static_cast<long long>(h) * D) + c);
-        slot = token_slot(a, i, ps_log2, num_pages, status, false, &pos);
+    const float mul = __uint_as_float(static_cast<uint32_t>(127 + old - e) << 23);
+    for (int r = 0; r < off; ++r) {
+        uint2* at = reinterpret_cast<uint2*>(row + static_cast<long long>(r) * D) + c;
+        const uint2 v = *at;
+        const uint32_t two[4] = {v.x & 0xffffu, v.x >> 16, v.y & 0xffffu, v.y >> 16};
+        f2 g[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two[k]), __NV_E4M3);
+            const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&hr));
+            g[k] = pair(u.x, u.y);
+        }
+        *at = quant8(g, mul);
     }
-    float f[8];
-    unpack8<BF16>(x, f);
-    norm_rotate<D, BF16>(a, a.q_weight, slot >= 0, slot >= 0 ? table_row(a, pos) : nullptr, lane, f);
-    if (slot >= 0)
-        reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.q_out) + i * a.q_out_stride + static_cast<long long>(h) * D)[c] = pack8<BF16>(f);
+    static_assert(CPR <= 32, "a row within a warp");
+}
+
+// The largest magnitude of a lane's 8 elements (a NaN is passed over), and of a row, on all of its lanes.
+__device__ __forceinline__ float lane_top(const f2 (&f)[4]) {
+    float m = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 v = halves(f[e]);
+        m = fmaxf(m, fmaxf(fabsf(v.x), fabsf(v.y)));
+    }
+    return m;
+}
+template <int D>
+__device__ __forceinline__ float row_top(float m) {
+#pragma unroll
+    for (int o = D / 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    return m;
+}
+
+// The run of token i: the tokens next to it whose slots are in its block (block_log2); its place in the run and the
+// run's length. A run has at most 32 tokens.
+__device__ __forceinline__ void find_run(const NormAppendParams& p, int i, int slot, int lane, int* place, int* length) {
+    const int block = slot >> p.block_log2;
+    *place = 0;
+    *length = 1;
+    int unused;
+    auto next_to = [&](int j) -> bool {  // (a step's tokens stand alone: two uniform reads tell)
+        if (j < 0 || j >= p.a.n) return false;
+        const int s = token_slot(p, j, false, &unused);
+        return s >= 0 && (s >> p.block_log2) == block;
+    };
+    if (!next_to(i - 1) && !next_to(i + 1)) return;
+    auto same = [&](int j) -> bool {
+        if (j < 0 || j >= p.a.n) return false;
+        int pos;
+        const int s = token_slot(p, j, false, &pos);
+        return s >= 0 && (s >> p.block_log2) == block;
+    };
+    const uint32_t before = __ballot_sync(kFull, same(i - 1 - lane)), after = __ballot_sync(kFull, same(i + 1 + lane));
+    *place = __ffs(~before) - 1;  // (a run of 32 has 31 others at most)
+    if (before == ~0u) *place = 31;
+    const int rest = after == ~0u ? 31 : __ffs(~after) - 1;
+    *length = *place + 1 + rest;
+}
+
+constexpr int kItems = 4;  // rows that a lane has in flight
+
+// Batch b of a token's query rows: kItems groups of RPW heads side by side. m: the mix, made here once (`have`).
+template <int D, bool BF16>
+__device__ __forceinline__ void query_rows(const NormAppendParams& p, int i, int pos, int b, int lane, Mix& m, bool& have) {
+    constexpr int CPR = D / 8, RPW = 32 / CPR;
+    const NormRope& a = p.a;
+    const int c = lane & (CPR - 1), seg = lane / CPR;
+    const int h0 = b * kItems * RPW + seg;
+    const uint16_t* src = static_cast<const uint16_t*>(a.q) + i * a.q_stride + h0 * D + 8 * c;
+    uint4 x[kItems];
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+        x[k] = make_uint4(0, 0, 0, 0);
+        if (h0 + k * RPW < a.Hq) x[k] = __ldcs(reinterpret_cast<const uint4*>(src + k * RPW * D));
+    }
+    if (!have) load_mix<D, BF16>(a, a.q_weight, pos, lane, m);
+    have = true;
+    uint16_t* out = static_cast<uint16_t*>(a.q_out) + i * a.q_out_stride + h0 * D + 8 * c;
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+        if (h0 - seg + k * RPW >= a.Hq) break;  // (uniform)
+        f2 f[4];
+        norm_rotate<D, BF16>(a, m, lane, x[k], f);
+        if (h0 + k * RPW < a.Hq) *reinterpret_cast<uint4*>(out + k * RPW * D) = pack8<BF16>(f);
+    }
+}
+
+// Batch b of a token's K (or V) rows, each by itself, to the slot whose row of kv head 0 is `base`.
+template <int D, bool BF16, int POOL, bool IS_V>
+__device__ __forceinline__ void kv_rows(const NormAppendParams& p, int i, int pos, int slot, long long base, int b, int lane, Mix& m, bool& have) {
+    constexpr int CPR = D / 8, RPW = 32 / CPR;
+    const NormRope& a = p.a;
+    const int c = lane & (CPR - 1), seg = lane / CPR;
+    const int h0 = b * kItems * RPW + seg;
+    const uint16_t* src = static_cast<const uint16_t*>(IS_V ? p.v_new : p.k_new) + i * p.src_stride + h0 * D + 8 * c;
+    void* pool = IS_V ? p.v_pool : p.k_pool;
+    uint8_t* exps = IS_V ? p.v_exp : p.k_exp;
+    const int off = slot & ((1 << p.block_log2) - 1);  // rows of the block before the token's
+    uint4 x[kItems];
+    int old[kItems];
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+        const int h = h0 + k * RPW;
+        x[k] = make_uint4(0, 0, 0, 0);
+        old[k] = 0;
+        if (h < p.Hkv) {
+            x[k] = __ldcs(reinterpret_cast<const uint4*>(src + k * RPW * D));
+            // the exponent that the block has, unless the token starts it anew
+            if (POOL == kPoolBlocks && off != 0) old[k] = exps[(base + (static_cast<long long>(h) << p.ps_log2)) >> p.block_log2];
+        }
+    }
+    if (!IS_V) {
+        if (!have) load_mix<D, BF16>(a, a.k_weight, pos, lane, m);
+        have = true;
+    }
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+        const int h = h0 + k * RPW;
+        if (h - seg >= p.Hkv) break;  // (uniform)
+        f2 f[4];
+        if constexpr (!IS_V) norm_rotate<D, BF16>(a, m, lane, x[k], f);
+        else if constexpr (POOL != kPool16) unpack8<BF16>(x[k], f);
+        const long long row = base + (static_cast<long long>(h) << p.ps_log2);
+        if constexpr (POOL == kPool16) {
+            if (h < p.Hkv) {
+                uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(pool) + row * D) + c;
+                if constexpr (IS_V) *to = x[k];
+                else *to = pack8<BF16>(f);
+            }
+        } else if constexpr (POOL == kPoolE4m3) {
+            if (h < p.Hkv) reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + row * D)[c] = quant8(f, IS_V ? p.v_mul : p.k_mul);
+        } else {
+            const int e = block_exponent(p, __float_as_uint(row_top<D>(lane_top(f))), old[k]);
+            if (h >= p.Hkv) continue;
+            reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + row * D)[c] = quant8(f, code_factor(e));
+            const long long head = row >> p.block_log2;
+            if (c == 0 && (e != old[k] || e == 0)) exps[head] = static_cast<uint8_t>(e);  // (0: zeros that start it anew)
+            if (old[k] != 0 && e != old[k]) raise_rows<D>(static_cast<uint8_t*>(pool) + (head << p.block_log2) * D, off, old[k], e, c);
+        }
+    }
+}
+
+// One group of heads of K (or V) over the rows of a run of several tokens from `lead` on: once for the largest magnitude,
+// once for the codes, the second time out of L1 or L2.
+template <int D, bool BF16>
+__device__ __forceinline__ void run_rows(const NormAppendParams& p, int lead, int length, int slot, int group, bool is_v, int lane) {
+    constexpr int CPR = D / 8, RPW = 32 / CPR;
+    const NormRope& a = p.a;
+    const int c = lane & (CPR - 1), seg = lane / CPR;
+    const int h = group * RPW + seg;
+    const bool live = h < p.Hkv;
+    uint8_t* pool = static_cast<uint8_t*>(is_v ? p.v_pool : p.k_pool);
+    uint8_t* exps = is_v ? p.v_exp : p.k_exp;
+    const int off = __ldg(a.loc + lead) & ((1 << p.block_log2) - 1);
+    const long long head = live ? pool_row(p, slot, h) >> p.block_log2 : 0;  // the block's place in the table
+    const int old = live && off != 0 ? exps[head] : 0;
+    auto rows = [&](auto&& each) {
+        for (int r = 0; r < length; ++r) {
+            uint4 raw = make_uint4(0, 0, 0, 0);
+            if (live) raw = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(is_v ? p.v_new : p.k_new) + (lead + r) * p.src_stride + h * D) + c);
+            f2 f[4];
+            if (is_v) {
+                unpack8<BF16>(raw, f);
+            } else {
+                Mix m;
+                load_mix<D, BF16>(a, a.k_weight, a.cos_sin ? __ldg(a.pos + lead + r) : 0, lane, m);
+                norm_rotate<D, BF16>(a, m, lane, raw, f);
+            }
+            each(r, f);
+        }
+    };
+    float top = 0.f;
+    rows([&](int, const f2(&f)[4]) { top = fmaxf(top, lane_top(f)); });
+    const int e = block_exponent(p, __float_as_uint(row_top<D>(top)), old);
+    const float mul = code_factor(e);
+    rows([&](int r, const f2(&f)[4]) {
+        if (live) reinterpret_cast<uint2*>(pool + pool_row(p, __ldg(a.loc + lead + r), h) * D)[c] = quant8(f, mul);
+    });
+    if (!live) return;
+    if (c == 0) exps[head] = static_cast<uint8_t>(e);
+    if (old != 0 && e != old) raise_rows<D>(pool + (head << p.block_log2) * D, off, old, e, c);
 }
 
 }  // namespace
 
-// 16-bit pools, or (FP8) E4M3 pools with one multiplier per tensor: one row a warp segment, the kinds of rows in
-// order: K and V rows of all tokens, then their query rows.
-// Bound by its traffic; small steps by the launch.
-template <int D, bool BF16, bool FP8>
-__global__ void __launch_bounds__(256) norm_append_kernel(const NormAppendParams p) {
-    constexpr int CPR = D / 8, RPW = 32 / CPR;
-    const NormRope& a = p.a;
-    const int lane = threadIdx.x & 31, c = lane & (CPR - 1);
-    const long long gr = (static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * RPW + lane / CPR;
-    const long long kv_rows = static_cast<long long>(a.n) * 2 * p.Hkv;
-    // (kv_rows is made a multiple of a warp's rows, so that a warp has one kind)
-    const long long first_q = (kv_rows + RPW - 1) / RPW * RPW;
-    if (gr - lane / CPR >= first_q) {
-        query_row<D, BF16>(a, gr - first_q, lane, p.ps_log2, p.num_pages, p.status);
-        return;
-    }
-    const bool live = gr < kv_rows;
-    const int i = live ? static_cast<int>(gr / (2 * p.Hkv)) : 0;
-    const int r = live ? static_cast<int>(gr - static_cast<long long>(i) * 2 * p.Hkv) : 0;
-    const bool is_k = r < p.Hkv;
-    const int h = is_k ? r : r - p.Hkv;
-    uint4 x = make_uint4(0, 0, 0, 0);
-    int pos = 0, slot = -1;
-    if (live) {
-        const uint16_t* src = static_cast<const uint16_t*>(is_k ? p.k_new : p.v_new) + i * p.src_stride + static_cast<long long>(h) * D;
-        x = __ldcs(reinterpret_cast<const uint4*>(src) + c);
-        slot = token_slot(a, i, p.ps_log2, p.num_pages, p.status, r == 0 && c == 0, &pos);
-    }
-    float f[8];
-    unpack8<BF16>(x, f);
-    norm_rotate<D, BF16>(a, a.k_weight, is_k && slot >= 0, slot >= 0 ? table_row(a, pos) : nullptr, lane, f);
+// One launch for the K, V and query rows of n tokens. A group is the 32 / (D / 8) heads side by side that fill a warp;
+// a batch is kItems groups of a token's K, V or query rows, all in flight together. `units` warps take a token, one
+// for all of its batches where there are tokens enough, so that its slot, position and angles are read once and the
+// norm's weights are mixed with them once per kind; a warp per batch where there are few.
+// POOL: what K and V become. kPool16, kPoolE4m3 (one multiplier per tensor): each row by itself. kPoolBlocks: the scale
+// of a block has to cover the largest of the call's rows in it. Tokens next to one another in one block are a run. A
+// run of one token (a decode step's) takes the same path, and finds its exponent by shuffles. The warps of a longer run
+// share its groups (run_rows). Nothing is shared between warps. Where a block's exponent grows, its rows before the
+// run are brought to the new one in place.
+// Measured: see launch_norm_append.
+template <int D, bool BF16, int POOL>
+__global__ void __launch_bounds__(256, 3) norm_append_kernel(const NormAppendParams p) {
+    const int lane = threadIdx.x & 31;
+    const unsigned w = blockIdx.x * 8u + (threadIdx.x >> 5);
+    const int i = static_cast<int>(w / p.units), u = static_cast<int>(w - static_cast<unsigned>(i) * p.units);
+    if (i >= p.a.n) return;
+    int pos;
+    const int slot = token_slot(p, i, u == 0 && lane == 0, &pos);
     if (slot < 0) return;
-    const long long page = slot >> p.ps_log2;
-    const long long dst = (((page * p.Hkv + h) << p.ps_log2) + (slot & ((1 << p.ps_log2) - 1))) * D;
-    if constexpr (FP8)
-        reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_k ? p.k_pool : p.v_pool) + dst)[c] = quant8(f, is_k ? p.k_mul : p.v_mul);
-    else
-        reinterpret_cast<uint4*>(static_cast<uint16_t*>(is_k ? p.k_pool : p.v_pool) + dst)[c] = is_k ? pack8<BF16>(f) : x;
+    const long long base = pool_row(p, slot, 0);
+    int first = u;  // the warp's first batch
+    if constexpr (POOL == kPoolBlocks) {
+        int place = 0, length = 1;
+        if (p.block_log2 > 0) find_run(p, i, slot, lane, &place, &length);
+        if (length > 1) {
+            for (int item = place * p.units + u; item < 2 * p.groups; item += length * p.units) {
+                const bool is_v = item >= p.groups;
+                run_rows<D, BF16>(p, i - place, length, slot, is_v ? item - p.groups : item, is_v, lane);
+            }
+            while (first < 2 * p.kv_batches) first += p.units;
+        }
+    }
+    Mix m;
+    bool have = false;
+    int b = first;
+    for (; b < p.kv_batches; b += p.units) kv_rows<D, BF16, POOL, false>(p, i, pos, slot, base, b, lane, m, have);
+    for (; b < 2 * p.kv_batches; b += p.units) kv_rows<D, BF16, POOL, true>(p, i, pos, slot, base, b - p.kv_batches, lane, m, have);
+    have = false;
+    for (; b < p.batches; b += p.units) query_rows<D, BF16>(p, i, pos, b - 2 * p.kv_batches, lane, m, have);
 }
 
-// E4M3 pools with block scales. The scale of a block has to cover the largest of the call's rows in it, so the rows of
-// a block are written by one CTA: a CTA takes the runs (tokens next to one another whose slots are in one block) that
-// begin among its kWindow tokens, of one kv head and of K or V, holds their rows in registers, finds each run's largest
-// magnitude in shared memory, and then quantises. A run has at most `block` <= kWindow tokens, so a CTA's last run ends
-// within 2 kWindow - 1 tokens of its first. The exponent is the smallest with which that magnitude is at most 448 codes,
-// but never below the block's own, unless the run begins at the block's first slot (what the block held is over then);
-// where it grows, the leading rows of the block are brought to it, in place (a power of two: exact but for codes that
-// fall below the format's smallest).
-// The query rows are the CTAs behind (kv_ctas), as in norm_append_kernel.
+// Block scales for tokens that come in runs, a prompt's: a CTA takes kWindow tokens of one group of heads, K or V, a
+// warp four of the tokens, and finds the largest magnitude of each run in shared memory. A run that reaches out of the
+// window has its rows there read too, for that magnitude alone, so that every CTA with rows of a run finds the same
+// exponent for them by itself; the one with the run's first token writes it to the table and raises the rows before the
+// run. (Another may read the table's byte before or after: the larger of the run's exponent and either is the same.)
+// The query rows' CTAs are dealt between the others', which wait more than they move.
+// Bound by the rows' traffic. Measured: see launch_norm_append.
 constexpr int kWindow = 32;
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(256) block_append_kernel(const BlockAppendParams p) {
-    constexpr int CPR = D / 8, RPW = 32 / CPR, RPP = 8 * RPW;      // rows of a warp, and of a pass of the CTA
-    constexpr int PASSES = 2 * kWindow / RPP;
+__global__ void __launch_bounds__(256, 3) block_window_kernel(const NormAppendParams p, unsigned kv_ctas, unsigned ctas) {
+    constexpr int CPR = D / 8, RPW = 32 / CPR, ROWS = kWindow / 8;  // tokens of a warp
     const NormRope& a = p.a;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = lane & (CPR - 1);
-    if (blockIdx.x >= p.kv_ctas) {
-        const long long r = (static_cast<long long>(blockIdx.x - p.kv_ctas) * 8 + warp) * RPW + lane / CPR;
-        query_row<D, BF16>(a, r, lane, p.ps_log2, p.num_pages, p.status);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = lane & (CPR - 1), seg = lane / CPR;
+    // CTA x is the y-th for K and V where the running share of those steps up at x
+    const unsigned y = static_cast<unsigned>(static_cast<unsigned long long>(blockIdx.x) * kv_ctas / ctas);
+    const bool kv = static_cast<unsigned>(static_cast<unsigned long long>(blockIdx.x + 1) * kv_ctas / ctas) != y;
+    if (!kv) {
+        const int i = static_cast<int>((blockIdx.x - y) * 8u + warp);  // a warp takes a token's query rows
+        if (i >= a.n) return;
+        int pos;
+        if (token_slot(p, i, false, &pos) < 0) return;
+        Mix m;
+        bool have = false;
+        for (int b = 0; b < p.batches - 2 * p.kv_batches; ++b) query_rows<D, BF16>(p, i, pos, b, lane, m, have);
         return;
     }
-    __shared__ int s_slot[2 * kWindow], s_pos[2 * kWindow];
-    __shared__ uint32_t s_lead[2];              // tokens at which a run begins
-    __shared__ uint32_t s_top[kWindow];         // a run's largest magnitude, at its first token
-    __shared__ int s_new[kWindow], s_old[kWindow];
-    const int per = 2 * p.Hkv;
-    const int w = static_cast<int>(blockIdx.x / per), kind = static_cast<int>(blockIdx.x - static_cast<unsigned>(w) * per);
-    const bool is_k = kind < p.Hkv;
-    const int h = is_k ? kind : kind - p.Hkv;
-    const long long i0 = static_cast<long long>(w) * kWindow;
-    uint8_t* pool = is_k ? p.k_pool : p.v_pool;
-    uint8_t* exps = is_k ? p.k_exp : p.v_exp;
-    const int block = 1 << p.block_log2;
-    auto pool_row = [&](int slot) -> long long {
-        return ((static_cast<long long>(slot >> p.ps_log2) * p.Hkv + h) << p.ps_log2) + (slot & ((1 << p.ps_log2) - 1));
-    };
-
-    int old = 0;  // of the run that begins at token tid
-    if (tid < 2 * kWindow) {
-        const long long i = i0 + tid;
-        int pos = 0, slot = -1, before = -1;
-        if (i < a.n) slot = token_slot(a, static_cast<int>(i), p.ps_log2, p.num_pages, p.status, kind == 0 && tid < kWindow, &pos);
-        if (i < a.n && i > 0) {
-            int q;
-            before = token_slot(a, static_cast<int>(i - 1), p.ps_log2, p.num_pages, p.status, false, &q);
-        }
+    __shared__ int s_slot[3 * kWindow], s_pos[3 * kWindow];  // tokens i0 - kWindow .. i0 + 2 kWindow - 1
+    __shared__ uint32_t s_lead[3];                           // tokens at which a run begins
+    __shared__ uint32_t s_top[2 * kWindow][RPW];             // a run's largest magnitude, at its first token
+    const int items = 2 * p.groups;
+    const int window = static_cast<int>(y / items), item = static_cast<int>(y - static_cast<unsigned>(window) * items);
+    const bool is_v = item >= p.groups;
+    const int h = (is_v ? item - p.groups : item) * RPW + seg;
+    const bool live = h < p.Hkv;
+    const int i0 = window * kWindow;
+    if (tid < 3 * kWindow) {
+        const int i = i0 - kWindow + tid;
+        int pos = 0, slot = -1, before = -1, unused;
+        if (i >= 0 && i < a.n) slot = token_slot(p, i, item == 0 && warp == 1, &pos);
+        if (i >= 1 && i < a.n) before = token_slot(p, i - 1, false, &unused);
         s_slot[tid] = slot;
         s_pos[tid] = pos;
-        // -1 >> n is -1: a token that is skipped is no run's, and the next one begins a run
-        const bool lead = slot >= 0 && (slot >> p.block_log2) != (before >> p.block_log2);
-        const uint32_t m = __ballot_sync(kFull, lead);
-        if (lane == 0) s_lead[warp] = m;
-        if (tid < kWindow) {
-            s_top[tid] = 0u;
-            if (lead && (slot & (block - 1)) != 0) old = exps[pool_row(slot) >> p.block_log2];
-        }
+        // (-1 >> n is -1: a token that is skipped is no run's)
+        const uint32_t b = __ballot_sync(kFull, slot >= 0 && (slot >> p.block_log2) != (before >> p.block_log2));
+        if (lane == 0) s_lead[warp] = b;
     }
+    for (int x = tid; x < 2 * kWindow * RPW; x += 256) s_top[x / RPW][x % RPW] = 0u;
     __syncthreads();
-    const uint32_t lead0 = s_lead[0], lead1 = s_lead[1];
-    // the run that token t belongs to, by its first token; -1: none, or one that another CTA writes
-    auto run_of = [&](int t) -> int {
+    // the first token of token t's run (both counted from i0 - kWindow): a run's first is at most 31 before it
+    auto first_of = [&](int t) -> int {
         if (s_slot[t] < 0) return -1;
-        if (t < kWindow) return 31 - __clz(lead0 & (~0u >> (31 - t)));
-        return (lead1 & (~0u >> (63 - t))) ? -1 : 31 - __clz(lead0);
+        const int w = t >> 5;
+        const uint32_t here = s_lead[w] & (~0u >> (31 - (t & 31)));
+        if (here) return 32 * w + 31 - __clz(here);
+        const uint32_t b = w ? s_lead[w - 1] : 0u;
+        return b ? 32 * (w - 1) + 31 - __clz(b) : -1;
     };
-
-    float f[PASSES][8];
-    int run[PASSES];
+    uint8_t* pool = static_cast<uint8_t*>(is_v ? p.v_pool : p.k_pool);
+    uint8_t* exps = is_v ? p.v_exp : p.k_exp;
+    const int run_in = first_of(kWindow), run_out = first_of(2 * kWindow - 1);  // of the window's first and last token
+    f2 f[ROWS][4];
+    int run[ROWS];
+    // which: 0 the tokens before the window, 2 behind it (rows of its first and its last run), 1 its own, last, to be kept
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+        const int which = pass == 2 ? 1 : 2 * pass;
+        uint4 x[ROWS];
+        bool some = false;
 #pragma unroll
-    for (int s = 0; s < PASSES; ++s) {
-        const int t = s * RPP + warp * RPW + lane / CPR;
-        run[s] = run_of(t);
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (run[s] >= 0) {
-            const uint16_t* src = static_cast<const uint16_t*>(is_k ? p.k_new : p.v_new) + (i0 + t) * p.src_stride + static_cast<long long>(h) * D;
-            x = __ldcs(reinterpret_cast<const uint4*>(src) + c);
-        }
-        unpack8<BF16>(x, f[s]);
-    }
-#pragma unroll
-    for (int s = 0; s < PASSES; ++s) {
-        const int t = s * RPP + warp * RPW + lane / CPR;
-        if (!__any_sync(kFull, run[s] >= 0)) continue;
-        if (is_k) norm_rotate<D, BF16>(a, a.k_weight, run[s] >= 0, run[s] >= 0 ? table_row(a, s_pos[t]) : nullptr, lane, f[s]);
-        float m = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[s][e]));  // (a NaN is passed over)
-#pragma unroll
-        for (int o = CPR / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-        if (c == 0 && run[s] >= 0) atomicMax(&s_top[run[s]], __float_as_uint(m));  // (not negative: ordered as integers)
-    }
-    __syncthreads();
-    if (tid < kWindow) {
-        int e = 0;
-        if (lead0 >> tid & 1) {
-            const uint32_t top = s_top[tid];
-            // 448 = 1.75 * 2^8
-            if (top) e = min(max(static_cast<int>(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u), p.exp_lo), p.exp_hi);
-            e = max(e, old);
-            exps[pool_row(s_slot[tid]) >> p.block_log2] = static_cast<uint8_t>(e);
-        }
-        s_new[tid] = e;
-        s_old[tid] = old;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int s = 0; s < PASSES; ++s) {
-        if (run[s] < 0) continue;
-        const int t = s * RPP + warp * RPW + lane / CPR;
-        const int e = s_new[run[s]];
-        const float mul = e == 0 ? 0.f : __uint_as_float(static_cast<uint32_t>(254 - e) << 23);  // 2^(127 - E)
-        reinterpret_cast<uint2*>(pool + pool_row(s_slot[t]) * D)[c] = quant8(f[s], mul);
-    }
-    // leading rows of blocks whose scale grew
-    for (int t = warp; t < kWindow; t += 8) {
-        if (!(lead0 >> t & 1) || s_old[t] == 0 || s_new[t] == s_old[t]) continue;  // (uniform in the warp)
-        const int slot = s_slot[t], off = slot & (block - 1);
-        const float mul = __uint_as_float(static_cast<uint32_t>(127 + s_old[t] - s_new[t]) << 23);
-        uint2* row = reinterpret_cast<uint2*>(pool + (pool_row(slot) - off) * D);
-        for (int x = lane; x < off * CPR; x += 32) {
-            const uint2 v = row[x];
-            const uint32_t two[4] = {v.x & 0xffffu, v.x >> 16, v.y & 0xffffu, v.y >> 16};
-            float g[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two[e]), __NV_E4M3);
-                const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&hr));
-                g[2 * e] = u.x;
-                g[2 * e + 1] = u.y;
+        for (int k = 0; k < ROWS; ++k) {
+            const int t = which * kWindow + warp * ROWS + k;
+            int r = first_of(t);
+            if (which != 1 && (r != (which == 0 ? run_in : run_out) || r < 0)) r = -1;
+            if (which == 2 && r >= 2 * kWindow) r = -1;
+            run[k] = r;  // (uniform)
+            some |= r >= 0;
+            x[k] = make_uint4(0, 0, 0, 0);
+            if (r >= 0 && live) {
+                const uint16_t* src = static_cast<const uint16_t*>(is_v ? p.v_new : p.k_new) + static_cast<long long>(i0 - kWindow + t) * p.src_stride + h * D;
+                x[k] = __ldg(reinterpret_cast<const uint4*>(src) + c);
             }
-            row[x] = quant8(g, mul);
+        }
+        if (!some) continue;
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k) {
+            if (run[k] < 0) continue;  // (uniform)
+            if (is_v) {
+                unpack8<BF16>(x[k], f[k]);
+            } else {
+                Mix m;
+                load_mix<D, BF16>(a, a.k_weight, s_pos[which * kWindow + warp * ROWS + k], lane, m);
+                norm_rotate<D, BF16>(a, m, lane, x[k], f[k]);
+            }
+            const float top = row_top<D>(lane_top(f[k]));
+            if (c == 0) atomicMax(&s_top[run[k]][seg], __float_as_uint(top));  // (not negative: ordered as integers)
+        }
+    }
+    __syncthreads();
+    const unsigned mine = __ballot_sync(kFull, live);
+    if (!live) return;
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+        if (run[k] < 0) continue;  // (uniform)
+        const int t = kWindow + warp * ROWS + k, slot = s_slot[t];
+        const int off = s_slot[run[k]] & ((1 << p.block_log2) - 1);  // of the run's first row in the block
+        const long long row = pool_row(p, slot, h), head = row >> p.block_log2;
+        const int old = off != 0 ? *static_cast<volatile const uint8_t*>(exps + head) : 0;
+        const int e = block_exponent(p, s_top[run[k]][seg], old);
+        reinterpret_cast<uint2*>(pool + row * D)[c] = quant8(f[k], code_factor(e));
+        if (run[k] == t) {  // the run's first token
+            __syncwarp(mine);  // every lane has read the old byte
+            if (c == 0) exps[head] = static_cast<uint8_t>(e);
+            if (old != 0 && e != old) raise_rows<D>(pool + (head << p.block_log2) * D, off, old, e, c);
         }
     }
 }
@@ -351,45 +573,40 @@ __global__ void __launch_bounds__(256) block_append_kernel(const BlockAppendPara
 namespace {
 
 template <int D, bool BF16>
-cudaError_t launch_norm_t(const NormAppendParams& p, bool fp8, cudaStream_t stream) {
+cudaError_t launch_norm_t(NormAppendParams p, PoolKind pools, bool runs, int num_sms, cudaStream_t stream) {
     constexpr int RPW = 32 / (D / 8);
-    const long long kv = (static_cast<long long>(p.a.n) * 2 * p.Hkv + RPW - 1) / RPW;  // warps
-    const long long q = p.a.q ? (static_cast<long long>(p.a.n) * p.a.Hq + RPW - 1) / RPW : 0;
-    const unsigned blocks = static_cast<unsigned>((kv + q + 7) / 8);
-    if (fp8) norm_append_kernel<D, BF16, true><<<blocks, 256, 0, stream>>>(p);
-    else norm_append_kernel<D, BF16, false><<<blocks, 256, 0, stream>>>(p);
-    return cudaGetLastError();
-}
-
-template <int D, bool BF16>
-cudaError_t launch_block_t(BlockAppendParams p, cudaStream_t stream) {
-    constexpr int RPW = 32 / (D / 8);
-    const long long windows = (p.a.n + kWindow - 1) / kWindow;
-    const long long kv = windows * 2 * p.Hkv;
-    const long long q = p.a.q ? (static_cast<long long>(p.a.n) * p.a.Hq + 8 * RPW - 1) / (8 * RPW) : 0;
-    if (kv + q > INT32_MAX) return cudaErrorInvalidValue;
-    p.kv_ctas = static_cast<unsigned>(kv);
-    block_append_kernel<D, BF16><<<static_cast<unsigned>(kv + q), 256, 0, stream>>>(p);
+    p.groups = (p.Hkv + RPW - 1) / RPW;
+    p.kv_batches = (p.groups + kItems - 1) / kItems;
+    p.batches = 2 * p.kv_batches + (p.a.q ? (p.a.Hq + RPW * kItems - 1) / (RPW * kItems) : 0);
+    if (pools == kPoolBlocks && p.block_log2 > 0 && runs) {
+        const long long kv = static_cast<long long>((p.a.n + kWindow - 1) / kWindow) * 2 * p.groups;
+        const long long q = p.a.q ? (p.a.n + 7) / 8 : 0;
+        if (kv + q > INT32_MAX) return cudaErrorInvalidValue;
+        block_window_kernel<D, BF16><<<static_cast<unsigned>(kv + q), 256, 0, stream>>>(p, static_cast<unsigned>(kv), static_cast<unsigned>(kv + q));
+        return cudaGetLastError();
+    }
+    // warps of a token: as many as keep the SMs' resident warps (24 of each) busy
+    p.units = std::max(1, std::min(p.batches, 24 * num_sms / p.a.n));
+    const long long warps = static_cast<long long>(p.a.n) * p.units;
+    if (warps > INT32_MAX) return cudaErrorInvalidValue;
+    const unsigned blocks = static_cast<unsigned>((warps + 7) / 8);
+    switch (pools) {
+        case kPool16: norm_append_kernel<D, BF16, kPool16><<<blocks, 256, 0, stream>>>(p); break;
+        case kPoolE4m3: norm_append_kernel<D, BF16, kPoolE4m3><<<blocks, 256, 0, stream>>>(p); break;
+        case kPoolBlocks: norm_append_kernel<D, BF16, kPoolBlocks><<<blocks, 256, 0, stream>>>(p); break;
+    }
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_norm_append(int head_dim, bool bf16, bool fp8, const NormAppendParams& p, cudaStream_t stream) {
+cudaError_t launch_norm_append(int head_dim, bool bf16, PoolKind pools, bool runs, const NormAppendParams& p, int num_sms,
+                               cudaStream_t stream) {
+    static_assert(BSP_MAX_SCALE_BLOCK <= 32, "a run within a warp's look around");
     switch (head_dim) {
-        case 64: return bf16 ? launch_norm_t<64, true>(p, fp8, stream) : launch_norm_t<64, false>(p, fp8, stream);
-        case 128: return bf16 ? launch_norm_t<128, true>(p, fp8, stream) : launch_norm_t<128, false>(p, fp8, stream);
-        case 256: return bf16 ? launch_norm_t<256, true>(p, fp8, stream) : launch_norm_t<256, false>(p, fp8, stream);
-        default: return cudaErrorInvalidValue;
-    }
-}
-
-cudaError_t launch_block_append(int head_dim, bool bf16, const BlockAppendParams& p, cudaStream_t stream) {
-    static_assert(kWindow >= BSP_MAX_SCALE_BLOCK, "a run ends within a second window");
-    switch (head_dim) {
-        case 64: return bf16 ? launch_block_t<64, true>(p, stream) : launch_block_t<64, false>(p, stream);
-        case 128: return bf16 ? launch_block_t<128, true>(p, stream) : launch_block_t<128, false>(p, stream);
-        case 256: return bf16 ? launch_block_t<256, true>(p, stream) : launch_block_t<256, false>(p, stream);
+        case 64: return bf16 ? launch_norm_t<64, true>(p, pools, runs, num_sms, stream) : launch_norm_t<64, false>(p, pools, runs, num_sms, stream);
+        case 128: return bf16 ? launch_norm_t<128, true>(p, pools, runs, num_sms, stream) : launch_norm_t<128, false>(p, pools, runs, num_sms, stream);
+        case 256: return bf16 ? launch_norm_t<256, true>(p, pools, runs, num_sms, stream) : launch_norm_t<256, false>(p, pools, runs, num_sms, stream);
         default: return cudaErrorInvalidValue;
     }
 }

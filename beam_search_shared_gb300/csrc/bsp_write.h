@@ -6,6 +6,7 @@
 #include <cstdint>
 
 #include "../../include/bsp.h"
+#include "bsp_internal.h"
 
 namespace bsp {
 
@@ -68,27 +69,19 @@ struct NormAppendParams {
     int64_t src_stride;
     void* k_pool;
     void* v_pool;
-    int32_t* status;
-    int Hkv, ps_log2, num_pages;
-    float k_mul, v_mul;        // E4M3 pools
-};
-// fp8: the pools are E4M3 bytes with one multiplier per tensor, else the q dtype
-cudaError_t launch_norm_append(int head_dim, bool bf16, bool fp8, const NormAppendParams& p, cudaStream_t stream);
-struct BlockAppendParams {
-    NormRope a;
-    const void* k_new;
-    const void* v_new;
-    int64_t src_stride;
-    uint8_t* k_pool;
-    uint8_t* v_pool;
-    uint8_t* k_exp;            // exponent bytes of the blocks
+    uint8_t* k_exp;            // block scales: exponent bytes, and the range that a write chooses from
     uint8_t* v_exp;
     int32_t* status;
-    int Hkv, ps_log2, num_pages, block_log2;
-    int exp_lo, exp_hi;        // exponent bytes that a write chooses from
-    unsigned kv_ctas;          // set by launch_block_append
+    int Hkv, ps_log2, num_pages;
+    int block_log2, exp_lo, exp_hi;
+    float k_mul, v_mul;        // E4M3 pools with one multiplier per tensor
+    // set by launch_norm_append: groups of heads that fill a warp, batches of K (and of V) of a token, all of its batches,
+    // warps of a token
+    int groups, kv_batches, batches, units;
 };
-cudaError_t launch_block_append(int head_dim, bool bf16, const BlockAppendParams& p, cudaStream_t stream);
+// runs: the tokens are prompts', many of a block next to one another (the kernels differ in speed only)
+cudaError_t launch_norm_append(int head_dim, bool bf16, PoolKind pools, bool runs, const NormAppendParams& p, int num_sms,
+                               cudaStream_t stream);
 cudaError_t launch_rope_scaled(int max_pos, int rot, double base, const bsp_rope_scaling& sc, float* cos_sin,
                                cudaStream_t stream);
 

@@ -40,7 +40,8 @@ class Tokens:
         self.geo = bsp.geometry(Hq, Hkv, D, ps, pages, dtype, kv_dtype)
         self.ws = bsp.Workspace(self.geo, 1, max(n, 1), 1)
         if prefill:
-            self.plan = bsp.plan_prefill(self.geo, 1, [0], [n], np.arange(-(-n // ps) or 1)[None], True, bsp.Workspace(self.geo, 1, n, -(-n // ps) or 1))
+            self.ws = bsp.Workspace(self.geo, 1, n, -(-n // ps))
+            self.plan = bsp.plan_prefill(self.geo, 1, [0], [n], np.arange(-(-n // ps))[None], True, self.ws)
         else:
             self.plan = self.ws.plan(self.geo, 1, max(n, 1), [0], [0], np.zeros((1, 1), np.int32))
         width = (Hq + 2 * Hkv) * D
@@ -240,9 +241,10 @@ def prompt_slots(t, starts, rs):
     (CASES[5], 128, 32, 300, (17, 100)),
     (CASES[6], 32, 16, 33, (0,)),
 ], ids=lambda x: str(x) if isinstance(x, (int, tuple)) and not (isinstance(x, tuple) and isinstance(x[0], str)) else "")
-def test_block_append_of_prompts(case, ps, block, n, starts):
+@pytest.mark.parametrize("prefill", [False, True])
+def test_block_append_of_prompts(case, ps, block, n, starts, prefill):
     dtype, Hq, Hkv, D = case[:4]
-    t = Tokens(dtype, Hq, Hkv, D, ps=ps, pages=max(6, 4 * n // ps + 8), n=n, seed=n)
+    t = Tokens(dtype, Hq, Hkv, D, ps=ps, pages=max(6, 4 * n // ps + 8), n=n, seed=n, prefill=prefill)
     prompt_slots(t, starts, np.random.RandomState(n))
     norm, rope, want = setup(t, case)
     q_out, flags = run_blocks(t, block, norm, rope, want, seed=n)
@@ -252,9 +254,10 @@ def test_block_append_of_prompts(case, ps, block, n, starts):
 
 
 @pytest.mark.parametrize("dtype,D,block,spread", [("bf16", 128, 8, 3.0), ("fp16", 64, 16, 1.0), ("bf16", 256, 2, 2.0), ("fp16", 128, 1, 1.0)])
-def test_block_append_of_single_tokens(dtype, D, block, spread):
+@pytest.mark.parametrize("prefill", [False, True])
+def test_block_append_of_single_tokens(dtype, D, block, spread, prefill):
     """A token per beam into blocks that hold rows: scales that grow, and that stay."""
-    t = Tokens(dtype, 4, 2, D, ps=16, pages=90, n=83, seed=5, spread=spread)
+    t = Tokens(dtype, 4, 2, D, ps=16, pages=90, n=83, seed=5, spread=spread, prefill=prefill)
     rs = np.random.RandomState(6)
     t.slots = (rs.permutation(90)[:83] * 16 + rs.randint(0, 16, 83)).astype(np.int32)
     _, flags = run_blocks(t, block, seed=7)
@@ -262,10 +265,11 @@ def test_block_append_of_single_tokens(dtype, D, block, spread):
     run_blocks(t, block, seed=8, empty=True)
 
 
-def test_block_append_extremes():
+@pytest.mark.parametrize("prefill", [False, True])
+def test_block_append_extremes(prefill):
     """Zeros, infinities, NaN, the largest and smallest values, and skipped tokens that part a run."""
     for dtype in ("bf16", "fp16"):
-        t = Tokens(dtype, 2, 1, 64, ps=32, pages=8, n=40, seed=9)
+        t = Tokens(dtype, 2, 1, 64, ps=32, pages=8, n=40, seed=9, prefill=prefill)
         t.slots = np.arange(35, 75).astype(np.int32)
         x = t.x.view(t.n, 4, 64)
         x[0:3] = 0
