@@ -713,8 +713,18 @@ def _table(name: str, t: torch.Tensor, dtype, shape, exact_last: bool = True):
     returns the row stride in elements."""
     if t.dtype is not dtype:
         raise ValueError(f"{name} is {t.dtype}, not {dtype}")
-    if t.shape == shape and t.is_contiguous():  # the usual case
-        return shape[-1]
+    s = t.shape
+    if t.is_contiguous():  # the usual case
+        if s == shape:
+            return s[-1]
+        n = len(s)
+        if n == len(shape):
+            for i in range(n):
+                w = shape[i]
+                if w is not None and s[i] != w and (exact_last or i < n - 1 or s[i] < w):
+                    break
+            else:
+                return s[-1]
     n = t.dim()
     if n != len(shape) or any(w is not None and (t.shape[i] != w if exact_last or i < n - 1 else t.shape[i] < w)
                               for i, w in enumerate(shape)):

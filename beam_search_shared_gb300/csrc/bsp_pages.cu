@@ -97,11 +97,46 @@ __device__ __forceinline__ int fresh_pages(const ForkParams& p, int b, int* full
     return ((P + T + (1 << p.ps_log2) - 1) >> p.ps_log2) - *full;
 }
 
-// Fork, first step: one cluster. The rows' needs are summed in order, row i = b * num_forks + j, into base[i] (-1: a row
-// without a beam, or one for which the free pages do not suffice); the free pages, lowest first, are listed as far as
-// they are needed, and taken.
+// The entries of a forked row's table and its fresh pages' counts, by `lanes` threads.
+__device__ __forceinline__ void fork_row_table(const ForkParams& p, int i, int lane, int lanes) {
+    const int b = i / p.num_forks;
+    int full;
+    const int need = fresh_pages(p, b, &full);
+    if (full + need > p.out_cols) {  // a replayed plan that outgrew the table
+        if (lane == 0) atomicOr(p.status, BSP_DEVFLAG_GRAPH);
+        return;
+    }
+    const int32_t* prompt = p.pages + __ldg(p.req + static_cast<long long>(b) * kReqFields + kReqPageOff);
+    const int base = p.base[i];
+    int32_t* out = p.pages_out + static_cast<long long>(i) * p.out_stride;
+    for (int c = lane; c < full + need; c += lanes) {
+        int page = -1;
+        if (base >= 0) {
+            page = c < full ? __ldg(prompt + c) : p.fresh[base + c - full];
+            if (c >= full) p.refs_out[page] = 1;
+        }
+        out[c] = page;
+    }
+}
+// The references that a request's served forks add to its full prompt pages, by a warp.
+__device__ __forceinline__ void fork_request_refs(const ForkParams& p, int b, int lane) {
+    int full;
+    if (fresh_pages(p, b, &full) + full > p.out_cols) return;
+    const int32_t* prompt = p.pages + __ldg(p.req + static_cast<long long>(b) * kReqFields + kReqPageOff);
+    int n = 0;
+    for (int j = lane; j < p.num_forks; j += 32) n += p.base[b * p.num_forks + j] >= 0;
+    n = __reduce_add_sync(kFull, n);
+    for (int c = lane; n > 0 && c < full; c += 32) {
+        const int page = __ldg(prompt + c);
+        if (static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages)) atomicAdd(p.refs_out + page, n);
+    }
+}
+
+// Fork: one cluster. The rows' needs are summed in order, row i = b * num_forks + j, into base[i] (-1: a row without a
+// beam, or one for which the free pages do not suffice); the free pages, lowest first, are listed as far as they are
+// needed. Where the rows are few (`whole`) the cluster goes on to their tables, else fork_tables_kernel does.
 // A few passes over one int per page and per row: bound by their latency (figures at launch_fork_tables).
-__global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads) fork_scan_kernel(const ForkParams p) {
+__global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads) fork_scan_kernel(const ForkParams p, bool whole) {
     __shared__ int s_warp[33], s_free, s_need;
     cg::cluster_group cl = cg::this_cluster();
     const int rank = static_cast<int>(cl.block_rank()), tid = threadIdx.x;
@@ -133,7 +168,6 @@ __global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads
     int available, wanted;
     int at = cluster_sum(cl, &s_free, &available);
     int row_at = cluster_sum(cl, &s_need, &wanted);
-    cl.sync();  // (no CTA leaves while another reads its sums)
     for (int i0 = rlo; i0 < rhi; i0 += kScanThreads) {
         const int i = i0 + tid;
         int n = 0, total;
@@ -151,7 +185,7 @@ __global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads
         }
         row_at += total;
     }
-    const int most = min(wanted, available);  // (pages listed beyond the last served row's stay free: second step)
+    const int most = min(wanted, available);  // (pages listed beyond the last served row's stay free)
     for (int i0 = lo; i0 < hi && at < most; i0 += 4 * kScanThreads) {
         const int i = i0 + 4 * tid;
         int n = 0, total;
@@ -171,43 +205,23 @@ __global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads
         }
         at += total;
     }
+    cl.sync();  // base, fresh and the counts are complete, and no CTA leaves while another reads its sums
+    if (!whole) return;
+    const int warps = kScanCtas * kScanThreads / 32, lane = tid & 31;
+    for (int x = rank * (kScanThreads / 32) + (tid >> 5); x < p.rows + p.batch; x += warps) {
+        if (x < p.rows) fork_row_table(p, x, lane, 32);
+        else fork_request_refs(p, x - p.rows, lane);
+    }
 }
 
-// Fork, second step: a warp per row writes its table and takes its fresh pages; a warp per request counts its forks
-// and adds them to the references of the full prompt pages.
+// A warp per row writes its table and takes its fresh pages; a warp per request counts its forks and adds them to the
+// references of the full prompt pages.
 __global__ void __launch_bounds__(256) fork_tables_kernel(const ForkParams p) {
-    if (!plan_matches(p.plan_hdr, p.shape)) return;  // (flagged by the first step)
+    if (!plan_matches(p.plan_hdr, p.shape)) return;  // (flagged by the scan)
     const int lane = threadIdx.x & 31;
-    const int i = static_cast<int>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (i >= p.rows + p.batch) return;
-    const int b = i < p.rows ? i / p.num_forks : i - p.rows;
-    int full;
-    const int need = fresh_pages(p, b, &full);
-    const int32_t* prompt = p.pages + __ldg(p.req + static_cast<long long>(b) * kReqFields + kReqPageOff);
-    if (i < p.rows) {
-        const int base = p.base[i];
-        int32_t* out = p.pages_out + static_cast<long long>(i) * p.out_stride;
-        if (full + need > p.out_cols) {  // a replayed plan that outgrew the table
-            if (lane == 0) atomicOr(p.status, BSP_DEVFLAG_GRAPH);
-            return;
-        }
-        for (int c = lane; c < full + need; c += 32) {
-            int page = -1;
-            if (base >= 0) {
-                page = c < full ? __ldg(prompt + c) : p.fresh[base + c - full];
-                if (c >= full) p.refs_out[page] = 1;
-            }
-            out[c] = page;
-        }
-    } else if (full + need <= p.out_cols) {
-        int n = 0;
-        for (int j = lane; j < p.num_forks; j += 32) n += p.base[b * p.num_forks + j] >= 0;
-        n = __reduce_add_sync(kFull, n);
-        for (int c = lane; n > 0 && c < full; c += 32) {
-            const int page = __ldg(prompt + c);
-            if (static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages)) atomicAdd(p.refs_out + page, n);
-        }
-    }
+    const int x = static_cast<int>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (x < p.rows) fork_row_table(p, x, lane, 32);
+    else if (x < p.rows + p.batch) fork_request_refs(p, x - p.rows, lane);
 }
 
 // 8 E4M3 codes times a power of two, rounded to the nearest code
@@ -339,26 +353,46 @@ __global__ void __launch_bounds__(256) fork_rows_kernel(const ForkRowsParams p) 
     }
 }
 
-// One reference less for every page listed. A page whose count would fall below zero keeps zero and is flagged.
-__global__ void __launch_bounds__(256) free_pages_kernel(const FreeParams p) {
-    const long long total = static_cast<long long>(p.rows) * p.cols;
-    for (long long x = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; x < total; x += static_cast<long long>(gridDim.x) * 256) {
-        const long long r = x / p.cols;
-        const int page = __ldg(p.tables + r * p.stride + (x - r * p.cols));
-        if (page == -1) continue;
-        if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) {
-            atomicOr(p.status, BSP_DEVFLAG_PAGE_INDEX);
-        } else if (atomicSub(p.refs_out + page, 1) <= 0) {
-            atomicAdd(p.refs_out + page, 1);
-            atomicOr(p.status, BSP_DEVFLAG_PAGE_INDEX);
-        }
+// One reference less for the page of entry x of the tables. A page whose count would fall below zero keeps zero and is
+// flagged.
+__device__ __forceinline__ void free_entry(const FreeParams& p, long long x) {
+    const long long r = x / p.cols;
+    const int page = __ldg(p.tables + r * p.stride + (x - r * p.cols));
+    if (page == -1) return;
+    if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.num_pages)) {
+        atomicOr(p.status, BSP_DEVFLAG_PAGE_INDEX);
+    } else if (atomicSub(p.refs_out + page, 1) <= 0) {
+        atomicAdd(p.refs_out + page, 1);
+        atomicOr(p.status, BSP_DEVFLAG_PAGE_INDEX);
     }
 }
+__global__ void __launch_bounds__(256) free_pages_kernel(const FreeParams p) {
+    const long long total = static_cast<long long>(p.rows) * p.cols;
+    for (long long x = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; x < total; x += static_cast<long long>(gridDim.x) * 256)
+        free_entry(p, x);
+}
+// The same for few pages and entries, with the copy of the counts before it: one cluster.
+__global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads) free_few_kernel(const FreeParams p, const int32_t* refs_in) {
+    const int at = static_cast<int>(blockIdx.x * kScanThreads + threadIdx.x);
+    for (int i = at; i < p.num_pages; i += kScanCtas * kScanThreads) p.refs_out[i] = refs_in[i];
+    cg::this_cluster().sync();
+    const int total = p.rows * p.cols;
+    for (int x = at; x < total; x += kScanCtas * kScanThreads) free_entry(p, x);
+}
 
-// Compaction, first step: one cluster. L pages are live; the i-th live page with an id of at least L goes to the i-th
+// The new id of entry x of the tables. -1 and entries outside the pool are copied as they are.
+__device__ __forceinline__ void remap_entry(const CompactParams& p, long long x) {
+    const long long r = x / p.cols, c = x - r * p.cols;
+    const int page = p.tables_in[r * p.stride + c];
+    const bool inside = static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages);
+    if (!inside && page != -1) atomicOr(p.status, BSP_DEVFLAG_PAGE_INDEX);
+    p.tables_out[r * p.stride + c] = inside ? p.remap[page] : page;
+}
+
+// Compaction: one cluster, which goes on to the tables where they are short (`whole`). L pages are live; the i-th live page with an id of at least L goes to the i-th
 // free page below L. With before(p) the live pages below p, a free page p < L is hole p - before(p), and a live page
 // p >= L is mover before(p) - before(L): one running count ranks both.
-__global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads) compact_scan_kernel(const CompactParams p) {
+__global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads) compact_scan_kernel(const CompactParams p, bool whole) {
     __shared__ int s_warp[33], s_live, s_front;
     cg::cluster_group cl = cg::this_cluster();
     const int rank = static_cast<int>(cl.block_rank()), tid = threadIdx.x;
@@ -415,18 +449,16 @@ __global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads
         p.refs_out[to] = p.refs_in[from];
         p.refs_out[from] = 0;
     }
+    if (!whole) return;  // (uniform)
+    cl.sync();  // remap is complete
+    for (int x = rank * kScanThreads + tid; x < p.rows * p.cols; x += kScanCtas * kScanThreads) remap_entry(p, x);
 }
 
-// Compaction, second step: the tables' entries. -1 and entries outside the pool are copied as they are.
+// The entries of longer tables.
 __global__ void __launch_bounds__(256) remap_tables_kernel(const CompactParams p) {
     const long long total = static_cast<long long>(p.rows) * p.cols;
-    for (long long x = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; x < total; x += static_cast<long long>(gridDim.x) * 256) {
-        const long long r = x / p.cols, c = x - r * p.cols;
-        const int page = p.tables_in[r * p.stride + c];
-        const bool inside = static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages);
-        if (!inside && page != -1) atomicOr(p.status, BSP_DEVFLAG_PAGE_INDEX);
-        p.tables_out[r * p.stride + c] = inside ? p.remap[page] : page;
-    }
+    for (long long x = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; x < total; x += static_cast<long long>(gridDim.x) * 256)
+        remap_entry(p, x);
 }
 
 // Pages copied pair by pair, (from, to), K and V and their exponents. CTAs share the 16-byte vectors of all pages in
@@ -477,9 +509,11 @@ unsigned grid_for(long long items, int sms) {
 }  // namespace
 
 cudaError_t launch_fork_tables(const ForkParams& p, cudaStream_t stream) {
-    fork_scan_kernel<<<kScanCtas, kScanThreads, 0, stream>>>(p);
+    // up to four rows (or requests) for each of the cluster's warps
+    const bool whole = p.rows + p.batch <= 4 * kScanCtas * kScanThreads / 32;
+    fork_scan_kernel<<<kScanCtas, kScanThreads, 0, stream>>>(p, whole);
     const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || whole) return e;
     fork_tables_kernel<<<(p.rows + p.batch + 7) / 8, 256, 0, stream>>>(p);
     return cudaGetLastError();
 }
@@ -498,21 +532,27 @@ cudaError_t launch_fork_rows(ForkRowsParams p, int num_sms, cudaStream_t stream)
 }
 
 cudaError_t launch_free_pages(const FreeParams& p, const int32_t* refs_in, int num_sms, cudaStream_t stream) {
+    const long long total = static_cast<long long>(p.rows) * p.cols;
+    const int few = 8 * kScanCtas * kScanThreads;  // eight for each of the cluster's threads
+    if (refs_in != p.refs_out && p.num_pages <= few && total <= few) {
+        free_few_kernel<<<kScanCtas, kScanThreads, 0, stream>>>(p, refs_in);
+        return cudaGetLastError();
+    }
     if (refs_in != p.refs_out) {
         const cudaError_t e = cudaMemcpyAsync(p.refs_out, refs_in, static_cast<size_t>(p.num_pages) * 4, cudaMemcpyDeviceToDevice, stream);
         if (e != cudaSuccess) return e;
     }
-    const long long total = static_cast<long long>(p.rows) * p.cols;
     if (total == 0) return cudaSuccess;
     free_pages_kernel<<<grid_for(total, num_sms), 256, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
 cudaError_t launch_compact_tables(const CompactParams& p, int num_sms, cudaStream_t stream) {
-    compact_scan_kernel<<<kScanCtas, kScanThreads, 0, stream>>>(p);
-    const cudaError_t e = cudaGetLastError();
     const long long total = static_cast<long long>(p.rows) * p.cols;
-    if (e != cudaSuccess || total == 0) return e;
+    const bool whole = total <= 8 * kScanCtas * kScanThreads;  // eight for each of the cluster's threads
+    compact_scan_kernel<<<kScanCtas, kScanThreads, 0, stream>>>(p, whole);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || whole) return e;
     remap_tables_kernel<<<grid_for(total, num_sms), 256, 0, stream>>>(p);
     return cudaGetLastError();
 }
