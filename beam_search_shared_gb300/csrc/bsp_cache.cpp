@@ -268,6 +268,7 @@ bsp_status bsp_fork_rows(const bsp_plan_t* plan, const int32_t* beams, int64_t b
         st = check_block_scales(scales, geo.page_size, true);
         if (st != BSP_OK) return st;
     }
+    if (static_cast<int64_t>(geo.num_kv_heads) * geo.page_size * row_bytes(geo) > INT32_MAX) return BSP_ERR_UNSUPPORTED;
     if (plan->batch == 0) return BSP_OK;
     if (!plan_here(plan) || !device_ptr(beams, 4) || !device_ptr(pages_out, 4) || !device_ptr(k_pool, 16) || !device_ptr(v_pool, 16) ||
         !optional_ptr(beam_pages, 4) || !optional_ptr(cache_indirection, 4))

@@ -15,6 +15,7 @@
 #include <cstdint>
 
 #include "../../include/bsp.h"
+#include "bsp_ptx.cuh"
 #include "bsp_write.h"
 
 namespace bsp {
@@ -263,15 +264,6 @@ __device__ __forceinline__ float row_top(float m) {
 // run's length. A run has at most 32 tokens.
 __device__ __forceinline__ void find_run(const NormAppendParams& p, int i, int slot, int lane, int* place, int* length) {
     const int block = slot >> p.block_log2;
-    *place = 0;
-    *length = 1;
-    int unused;
-    auto next_to = [&](int j) -> bool {  // (a step's tokens stand alone: two uniform reads tell)
-        if (j < 0 || j >= p.a.n) return false;
-        const int s = token_slot(p, j, false, &unused);
-        return s >= 0 && (s >> p.block_log2) == block;
-    };
-    if (!next_to(i - 1) && !next_to(i + 1)) return;
     auto same = [&](int j) -> bool {
         if (j < 0 || j >= p.a.n) return false;
         int pos;
@@ -279,8 +271,7 @@ __device__ __forceinline__ void find_run(const NormAppendParams& p, int i, int s
         return s >= 0 && (s >> p.block_log2) == block;
     };
     const uint32_t before = __ballot_sync(kFull, same(i - 1 - lane)), after = __ballot_sync(kFull, same(i + 1 + lane));
-    *place = __ffs(~before) - 1;  // (a run of 32 has 31 others at most)
-    if (before == ~0u) *place = 31;
+    *place = before == ~0u ? 31 : __ffs(~before) - 1;  // (a run of 32 has 31 others at most)
     const int rest = after == ~0u ? 31 : __ffs(~after) - 1;
     *length = *place + 1 + rest;
 }
@@ -427,15 +418,33 @@ __global__ void __launch_bounds__(256, 3) norm_append_kernel(const NormAppendPar
     const unsigned w = blockIdx.x * 8u + (threadIdx.x >> 5);
     const int i = static_cast<int>(w / p.units), u = static_cast<int>(w - static_cast<unsigned>(i) * p.units);
     if (i >= p.a.n) return;
-    int pos;
-    const int slot = token_slot(p, i, u == 0 && lane == 0, &pos);
+    if (p.units == 1) {
+        // all of the token's rows will be read here: those of the later batches come into L2 meanwhile
+        const uint8_t* v = reinterpret_cast<const uint8_t*>(static_cast<const uint16_t*>(p.v_new) + i * p.src_stride);
+        for (int at = lane * 128; at < p.Hkv * D * 2; at += 32 * 128) prefetch_l2(v + at);
+        if (p.a.q) {
+            const uint8_t* q = reinterpret_cast<const uint8_t*>(static_cast<const uint16_t*>(p.a.q) + i * p.a.q_stride);
+            for (int at = lane * 128; at < p.a.Hq * D * 2; at += 32 * 128) prefetch_l2(q + at);
+        }
+    }
+    // lanes 0 to 2 look at the token before, the token and the one behind (only a block's scale asks for the others)
+    int pos = 0, slot = -1;
+    {
+        const int j = i - 1 + lane;
+        const bool look = POOL == kPoolBlocks ? lane < 3 && j >= 0 && j < p.a.n : lane == 1;
+        if (look) slot = token_slot(p, j, u == 0 && lane == 1, &pos);
+    }
+    const int before = __shfl_sync(kFull, slot, 0), behind = __shfl_sync(kFull, slot, 2);
+    slot = __shfl_sync(kFull, slot, 1);
+    pos = __shfl_sync(kFull, pos, 1);
     if (slot < 0) return;
     const long long base = pool_row(p, slot, 0);
     int first = u;  // the warp's first batch
     if constexpr (POOL == kPoolBlocks) {
-        int place = 0, length = 1;
-        if (p.block_log2 > 0) find_run(p, i, slot, lane, &place, &length);
-        if (length > 1) {
+        auto near = [&](int s) { return s >= 0 && (s >> p.block_log2) == (slot >> p.block_log2); };
+        if (near(before) || near(behind)) {  // (uniform; a step's tokens stand alone)
+            int place, length;
+            find_run(p, i, slot, lane, &place, &length);
             for (int item = place * p.units + u; item < 2 * p.groups; item += length * p.units) {
                 const bool is_v = item >= p.groups;
                 run_rows<D, BF16>(p, i - place, length, slot, is_v ? item - p.groups : item, is_v, lane);
@@ -452,18 +461,18 @@ __global__ void __launch_bounds__(256, 3) norm_append_kernel(const NormAppendPar
     for (; b < p.batches; b += p.units) query_rows<D, BF16>(p, i, pos, b - 2 * p.kv_batches, lane, m, have);
 }
 
-// Block scales for tokens that come in runs, a prompt's: a CTA takes kWindow tokens of one group of heads, K or V, a
-// warp four of the tokens, and finds the largest magnitude of each run in shared memory. A run that reaches out of the
-// window has its rows there read too, for that magnitude alone, so that every CTA with rows of a run finds the same
-// exponent for them by itself; the one with the run's first token writes it to the table and raises the rows before the
-// run. (Another may read the table's byte before or after: the larger of the run's exponent and either is the same.)
+// Block scales for tokens that come in runs, a prompt's: a CTA takes the runs that begin among kWindow tokens, of one
+// group of heads, K or V. A run has at most kWindow tokens, so they end within the window behind. Its warps take the
+// tokens in turn, normalise and rotate their rows into shared memory (fp32) and find each run's largest magnitude there;
+// then the rows' codes follow. Each row is read and worked out once, and no CTA depends on another.
 // The query rows' CTAs are dealt between the others', which wait more than they move.
-// Bound by the rows' traffic. Measured: see launch_norm_append.
+// Measured: see launch_norm_append.
 constexpr int kWindow = 32;
+constexpr size_t kWindowSmem = 2 * kWindow * 256 * sizeof(float);  // (a group of heads has 256 elements)
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(256, 3) block_window_kernel(const NormAppendParams p, unsigned kv_ctas, unsigned ctas) {
-    constexpr int CPR = D / 8, RPW = 32 / CPR, ROWS = kWindow / 8;  // tokens of a warp
+    constexpr int CPR = D / 8, RPW = 32 / CPR, BATCH = 4;
     const NormRope& a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = lane & (CPR - 1), seg = lane / CPR;
     // CTA x is the y-th for K and V where the running share of those steps up at x
@@ -479,19 +488,21 @@ __global__ void __launch_bounds__(256, 3) block_window_kernel(const NormAppendPa
         for (int b = 0; b < p.batches - 2 * p.kv_batches; ++b) query_rows<D, BF16>(p, i, pos, b, lane, m, have);
         return;
     }
-    __shared__ int s_slot[3 * kWindow], s_pos[3 * kWindow];  // tokens i0 - kWindow .. i0 + 2 kWindow - 1
-    __shared__ uint32_t s_lead[3];                           // tokens at which a run begins
-    __shared__ uint32_t s_top[2 * kWindow][RPW];             // a run's largest magnitude, at its first token
+    extern __shared__ f2 s_rows[];                // [2 kWindow][4][32]: pair e of lane l's elements of a token
+    __shared__ int s_slot[2 * kWindow], s_pos[2 * kWindow];
+    __shared__ uint32_t s_lead[2];                // tokens at which a run begins
+    __shared__ uint32_t s_top[kWindow][RPW];      // a run's largest magnitude, at its first token
+    __shared__ ushort2 s_exp[kWindow][RPW];       // its block's exponent before and after
     const int items = 2 * p.groups;
     const int window = static_cast<int>(y / items), item = static_cast<int>(y - static_cast<unsigned>(window) * items);
     const bool is_v = item >= p.groups;
     const int h = (is_v ? item - p.groups : item) * RPW + seg;
     const bool live = h < p.Hkv;
     const int i0 = window * kWindow;
-    if (tid < 3 * kWindow) {
-        const int i = i0 - kWindow + tid;
+    if (tid < 2 * kWindow) {
+        const int i = i0 + tid;
         int pos = 0, slot = -1, before = -1, unused;
-        if (i >= 0 && i < a.n) slot = token_slot(p, i, item == 0 && warp == 1, &pos);
+        if (i < a.n) slot = token_slot(p, i, item == 0 && warp == 0, &pos);
         if (i >= 1 && i < a.n) before = token_slot(p, i - 1, false, &unused);
         s_slot[tid] = slot;
         s_pos[tid] = pos;
@@ -499,74 +510,75 @@ __global__ void __launch_bounds__(256, 3) block_window_kernel(const NormAppendPa
         const uint32_t b = __ballot_sync(kFull, slot >= 0 && (slot >> p.block_log2) != (before >> p.block_log2));
         if (lane == 0) s_lead[warp] = b;
     }
-    for (int x = tid; x < 2 * kWindow * RPW; x += 256) s_top[x / RPW][x % RPW] = 0u;
+    if (tid < kWindow * RPW) s_top[tid / RPW][tid % RPW] = 0u;
     __syncthreads();
-    // the first token of token t's run (both counted from i0 - kWindow): a run's first is at most 31 before it
-    auto first_of = [&](int t) -> int {
+    const uint32_t lead0 = s_lead[0], lead1 = s_lead[1];
+    // the first token of token t's run; -1: of none, or of one that another CTA writes
+    auto run_of = [&](int t) -> int {
         if (s_slot[t] < 0) return -1;
-        const int w = t >> 5;
-        const uint32_t here = s_lead[w] & (~0u >> (31 - (t & 31)));
-        if (here) return 32 * w + 31 - __clz(here);
-        const uint32_t b = w ? s_lead[w - 1] : 0u;
-        return b ? 32 * (w - 1) + 31 - __clz(b) : -1;
+        if (t < kWindow) return 31 - __clz(lead0 & (~0u >> (31 - t)));
+        return (lead1 & (~0u >> (63 - t))) ? -1 : 31 - __clz(lead0);
     };
-    uint8_t* pool = static_cast<uint8_t*>(is_v ? p.v_pool : p.k_pool);
-    uint8_t* exps = is_v ? p.v_exp : p.k_exp;
-    const int run_in = first_of(kWindow), run_out = first_of(2 * kWindow - 1);  // of the window's first and last token
-    f2 f[ROWS][4];
-    int run[ROWS];
-    // which: 0 the tokens before the window, 2 behind it (rows of its first and its last run), 1 its own, last, to be kept
+    const uint16_t* src = static_cast<const uint16_t*>(is_v ? p.v_new : p.k_new) + static_cast<long long>(i0) * p.src_stride + h * D + 8 * c;
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-        const int which = pass == 2 ? 1 : 2 * pass;
-        uint4 x[ROWS];
-        bool some = false;
+    for (int t0 = warp; t0 < 2 * kWindow; t0 += 8 * BATCH) {
+        uint4 x[BATCH];
+        int run[BATCH];
 #pragma unroll
-        for (int k = 0; k < ROWS; ++k) {
-            const int t = which * kWindow + warp * ROWS + k;
-            int r = first_of(t);
-            if (which != 1 && (r != (which == 0 ? run_in : run_out) || r < 0)) r = -1;
-            if (which == 2 && r >= 2 * kWindow) r = -1;
-            run[k] = r;  // (uniform)
-            some |= r >= 0;
+        for (int k = 0; k < BATCH; ++k) {
+            const int t = t0 + 8 * k;
+            run[k] = run_of(t);  // (uniform)
             x[k] = make_uint4(0, 0, 0, 0);
-            if (r >= 0 && live) {
-                const uint16_t* src = static_cast<const uint16_t*>(is_v ? p.v_new : p.k_new) + static_cast<long long>(i0 - kWindow + t) * p.src_stride + h * D;
-                x[k] = __ldg(reinterpret_cast<const uint4*>(src) + c);
-            }
+            if (run[k] >= 0 && live) x[k] = __ldcs(reinterpret_cast<const uint4*>(src + t * p.src_stride));
         }
-        if (!some) continue;
 #pragma unroll
-        for (int k = 0; k < ROWS; ++k) {
-            if (run[k] < 0) continue;  // (uniform)
+        for (int k = 0; k < BATCH; ++k) {
+            if (run[k] < 0) continue;
+            const int t = t0 + 8 * k;
+            f2 f[4];
             if (is_v) {
-                unpack8<BF16>(x[k], f[k]);
+                unpack8<BF16>(x[k], f);
             } else {
                 Mix m;
-                load_mix<D, BF16>(a, a.k_weight, s_pos[which * kWindow + warp * ROWS + k], lane, m);
-                norm_rotate<D, BF16>(a, m, lane, x[k], f[k]);
+                load_mix<D, BF16>(a, a.k_weight, s_pos[t], lane, m);
+                norm_rotate<D, BF16>(a, m, lane, x[k], f);
             }
-            const float top = row_top<D>(lane_top(f[k]));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s_rows[(t * 4 + e) * 32 + lane] = f[e];
+            const float top = row_top<D>(lane_top(f));
             if (c == 0) atomicMax(&s_top[run[k]][seg], __float_as_uint(top));  // (not negative: ordered as integers)
         }
     }
     __syncthreads();
-    const unsigned mine = __ballot_sync(kFull, live);
-    if (!live) return;
-#pragma unroll
-    for (int k = 0; k < ROWS; ++k) {
-        if (run[k] < 0) continue;  // (uniform)
-        const int t = kWindow + warp * ROWS + k, slot = s_slot[t];
-        const int off = s_slot[run[k]] & ((1 << p.block_log2) - 1);  // of the run's first row in the block
-        const long long row = pool_row(p, slot, h), head = row >> p.block_log2;
-        const int old = off != 0 ? *static_cast<volatile const uint8_t*>(exps + head) : 0;
-        const int e = block_exponent(p, s_top[run[k]][seg], old);
-        reinterpret_cast<uint2*>(pool + row * D)[c] = quant8(f[k], code_factor(e));
-        if (run[k] == t) {  // the run's first token
-            __syncwarp(mine);  // every lane has read the old byte
-            if (c == 0) exps[head] = static_cast<uint8_t>(e);
-            if (old != 0 && e != old) raise_rows<D>(pool + (head << p.block_log2) * D, off, old, e, c);
+    uint8_t* pool = static_cast<uint8_t*>(is_v ? p.v_pool : p.k_pool);
+    uint8_t* exps = is_v ? p.v_exp : p.k_exp;
+    if (tid < kWindow * RPW) {
+        // a thread for each run and head
+        const int t = tid / RPW, s = tid % RPW, hs = h - seg + s;
+        int e = 0, old = 0;
+        if ((lead0 >> t & 1) && hs < p.Hkv) {
+            uint8_t* at = exps + (pool_row(p, s_slot[t], hs) >> p.block_log2);
+            if ((s_slot[t] & ((1 << p.block_log2) - 1)) != 0) old = *at;
+            e = block_exponent(p, s_top[t][s], old);
+            *at = static_cast<uint8_t>(e);
         }
+        s_exp[t][s] = make_ushort2(static_cast<unsigned short>(old), static_cast<unsigned short>(e));
+    }
+    __syncthreads();
+    if (!live) return;
+#pragma unroll 2
+    for (int t = warp; t < 2 * kWindow; t += 8) {
+        const int run = run_of(t);
+        if (run < 0) continue;
+        f2 f[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = s_rows[(t * 4 + e) * 32 + lane];
+        reinterpret_cast<uint2*>(pool + pool_row(p, s_slot[t], h) * D)[c] = quant8(f, code_factor(s_exp[run][seg].y));
+    }
+    for (int t = warp; t < kWindow; t += 8) {
+        if (!(lead0 >> t & 1)) continue;
+        const int old = s_exp[t][seg].x, e = s_exp[t][seg].y, off = s_slot[t] & ((1 << p.block_log2) - 1);
+        if (old != 0 && e != old) raise_rows<D>(pool + (pool_row(p, s_slot[t], h) - off) * D, off, old, e, c);
     }
 }
 
@@ -582,7 +594,9 @@ cudaError_t launch_norm_t(NormAppendParams p, PoolKind pools, bool runs, int num
         const long long kv = static_cast<long long>((p.a.n + kWindow - 1) / kWindow) * 2 * p.groups;
         const long long q = p.a.q ? (p.a.n + 7) / 8 : 0;
         if (kv + q > INT32_MAX) return cudaErrorInvalidValue;
-        block_window_kernel<D, BF16><<<static_cast<unsigned>(kv + q), 256, 0, stream>>>(p, static_cast<unsigned>(kv), static_cast<unsigned>(kv + q));
+        const cudaError_t e = cudaFuncSetAttribute(block_window_kernel<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWindowSmem);
+        if (e != cudaSuccess) return e;
+        block_window_kernel<D, BF16><<<static_cast<unsigned>(kv + q), 256, kWindowSmem, stream>>>(p, static_cast<unsigned>(kv), static_cast<unsigned>(kv + q));
         return cudaGetLastError();
     }
     // warps of a token: as many as keep the SMs' resident warps (24 of each) busy

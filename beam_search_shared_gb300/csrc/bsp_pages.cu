@@ -149,10 +149,22 @@ __global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads
     share_of(p.num_pages, rank, &lo, &hi);
     share_of(p.rows, rank, &rlo, &rhi);
     int free = 0, need = 0, full;
-    for (int i = lo + tid; i < hi; i += kScanThreads) {
-        const int r = p.refs_in[i];
-        free += r == 0;
-        if (p.refs_out != p.refs_in) p.refs_out[i] = r;
+    // a thread's four counts of the share's first round are kept for the second pass
+    int first[4];
+    for (int i0 = lo; i0 < hi; i0 += 4 * kScanThreads) {
+        const int i = i0 + 4 * tid;
+        int r[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            r[e] = i + e < hi ? p.refs_in[i + e] : 1;
+            free += r[e] == 0;
+            if (i0 == lo) first[e] = r[e];
+        }
+        if (p.refs_out != p.refs_in) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (i + e < hi) p.refs_out[i + e] = r[e];
+        }
     }
     for (int i = rlo + tid; i < rhi; i += kScanThreads) {
         const int b = i / p.num_forks;
@@ -192,7 +204,7 @@ __global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads
         bool f[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            f[e] = i + e < hi && p.refs_in[i + e] == 0;
+            f[e] = (i0 == lo ? first[e] : i + e < hi ? p.refs_in[i + e] : 1) == 0;
             n += f[e];
         }
         int k = at + cta_scan(n, s_warp, &total);
@@ -315,31 +327,32 @@ __global__ void __launch_bounds__(256) fork_rows_kernel(const ForkRowsParams p) 
             (t ? p.v_exp : p.k_exp)[((static_cast<long long>(to) * p.Hkv + h0 + h) << (p.ps_log2 - p.block_log2)) + q] = s_new[t][h][q << p.block_log2];
         }
     }
-    const int chunks = p.row_bytes >> 4;  // a power of two
+    const int cl2 = __ffs(p.row_bytes) - 5, chunks = 1 << cl2;  // 16-byte chunks of a row
     const int total = 2 * heads * n * chunks;
+    // y / n for y < 2 * 8 * 128 as a product: y (n - 1) < 2^20
+    const uint32_t inv = ((1u << 20) + n - 1) / n;
+    const int page_bytes = (p.Hkv << p.ps_log2) * p.row_bytes;  // (below 2^31: 128 slots of 512 bytes, and heads to match)
+    const int first_off = ((h0 << p.ps_log2) * p.row_bytes), row_bytes = p.row_bytes;
     for (int x0 = tid; x0 < total; x0 += 4 * 256) {
         uint4 v[4];
-        long long dst[4];
-        int at[4];
+        int off[4], at[4];  // bytes from a page's start (-1: nothing to copy), place in the exponents' tables
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const int x = x0 + u * 256;
-            dst[u] = -1;
+            off[u] = -1;
             if (x >= total) continue;
-            const int c = x & (chunks - 1), y = x / chunks;  // y: (tensor, head, slot)
-            const int s = y % n, z = y / n;
+            const int c = x & (chunks - 1), y = x >> cl2;  // y: (tensor, head, slot)
+            const int z = static_cast<int>((static_cast<uint32_t>(y) * inv) >> 20), s = y - z * n;
             const int t = z >= heads, h = t ? z - heads : z;
             const int src = s_src[s];
             if (src < 0) continue;
-            const long long off = (static_cast<long long>(h0 + h) << p.ps_log2) + s, page_rows = static_cast<long long>(p.Hkv) << p.ps_log2;
-            const uint8_t* pool = t ? p.v_pool : p.k_pool;
-            v[u] = *reinterpret_cast<const uint4*>(pool + (src * page_rows + off) * p.row_bytes + 16 * c);
-            dst[u] = (to * page_rows + off) * p.row_bytes + 16 * c;
+            off[u] = first_off + ((h << p.ps_log2) + s) * row_bytes + 16 * c;
             at[u] = (t * 8 + h) * 128 + s;
+            v[u] = *reinterpret_cast<const uint4*>((t ? p.v_pool : p.k_pool) + static_cast<long long>(src) * page_bytes + off[u]);
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            if (dst[u] < 0) continue;
+            if (off[u] < 0) continue;
             if constexpr (SCALES) {
                 const int eo = (&s_exp[0][0][0])[at[u]], en = (&s_new[0][0][0])[at[u]];
                 if (eo != en) {
@@ -348,7 +361,7 @@ __global__ void __launch_bounds__(256) fork_rows_kernel(const ForkRowsParams p) 
                     v[u] = make_uint4(lo.x, lo.y, hi.x, hi.y);
                 }
             }
-            *reinterpret_cast<uint4*>((at[u] >= 8 * 128 ? p.v_pool : p.k_pool) + dst[u]) = v[u];
+            *reinterpret_cast<uint4*>((at[u] >= 8 * 128 ? p.v_pool : p.k_pool) + static_cast<long long>(to) * page_bytes + off[u]) = v[u];
         }
     }
 }
@@ -398,15 +411,28 @@ __global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads
     const int rank = static_cast<int>(cl.block_rank()), tid = threadIdx.x;
     int lo, hi;
     share_of(p.num_pages, rank, &lo, &hi);
-    int live = 0;
-    for (int i = lo + tid; i < hi; i += kScanThreads) live += p.refs_in[i] > 0;
+    int live = 0, kept[4] = {0, 0, 0, 0};  // a thread's counts of the share's first round stay for the later passes
+    for (int i0 = lo; i0 < hi; i0 += 4 * kScanThreads) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = i0 + 4 * tid + e, r = i < hi ? p.refs_in[i] : 0;
+            live += r > 0;
+            if (i0 == lo) kept[e] = r;
+        }
+    }
     live = cta_sum(live, s_warp);
     if (tid == 0) s_live = live;
     cl.sync();
     int L;
     int at = cluster_sum(cl, &s_live, &L);
     int front = 0;  // of the CTA's live pages, those below L
-    for (int i = lo + tid; i < min(hi, L); i += kScanThreads) front += p.refs_in[i] > 0;
+    for (int i0 = lo; i0 < min(hi, L); i0 += 4 * kScanThreads) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = i0 + 4 * tid + e;
+            if (i < min(hi, L)) front += (i0 == lo ? kept[e] : p.refs_in[i]) > 0;
+        }
+    }
     front = cta_sum(front, s_warp);
     if (tid == 0) s_front = front;
     cl.sync();
@@ -418,7 +444,7 @@ __global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads
         int r[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            r[e] = i + e < hi ? p.refs_in[i + e] : 0;
+            r[e] = i0 == lo ? kept[e] : i + e < hi ? p.refs_in[i + e] : 0;
             n += r[e] > 0;
         }
         int before = at + cta_scan(n, s_warp, &total);
