@@ -413,9 +413,9 @@ __device__ __forceinline__ void run_rows(const NormAppendParams& p, int lead, in
 // run are brought to the new one in place.
 // Measured: see launch_norm_append.
 template <int D, bool BF16, int POOL>
-__global__ void __launch_bounds__(256, 3) norm_append_kernel(const NormAppendParams p) {
+__global__ void __launch_bounds__(128, 6) norm_append_kernel(const NormAppendParams p) {
     const int lane = threadIdx.x & 31;
-    const unsigned w = blockIdx.x * 8u + (threadIdx.x >> 5);
+    const unsigned w = blockIdx.x * 4u + (threadIdx.x >> 5);
     const int i = static_cast<int>(w / p.units), u = static_cast<int>(w - static_cast<unsigned>(i) * p.units);
     if (i >= p.a.n) return;
     if (p.units == 1) {
@@ -603,11 +603,11 @@ cudaError_t launch_norm_t(NormAppendParams p, PoolKind pools, bool runs, int num
     p.units = std::max(1, std::min(p.batches, 24 * num_sms / p.a.n));
     const long long warps = static_cast<long long>(p.a.n) * p.units;
     if (warps > INT32_MAX) return cudaErrorInvalidValue;
-    const unsigned blocks = static_cast<unsigned>((warps + 7) / 8);
+    const unsigned blocks = static_cast<unsigned>((warps + 3) / 4);
     switch (pools) {
-        case kPool16: norm_append_kernel<D, BF16, kPool16><<<blocks, 256, 0, stream>>>(p); break;
-        case kPoolE4m3: norm_append_kernel<D, BF16, kPoolE4m3><<<blocks, 256, 0, stream>>>(p); break;
-        case kPoolBlocks: norm_append_kernel<D, BF16, kPoolBlocks><<<blocks, 256, 0, stream>>>(p); break;
+        case kPool16: norm_append_kernel<D, BF16, kPool16><<<blocks, 128, 0, stream>>>(p); break;
+        case kPoolE4m3: norm_append_kernel<D, BF16, kPoolE4m3><<<blocks, 128, 0, stream>>>(p); break;
+        case kPoolBlocks: norm_append_kernel<D, BF16, kPoolBlocks><<<blocks, 128, 0, stream>>>(p); break;
     }
     return cudaGetLastError();
 }
