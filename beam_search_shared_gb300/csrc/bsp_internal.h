@@ -145,6 +145,10 @@ cudaError_t launch_prefix(int head_dim, bool bf16, int ctas, const CUtensorMap& 
 // Kernel attributes (shared-memory size and split) are set by the prepare_* calls, once before
 // the launches, so that timing events recorded around a launch bracket the launch alone.
 cudaError_t prepare_prefix(int head_dim, bool bf16);
+// The same kernel's half-row layout over E4M3 pools with block scales (p.bq = beams per quadrant, bq * G <= 16).
+cudaError_t prepare_prefix_blocks(int head_dim, bool bf16);
+cudaError_t launch_prefix_blocks(int head_dim, bool bf16, int ctas, const CUtensorMap& tq, const CUtensorMap& tk,
+                                 const CUtensorMap& tv, const PrefixParams& p, cudaStream_t stream);
 // What a kernel's pools hold: elements of q's dtype, E4M3 bytes with one scale per tensor, or E4M3 bytes with block
 // scales.
 enum PoolKind { kPool16 = 0, kPoolE4m3 = 1, kPoolBlocks = 2 };

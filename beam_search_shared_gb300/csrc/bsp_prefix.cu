@@ -61,6 +61,13 @@
 // order, and the Q*K^T that overwrites S[t%2] is issued after the P*V that
 // reads P_t), then NO O buffers of D columns (two where they fit, one at
 // head_dim 256).
+// E4M3 pools with block scales, in the half-row layout (BLK, 448 threads): the
+// producer loads each E4M3 tile into the upper half of its 16-bit ring slot;
+// warps 10-11 widen every K tile, warps 12-13 every V tile, in place, with their
+// rows' scales, and complete the slot's full barrier; the epilogue warps widen
+// the tail tiles' rows as they gather them. Two S buffers and three K slots let
+// the widening run beside the softmax: 64 x 30 beams over 500 keys 102 us on the
+// alternating-tile kernel (bsp_alt.cu), 64 here.
 // Every wait is bounded (1 s without progress); on expiry the CTA flags
 // BSP_DEVFLAG_TIMEOUT, drains its own copies and MMAs, frees TMEM and exits.
 #include <cuda.h>
@@ -77,13 +84,14 @@ namespace bsp {
 
 // SPLIT: the half-row layout, whose MMAs have M = 64 (the accumulator's 64 rows sit in TMEM
 // lanes 0-15 of each quadrant), so a Q buffer holds 64 rows and the K ring gets a third slot
-template <int D, bool SPLIT>
+// BLK: E4M3 pools with block scales (SPLIT only)
+template <int D, bool SPLIT, bool BLK = false>
 struct PrefixCfg {
     static constexpr int TK = D <= 128 ? 128 : 64;            // keys per tile
     static constexpr int NC = D / 64;                        // 128-byte column regions per row
     static constexpr int NQ = D <= 128 ? 2 : 1;              // Q buffers
     static constexpr int MR = SPLIT ? 64 : kRowsPerBlock;    // MMA M: query rows of a Q buffer
-    static constexpr int KST = D == 64 ? (SPLIT ? 6 : 4) : (SPLIT ? 3 : 2);  // K ring depth
+    static constexpr int KST = D == 64 ? (SPLIT ? (BLK ? 5 : 6) : 4) : (SPLIT ? 3 : 2);  // K ring depth
     static constexpr int VST = D == 64 ? 7 : 3;              // V ring depth
     static constexpr int Q_BYTES = MR * D * 2;               // NC regions of MR rows x 128 B
     static constexpr int KV_BYTES = TK * D * 2;              // one K (or V) tile
@@ -101,14 +109,20 @@ struct PrefixCfg {
     static_assert(TK % 64 == 0 && TK / 16 <= 8 && D / 16 <= 16, "tile shape");
     static_assert(TK == prefix_tile_keys(D), "the host's fused-tail bound");
     static constexpr int TAIL_CHUNKS = TK * (D / 8) / 128;  // 16-byte chunks per epilogue thread and tensor
-    static constexpr int THREADS = 320;
+    static constexpr int THREADS = BLK ? 448 : 320;
+    static constexpr int CONV_TID0 = 320;                    // BLK: warps 10-11 widen K tiles, 12-13 V tiles
+    static constexpr int CONV_THREADS = 64;
+    static_assert(!BLK || SPLIT, "block scales: the half-row layout");
 };
 
+template <class C, bool BLK>
 struct PrefixBarriers {
-    uint64_t k_full[8];
-    uint64_t k_empty[8];  // KST <= 8; arrived by softmax warp 2 when it sees the tile's S complete
-    uint64_t v_full[8];
-    uint64_t v_empty[8];  // VST <= 8; the tile's P*V completed (also what a rescale of O waits for)
+    uint64_t k_full[C::KST];
+    uint64_t k_empty[C::KST];  // arrived by softmax warp 2 when it sees the tile's S complete
+    uint64_t v_full[C::VST];
+    uint64_t v_empty[C::VST];  // the tile's P*V completed (also what a rescale of O waits for)
+    uint64_t k8_full[BLK ? C::KST : 1];  // BLK: the E4M3 K tile landed in the upper half of the K slot
+    uint64_t v8_full[BLK ? C::VST : 1];  // ... the E4M3 V tile in the V slot
     uint64_t q_full[2];   // Q of unit k landed in shared-memory buffer k % NQ
     uint64_t q_empty[2];  // ... and its last Q*K^T completed
     uint64_t s_full[2];
@@ -141,11 +155,25 @@ __device__ __forceinline__ int unit_tiles(const UnitInfo& ui, int wblk) {
     return prompt_tiles<TK>(ui) + tail_tiles<TK>(ui, wblk);
 }
 
-template <int D, bool BF16, bool SPLIT>
-__global__ void __launch_bounds__(320, 1)
+// Named barrier `id` over `n` threads, returning the AND of their flags (every one of them takes part).
+__device__ __forceinline__ bool stream_sync_and(int id, int n, bool ok) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.and.pred q, %2, %3, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(ok)), "r"(id), "r"(n)
+        : "memory");
+    return r != 0;
+}
+
+template <int D, bool BF16, bool SPLIT, bool BLK>
+__global__ void __launch_bounds__(BLK ? 448 : 320, 1)
 prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const PrefixParams p) {
-    using C = PrefixCfg<D, SPLIT>;
+    using C = PrefixCfg<D, SPLIT, BLK>;
     constexpr int TK = C::TK, NC = C::NC, NQ = C::NQ, KST = C::KST, VST = C::VST, NO = C::NO, MR = C::MR;
     constexpr unsigned FULL = 0xffffffffu;
     static_assert(!SPLIT || TK == 128, "half-row softmax: 128-key tiles");
@@ -177,7 +205,8 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     // [kPrefixMaxTailTiles][TK]: per tail tile of the current unit and key column, 1 if the key is readable
     uint8_t* s_tok = smem + C::OFF_TROW;
     static_assert(kPrefixMaxTailTiles * TK <= TK * 4, "tail-key flags fit the table area");
-    PrefixBarriers* bars = reinterpret_cast<PrefixBarriers*>(smem + C::OFF_BAR);
+    using Barriers = PrefixBarriers<C, BLK>;
+    Barriers* bars = reinterpret_cast<Barriers*>(smem + C::OFF_BAR);
     volatile int* abort_flag = &bars->abort_flag;
 
     if (p.graph_hdr != nullptr) {
@@ -222,6 +251,10 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         for (int i = 0; i < 8; ++i) mbar_init(&bars->tail_ready[i], 1);
         mbar_init(&bars->drain, 1);
+        if constexpr (BLK) {
+            for (int s = 0; s < KST; ++s) mbar_init(&bars->k8_full[s], 1);
+            for (int s = 0; s < VST; ++s) mbar_init(&bars->v8_full[s], 1);
+        }
         bars->abort_flag = 0;
         bars->tail_granted = 0;
         fence_mbar_init();
@@ -299,35 +332,46 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     // hand them over by a counter: the producer may run several tail tiles ahead of the
                     // epilogue warps (short units, deep rings), which a parity wait could not follow
                     ++ntail;
-                    if (lane == 0) counter_release(&bars->tail_granted, ntail);
+                    if (lane == 0) {
+                        counter_release(&bars->tail_granted, ntail);
+                        if constexpr (BLK) {
+                            // no E4M3 tile here: complete the slots' E4M3 phases (the widening warps wait for every
+                            // phase in order and have nothing to widen for a tail tile)
+                            mbar_arrive(&bars->k8_full[gt % KST]);
+                            mbar_arrive(&bars->v8_full[gt % VST]);
+                        }
+                    }
                     __syncwarp();
                     continue;
                 }
                 const int key0 = ui.key_begin + t * TK;
                 const int valid = min(TK, ui.key_end - key0);
                 const int nchunks = (valid + BR - 1) / BR;  // pages (or 64-row slices) with valid keys
-                const int tile_bytes = nchunks * BR * D * 2;
+                const int tile_bytes = nchunks * BR * D * (BLK ? 1 : 2);
                 const int pidx0 = key0 >> p.ps_log2;
                 const int pidx_last = (key0 + (nchunks - 1) * BR) >> p.ps_log2;
                 if (win_base < 0 || pidx_last >= win_base + 32) {  // warp-uniform
                     win_base = pidx0;
                     my_page = (win_base + lane < npages) ? __ldg(pg + win_base + lane) : 0;
                 }
-                // box b of a tensor: column half b % NC of chunk b / NC
-                const int nbox = nchunks * NC;
+                // box b of a tensor: column half b % NC of chunk b / NC (E4M3: one box of head_dim bytes per chunk,
+                // into the upper half of the slot, where the widening warps pick it up)
+                constexpr int NB = BLK ? 1 : NC;
+                const int nbox = nchunks * NB;
                 for (int tensor = 0; tensor < 2; ++tensor) {
                     if (tensor == 1 && gt >= VST) {
                         ok = mbar_wait(&bars->v_empty[gt % VST], ((gt / VST) - 1) & 1, abort_flag, kWaitTimeoutNs);
                         ok = __all_sync(FULL, ok);
                         if (!ok) break;
                     }
-                    uint64_t* full = tensor == 0 ? &bars->k_full[gt % KST] : &bars->v_full[gt % VST];
+                    uint64_t* full = BLK ? (tensor == 0 ? &bars->k8_full[gt % KST] : &bars->v8_full[gt % VST])
+                                         : (tensor == 0 ? &bars->k_full[gt % KST] : &bars->v_full[gt % VST]);
                     uint8_t* base = tensor == 0 ? k_tile(gt) : v_tile(gt);
                     const CUtensorMap* map = tensor == 0 ? &tm_k : &tm_v;
                     if (lane == 0) mbar_arrive_expect_tx(full, tile_bytes);
                     for (int b0 = 0; b0 < nbox; b0 += 32) {
                         const int bx = b0 + lane;
-                        const int ch = min(bx / NC, nchunks - 1);
+                        const int ch = min(bx / NB, nchunks - 1);
                         const int key = key0 + ch * BR;
                         int page = __shfl_sync(FULL, my_page, (key >> p.ps_log2) - win_base);
                         if (bx < nbox) {
@@ -335,9 +379,13 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                 atomicOr(p.status, BSP_DEVFLAG_PAGE_INDEX);
                                 page = 0;
                             }
-                            const int c = bx % NC;
                             const int row = ((page * p.Hkv + ui.g) << p.ps_log2) + (key & (ps - 1));
-                            tma_load_2d(base + c * TK * 128 + ch * BR * 128, map, full, c * 64, row);
+                            if constexpr (BLK) {
+                                tma_load_2d(base + TK * D + ch * BR * D, map, full, 0, row);
+                            } else {
+                                const int c = bx % NC;
+                                tma_load_2d(base + c * TK * 128 + ch * BR * 128, map, full, c * 64, row);
+                            }
                         }
                     }
                 }
@@ -352,11 +400,14 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             // drain: let this CTA's own copies land before the CTA exits
             const uint64_t t0 = globaltimer_ns();
+            // (the TMA loads complete the E4M3 barriers over E4M3 pools)
+            uint64_t* kf = BLK ? bars->k8_full : bars->k_full;
+            uint64_t* vf = BLK ? bars->v8_full : bars->v_full;
             for (int j = max(0, gt - KST); j <= gt; ++j)
-                while (!mbar_try_wait(&bars->k_full[j % KST], (j / KST) & 1) && globaltimer_ns() - t0 < kDrainNs) {
+                while (!mbar_try_wait(&kf[j % KST], (j / KST) & 1) && globaltimer_ns() - t0 < kDrainNs) {
                 }
             for (int j = max(0, gt - VST); j <= gt; ++j)
-                while (!mbar_try_wait(&bars->v_full[j % VST], (j / VST) & 1) && globaltimer_ns() - t0 < kDrainNs) {
+                while (!mbar_try_wait(&vf[j % VST], (j / VST) & 1) && globaltimer_ns() - t0 < kDrainNs) {
                 }
             for (int j = max(0, k - NQ); j <= k; ++j)
                 while (!mbar_try_wait(&bars->q_full[j % NQ], (j / NQ) & 1) && globaltimer_ns() - t0 < kDrainNs) {
@@ -632,9 +683,9 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     l += (rsp[0] + rsp[1]) + (rsp[2] + rsp[3]);
                 }
                 if (!ok) break;
-                if (valid < TK) {
+                if (!BLK && valid < TK) {
                     // a unit's last tile: zero V rows past the valid keys (stale or garbage rows
-                    // times P = 0 must not produce NaN)
+                    // times P = 0 must not produce NaN; the widening warps write such rows as zeros)
                     ok = mbar_wait(&bars->v_full[gt % VST], (gt / VST) & 1, abort_flag, kWaitTimeoutNs);
                     ok = __all_sync(FULL, ok);
                     if (!ok) break;
@@ -676,8 +727,49 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             *abort_flag = 1;
             atomicOr(p.status, BSP_DEVFLAG_TIMEOUT);
         }
+    } else if (BLK && warp >= 10) {
+        // ================= E4M3 pools: widening of the prompt tiles (warps 10-13) =================
+        if constexpr (BLK) {
+            const int ctid = tid - C::CONV_TID0;
+            const int tensor = ctid / C::CONV_THREADS;  // 0: K tiles (warps 10-11), 1: V tiles (warps 12-13)
+            const int stid = ctid % C::CONV_THREADS;
+            const int bar = 2 + tensor;                 // named barrier of the stream's threads
+            bool ok = true;
+            int gt = 0;
+            const uint8_t* exps = tensor == 0 ? p.k_exp : p.v_exp;
+            BlockFactors<D, TK, BF16, C::CONV_THREADS> ahead;
+            uint32_t factor[TK / C::CONV_THREADS] = {};
+            ahead.begin(p, exps, u_begin, nunits, stid);
+            for (int k = 0; k < nunits && ok; ++k) {
+                const UnitInfo cur = load_unit(p, u_begin + k);
+                const int ptiles = prompt_tiles<TK>(cur);
+                const int ntiles = unit_tiles<TK>(cur, p.Wblk);
+                for (int t = 0; t < ntiles && ok; ++t, ++gt) {
+                    // every tile's E4M3 phase in order, a tail tile's too (the producer completes it when it hands the
+                    // slots over; nothing to widen): so each parity wait names the phase it means
+                    uint64_t* full8 = tensor == 0 ? &bars->k8_full[gt % KST] : &bars->v8_full[gt % VST];
+                    const uint32_t ph = tensor == 0 ? (gt / KST) & 1 : (gt / VST) & 1;
+                    if (t < ptiles) ahead.next(p, exps, u_begin, nunits, stid, factor);
+                    ok = mbar_wait(full8, ph, abort_flag, kWaitTimeoutNs);
+                    ok = __all_sync(FULL, ok);
+                    ok = stream_sync_and(bar, C::CONV_THREADS, ok);
+                    if (!ok || t >= ptiles) continue;
+                    const int valid = min(TK, cur.key_end - (cur.key_begin + t * TK));
+                    widen_e4m3_tile<D, TK, BF16, C::CONV_THREADS, BLK>(tensor == 0 ? k_tile(gt) : v_tile(gt), valid, stid,
+                                                                       bar, factor);
+                    fence_proxy_async_smem();
+                    ok = stream_sync_and(bar, C::CONV_THREADS, ok);
+                    if (ok && stid == 0) mbar_arrive(tensor == 0 ? &bars->k_full[gt % KST] : &bars->v_full[gt % VST]);
+                }
+            }
+            if (!ok && stid == 0) {
+                *abort_flag = 1;
+                atomicOr(p.status, BSP_DEVFLAG_TIMEOUT);
+            }
+        }
     } else {
         // ================= epilogue warps =================
+        constexpr int EB = BLK ? 1 : 2;         // bytes per pool element
         constexpr int CH = D / 8;               // 16-byte chunks of a K or V row
         constexpr int RPW = 32 / CH;            // tail-tile rows a warp covers per gather step
         constexpr int RS = kRowsPerBlock / CH;  // row step between one thread's gather steps
@@ -713,15 +805,19 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             } else {
                 // the gather runs a few tiles later: bring the row's K and V into L2 now
 #pragma unroll
-                for (int off = 0; off < D * 2; off += 128) {
-                    prefetch_l2(static_cast<const uint8_t*>(p.k_pool) + static_cast<long long>(r) * (D * 2) + off);
-                    prefetch_l2(static_cast<const uint8_t*>(p.v_pool) + static_cast<long long>(r) * (D * 2) + off);
+                for (int off = 0; off < D * EB; off += 128) {
+                    prefetch_l2(static_cast<const uint8_t*>(p.k_pool) + static_cast<long long>(r) * (D * EB) + off);
+                    prefetch_l2(static_cast<const uint8_t*>(p.v_pool) + static_cast<long long>(r) * (D * EB) + off);
+                }
+                if constexpr (BLK) {
+                    prefetch_l2(p.k_exp + (r >> p.block_log2));
+                    prefetch_l2(p.v_exp + (r >> p.block_log2));
                 }
             }
             return r;
         };
-        const uint16_t* k_pool = static_cast<const uint16_t*>(p.k_pool);
-        const uint16_t* v_pool = static_cast<const uint16_t*>(p.v_pool);
+        const uint8_t* k_pool = static_cast<const uint8_t*>(p.k_pool);
+        const uint8_t* v_pool = static_cast<const uint8_t*>(p.v_pool);
         bool ok = true;
         int gt = 0, ntail = 0;
         UnitInfo cur;
@@ -771,11 +867,23 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     // the layout of a TMA box with 128-byte swizzle: chunk kc of row c in column half kc/8
                     const uint32_t off = (kc >> 3) * (TK * 128) + c * 128 + (((kc & 7) ^ (c & 7)) << 4);
                     const long long e = static_cast<long long>(r < 0 ? 0 : r) * D + kc * 8;
-                    const uint32_t nb = r < 0 ? 0u : 16u;  // absent keys are zero rows
-                    cp_async16(kt + off, k_pool + e, nb);
-                    cp_async16(vt + off, v_pool + e, nb);
+                    if constexpr (BLK) {
+                        uint4 kw = make_uint4(0, 0, 0, 0), vw = kw;  // absent keys are zero rows
+                        if (r >= 0) {
+                            const uint32_t kfac = block_factor<BF16>(__ldg(p.k_exp + (r >> p.block_log2)));
+                            const uint32_t vfac = block_factor<BF16>(__ldg(p.v_exp + (r >> p.block_log2)));
+                            kw = widen_e4m3x8<BF16, true>(__ldg(reinterpret_cast<const uint2*>(k_pool + e)), kfac);
+                            vw = widen_e4m3x8<BF16, true>(__ldg(reinterpret_cast<const uint2*>(v_pool + e)), vfac);
+                        }
+                        *reinterpret_cast<uint4*>(kt + off) = kw;
+                        *reinterpret_cast<uint4*>(vt + off) = vw;
+                    } else {
+                        const uint32_t nb = r < 0 ? 0u : 16u;  // absent keys are zero rows
+                        cp_async16(kt + off, k_pool + 2 * e, nb);
+                        cp_async16(vt + off, v_pool + 2 * e, nb);
+                    }
                 }
-                cp_async_commit_wait_all();
+                if constexpr (!BLK) cp_async_commit_wait_all();
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars->fill_done[ntail & 1]);
@@ -903,15 +1011,15 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     }
 }
 
-template <int D, bool BF16, bool SPLIT>
+template <int D, bool BF16, bool SPLIT, bool BLK = false>
 static cudaError_t prepare_prefix_k() {
-    using C = PrefixCfg<D, SPLIT>;
-    static_assert(sizeof(PrefixBarriers) <= 512, "barrier block");
+    using C = PrefixCfg<D, SPLIT, BLK>;
+    static_assert(sizeof(PrefixBarriers<C, BLK>) <= 512, "barrier block");
     static_assert(C::SMEM <= 227 * 1024, "shared memory");
     cudaError_t e =
-        cudaFuncSetAttribute(prefix_attn_kernel<D, BF16, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        cudaFuncSetAttribute(prefix_attn_kernel<D, BF16, SPLIT, BLK>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(prefix_attn_kernel<D, BF16, SPLIT>, cudaFuncAttributePreferredSharedMemoryCarveout,
+    return cudaFuncSetAttribute(prefix_attn_kernel<D, BF16, SPLIT, BLK>, cudaFuncAttributePreferredSharedMemoryCarveout,
                                 cudaSharedmemCarveoutMaxShared);
 }
 
@@ -930,13 +1038,13 @@ static cudaError_t launch_prefix_t(int ctas, const CUtensorMap& tq, const CUtens
     if constexpr (PrefixCfg<D, true>::TK == 128) {
         using CS = PrefixCfg<D, true>;
         if (p.bq > 0) {
-            prefix_attn_kernel<D, BF16, true><<<ctas, CS::THREADS, CS::SMEM, stream>>>(tq, tk, tv, p);
+            prefix_attn_kernel<D, BF16, true, false><<<ctas, CS::THREADS, CS::SMEM, stream>>>(tq, tk, tv, p);
             return cudaGetLastError();
         }
     }
     if (p.bq > 0) return cudaErrorInvalidValue;
     using C = PrefixCfg<D, false>;
-    prefix_attn_kernel<D, BF16, false><<<ctas, C::THREADS, C::SMEM, stream>>>(tq, tk, tv, p);
+    prefix_attn_kernel<D, BF16, false, false><<<ctas, C::THREADS, C::SMEM, stream>>>(tq, tk, tv, p);
     return cudaGetLastError();
 }
 
@@ -959,6 +1067,33 @@ cudaError_t launch_prefix(int head_dim, bool bf16, int ctas, const CUtensorMap& 
                               : launch_prefix_t<128, false>(ctas, tq, tk, tv, p, stream);
         case 256: return bf16 ? launch_prefix_t<256, true>(ctas, tq, tk, tv, p, stream)
                               : launch_prefix_t<256, false>(ctas, tq, tk, tv, p, stream);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t prepare_prefix_blocks(int head_dim, bool bf16) {
+    switch (head_dim) {
+        case 64: return bf16 ? prepare_prefix_k<64, true, true, true>() : prepare_prefix_k<64, false, true, true>();
+        case 128: return bf16 ? prepare_prefix_k<128, true, true, true>() : prepare_prefix_k<128, false, true, true>();
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+template <int D, bool BF16>
+static cudaError_t launch_blocks_t(int ctas, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                   const PrefixParams& p, cudaStream_t stream) {
+    using C = PrefixCfg<D, true, true>;
+    prefix_attn_kernel<D, BF16, true, true><<<ctas, C::THREADS, C::SMEM, stream>>>(tq, tk, tv, p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_prefix_blocks(int head_dim, bool bf16, int ctas, const CUtensorMap& tq, const CUtensorMap& tk,
+                                 const CUtensorMap& tv, const PrefixParams& p, cudaStream_t stream) {
+    if (ctas == 0 || p.num_units == 0) return cudaSuccess;
+    if (p.bq <= 0 || p.bq * p.G > 16) return cudaErrorInvalidValue;
+    switch (head_dim) {
+        case 64: return bf16 ? launch_blocks_t<64, true>(ctas, tq, tk, tv, p, stream) : launch_blocks_t<64, false>(ctas, tq, tk, tv, p, stream);
+        case 128: return bf16 ? launch_blocks_t<128, true>(ctas, tq, tk, tv, p, stream) : launch_blocks_t<128, false>(ctas, tq, tk, tv, p, stream);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -164,7 +164,7 @@ struct BlockFactors {
             if (k < nunits && key < key_end) {
                 const int page = __ldg(p.pages + page_off + (key >> p.ps_log2));
                 if (static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages)) {
-                    const long long row = ((static_cast<long long>(page) * p.Hkv + g) << p.ps_log2) + (key & ((1 << p.ps_log2) - 1));
+                    const int row = ((page * p.Hkv + g) << p.ps_log2) + (key & ((1 << p.ps_log2) - 1));  // (as the loads' rows)
                     x = __ldg(exps + (row >> p.block_log2));
                 }
             }
