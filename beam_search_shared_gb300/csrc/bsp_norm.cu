@@ -13,6 +13,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "../../include/bsp.h"
 #include "bsp_ptx.cuh"
@@ -99,7 +100,8 @@ __device__ __forceinline__ void load_weight(const NormRope& a, const void* weigh
         return;
     }
     if (a.weight_fp32) {
-        const float4 lo = __ldg(static_cast<const float4*>(weight) + 2 * c), hi = __ldg(static_cast<const float4*>(weight) + 2 * c + 1);
+        const float4 lo = __ldg(static_cast<const float4*>(weight) + 2 * c);
+        const float4 hi = __ldg(static_cast<const float4*>(weight) + 2 * c + 1);
         w[0] = pair(lo.x, lo.y), w[1] = pair(lo.z, lo.w), w[2] = pair(hi.x, hi.y), w[3] = pair(hi.z, hi.w);
     } else {
         unpack8<BF16>(__ldg(static_cast<const uint4*>(weight) + c), w);
@@ -126,7 +128,8 @@ __device__ __forceinline__ void load_mix(const NormRope& a, const void* weight, 
     const int half = a.rot >> 1;
     const float* row = a.cos_sin + static_cast<long long>(pos) * a.rot;
     if (a.interleaved) {
-        const float4 x = __ldg(reinterpret_cast<const float4*>(row + 4 * c)), y = __ldg(reinterpret_cast<const float4*>(row + half + 4 * c));
+        const float4 x = __ldg(reinterpret_cast<const float4*>(row + 4 * c));
+        const float4 y = __ldg(reinterpret_cast<const float4*>(row + half + 4 * c));
         const float cs[4] = {x.x, x.y, x.z, x.w}, sn[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -137,8 +140,10 @@ __device__ __forceinline__ void load_mix(const NormRope& a, const void* weight, 
     } else {
         const int hc = a.rot >> 4;  // the partner chunk is hc away
         const int pc = c < hc ? c + hc : c - hc, j = 8 * min(c, pc);
-        const float4 c0 = __ldg(reinterpret_cast<const float4*>(row + j)), c1 = __ldg(reinterpret_cast<const float4*>(row + j + 4));
-        const float4 s0 = __ldg(reinterpret_cast<const float4*>(row + half + j)), s1 = __ldg(reinterpret_cast<const float4*>(row + half + j + 4));
+        const float4 c0 = __ldg(reinterpret_cast<const float4*>(row + j));
+        const float4 c1 = __ldg(reinterpret_cast<const float4*>(row + j + 4));
+        const float4 s0 = __ldg(reinterpret_cast<const float4*>(row + half + j));
+        const float4 s1 = __ldg(reinterpret_cast<const float4*>(row + half + j + 4));
         const float sign = c < hc ? -1.f : 1.f;  // x cos - z sin in the first half, x cos + z sin in the second
         const f2 sg = pair(sign, sign);
         load_weight<BF16>(a, weight, pc, m.B);
@@ -149,24 +154,40 @@ __device__ __forceinline__ void load_mix(const NormRope& a, const void* weight, 
     }
 }
 
-// The lane's 8 elements of a head row (raw: as read), normalised and rotated. Every lane of the warp takes part.
-template <int D, bool BF16>
-__device__ __forceinline__ void norm_rotate(const NormRope& a, const Mix& m, int lane, const uint4& raw, f2 (&f)[4]) {
-    constexpr int CPR = D / 8;
-    const int c = lane & (CPR - 1);
-    f2 x[4];
-    unpack8<BF16>(raw, x);
-    float r = 1.f;
-    if (a.norm) {  // (uniform)
+// 1 / sqrt(mean + eps) of N head rows (raw: a lane's 8 elements as read), on all lanes of a row. Every lane of the warp
+// takes part. The rows' sums go side by side: one after another, each waits for its own shuffles.
+template <int D, bool BF16, int N>
+__device__ __forceinline__ void row_factors(const NormRope& a, const uint4 (&raw)[N], float (&r)[N]) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) r[k] = 1.f;
+    if (!a.norm) return;  // (uniform)
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        f2 x[4];
+        unpack8<BF16>(raw[k], x);
         f2 s2 = mul2(x[0], x[0]);
 #pragma unroll
         for (int e = 1; e < 4; ++e) s2 = fma2(x[e], x[e], s2);
         const float2 s = halves(s2);
-        float ss = s.x + s.y;
-#pragma unroll
-        for (int o = CPR / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
-        r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+        r[k] = s.x + s.y;
     }
+#pragma unroll
+    for (int o = D / 16; o >= 1; o >>= 1) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) r[k] += __shfl_xor_sync(kFull, r[k], o);
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) r[k] = rsqrtf(fmaf(r[k], 1.f / D, a.eps));
+}
+
+// The lane's 8 elements of a head row with the factor r, normalised and rotated. Every lane of the warp takes part.
+template <int D, bool BF16>
+__device__ __forceinline__ void norm_rotate(const NormRope& a, const Mix& m, int lane, const uint4& raw, float r,
+                                            f2 (&f)[4]) {
+    constexpr int CPR = D / 8;
+    const int c = lane & (CPR - 1);
+    f2 x[4];
+    unpack8<BF16>(raw, x);
     const f2 rr = pair(r, r);
     if (!a.cos_sin) {  // (uniform)
 #pragma unroll
@@ -193,6 +214,21 @@ __device__ __forceinline__ void norm_rotate(const NormRope& a, const Mix& m, int
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) f[e] = mul2(rr, fma2(x[e], m.A[e], mul2(z[e], m.B[e])));
+}
+
+// The same for a row by itself.
+template <int D, bool BF16>
+__device__ __forceinline__ void norm_rotate_row(const NormRope& a, const Mix& m, int lane, const uint4& raw,
+                                                f2 (&f)[4]) {
+    const uint4 one[1] = {raw};
+    float r[1];
+    row_factors<D, BF16>(a, one, r);
+    norm_rotate<D, BF16>(a, m, lane, raw, r[0], f);
+}
+
+// A token's rows of n elements into L2, by a warp.
+__device__ __forceinline__ void prefetch_row(const uint16_t* row, int n, int lane) {
+    for (int at = lane * 64; at < n; at += 32 * 64) prefetch_l2(row + at);
 }
 
 // A token's slot (-1: the token is skipped) and position; what is wrong with it is flagged where `tell`.
@@ -253,16 +289,19 @@ __device__ __forceinline__ float lane_top(const f2 (&f)[4]) {
     }
     return m;
 }
-template <int D>
-__device__ __forceinline__ float row_top(float m) {
+template <int D, int N>
+__device__ __forceinline__ void row_tops(float (&m)[N]) {  // (side by side, as row_factors)
 #pragma unroll
-    for (int o = D / 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-    return m;
+    for (int o = D / 16; o >= 1; o >>= 1) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) m[k] = fmaxf(m[k], __shfl_xor_sync(kFull, m[k], o));
+    }
 }
 
 // The run of token i: the tokens next to it whose slots are in its block (block_log2); its place in the run and the
 // run's length. A run has at most 32 tokens.
-__device__ __forceinline__ void find_run(const NormAppendParams& p, int i, int slot, int lane, int* place, int* length) {
+__device__ __forceinline__ void find_run(const NormAppendParams& p, int i, int slot, int lane, int* place,
+                                         int* length) {
     const int block = slot >> p.block_log2;
     auto same = [&](int j) -> bool {
         if (j < 0 || j >= p.a.n) return false;
@@ -277,10 +316,12 @@ __device__ __forceinline__ void find_run(const NormAppendParams& p, int i, int s
 }
 
 constexpr int kItems = 4;  // rows that a lane has in flight
+constexpr int kAbreast = 2;  // ... and works on without a branch between
 
 // Batch b of a token's query rows: kItems groups of RPW heads side by side. m: the mix, made here once (`have`).
 template <int D, bool BF16>
-__device__ __forceinline__ void query_rows(const NormAppendParams& p, int i, int pos, int b, int lane, Mix& m, bool& have) {
+__device__ __forceinline__ void query_rows(const NormAppendParams& p, int i, int pos, int b, int lane, Mix& m,
+                                           bool& have) {
     constexpr int CPR = D / 8, RPW = 32 / CPR;
     const NormRope& a = p.a;
     const int c = lane & (CPR - 1), seg = lane / CPR;
@@ -294,19 +335,22 @@ __device__ __forceinline__ void query_rows(const NormAppendParams& p, int i, int
     }
     if (!have) load_mix<D, BF16>(a, a.q_weight, pos, lane, m);
     have = true;
+    float r[kItems];
+    row_factors<D, BF16>(a, x, r);
     uint16_t* out = static_cast<uint16_t*>(a.q_out) + i * a.q_out_stride + h0 * D + 8 * c;
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
-        if (h0 - seg + k * RPW >= a.Hq) break;  // (uniform)
+        if (k % kAbreast == 0 && h0 - seg + k * RPW >= a.Hq) break;  // (uniform)
         f2 f[4];
-        norm_rotate<D, BF16>(a, m, lane, x[k], f);
+        norm_rotate<D, BF16>(a, m, lane, x[k], r[k], f);
         if (h0 + k * RPW < a.Hq) *reinterpret_cast<uint4*>(out + k * RPW * D) = pack8<BF16>(f);
     }
 }
 
 // Batch b of a token's K (or V) rows, each by itself, to the slot whose row of kv head 0 is `base`.
 template <int D, bool BF16, int POOL, bool IS_V>
-__device__ __forceinline__ void kv_rows(const NormAppendParams& p, int i, int pos, int slot, long long base, int b, int lane, Mix& m, bool& have) {
+__device__ __forceinline__ void kv_rows(const NormAppendParams& p, int i, int pos, int slot, long long base, int b,
+                                        int lane, Mix& m, bool& have) {
     constexpr int CPR = D / 8, RPW = 32 / CPR;
     const NormRope& a = p.a;
     const int c = lane & (CPR - 1), seg = lane / CPR;
@@ -325,44 +369,58 @@ __device__ __forceinline__ void kv_rows(const NormAppendParams& p, int i, int po
         if (h < p.Hkv) {
             x[k] = __ldcs(reinterpret_cast<const uint4*>(src + k * RPW * D));
             // the exponent that the block has, unless the token starts it anew
-            if (POOL == kPoolBlocks && off != 0) old[k] = exps[(base + (static_cast<long long>(h) << p.ps_log2)) >> p.block_log2];
+            if (POOL == kPoolBlocks && off != 0)
+                old[k] = exps[(base + (static_cast<long long>(h) << p.ps_log2)) >> p.block_log2];
         }
     }
     if (!IS_V) {
         if (!have) load_mix<D, BF16>(a, a.k_weight, pos, lane, m);
         have = true;
     }
+    float r[kItems];
+    if constexpr (!IS_V) row_factors<D, BF16>(a, x, r);
 #pragma unroll
-    for (int k = 0; k < kItems; ++k) {
-        const int h = h0 + k * RPW;
-        if (h - seg >= p.Hkv) break;  // (uniform)
-        f2 f[4];
-        if constexpr (!IS_V) norm_rotate<D, BF16>(a, m, lane, x[k], f);
-        else if constexpr (POOL != kPool16) unpack8<BF16>(x[k], f);
-        const long long row = base + (static_cast<long long>(h) << p.ps_log2);
-        if constexpr (POOL == kPool16) {
-            if (h < p.Hkv) {
+    for (int k0 = 0; k0 < kItems; k0 += kAbreast) {
+        if (h0 - seg + k0 * RPW >= p.Hkv) break;  // (uniform)
+        f2 f[kAbreast][4];
+        float top[kAbreast];
+#pragma unroll
+        for (int j = 0; j < kAbreast; ++j) {
+            if constexpr (!IS_V) norm_rotate<D, BF16>(a, m, lane, x[k0 + j], r[k0 + j], f[j]);
+            else if constexpr (POOL != kPool16) unpack8<BF16>(x[k0 + j], f[j]);
+            if constexpr (POOL == kPoolBlocks) top[j] = lane_top(f[j]);
+        }
+        if constexpr (POOL == kPoolBlocks) row_tops<D>(top);
+#pragma unroll
+        for (int j = 0; j < kAbreast; ++j) {
+            const int k = k0 + j, h = h0 + k * RPW;
+            if (h >= p.Hkv) continue;
+            const long long row = base + (static_cast<long long>(h) << p.ps_log2);
+            if constexpr (POOL == kPool16) {
                 uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(pool) + row * D) + c;
                 if constexpr (IS_V) *to = x[k];
-                else *to = pack8<BF16>(f);
+                else *to = pack8<BF16>(f[j]);
+            } else if constexpr (POOL == kPoolE4m3) {
+                const float mul = IS_V ? p.v_mul : p.k_mul;
+                reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + row * D)[c] = quant8(f[j], mul);
+            } else {
+                const int e = block_exponent(p, __float_as_uint(top[j]), old[k]);
+                reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + row * D)[c] = quant8(f[j], code_factor(e));
+                const long long head = row >> p.block_log2;
+                // (0: zeros that start it anew)
+                if (c == 0 && (e != old[k] || e == 0)) exps[head] = static_cast<uint8_t>(e);
+                if (old[k] != 0 && e != old[k])
+                    raise_rows<D>(static_cast<uint8_t*>(pool) + (head << p.block_log2) * D, off, old[k], e, c);
             }
-        } else if constexpr (POOL == kPoolE4m3) {
-            if (h < p.Hkv) reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + row * D)[c] = quant8(f, IS_V ? p.v_mul : p.k_mul);
-        } else {
-            const int e = block_exponent(p, __float_as_uint(row_top<D>(lane_top(f))), old[k]);
-            if (h >= p.Hkv) continue;
-            reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + row * D)[c] = quant8(f, code_factor(e));
-            const long long head = row >> p.block_log2;
-            if (c == 0 && (e != old[k] || e == 0)) exps[head] = static_cast<uint8_t>(e);  // (0: zeros that start it anew)
-            if (old[k] != 0 && e != old[k]) raise_rows<D>(static_cast<uint8_t*>(pool) + (head << p.block_log2) * D, off, old[k], e, c);
         }
     }
 }
 
-// One group of heads of K (or V) over the rows of a run of several tokens from `lead` on: once for the largest magnitude,
-// once for the codes, the second time out of L1 or L2.
+// One group of heads of K (or V) over the rows of a run of several tokens from `lead` on: once for the largest
+// magnitude, once for the codes, the second time out of L1 or L2.
 template <int D, bool BF16>
-__device__ __forceinline__ void run_rows(const NormAppendParams& p, int lead, int length, int slot, int group, bool is_v, int lane) {
+__device__ __forceinline__ void run_rows(const NormAppendParams& p, int lead, int length, int slot, int group,
+                                         bool is_v, int lane) {
     constexpr int CPR = D / 8, RPW = 32 / CPR;
     const NormRope& a = p.a;
     const int c = lane & (CPR - 1), seg = lane / CPR;
@@ -373,24 +431,27 @@ __device__ __forceinline__ void run_rows(const NormAppendParams& p, int lead, in
     const int off = __ldg(a.loc + lead) & ((1 << p.block_log2) - 1);
     const long long head = live ? pool_row(p, slot, h) >> p.block_log2 : 0;  // the block's place in the table
     const int old = live && off != 0 ? exps[head] : 0;
+    const uint16_t* src = static_cast<const uint16_t*>(is_v ? p.v_new : p.k_new);
     auto rows = [&](auto&& each) {
         for (int r = 0; r < length; ++r) {
             uint4 raw = make_uint4(0, 0, 0, 0);
-            if (live) raw = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(is_v ? p.v_new : p.k_new) + (lead + r) * p.src_stride + h * D) + c);
+            if (live) raw = __ldg(reinterpret_cast<const uint4*>(src + (lead + r) * p.src_stride + h * D) + c);
             f2 f[4];
             if (is_v) {
                 unpack8<BF16>(raw, f);
             } else {
                 Mix m;
                 load_mix<D, BF16>(a, a.k_weight, a.cos_sin ? __ldg(a.pos + lead + r) : 0, lane, m);
-                norm_rotate<D, BF16>(a, m, lane, raw, f);
+                norm_rotate_row<D, BF16>(a, m, lane, raw, f);
             }
             each(r, f);
         }
     };
     float top = 0.f;
     rows([&](int, const f2(&f)[4]) { top = fmaxf(top, lane_top(f)); });
-    const int e = block_exponent(p, __float_as_uint(row_top<D>(top)), old);
+    float tops[1] = {top};
+    row_tops<D>(tops);
+    const int e = block_exponent(p, __float_as_uint(tops[0]), old);
     const float mul = code_factor(e);
     rows([&](int r, const f2(&f)[4]) {
         if (live) reinterpret_cast<uint2*>(pool + pool_row(p, __ldg(a.loc + lead + r), h) * D)[c] = quant8(f, mul);
@@ -411,21 +472,21 @@ __device__ __forceinline__ void run_rows(const NormAppendParams& p, int lead, in
 // run of one token (a decode step's) takes the same path, and finds its exponent by shuffles. The warps of a longer run
 // share its groups (run_rows). Nothing is shared between warps. Where a block's exponent grows, its rows before the
 // run are brought to the new one in place.
-// Measured: see launch_norm_append.
+// Bound by latency at a step's sizes (16 query and 8 K and V heads of 128: 4 tokens 2.6 us in a graph, the chain of
+// slot, position, angles and rows; 1920 tokens into 16-bit pools 7.8 us where the bytes take 4.6) and by the scattered
+// row writes at large ones (12288 tokens into 8-bit blocks 45 us, 26 for the bytes: writes of 128 bytes to rows of their
+// own run at about half of the copy rate, in bsp_append.cu too).
+// Seven CTAs an SM: 1920 tokens 7.8 us, 12288 into blocks 44.8; six 9.0 and 45.3, eight 8.1 and 47.1 (spills).
 template <int D, bool BF16, int POOL>
-__global__ void __launch_bounds__(128, 6) norm_append_kernel(const NormAppendParams p) {
+__global__ void __launch_bounds__(128, 7) norm_append_kernel(const NormAppendParams p) {
     const int lane = threadIdx.x & 31;
     const unsigned w = blockIdx.x * 4u + (threadIdx.x >> 5);
     const int i = static_cast<int>(w / p.units), u = static_cast<int>(w - static_cast<unsigned>(i) * p.units);
     if (i >= p.a.n) return;
     if (p.units == 1) {
         // all of the token's rows will be read here: those of the later batches come into L2 meanwhile
-        const uint8_t* v = reinterpret_cast<const uint8_t*>(static_cast<const uint16_t*>(p.v_new) + i * p.src_stride);
-        for (int at = lane * 128; at < p.Hkv * D * 2; at += 32 * 128) prefetch_l2(v + at);
-        if (p.a.q) {
-            const uint8_t* q = reinterpret_cast<const uint8_t*>(static_cast<const uint16_t*>(p.a.q) + i * p.a.q_stride);
-            for (int at = lane * 128; at < p.a.Hq * D * 2; at += 32 * 128) prefetch_l2(q + at);
-        }
+        prefetch_row(static_cast<const uint16_t*>(p.v_new) + i * p.src_stride, p.Hkv * D, lane);
+        if (p.a.q) prefetch_row(static_cast<const uint16_t*>(p.a.q) + i * p.a.q_stride, p.a.Hq * D, lane);
     }
     // lanes 0 to 2 look at the token before, the token and the one behind (only a block's scale asks for the others)
     int pos = 0, slot = -1;
@@ -456,23 +517,30 @@ __global__ void __launch_bounds__(128, 6) norm_append_kernel(const NormAppendPar
     bool have = false;
     int b = first;
     for (; b < p.kv_batches; b += p.units) kv_rows<D, BF16, POOL, false>(p, i, pos, slot, base, b, lane, m, have);
-    for (; b < 2 * p.kv_batches; b += p.units) kv_rows<D, BF16, POOL, true>(p, i, pos, slot, base, b - p.kv_batches, lane, m, have);
+    for (; b < 2 * p.kv_batches; b += p.units)
+        kv_rows<D, BF16, POOL, true>(p, i, pos, slot, base, b - p.kv_batches, lane, m, have);
     have = false;
     for (; b < p.batches; b += p.units) query_rows<D, BF16>(p, i, pos, b - 2 * p.kv_batches, lane, m, have);
 }
 
 // Block scales for tokens that come in runs, a prompt's: a CTA takes the runs that begin among kWindow tokens, of one
 // group of heads, K or V. A run has at most kWindow tokens, so they end within the window behind. Its warps take the
-// tokens in turn, normalise and rotate their rows into shared memory (fp32) and find each run's largest magnitude there;
-// then the rows' codes follow. Each row is read and worked out once, and no CTA depends on another.
+// tokens piece by piece, normalise and rotate their rows into shared memory (fp32) and find each run's largest
+// magnitude there; then the rows' codes follow. Each row is read and worked out once, and no CTA depends on another.
 // The query rows' CTAs are dealt between the others', which wait more than they move.
-// Measured: see launch_norm_append.
+// 3540 prompt tokens, 32 query and 8 K and V heads, blocks of 32: 27 us (12 for the bytes), 18 of them for K and V,
+// bound by the phases of a CTA one after another and a warp's chain for each of its tokens; runs by warps
+// (norm_append_kernel), which read and normalise their rows twice, took 41. Windows of 16 tokens 34 us, four warps 38,
+// sixteen 33.
 constexpr int kWindow = 32;
-constexpr size_t kWindowSmem = 2 * kWindow * 256 * sizeof(float);  // (a group of heads has 256 elements)
+constexpr int kSpan = kWindow + BSP_MAX_SCALE_BLOCK;         // tokens that the runs of a window reach over
+constexpr size_t kWindowSmem = kSpan * 256 * sizeof(float);  // (a group of heads has 256 elements)
+static_assert(kWindow == 32 && kSpan == 64, "two tokens a lane");
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(256, 3) block_window_kernel(const NormAppendParams p, unsigned kv_ctas, unsigned ctas) {
-    constexpr int CPR = D / 8, RPW = 32 / CPR, BATCH = 4;
+__global__ void __launch_bounds__(256, 3) block_window_kernel(const NormAppendParams p, unsigned kv_ctas,
+                                                              unsigned ctas) {
+    constexpr int CPR = D / 8, RPW = 32 / CPR, BATCH = 2;
     const NormRope& a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = lane & (CPR - 1), seg = lane / CPR;
     // CTA x is the y-th for K and V where the running share of those steps up at x
@@ -481,6 +549,7 @@ __global__ void __launch_bounds__(256, 3) block_window_kernel(const NormAppendPa
     if (!kv) {
         const int i = static_cast<int>((blockIdx.x - y) * 8u + warp);  // a warp takes a token's query rows
         if (i >= a.n) return;
+        prefetch_row(static_cast<const uint16_t*>(a.q) + i * a.q_stride, a.Hq * D, lane);
         int pos;
         if (token_slot(p, i, false, &pos) < 0) return;
         Mix m;
@@ -488,97 +557,132 @@ __global__ void __launch_bounds__(256, 3) block_window_kernel(const NormAppendPa
         for (int b = 0; b < p.batches - 2 * p.kv_batches; ++b) query_rows<D, BF16>(p, i, pos, b, lane, m, have);
         return;
     }
-    extern __shared__ f2 s_rows[];                // [2 kWindow][4][32]: pair e of lane l's elements of a token
-    __shared__ int s_slot[2 * kWindow], s_pos[2 * kWindow];
-    __shared__ uint32_t s_lead[2];                // tokens at which a run begins
+    extern __shared__ f2 s_rows[];                // [kSpan][4][32]: pair e of lane l's elements of a token
     __shared__ uint32_t s_top[kWindow][RPW];      // a run's largest magnitude, at its first token
     __shared__ ushort2 s_exp[kWindow][RPW];       // its block's exponent before and after
     const int items = 2 * p.groups;
     const int window = static_cast<int>(y / items), item = static_cast<int>(y - static_cast<unsigned>(window) * items);
     const bool is_v = item >= p.groups;
-    const int h = (is_v ? item - p.groups : item) * RPW + seg;
-    const bool live = h < p.Hkv;
+    const int h0 = (is_v ? item - p.groups : item) * RPW;  // the group's first head
+    const bool live = h0 + seg < p.Hkv;
     const int i0 = window * kWindow;
-    if (tid < 2 * kWindow) {
-        const int i = i0 + tid;
-        int pos = 0, slot = -1, before = -1, unused;
-        if (i < a.n) slot = token_slot(p, i, item == 0 && warp == 0, &pos);
-        if (i >= 1 && i < a.n) before = token_slot(p, i - 1, false, &unused);
-        s_slot[tid] = slot;
-        s_pos[tid] = pos;
-        // (-1 >> n is -1: a token that is skipped is no run's)
-        const uint32_t b = __ballot_sync(kFull, slot >= 0 && (slot >> p.block_log2) != (before >> p.block_log2));
-        if (lane == 0) s_lead[warp] = b;
+    const uint16_t* src = static_cast<const uint16_t*>(is_v ? p.v_new : p.k_new) + i0 * p.src_stride + h0 * D;
+    {
+        // the rows come into L2 while the slots are looked up
+        const int t = tid >> 2, at = 64 * (tid & 3);
+        if (t < kSpan && i0 + t < a.n && h0 * D + at < p.Hkv * D) prefetch_l2(src + t * p.src_stride + at);
     }
     if (tid < kWindow * RPW) s_top[tid / RPW][tid % RPW] = 0u;
+    // every warp looks at all of the tokens, two a lane: their slots, positions and runs stay in registers
+    int slot[2], pos[2] = {0, 0}, run[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int i = i0 + 32 * j + lane;
+        slot[j] = i < a.n ? token_slot(p, i, item == 0 && warp == 0 && j == 0, &pos[j]) : -1;
+    }
+    unsigned long long lead = 0;  // tokens at which a run begins
+    {
+        int before = -1, unused;
+        if (lane == 0 && i0 > 0) before = token_slot(p, i0 - 1, false, &unused);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int up = __shfl_up_sync(kFull, slot[j], 1);
+            if (lane != 0) before = up;
+            else if (j == 1) before = run[0];
+            run[0] = __shfl_sync(kFull, slot[j], 31);  // (for the next half's first lane)
+            // (-1 >> n is -1: a token that is skipped is no run's)
+            const bool leads = slot[j] >= 0 && (slot[j] >> p.block_log2) != (before >> p.block_log2);
+            lead |= static_cast<unsigned long long>(__ballot_sync(kFull, leads)) << (32 * j);
+        }
+    }
+    // the first token of a token's run; -1: of none, or of one that another CTA writes
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int first = 63 - __clzll(lead & (~0ull >> (63 - 32 * j - lane)));
+        run[j] = slot[j] >= 0 && first < kWindow ? first : -1;
+    }
+    auto of = [&](const int (&x)[2], int t) -> int { return __shfl_sync(kFull, t < 32 ? x[0] : x[1], t & 31); };
+    // the tokens from the first to the last of these runs, shared out among the warps piece by piece: a warp's tokens
+    // are of few runs
+    const unsigned long long mine = __ballot_sync(kFull, run[0] >= 0) |
+                                    static_cast<unsigned long long>(__ballot_sync(kFull, run[1] >= 0)) << 32;
+    if (mine == 0) return;  // (every warp finds the same)
+    const int begin = __ffsll(mine) - 1, share = (63 - __clzll(mine) - begin) / 8 + 1;
+    const int t_begin = min(kSpan, begin + warp * share), t_end = min(kSpan, t_begin + share);
     __syncthreads();
-    const uint32_t lead0 = s_lead[0], lead1 = s_lead[1];
-    // the first token of token t's run; -1: of none, or of one that another CTA writes
-    auto run_of = [&](int t) -> int {
-        if (s_slot[t] < 0) return -1;
-        if (t < kWindow) return 31 - __clz(lead0 & (~0u >> (31 - t)));
-        return (lead1 & (~0u >> (63 - t))) ? -1 : 31 - __clz(lead0);
+    int at_run = -1;  // the run that `top` is of
+    float top[1] = {0.f};
+    auto give = [&] {
+        if (at_run < 0) return;
+        row_tops<D>(top);
+        if (c == 0) atomicMax(&s_top[at_run][seg], __float_as_uint(top[0]));  // (not negative: ordered as integers)
     };
-    const uint16_t* src = static_cast<const uint16_t*>(is_v ? p.v_new : p.k_new) + static_cast<long long>(i0) * p.src_stride + h * D + 8 * c;
 #pragma unroll 1
-    for (int t0 = warp; t0 < 2 * kWindow; t0 += 8 * BATCH) {
+    for (int t0 = t_begin; t0 < t_end; t0 += BATCH) {
         uint4 x[BATCH];
-        int run[BATCH];
+        int first[BATCH];
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
-            const int t = t0 + 8 * k;
-            run[k] = run_of(t);  // (uniform)
+            const int t = t0 + k;
+            first[k] = t < t_end ? of(run, t) : -1;  // (uniform)
             x[k] = make_uint4(0, 0, 0, 0);
-            if (run[k] >= 0 && live) x[k] = __ldcs(reinterpret_cast<const uint4*>(src + t * p.src_stride));
+            if (first[k] >= 0 && live) x[k] = __ldcs(reinterpret_cast<const uint4*>(src + t * p.src_stride) + lane);
         }
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
-            if (run[k] < 0) continue;
-            const int t = t0 + 8 * k;
+            if (first[k] < 0) continue;
+            const int t = t0 + k;
             f2 f[4];
             if (is_v) {
                 unpack8<BF16>(x[k], f);
             } else {
                 Mix m;
-                load_mix<D, BF16>(a, a.k_weight, s_pos[t], lane, m);
-                norm_rotate<D, BF16>(a, m, lane, x[k], f);
+                load_mix<D, BF16>(a, a.k_weight, of(pos, t), lane, m);
+                norm_rotate_row<D, BF16>(a, m, lane, x[k], f);
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) s_rows[(t * 4 + e) * 32 + lane] = f[e];
-            const float top = row_top<D>(lane_top(f));
-            if (c == 0) atomicMax(&s_top[run[k]][seg], __float_as_uint(top));  // (not negative: ordered as integers)
+            if (first[k] != at_run) {
+                give();
+                at_run = first[k];
+                top[0] = 0.f;
+            }
+            top[0] = fmaxf(top[0], lane_top(f));
         }
     }
+    give();
     __syncthreads();
     uint8_t* pool = static_cast<uint8_t*>(is_v ? p.v_pool : p.k_pool);
     uint8_t* exps = is_v ? p.v_exp : p.k_exp;
-    if (tid < kWindow * RPW) {
+    if (warp < RPW) {
         // a thread for each run and head
-        const int t = tid / RPW, s = tid % RPW, hs = h - seg + s;
+        const int hs = h0 + warp;
         int e = 0, old = 0;
-        if ((lead0 >> t & 1) && hs < p.Hkv) {
-            uint8_t* at = exps + (pool_row(p, s_slot[t], hs) >> p.block_log2);
-            if ((s_slot[t] & ((1 << p.block_log2) - 1)) != 0) old = *at;
-            e = block_exponent(p, s_top[t][s], old);
+        if ((lead >> lane & 1) && hs < p.Hkv) {
+            uint8_t* at = exps + (pool_row(p, slot[0], hs) >> p.block_log2);
+            if ((slot[0] & ((1 << p.block_log2) - 1)) != 0) old = *at;
+            e = block_exponent(p, s_top[lane][warp], old);
             *at = static_cast<uint8_t>(e);
         }
-        s_exp[t][s] = make_ushort2(static_cast<unsigned short>(old), static_cast<unsigned short>(e));
+        s_exp[lane][warp] = make_ushort2(static_cast<unsigned short>(old), static_cast<unsigned short>(e));
     }
     __syncthreads();
-    if (!live) return;
+    const long long head = static_cast<long long>(h0 + seg) << p.ps_log2;  // rows before the lane's head in a page
 #pragma unroll 2
-    for (int t = warp; t < 2 * kWindow; t += 8) {
-        const int run = run_of(t);
-        if (run < 0) continue;
+    for (int t = t_begin; t < t_end; ++t) {
+        const int first = of(run, t), at = of(slot, t);
+        if (first < 0 || !live) continue;
         f2 f[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) f[e] = s_rows[(t * 4 + e) * 32 + lane];
-        reinterpret_cast<uint2*>(pool + pool_row(p, s_slot[t], h) * D)[c] = quant8(f, code_factor(s_exp[run][seg].y));
+        uint2* to = reinterpret_cast<uint2*>(pool + (pool_row(p, at, 0) + head) * D) + c;
+        *to = quant8(f, code_factor(s_exp[first][seg].y));
     }
     for (int t = warp; t < kWindow; t += 8) {
-        if (!(lead0 >> t & 1)) continue;
-        const int old = s_exp[t][seg].x, e = s_exp[t][seg].y, off = s_slot[t] & ((1 << p.block_log2) - 1);
-        if (old != 0 && e != old) raise_rows<D>(pool + (pool_row(p, s_slot[t], h) - off) * D, off, old, e, c);
+        const int at = of(slot, t);
+        if (!(lead >> t & 1) || !live) continue;
+        const int old = s_exp[t][seg].x, e = s_exp[t][seg].y, off = at & ((1 << p.block_log2) - 1);
+        if (old != 0 && e != old) raise_rows<D>(pool + (pool_row(p, at, h0 + seg) - off) * D, off, old, e, c);
     }
 }
 
@@ -594,13 +698,16 @@ cudaError_t launch_norm_t(NormAppendParams p, PoolKind pools, bool runs, int num
         const long long kv = static_cast<long long>((p.a.n + kWindow - 1) / kWindow) * 2 * p.groups;
         const long long q = p.a.q ? (p.a.n + 7) / 8 : 0;
         if (kv + q > INT32_MAX) return cudaErrorInvalidValue;
-        const cudaError_t e = cudaFuncSetAttribute(block_window_kernel<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWindowSmem);
+        const cudaError_t e = cudaFuncSetAttribute(block_window_kernel<D, BF16>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kWindowSmem);
         if (e != cudaSuccess) return e;
-        block_window_kernel<D, BF16><<<static_cast<unsigned>(kv + q), 256, kWindowSmem, stream>>>(p, static_cast<unsigned>(kv), static_cast<unsigned>(kv + q));
+        const unsigned kv_ctas = static_cast<unsigned>(kv), ctas = static_cast<unsigned>(kv + q);
+        block_window_kernel<D, BF16><<<ctas, 256, kWindowSmem, stream>>>(p, kv_ctas, ctas);
         return cudaGetLastError();
     }
-    // warps of a token: as many as keep the SMs' resident warps (24 of each) busy
-    p.units = std::max(1, std::min(p.batches, 24 * num_sms / p.a.n));
+    // warps of a token: as many as keep the SMs' resident warps (28 of each) busy. Twice as many: 1920 tokens 8.3 us
+    // for 7.8, 3540 tokens 17.9 for 18.4; four times as many: 8.3 and 21.4. 4 tokens with one warp each: 2 us more
+    p.units = std::max(1, std::min(p.batches, 28 * num_sms / p.a.n));
     const long long warps = static_cast<long long>(p.a.n) * p.units;
     if (warps > INT32_MAX) return cudaErrorInvalidValue;
     const unsigned blocks = static_cast<unsigned>((warps + 3) / 4);
@@ -614,13 +721,18 @@ cudaError_t launch_norm_t(NormAppendParams p, PoolKind pools, bool runs, int num
 
 }  // namespace
 
-cudaError_t launch_norm_append(int head_dim, bool bf16, PoolKind pools, bool runs, const NormAppendParams& p, int num_sms,
-                               cudaStream_t stream) {
+cudaError_t launch_norm_append(int head_dim, bool bf16, PoolKind pools, bool runs, const NormAppendParams& p,
+                               int num_sms, cudaStream_t stream) {
     static_assert(BSP_MAX_SCALE_BLOCK <= 32, "a run within a warp's look around");
+    auto by_type = [&](auto dim) {
+        constexpr int D = decltype(dim)::value;
+        return bf16 ? launch_norm_t<D, true>(p, pools, runs, num_sms, stream)
+                    : launch_norm_t<D, false>(p, pools, runs, num_sms, stream);
+    };
     switch (head_dim) {
-        case 64: return bf16 ? launch_norm_t<64, true>(p, pools, runs, num_sms, stream) : launch_norm_t<64, false>(p, pools, runs, num_sms, stream);
-        case 128: return bf16 ? launch_norm_t<128, true>(p, pools, runs, num_sms, stream) : launch_norm_t<128, false>(p, pools, runs, num_sms, stream);
-        case 256: return bf16 ? launch_norm_t<256, true>(p, pools, runs, num_sms, stream) : launch_norm_t<256, false>(p, pools, runs, num_sms, stream);
+        case 64: return by_type(std::integral_constant<int, 64>());
+        case 128: return by_type(std::integral_constant<int, 128>());
+        case 256: return by_type(std::integral_constant<int, 256>());
         default: return cudaErrorInvalidValue;
     }
 }
@@ -654,7 +766,8 @@ __global__ void rope_scaled_kernel(int max_pos, int rot, double base, bsp_rope_s
     cs[static_cast<long long>(pos) * rot + half + j] = __double2float_rn(sn * sc.amplitude);
 }
 
-cudaError_t launch_rope_scaled(int max_pos, int rot, double base, const bsp_rope_scaling& sc, float* cos_sin, cudaStream_t stream) {
+cudaError_t launch_rope_scaled(int max_pos, int rot, double base, const bsp_rope_scaling& sc, float* cos_sin,
+                               cudaStream_t stream) {
     const long long n = static_cast<long long>(max_pos) * (rot / 2), blocks = (n + 255) / 256;
     if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     rope_scaled_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(max_pos, rot, base, sc, cos_sin);
