@@ -67,7 +67,10 @@
 // rows' scales, and complete the slot's full barrier; the epilogue warps widen
 // the tail tiles' rows as they gather them. Two S buffers and three K slots let
 // the widening run beside the softmax: 64 x 30 beams over 500 keys 102 us on the
-// alternating-tile kernel (bsp_alt.cu), 64 here.
+// alternating-tile kernel (bsp_alt.cu), 71 here. A tile takes about 4.5k cycles,
+// the time a pair of warps needs to widen it next to the softmax's instructions
+// (16-bit pools: 2.5k); more or faster widening warps take the softmax's issue
+// slots instead (eight: 71, shared-space accesses with 8 rows in flight: 77 to 88).
 // Every wait is bounded (1 s without progress); on expiry the CTA flags
 // BSP_DEVFLAG_TIMEOUT, drains its own copies and MMAs, frees TMEM and exits.
 #include <cuda.h>
@@ -858,26 +861,51 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 if (lrow_ok) s_tok[n * TK + lrow] = myrow >= 0 ? 1 : 0;
                 uint8_t* kt = k_tile(gtt);
                 uint8_t* vt = v_tile(gtt);
-                // (not unrolled: this code runs next to the softmax's, and a smaller instruction footprint
-                // keeps the softmax loop in the instruction cache)
+                // the layout of a TMA box with 128-byte swizzle: chunk kc of row c in column half kc/8
+                auto chunk_row = [&](int i) -> int { return quad * RPW + lane / CH + i * RS; };
+                auto chunk_off = [&](int c) -> uint32_t {
+                    return (kc >> 3) * (TK * 128) + c * 128 + (((kc & 7) ^ (c & 7)) << 4);
+                };
+                // (the loops over the chunks are not unrolled: this code runs next to the softmax's, and a
+                // smaller instruction footprint keeps the softmax loop in the instruction cache)
+                if constexpr (BLK) {
+                    // kBatch chunks of both tensors in flight: one at a time, every chunk of a thread waits
+                    // for its own reads
+                    constexpr int kBatch = 8;
+                    static_assert(C::TAIL_CHUNKS % kBatch == 0, "batches");
+                    uint32_t kfac = 0, vfac = 0;  // of the lane's resolved row
+                    if (myrow >= 0) {
+                        kfac = block_factor<BF16>(__ldg(p.k_exp + (myrow >> p.block_log2)));
+                        vfac = block_factor<BF16>(__ldg(p.v_exp + (myrow >> p.block_log2)));
+                    }
 #pragma unroll 1
-                for (int i = 0; i < C::TAIL_CHUNKS; ++i) {
-                    const int r = __shfl_sync(FULL, myrow, i * RPW + lane / CH);
-                    const int c = quad * RPW + lane / CH + i * RS;
-                    // the layout of a TMA box with 128-byte swizzle: chunk kc of row c in column half kc/8
-                    const uint32_t off = (kc >> 3) * (TK * 128) + c * 128 + (((kc & 7) ^ (c & 7)) << 4);
-                    const long long e = static_cast<long long>(r < 0 ? 0 : r) * D + kc * 8;
-                    if constexpr (BLK) {
-                        uint4 kw = make_uint4(0, 0, 0, 0), vw = kw;  // absent keys are zero rows
-                        if (r >= 0) {
-                            const uint32_t kfac = block_factor<BF16>(__ldg(p.k_exp + (r >> p.block_log2)));
-                            const uint32_t vfac = block_factor<BF16>(__ldg(p.v_exp + (r >> p.block_log2)));
-                            kw = widen_e4m3x8<BF16, true>(__ldg(reinterpret_cast<const uint2*>(k_pool + e)), kfac);
-                            vw = widen_e4m3x8<BF16, true>(__ldg(reinterpret_cast<const uint2*>(v_pool + e)), vfac);
+                    for (int i0 = 0; i0 < C::TAIL_CHUNKS; i0 += kBatch) {
+                        uint2 kw[kBatch], vw[kBatch];
+#pragma unroll
+                        for (int i = 0; i < kBatch; ++i) {
+                            const int r = __shfl_sync(FULL, myrow, (i0 + i) * RPW + lane / CH);
+                            const long long e = static_cast<long long>(r) * D + kc * 8;
+                            kw[i] = vw[i] = make_uint2(0, 0);  // absent keys are zero rows
+                            if (r >= 0) {
+                                kw[i] = __ldg(reinterpret_cast<const uint2*>(k_pool + e));
+                                vw[i] = __ldg(reinterpret_cast<const uint2*>(v_pool + e));
+                            }
                         }
-                        *reinterpret_cast<uint4*>(kt + off) = kw;
-                        *reinterpret_cast<uint4*>(vt + off) = vw;
-                    } else {
+#pragma unroll
+                        for (int i = 0; i < kBatch; ++i) {
+                            const int from = (i0 + i) * RPW + lane / CH;
+                            const uint32_t off = chunk_off(chunk_row(i0 + i));
+                            const uint32_t kf = __shfl_sync(FULL, kfac, from), vf = __shfl_sync(FULL, vfac, from);
+                            *reinterpret_cast<uint4*>(kt + off) = widen_e4m3x8<BF16, true>(kw[i], kf);
+                            *reinterpret_cast<uint4*>(vt + off) = widen_e4m3x8<BF16, true>(vw[i], vf);
+                        }
+                    }
+                } else {
+#pragma unroll 1
+                    for (int i = 0; i < C::TAIL_CHUNKS; ++i) {
+                        const int r = __shfl_sync(FULL, myrow, i * RPW + lane / CH);
+                        const uint32_t off = chunk_off(chunk_row(i));
+                        const long long e = static_cast<long long>(r < 0 ? 0 : r) * D + kc * 8;
                         const uint32_t nb = r < 0 ? 0u : 16u;  // absent keys are zero rows
                         cp_async16(kt + off, k_pool + 2 * e, nb);
                         cp_async16(vt + off, v_pool + 2 * e, nb);
