@@ -21,7 +21,8 @@ bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
     return x < y + nb && y < x + na;
 }
 
-// What the three appends share: the arguments but for the pools' own, checked, in *a. BSP_OK with a->n = 0: nothing to do.
+// What the three appends share: the arguments but for the pools' own, checked, in *a. BSP_OK with a->n = 0: nothing
+// to do.
 bsp_status check_norm_append(const bsp_plan_t* plan, const bsp_qk_norm* norm, const bsp_rope_config* rope,
                              const int32_t* positions, const void* q, int64_t q_row_stride, void* q_out,
                              int64_t q_out_stride, const void* k_new, const void* v_new, int64_t src_row_stride,
@@ -31,7 +32,8 @@ bsp_status check_norm_append(const bsp_plan_t* plan, const bsp_qk_norm* norm, co
     const int D = geo.head_dim;
     if (n < 0) return BSP_ERR_INVALID_ARG;
     if (norm) {
-        if (!(norm->eps >= 0.f) || !std::isfinite(norm->eps) || !std::isfinite(norm->weight_offset) || norm->reserved != 0 ||
+        if (!(norm->eps >= 0.f) || !std::isfinite(norm->eps) || !std::isfinite(norm->weight_offset) ||
+            norm->reserved != 0 ||
             (norm->weight_fp32 != 0 && norm->weight_fp32 != 1))
             return BSP_ERR_INVALID_ARG;
     }
@@ -42,11 +44,14 @@ bsp_status check_norm_append(const bsp_plan_t* plan, const bsp_qk_norm* norm, co
     }
     if (n == 0) return BSP_OK;
     if (n > plan->total_rows) return BSP_ERR_INVALID_ARG;
-    const int64_t kv_row = static_cast<int64_t>(geo.num_kv_heads) * D, q_row = static_cast<int64_t>(geo.num_q_heads) * D;
+    const int64_t kv_row = static_cast<int64_t>(geo.num_kv_heads) * D;
+    const int64_t q_row = static_cast<int64_t>(geo.num_q_heads) * D;
     if (src_row_stride < kv_row || (src_row_stride & 7)) return BSP_ERR_INVALID_ARG;
-    if (q && (q_row_stride < q_row || (q_row_stride & 7) || q_out_stride < q_row || (q_out_stride & 7))) return BSP_ERR_INVALID_ARG;
+    if (q && (q_row_stride < q_row || (q_row_stride & 7) || q_out_stride < q_row || (q_out_stride & 7)))
+        return BSP_ERR_INVALID_ARG;
     if (!plan_here(plan)) return BSP_ERR_INVALID_ARG;
-    if (!device_ptr(k_new, 16) || !device_ptr(v_new, 16) || !device_ptr(loc, 4) || !device_ptr(k_pool, 16) || !device_ptr(v_pool, 16))
+    if (!device_ptr(k_new, 16) || !device_ptr(v_new, 16) || !device_ptr(loc, 4) || !device_ptr(k_pool, 16) ||
+        !device_ptr(v_pool, 16))
         return BSP_ERR_INVALID_ARG;
     if (q && (!device_ptr(q, 16) || !device_ptr(q_out, 16))) return BSP_ERR_INVALID_ARG;
     if (rope && (!device_ptr(rope->cos_sin, 16) || !device_ptr(positions, 4))) return BSP_ERR_INVALID_ARG;
@@ -54,7 +59,8 @@ bsp_status check_norm_append(const bsp_plan_t* plan, const bsp_qk_norm* norm, co
     if (q && q_out == q && q_out_stride != q_row_stride) return BSP_ERR_INVALID_ARG;
     if (q && q_out != q) {
         const int64_t out = ((n - 1) * q_out_stride + q_row) * 2, kv = ((n - 1) * src_row_stride + kv_row) * 2;
-        if (overlap(q_out, out, q, ((n - 1) * q_row_stride + q_row) * 2) || overlap(q_out, out, k_new, kv) || overlap(q_out, out, v_new, kv))
+        if (overlap(q_out, out, q, ((n - 1) * q_row_stride + q_row) * 2) || overlap(q_out, out, k_new, kv) ||
+            overlap(q_out, out, v_new, kv))
             return BSP_ERR_INVALID_ARG;
     }
     a->loc = loc;
@@ -84,17 +90,18 @@ bsp_status check_norm_append(const bsp_plan_t* plan, const bsp_qk_norm* norm, co
 
 bsp_status norm_append_impl(const bsp_plan_t* plan, const bsp_qk_norm* norm, const bsp_rope_config* rope,
                             const int32_t* positions, const void* q, int64_t q_row_stride, void* q_out,
-                            int64_t q_out_stride, const void* k_new, const void* v_new, int64_t src_row_stride, bool fp8,
-                            float k_mul, float v_mul, const int32_t* loc, int32_t n, void* k_pool, void* v_pool,
-                            void* const* events, void* stream) {
+                            int64_t q_out_stride, const void* k_new, const void* v_new, int64_t src_row_stride,
+                            bool fp8, float k_mul, float v_mul, const int32_t* loc, int32_t n, void* k_pool,
+                            void* v_pool, void* const* events, void* stream) {
     bsp_status st = check_plan(plan);
     if (st != BSP_OK) return st;
     if (!norm) return BSP_ERR_INVALID_ARG;
     if (!fp8 && plan->geo.kv_dtype != BSP_KV_DTYPE_SAME) return BSP_ERR_INVALID_ARG;  // 16-bit pools only
-    if (fp8 && (!std::isfinite(k_mul) || !std::isfinite(v_mul) || !(k_mul > 0.f) || !(v_mul > 0.f))) return BSP_ERR_INVALID_ARG;
+    if (fp8 && (!std::isfinite(k_mul) || !std::isfinite(v_mul) || !(k_mul > 0.f) || !(v_mul > 0.f)))
+        return BSP_ERR_INVALID_ARG;
     NormAppendParams p{};
-    st = check_norm_append(plan, norm, rope, positions, q, q_row_stride, q_out, q_out_stride, k_new, v_new, src_row_stride,
-                           loc, n, k_pool, v_pool, &p.a);
+    st = check_norm_append(plan, norm, rope, positions, q, q_row_stride, q_out, q_out_stride, k_new, v_new,
+                           src_row_stride, loc, n, k_pool, v_pool, &p.a);
     if (st != BSP_OK || p.a.n == 0) return st;
     const bsp_geometry& geo = plan->geo;
     p.k_new = k_new;
@@ -110,7 +117,8 @@ bsp_status norm_append_impl(const bsp_plan_t* plan, const bsp_qk_norm* norm, con
     p.v_mul = v_mul;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (!record_event(events, 0, s)) return BSP_ERR_CUDA;
-    st = launched(launch_norm_append(geo.head_dim, geo.dtype == BSP_DTYPE_BF16, fp8 ? kPoolE4m3 : kPool16, false, p, plan->num_sms, s));
+    st = launched(launch_norm_append(geo.head_dim, geo.dtype == BSP_DTYPE_BF16, fp8 ? kPoolE4m3 : kPool16, false, p,
+                                     plan->num_sms, s));
     if (st != BSP_OK) return st;
     return record_event(events, 1, s) ? BSP_OK : BSP_ERR_CUDA;
 }
@@ -124,10 +132,12 @@ bsp_status check_pages(const bsp_plan_t* plan) {
 }
 int row_bytes(const bsp_geometry& geo) { return geo.head_dim * (geo.kv_dtype == BSP_KV_DTYPE_E4M3 ? 1 : 2); }
 
-bsp_status check_forks(const bsp_plan_t* plan, int64_t beams_stride, int32_t num_forks, int64_t out_stride, int32_t out_cols) {
+bsp_status check_forks(const bsp_plan_t* plan, int64_t beams_stride, int32_t num_forks, int64_t out_stride,
+                       int32_t out_cols) {
     if (plan->kind != 0 || num_forks < 1 || beams_stride < num_forks) return BSP_ERR_INVALID_ARG;
     if (static_cast<int64_t>(plan->batch) * num_forks > BSP_MAX_FORK_ROWS) return BSP_ERR_UNSUPPORTED;
-    if (out_cols < 0 || out_stride < out_cols || out_cols < ceil_div(plan->max_total_len, plan->geo.page_size)) return BSP_ERR_INVALID_ARG;
+    if (out_cols < 0 || out_stride < out_cols || out_cols < ceil_div(plan->max_total_len, plan->geo.page_size))
+        return BSP_ERR_INVALID_ARG;
     return BSP_OK;
 }
 
@@ -140,8 +150,8 @@ bsp_status bsp_norm_rope_append_kv(const bsp_plan_t* plan, const bsp_qk_norm* no
                                    int64_t q_out_stride, const void* k_new, const void* v_new, int64_t src_row_stride,
                                    const int32_t* out_cache_loc, int32_t n, void* k_pool, void* v_pool,
                                    void* const* events, void* stream) {
-    return norm_append_impl(plan, norm, rope, positions, q, q_row_stride, q_out, q_out_stride, k_new, v_new, src_row_stride,
-                            false, 1.f, 1.f, out_cache_loc, n, k_pool, v_pool, events, stream);
+    return norm_append_impl(plan, norm, rope, positions, q, q_row_stride, q_out, q_out_stride, k_new, v_new,
+                            src_row_stride, false, 1.f, 1.f, out_cache_loc, n, k_pool, v_pool, events, stream);
 }
 
 bsp_status bsp_norm_rope_append_kv_fp8(const bsp_plan_t* plan, const bsp_qk_norm* norm, const bsp_rope_config* rope,
@@ -149,8 +159,8 @@ bsp_status bsp_norm_rope_append_kv_fp8(const bsp_plan_t* plan, const bsp_qk_norm
                                        int64_t q_out_stride, const void* k_new, const void* v_new,
                                        int64_t src_row_stride, float k_mul, float v_mul, const int32_t* out_cache_loc,
                                        int32_t n, void* k_pool, void* v_pool, void* const* events, void* stream) {
-    return norm_append_impl(plan, norm, rope, positions, q, q_row_stride, q_out, q_out_stride, k_new, v_new, src_row_stride,
-                            true, k_mul, v_mul, out_cache_loc, n, k_pool, v_pool, events, stream);
+    return norm_append_impl(plan, norm, rope, positions, q, q_row_stride, q_out, q_out_stride, k_new, v_new,
+                            src_row_stride, true, k_mul, v_mul, out_cache_loc, n, k_pool, v_pool, events, stream);
 }
 
 bsp_status bsp_append_kv_fp8_blocks(const bsp_plan_t* plan, const bsp_qk_norm* norm, const bsp_rope_config* rope,
@@ -164,8 +174,8 @@ bsp_status bsp_append_kv_fp8_blocks(const bsp_plan_t* plan, const bsp_qk_norm* n
     st = check_block_scales(scales, geo.page_size, n > 0);
     if (st != BSP_OK) return st;
     NormAppendParams p{};
-    st = check_norm_append(plan, norm, rope, positions, q, q_row_stride, q_out, q_out_stride, k_new, v_new, src_row_stride,
-                           out_cache_loc, n, k_pool, v_pool, &p.a);
+    st = check_norm_append(plan, norm, rope, positions, q, q_row_stride, q_out, q_out_stride, k_new, v_new,
+                           src_row_stride, out_cache_loc, n, k_pool, v_pool, &p.a);
     if (st != BSP_OK || p.a.n == 0) return st;
     if (!device_ptr(scales->k, 16) || !device_ptr(scales->v, 16)) return BSP_ERR_INVALID_ARG;
     const bool bf16 = geo.dtype == BSP_DTYPE_BF16;
@@ -190,15 +200,17 @@ bsp_status bsp_append_kv_fp8_blocks(const bsp_plan_t* plan, const bsp_qk_norm* n
     return record_event(events, 1, s) ? BSP_OK : BSP_ERR_CUDA;
 }
 
-bsp_status bsp_rope_cos_sin_scaled(int32_t max_position, int32_t rotary_dim, double base, const bsp_rope_scaling* scaling,
-                                   float* cos_sin, void* stream) {
+bsp_status bsp_rope_cos_sin_scaled(int32_t max_position, int32_t rotary_dim, double base,
+                                   const bsp_rope_scaling* scaling, float* cos_sin, void* stream) {
     if (max_position <= 0 || rotary_dim < 2 || rotary_dim > 1024 || (rotary_dim & 1)) return BSP_ERR_INVALID_ARG;
     if (!(base > 1.0) || !std::isfinite(base) || !scaling) return BSP_ERR_INVALID_ARG;
     const bsp_rope_scaling& c = *scaling;
     if (c.kind < BSP_ROPE_LINEAR || c.kind > BSP_ROPE_RAMP) return BSP_ERR_UNSUPPORTED;
-    if (!(c.factor > 0) || !std::isfinite(c.factor) || !(c.amplitude > 0) || !std::isfinite(c.amplitude)) return BSP_ERR_INVALID_ARG;
+    if (!(c.factor > 0) || !std::isfinite(c.factor) || !(c.amplitude > 0) || !std::isfinite(c.amplitude))
+        return BSP_ERR_INVALID_ARG;
     if (c.kind == BSP_ROPE_BASE && rotary_dim == 2) return BSP_ERR_INVALID_ARG;
-    if (c.kind >= BSP_ROPE_BANDS && (c.original_positions <= 0 || !(c.low > 0) || !(c.high > c.low) || !std::isfinite(c.high)))
+    if (c.kind >= BSP_ROPE_BANDS &&
+        (c.original_positions <= 0 || !(c.low > 0) || !(c.high > c.low) || !std::isfinite(c.high)))
         return BSP_ERR_INVALID_ARG;
     if (!device_ptr(cos_sin, 16)) return BSP_ERR_INVALID_ARG;
     return launched(launch_rope_scaled(max_position, rotary_dim, base, c, cos_sin, static_cast<cudaStream_t>(stream)));
@@ -225,10 +237,12 @@ bsp_status bsp_fork_tables(const bsp_plan_t* plan, const int32_t* beams, int64_t
     const bsp_geometry& geo = plan->geo;
     if (plan->batch == 0) {  // nothing forks
         if (refs_in == refs_out) return BSP_OK;
-        return launched(cudaMemcpyAsync(refs_out, refs_in, static_cast<size_t>(geo.num_pages) * 4, cudaMemcpyDeviceToDevice, s));
+        return launched(cudaMemcpyAsync(refs_out, refs_in, static_cast<size_t>(geo.num_pages) * 4,
+                                        cudaMemcpyDeviceToDevice, s));
     }
     const int64_t rows = static_cast<int64_t>(plan->batch) * num_forks;
-    if (!device_ptr(beams, 4) || (pages_out_cols > 0 && !device_ptr(pages_out, 4)) || !device_ptr(workspace, 4)) return BSP_ERR_INVALID_ARG;
+    if (!device_ptr(beams, 4) || (pages_out_cols > 0 && !device_ptr(pages_out, 4)) || !device_ptr(workspace, 4))
+        return BSP_ERR_INVALID_ARG;
     if (static_cast<size_t>(rows) * 12 > workspace_bytes) return BSP_ERR_CAPACITY;
     ForkParams p{};
     p.req = section(plan, plan->off_req);
@@ -270,7 +284,8 @@ bsp_status bsp_fork_rows(const bsp_plan_t* plan, const int32_t* beams, int64_t b
     }
     if (static_cast<int64_t>(geo.num_kv_heads) * geo.page_size * row_bytes(geo) > INT32_MAX) return BSP_ERR_UNSUPPORTED;
     if (plan->batch == 0) return BSP_OK;
-    if (!plan_here(plan) || !device_ptr(beams, 4) || !device_ptr(pages_out, 4) || !device_ptr(k_pool, 16) || !device_ptr(v_pool, 16) ||
+    if (!plan_here(plan) || !device_ptr(beams, 4) || !device_ptr(pages_out, 4) || !device_ptr(k_pool, 16) ||
+        !device_ptr(v_pool, 16) ||
         !optional_ptr(beam_pages, 4) || !optional_ptr(cache_indirection, 4))
         return BSP_ERR_INVALID_ARG;
     if ((beam_pages == nullptr) != (cache_indirection == nullptr)) return BSP_ERR_INVALID_ARG;
@@ -333,7 +348,8 @@ bsp_status bsp_compact_tables(const bsp_plan_t* plan, const int32_t* refs_in, in
     bsp_status st = check_pages(plan);
     if (st != BSP_OK) return st;
     if (rows < 0 || cols < 0 || stride < cols) return BSP_ERR_INVALID_ARG;
-    if (!plan_here(plan) || !device_ptr(refs_in, 4) || !device_ptr(refs_out, 4) || !device_ptr(count, 4) || !device_ptr(remap, 4))
+    if (!plan_here(plan) || !device_ptr(refs_in, 4) || !device_ptr(refs_out, 4) || !device_ptr(count, 4) ||
+        !device_ptr(remap, 4))
         return BSP_ERR_INVALID_ARG;
     if (plan->geo.num_pages > 1 && !device_ptr(pairs, 4)) return BSP_ERR_INVALID_ARG;
     if (rows > 0 && cols > 0 && (!device_ptr(tables_in, 4) || !device_ptr(tables_out, 4))) return BSP_ERR_INVALID_ARG;
@@ -365,7 +381,8 @@ bsp_status bsp_copy_pages(const bsp_plan_t* plan, const int32_t* pairs, const in
         if (st != BSP_OK) return st;
     }
     if (max_pairs == 0) return BSP_OK;
-    if (!plan_here(plan) || !device_ptr(pairs, 4) || !device_ptr(count, 4) || !device_ptr(k_pool, 16) || !device_ptr(v_pool, 16))
+    if (!plan_here(plan) || !device_ptr(pairs, 4) || !device_ptr(count, 4) || !device_ptr(k_pool, 16) ||
+        !device_ptr(v_pool, 16))
         return BSP_ERR_INVALID_ARG;
     CopyParams p{};
     p.pairs = pairs;

@@ -75,12 +75,14 @@ struct NormAppendParams {
     int Hkv, ps_log2, num_pages;
     int block_log2, exp_lo, exp_hi;
     float k_mul, v_mul;        // E4M3 pools with one multiplier per tensor
-    // set by launch_norm_append: groups of heads that fill a warp, batches of K (and of V) of a token, all of its batches,
+    // set by launch_norm_append: groups of heads that fill a warp, batches of K (and of V) of a token, all of its
+    // batches,
     // warps of a token
     int groups, kv_batches, batches, units;
 };
 // runs: the tokens are prompts', many of a block next to one another (the kernels differ in speed only)
-cudaError_t launch_norm_append(int head_dim, bool bf16, PoolKind pools, bool runs, const NormAppendParams& p, int num_sms,
+cudaError_t launch_norm_append(int head_dim, bool bf16, PoolKind pools, bool runs, const NormAppendParams& p,
+                               int num_sms,
                                cudaStream_t stream);
 cudaError_t launch_rope_scaled(int max_pos, int rot, double base, const bsp_rope_scaling& sc, float* cos_sin,
                                cudaStream_t stream);

@@ -421,8 +421,8 @@ BSP_API bsp_status bsp_rope_cos_sin_scaled(int32_t max_position, int32_t rotary_
  * The append of a layer that normalises its queries and keys per head, one launch: every K row and query row x of
  * head_dim elements becomes
  *   y = x / sqrt(mean(x^2) + eps) * (w + weight_offset)
- * in fp32, is rotated by its token's position as in bsp_rope_append_kv (rope NULL: not), and is rounded once; K goes to
- * the pool, the query row to q_out. V rows are copied bit for bit (E4M3 pools: quantised as in bsp_append_kv_fp8).
+ * in fp32 (sum of squares too: rows with elements beyond about 1e18 leave its range), is rotated by its token's position
+ * as in bsp_rope_append_kv (rope NULL: not), and is rounded once; K goes to the pool, the query row to q_out. V rows are copied bit for bit (E4M3 pools: quantised as in bsp_append_kv_fp8).
  *   norm            weights and eps; q_weight, k_weight device [head_dim], 16-byte aligned, in the geometry's dtype or
  *                   fp32 (weight_fp32 = 1), or NULL: ones (weight_offset is then not added); eps >= 0, finite
  *   q, q_row_stride NULL, or device [n] rows of num_q_heads * head_dim elements q_row_stride apart
@@ -528,7 +528,8 @@ typedef struct bsp_block_scales {
  * of the geometry's dtype become codes and scales, query rows go to q_out as in bsp_norm_rope_append_kv. The tokens of
  * a call whose slots are in one block form a run and must stand next to one another in ascending order of their slots,
  * as a prompt's or a beam's do; otherwise, and where a skipped token (which is flagged) parts a run, the codes and scale
- * that the block ends up with are unspecified. With top the largest finite or infinite magnitude of the run's rows (of one head, of K or of V):
+ * that the block ends up with are unspecified. With top the largest finite or infinite magnitude of the run's rows (of
+ * one head, of K or of V):
  *  - E is the smallest exponent byte with top <= 448 * 2^(E - 127), within 27 .. 142 (fp16: 112 .. 134): for all but
  *    the largest values nothing saturates; 0 if top is 0;
  *  - a run that begins at the block's first slot starts the block anew with E. Another keeps the rows before it: the
@@ -547,9 +548,9 @@ BSP_API bsp_status bsp_append_kv_fp8_blocks(const bsp_plan_t* plan, const bsp_qk
 
 /*
  * bsp_decode_attn over E4M3 pools with block scales (the plan's geometry has kv_dtype = BSP_KV_DTYPE_E4M3 and head_dim
- * 64 or 128): bsp_decode_attn over the keys and values that the codes and scales stand for, prompt and tail alike. The
- * kernels are those of bsp_decode_attn_fp8; a tile's codes are widened together with their scales, exactly, so the
- * scales cost one byte read per row and no product of their own. Other arguments, flags, events and errors as there.
+ * 64 or 128): bsp_decode_attn over the keys and values that the codes and scales stand for, prompt and tail alike. A
+ * tile's codes are widened together with their scales, exactly, so the scales cost one byte read per row and no product
+ * of their own. Other arguments, flags, events and errors as bsp_decode_attn_fp8.
  */
 BSP_API bsp_status bsp_decode_attn_fp8_blocks(const bsp_plan_t* plan, const void* q, const void* k_pool,
                                               const void* v_pool, const bsp_block_scales* scales,
@@ -870,8 +871,7 @@ BSP_API bsp_status bsp_evict_prefix(const bsp_plan_t* plan, const float* weights
  *   workspace      4-byte aligned device memory of bsp_fork_workspace_size bytes, contents not kept; calls whose GPU
  *                  work overlaps (two graphs too) need one each
  * A row without a beam gets -1 entries and no pages. When the free pages do not suffice, the rows from the first that
- * finds too few on get -1 entries and hold nothing, and BSP_DEVFLAG_PAGES is set (a row that needs no fresh page is
- * served all the same).
+ * finds too few on get -1 entries and hold nothing, whatever they need, and BSP_DEVFLAG_PAGES is set.
  */
 BSP_API bsp_status bsp_fork_workspace_size(int32_t batch, int32_t num_forks, size_t* device_bytes);
 BSP_API bsp_status bsp_fork_tables(const bsp_plan_t* plan, const int32_t* beams, int64_t beams_stride, int32_t num_forks,
