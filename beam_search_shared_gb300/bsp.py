@@ -525,7 +525,8 @@ class BlockScales:
         self.k, self.v = new() if k is None else k, new() if v is None else v
         for name, t in (("k", self.k), ("v", self.v)):
             if t.dtype is not torch.uint8 or tuple(t.shape) != self.shape or not t.is_contiguous():
-                raise ValueError(f"the {name} scales must be contiguous uint8 {list(self.shape)}, not {t.dtype} {list(t.shape)}")
+                raise ValueError(f"the {name} scales must be contiguous uint8 {list(self.shape)}, not {t.dtype} "
+                                 f"{list(t.shape)}")
         self.c = _BlockScales(self.k.data_ptr(), self.v.data_ptr(), self.block, 0)
 
     def _of(self, plan_: Plan):
@@ -566,7 +567,8 @@ class QkNorm:
     def __init__(self, q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
                  weight_offset: float = 0.0):
         given = [w for w in (q_weight, k_weight) if w is not None]
-        if any(w.dim() != 1 or not w.is_contiguous() or w.dtype != given[0].dtype or w.shape != given[0].shape for w in given):
+        if any(w.dim() != 1 or not w.is_contiguous() or w.dtype != given[0].dtype or w.shape != given[0].shape
+               for w in given):
             raise ValueError("q_weight and k_weight must be contiguous vectors of one type and length")
         self.dtype = given[0].dtype if given else None
         self.dim = given[0].shape[0] if given else None
@@ -624,7 +626,8 @@ def _norm_append_args(plan_: Plan, norm, rope, positions, q, q_out, k_new, v_new
     elif q_out is not None:
         raise ValueError("q_out without q")
     if rope is not None:
-        if positions is None or positions.dtype is not torch.int32 or positions.numel() < n or not positions.is_contiguous():
+        if (positions is None or positions.dtype is not torch.int32 or positions.numel() < n or
+                not positions.is_contiguous()):
             raise ValueError(f"positions must be contiguous int32 [{n}]")
     return (ctypes.byref(plan_), None if norm is None else norm._of(plan_),
             None if rope is None else ctypes.byref(rope.config), None if rope is None else positions.data_ptr(),

@@ -1120,8 +1120,12 @@ cudaError_t launch_prefix_blocks(int head_dim, bool bf16, int ctas, const CUtens
     if (ctas == 0 || p.num_units == 0) return cudaSuccess;
     if (p.bq <= 0 || p.bq * p.G > 16) return cudaErrorInvalidValue;
     switch (head_dim) {
-        case 64: return bf16 ? launch_blocks_t<64, true>(ctas, tq, tk, tv, p, stream) : launch_blocks_t<64, false>(ctas, tq, tk, tv, p, stream);
-        case 128: return bf16 ? launch_blocks_t<128, true>(ctas, tq, tk, tv, p, stream) : launch_blocks_t<128, false>(ctas, tq, tk, tv, p, stream);
+        case 64:
+            return bf16 ? launch_blocks_t<64, true>(ctas, tq, tk, tv, p, stream)
+                        : launch_blocks_t<64, false>(ctas, tq, tk, tv, p, stream);
+        case 128:
+            return bf16 ? launch_blocks_t<128, true>(ctas, tq, tk, tv, p, stream)
+                        : launch_blocks_t<128, false>(ctas, tq, tk, tv, p, stream);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -573,8 +573,10 @@ prefix_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                         kfac = block_factor<BF16>(__ldg(p.k_exp + (r >> p.block_log2)));
                                         vfac = block_factor<BF16>(__ldg(p.v_exp + (r >> p.block_log2)));
                                     }
-                                    kw = widen_e4m3x8<BF16, BLK>(__ldg(reinterpret_cast<const uint2*>(k_pool + e)), kfac);
-                                    vw = widen_e4m3x8<BF16, BLK>(__ldg(reinterpret_cast<const uint2*>(v_pool + e)), vfac);
+                                    const uint2 k8 = __ldg(reinterpret_cast<const uint2*>(k_pool + e));
+                                    kw = widen_e4m3x8<BF16, BLK>(k8, kfac);
+                                    const uint2 v8 = __ldg(reinterpret_cast<const uint2*>(v_pool + e));
+                                    vw = widen_e4m3x8<BF16, BLK>(v8, vfac);
                                 }
                                 *reinterpret_cast<uint4*>(kt + off) = kw;
                                 *reinterpret_cast<uint4*>(vt + off) = vw;

@@ -421,8 +421,9 @@ BSP_API bsp_status bsp_rope_cos_sin_scaled(int32_t max_position, int32_t rotary_
  * The append of a layer that normalises its queries and keys per head, one launch: every K row and query row x of
  * head_dim elements becomes
  *   y = x / sqrt(mean(x^2) + eps) * (w + weight_offset)
- * in fp32 (sum of squares too: rows with elements beyond about 1e18 leave its range), is rotated by its token's position
- * as in bsp_rope_append_kv (rope NULL: not), and is rounded once; K goes to the pool, the query row to q_out. V rows are copied bit for bit (E4M3 pools: quantised as in bsp_append_kv_fp8).
+ * in fp32 (sum of squares too: rows with elements beyond about 1e18 leave its range), is rotated by its token's
+ * position as in bsp_rope_append_kv (rope NULL: not), and is rounded once; K goes to the pool, the query row to q_out.
+ * V rows are copied bit for bit (E4M3 pools: quantised as in bsp_append_kv_fp8).
  *   norm            weights and eps; q_weight, k_weight device [head_dim], 16-byte aligned, in the geometry's dtype or
  *                   fp32 (weight_fp32 = 1), or NULL: ones (weight_offset is then not added); eps >= 0, finite
  *   q, q_row_stride NULL, or device [n] rows of num_q_heads * head_dim elements q_row_stride apart
