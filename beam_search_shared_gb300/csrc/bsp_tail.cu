@@ -85,6 +85,7 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 }  // namespace
 
 constexpr int kTailThreads = 128;
+constexpr int kFewMerge = 16, kMerge = 8, kRowMerge = 4;  // KB below: few CTAs, more, CTAs of whole rows
 
 // MAXT: tail rows held in registers, the batch's longest tail rounded up to 2, 4 or 8.
 // MAXP: head passes whose tail state is held in registers across the wait for the prompt kernel
@@ -92,7 +93,9 @@ constexpr int kTailThreads = 128;
 // in groups of MAXP).
 // POOL: E4M3 pools (a lane reads 8 one-byte codes of a row instead of 8 16-bit elements; the keys'
 // scale is folded into scale_log2, the values' scale into the tail's share of O).
-template <int D, bool BF16, int MAXT, int MAXP, PoolKind POOL>
+// KB: prompt partial states (one per key split) that a lane has in flight in the merge, whose order does not depend
+// on it.
+template <int D, bool BF16, int MAXT, int MAXP, int KB, PoolKind POOL>
 __global__ void __launch_bounds__(kTailThreads) tail_merge_kernel(TailParams p) {
     constexpr bool FP8 = POOL != kPool16, BLK = POOL == kPoolBlocks;
     constexpr int LPR = D / 8;       // lanes per K/V row
@@ -241,7 +244,6 @@ __global__ void __launch_bounds__(kTailThreads) tail_merge_kernel(TailParams p) 
         // other partial LSEs in parallel (lane li: splits 1 + li, 1 + li + LPR, ...) and reduce
         // their maximum by shuffles, then the other partial O rows arrive KB splits per round.
         constexpr int KMAX = (kExtraParts + LPR - 1) / LPR;  // unrolled loads: up to kExtraParts more splits
-        constexpr int KB = 4;
         float lse0[MAXP];
         float4 o0a[MAXP], o0b[MAXP];
 #pragma unroll
@@ -344,7 +346,7 @@ __global__ void __launch_bounds__(kTailThreads) tail_merge_kernel(TailParams p) 
     }
 }
 
-template <int D, bool BF16, int MAXT, int MAXP, PoolKind POOL>
+template <int D, bool BF16, int MAXT, int MAXP, int KB, PoolKind POOL>
 static cudaError_t launch_tail_k(const TailParams& p, bool after_prefix, int pass_ctas, cudaStream_t stream) {
     const long long rows = static_cast<long long>(p.B) * p.W;
     cudaLaunchConfig_t cfg = {};
@@ -357,7 +359,7 @@ static cudaError_t launch_tail_k(const TailParams& p, bool after_prefix, int pas
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = after_prefix ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, tail_merge_kernel<D, BF16, MAXT, MAXP, POOL>, p);
+    return cudaLaunchKernelEx(&cfg, tail_merge_kernel<D, BF16, MAXT, MAXP, KB, POOL>, p);
 }
 
 // head passes of a 128-thread CTA: Hq / (4 warps x heads per warp pass)
@@ -384,11 +386,17 @@ template <int D, bool BF16, int MAXT, PoolKind POOL>
 static cudaError_t launch_tail_p(const TailParams& p, bool after_prefix, cudaStream_t stream) {
     const int passes = tail_passes<D>(p.Hq);
     const long long rows = static_cast<long long>(p.B) * p.W;
-    // fewer rows than SMs: one CTA per (row, head pass), so a row's heads merge in parallel
-    if (passes > 1 && rows < device_sms()) return launch_tail_k<D, BF16, MAXT, 1, POOL>(p, after_prefix, passes, stream);
-    if (passes <= 1) return launch_tail_k<D, BF16, MAXT, 1, POOL>(p, after_prefix, 1, stream);
-    if (passes <= 2) return launch_tail_k<D, BF16, MAXT, 2, POOL>(p, after_prefix, 1, stream);
-    return launch_tail_k<D, BF16, MAXT, 4, POOL>(p, after_prefix, 1, stream);
+    // fewer rows than SMs: one CTA per (row, head pass), so a row's heads merge in parallel. With two CTAs an SM at
+    // most, registers are plenty, and each round over the partial states costs its latency: 16 in flight. 10000 keys
+    // of one request: 4 beams of 32 heads 32.9 us with 4 in flight, 26.2 with 8, 20.8 with 16, 96 beams of 16 heads
+    // 44.8, 37.0 and 31.0. More CTAs need the registers: 2 x 60 beams of 32 heads 39.9, 35.6 and 39.0.
+    if (passes <= 1 || rows < device_sms()) {
+        if (rows * passes <= 2ll * device_sms())
+            return launch_tail_k<D, BF16, MAXT, 1, kFewMerge, POOL>(p, after_prefix, passes, stream);
+        return launch_tail_k<D, BF16, MAXT, 1, kMerge, POOL>(p, after_prefix, passes, stream);
+    }
+    if (passes <= 2) return launch_tail_k<D, BF16, MAXT, 2, kRowMerge, POOL>(p, after_prefix, 1, stream);
+    return launch_tail_k<D, BF16, MAXT, 4, kRowMerge, POOL>(p, after_prefix, 1, stream);
 }
 
 template <int D, bool BF16, PoolKind POOL>
@@ -406,12 +414,13 @@ template <int D, bool BF16, int MAXT, PoolKind POOL>
 static cudaError_t prepare_tail_p(int Hq) {
     const cudaFuncAttribute a = cudaFuncAttributePreferredSharedMemoryCarveout;
     const int passes = tail_passes<D>(Hq);
-    // the one-pass variant also serves steps with fewer rows than SMs
-    const cudaError_t e =
-        cudaFuncSetAttribute(tail_merge_kernel<D, BF16, MAXT, 1, POOL>, a, cudaSharedmemCarveoutMaxShared);
+    auto prepared = [&](auto kernel) { return cudaFuncSetAttribute(kernel, a, cudaSharedmemCarveoutMaxShared); };
+    // the one-pass variants also serve steps with fewer rows than SMs
+    cudaError_t e = prepared(tail_merge_kernel<D, BF16, MAXT, 1, kFewMerge, POOL>);
+    if (e == cudaSuccess) e = prepared(tail_merge_kernel<D, BF16, MAXT, 1, kMerge, POOL>);
     if (e != cudaSuccess || passes <= 1) return e;
-    if (passes <= 2) return cudaFuncSetAttribute(tail_merge_kernel<D, BF16, MAXT, 2, POOL>, a, cudaSharedmemCarveoutMaxShared);
-    return cudaFuncSetAttribute(tail_merge_kernel<D, BF16, MAXT, 4, POOL>, a, cudaSharedmemCarveoutMaxShared);
+    if (passes <= 2) return prepared(tail_merge_kernel<D, BF16, MAXT, 2, kRowMerge, POOL>);
+    return prepared(tail_merge_kernel<D, BF16, MAXT, 4, kRowMerge, POOL>);
 }
 
 template <int D, bool BF16, PoolKind POOL>
