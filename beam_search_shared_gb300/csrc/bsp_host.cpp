@@ -1178,8 +1178,8 @@ bsp_status attn_launches(const bsp_plan_t* plan, uint8_t* ws, const void* q, con
     const bool prefix = graph || plan->num_units > 0;
     // A plan over E4M3 pools deals row blocks of up to 128 rows to the alternating-tile kernel. Blocks that the half-row
     // layout holds (16 rows a quadrant) run on the one-set kernel with block scales: its units are the same, and its two
-    // S buffers and third K slot leave the widening room (64 x 30 beams of group 2 over 500 keys, 102 us there and 71;
-    // 1 x 4 of group 4 over 10000, 44 and 42).
+    // S buffers and third K slot leave the widening room (64 x 30 beams of group 2 over 500 keys, 102 us there and 71
+    // here; 2 us less for 1 x 4 of group 4 over 10000).
     const bool half_rows = pools == kPoolBlocks && alt && prefix_quad_beams(D, plan->beams_per_block, G) > 0;
     if (prefix && (half_rows ? prepare_prefix_blocks(D, bf16)
                    : alt     ? prepare_alt(D, bf16, pools)

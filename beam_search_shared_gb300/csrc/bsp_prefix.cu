@@ -67,10 +67,11 @@
 // rows' scales, and complete the slot's full barrier; the epilogue warps widen
 // the tail tiles' rows as they gather them. Two S buffers and three K slots let
 // the widening run beside the softmax: 64 x 30 beams over 500 keys 102 us on the
-// alternating-tile kernel (bsp_alt.cu), 71 here. A tile takes about 4.5k cycles,
-// the time a pair of warps needs to widen it next to the softmax's instructions
-// (16-bit pools: 2.5k); more or faster widening warps take the softmax's issue
-// slots instead (eight: 71, shared-space accesses with 8 rows in flight: 77 to 88).
+// alternating-tile kernel (bsp_alt.cu), 71 here. The softmax is back to back: a
+// tile takes it 2.6k to 4.5k cycles beside the widening, whose conversions share
+// its pipes, and 1.4k to 1.7k over 16-bit pools (43 us). More or faster widening
+// warps gain nothing (eight: 71, shared-space accesses with 8 rows in flight: 77
+// to 88), nor does a warp of its own for V's loads (69 for 69 in a graph).
 // Every wait is bounded (1 s without progress); on expiry the CTA flags
 // BSP_DEVFLAG_TIMEOUT, drains its own copies and MMAs, frees TMEM and exits.
 #include <cuda.h>
