@@ -20,6 +20,23 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kScanThreads = 1024;
 constexpr int kScanCtas = 8;  // of the cluster that scans
+// A pool of up to kSmallPool pages is scanned by a single CTA, a count a thread, without the cluster's barriers:
+// compaction of 96 pages 3.3 us for 6.8, of 1024 3.9 for 7.7 (4096 with four a thread 10.8 for 8.0); forks' tables over
+// 512 pages 4.9 for 7.5 (2048: 7.4 for 7.2).
+constexpr int kSmallPool = kScanThreads;
+// counts of a thread in a round of a scan by CTAS CTAs
+template <int CTAS>
+constexpr int kCounts = CTAS == 1 ? 1 : 4;
+
+template <int CTAS>
+__device__ __forceinline__ void scan_sync() {
+    if constexpr (CTAS == 1) __syncthreads();
+    else cg::this_cluster().sync();
+}
+template <int CTAS>
+__device__ __forceinline__ int scan_rank() {
+    return CTAS == 1 ? 0 : static_cast<int>(cg::this_cluster().block_rank());
+}
 
 // Exclusive running sum over the CTA's threads and the total, in s_warp[33] of shared memory.
 __device__ __forceinline__ int cta_scan(int x, int* s_warp, int* total) {
@@ -64,11 +81,17 @@ __device__ __forceinline__ int cta_sum(int x, int* s_warp) {
 
 // The sum of what the cluster's CTAs hold in `mine` (shared memory, the same variable in each), of those before this
 // one and of all. Every CTA's value is set before and stays until the cluster's next barrier.
-__device__ __forceinline__ int cluster_sum(cg::cluster_group& cl, int* mine, int* all) {
+template <int CTAS>
+__device__ __forceinline__ int cluster_sum(int* mine, int* all) {
+    if constexpr (CTAS == 1) {
+        *all = *mine;
+        return 0;
+    }
+    cg::cluster_group cl = cg::this_cluster();
     int before = 0, sum = 0;
     const unsigned me = cl.block_rank();
 #pragma unroll
-    for (unsigned r = 0; r < kScanCtas; ++r) {
+    for (unsigned r = 0; r < CTAS; ++r) {
         const int x = *cl.map_shared_rank(mine, r);
         if (r < me) before += x;
         sum += x;
@@ -78,8 +101,9 @@ __device__ __forceinline__ int cluster_sum(cg::cluster_group& cl, int* mine, int
 }
 
 // A CTA's share of n items, [lo, hi): even shares in whole vectors of four.
+template <int CTAS>
 __device__ __forceinline__ void share_of(int n, int rank, int* lo, int* hi) {
-    const int per = ((n + kScanCtas - 1) / kScanCtas + 3) & ~3;
+    const int per = ((n + CTAS - 1) / CTAS + 3) & ~3;
     *lo = min(n, rank * per);
     *hi = min(n, *lo + per);
 }
@@ -132,38 +156,39 @@ __device__ __forceinline__ void fork_request_refs(const ForkParams& p, int b, in
     }
 }
 
-// Fork: one cluster. The rows' needs are summed in order, row i = b * num_forks + j, into base[i] (-1: a row without a
-// beam, or one for which the free pages do not suffice); the free pages, lowest first, are listed as far as they are
-// needed. Where the rows are few (`whole`) the cluster goes on to their tables, else fork_tables_kernel does.
-// A few passes over one int per page and per row, bound by their latency: 9 us for 1920 rows, 10.5 with two tables.
-__global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads)
+// Fork: one cluster (or CTA). The rows' needs are summed in order, row i = b * num_forks + j, into base[i] (-1: a row
+// without a beam, or one for which the free pages do not suffice); the free pages, lowest first, are listed as far as
+// they are needed. Where the rows are few (`whole`) it goes on to their tables, else fork_tables_kernel does.
+// A few passes over one int per page and per row, bound by their latency: 9 us for 1920 rows of 64 requests.
+template <int CTAS>
+__global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kScanThreads)
     fork_scan_kernel(const ForkParams p, bool whole) {
     __shared__ int s_warp[33], s_free, s_need;
-    cg::cluster_group cl = cg::this_cluster();
-    const int rank = static_cast<int>(cl.block_rank()), tid = threadIdx.x;
+    constexpr int PER = kCounts<CTAS>;
+    const int rank = scan_rank<CTAS>(), tid = threadIdx.x;
     const bool ok = plan_matches(p.plan_hdr, p.shape);
     if (!ok) {
         if (tid == 0 && rank == 0) atomicOr(p.status, BSP_DEVFLAG_GRAPH);
         return;  // (uniform in the cluster)
     }
     int lo, hi, rlo, rhi;
-    share_of(p.num_pages, rank, &lo, &hi);
-    share_of(p.rows, rank, &rlo, &rhi);
+    share_of<CTAS>(p.num_pages, rank, &lo, &hi);
+    share_of<CTAS>(p.rows, rank, &rlo, &rhi);
     int free = 0, need = 0, full;
-    // a thread's four counts of the share's first round are kept for the second pass
-    int first[4];
-    for (int i0 = lo; i0 < hi; i0 += 4 * kScanThreads) {
-        const int i = i0 + 4 * tid;
-        int r[4];
+    // a thread's counts of the share's first round are kept for the second pass
+    int first[PER];
+    for (int i0 = lo; i0 < hi; i0 += PER * kScanThreads) {
+        const int i = i0 + PER * tid;
+        int r[PER];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < PER; ++e) {
             r[e] = i + e < hi ? p.refs_in[i + e] : 1;
             free += r[e] == 0;
             if (i0 == lo) first[e] = r[e];
         }
         if (p.refs_out != p.refs_in) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < PER; ++e)
                 if (i + e < hi) p.refs_out[i + e] = r[e];
         }
     }
@@ -177,10 +202,10 @@ __global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads
         s_free = free;
         s_need = need;
     }
-    cl.sync();
+    scan_sync<CTAS>();
     int available, wanted;
-    int at = cluster_sum(cl, &s_free, &available);
-    int row_at = cluster_sum(cl, &s_need, &wanted);
+    int at = cluster_sum<CTAS>(&s_free, &available);
+    int row_at = cluster_sum<CTAS>(&s_need, &wanted);
     for (int i0 = rlo; i0 < rhi; i0 += kScanThreads) {
         const int i = i0 + tid;
         int n = 0, total;
@@ -199,18 +224,18 @@ __global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads
         row_at += total;
     }
     const int most = min(wanted, available);  // (pages listed beyond the last served row's stay free)
-    for (int i0 = lo; i0 < hi && at < most; i0 += 4 * kScanThreads) {
-        const int i = i0 + 4 * tid;
+    for (int i0 = lo; i0 < hi && at < most; i0 += PER * kScanThreads) {
+        const int i = i0 + PER * tid;
         int n = 0, total;
-        bool f[4];
+        bool f[PER];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < PER; ++e) {
             f[e] = (i0 == lo ? first[e] : i + e < hi ? p.refs_in[i + e] : 1) == 0;
             n += f[e];
         }
         int k = at + cta_scan(n, s_warp, &total);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < PER; ++e) {
             if (f[e]) {
                 if (k < most) p.fresh[k] = i + e;
                 ++k;
@@ -218,9 +243,9 @@ __global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads
         }
         at += total;
     }
-    cl.sync();  // base, fresh and the counts are complete, and no CTA leaves while another reads its sums
+    scan_sync<CTAS>();  // base, fresh and the counts are complete, and no CTA leaves while another reads its sums
     if (!whole) return;
-    const int warps = kScanCtas * kScanThreads / 32, lane = tid & 31;
+    const int warps = CTAS * kScanThreads / 32, lane = tid & 31;
     for (int x = rank * (kScanThreads / 32) + (tid >> 5); x < p.rows + p.batch; x += warps) {
         if (x < p.rows) fork_row_table(p, x, lane, 32);
         else fork_request_refs(p, x - p.rows, lane);
@@ -395,14 +420,15 @@ __global__ void __launch_bounds__(256) free_pages_kernel(const FreeParams p) {
     for (long long x = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; x < total; x += step)
         free_entry(p, x);
 }
-// The same for few pages and entries, with the copy of the counts before it: one cluster.
-__global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads)
+// The same for few pages and entries, with the copy of the counts before it: one cluster (or CTA).
+template <int CTAS>
+__global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kScanThreads)
     free_few_kernel(const FreeParams p, const int32_t* refs_in) {
     const int at = static_cast<int>(blockIdx.x * kScanThreads + threadIdx.x);
-    for (int i = at; i < p.num_pages; i += kScanCtas * kScanThreads) p.refs_out[i] = refs_in[i];
-    cg::this_cluster().sync();
+    for (int i = at; i < p.num_pages; i += CTAS * kScanThreads) p.refs_out[i] = refs_in[i];
+    scan_sync<CTAS>();
     const int total = p.rows * p.cols;
-    for (int x = at; x < total; x += kScanCtas * kScanThreads) free_entry(p, x);
+    for (int x = at; x < total; x += CTAS * kScanThreads) free_entry(p, x);
 }
 
 // The new id of entry x of the tables. -1 and entries outside the pool are copied as they are.
@@ -414,56 +440,58 @@ __device__ __forceinline__ void remap_entry(const CompactParams& p, long long x)
     p.tables_out[r * p.stride + c] = inside ? p.remap[page] : page;
 }
 
-// Compaction: one cluster, which goes on to the tables where they are short (`whole`). L pages are live; the i-th live
-// page with an id of at least L goes to the i-th free page below L. With before(p) the live pages below p, a free page
-// p < L is hole p - before(p), and a live page p >= L is mover before(p) - before(L): one running count ranks both.
-// Bound by its latency, two sums and a scan: 9 us for 96 pages, 11 for 8192.
-__global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads)
+// Compaction: one cluster (or CTA), which goes on to the tables where they are short (`whole`). L pages are live; the
+// i-th live page with an id of at least L goes to the i-th free page below L. With before(p) the live pages below p, a
+// free page p < L is hole p - before(p), and a live page p >= L is mover before(p) - before(L): one running count
+// ranks both.
+// Bound by its latency, two sums and a scan: 3.3 us for 96 pages on one CTA, 8.5 for 8192 on the cluster.
+template <int CTAS>
+__global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(kScanThreads)
     compact_scan_kernel(const CompactParams p, bool whole) {
     __shared__ int s_warp[33], s_live, s_front;
-    cg::cluster_group cl = cg::this_cluster();
-    const int rank = static_cast<int>(cl.block_rank()), tid = threadIdx.x;
+    constexpr int PER = kCounts<CTAS>;
+    const int rank = scan_rank<CTAS>(), tid = threadIdx.x;
     int lo, hi;
-    share_of(p.num_pages, rank, &lo, &hi);
-    int live = 0, kept[4] = {0, 0, 0, 0};  // a thread's counts of the share's first round stay for the later passes
-    for (int i0 = lo; i0 < hi; i0 += 4 * kScanThreads) {
+    share_of<CTAS>(p.num_pages, rank, &lo, &hi);
+    int live = 0, kept[PER] = {};  // a thread's counts of the share's first round stay for the later passes
+    for (int i0 = lo; i0 < hi; i0 += PER * kScanThreads) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = i0 + 4 * tid + e, r = i < hi ? p.refs_in[i] : 0;
+        for (int e = 0; e < PER; ++e) {
+            const int i = i0 + PER * tid + e, r = i < hi ? p.refs_in[i] : 0;
             live += r > 0;
             if (i0 == lo) kept[e] = r;
         }
     }
     live = cta_sum(live, s_warp);
     if (tid == 0) s_live = live;
-    cl.sync();
+    scan_sync<CTAS>();
     int L;
-    int at = cluster_sum(cl, &s_live, &L);
+    int at = cluster_sum<CTAS>(&s_live, &L);
     int front = 0;  // of the CTA's live pages, those below L
-    for (int i0 = lo; i0 < min(hi, L); i0 += 4 * kScanThreads) {
+    for (int i0 = lo; i0 < min(hi, L); i0 += PER * kScanThreads) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = i0 + 4 * tid + e;
+        for (int e = 0; e < PER; ++e) {
+            const int i = i0 + PER * tid + e;
             if (i < min(hi, L)) front += (i0 == lo ? kept[e] : p.refs_in[i]) > 0;
         }
     }
     front = cta_sum(front, s_warp);
     if (tid == 0) s_front = front;
-    cl.sync();
+    scan_sync<CTAS>();
     int A;  // before(L)
-    cluster_sum(cl, &s_front, &A);
-    for (int i0 = lo; i0 < hi; i0 += 4 * kScanThreads) {
-        const int i = i0 + 4 * tid;
+    cluster_sum<CTAS>(&s_front, &A);
+    for (int i0 = lo; i0 < hi; i0 += PER * kScanThreads) {
+        const int i = i0 + PER * tid;
         int n = 0, total;
-        int r[4];
+        int r[PER];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < PER; ++e) {
             r[e] = i0 == lo ? kept[e] : i + e < hi ? p.refs_in[i + e] : 0;
             n += r[e] > 0;
         }
         int before = at + cta_scan(n, s_warp, &total);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < PER; ++e) {
             const int page = i + e;
             if (page < hi) {
                 p.remap[page] = page;
@@ -482,16 +510,16 @@ __global__ void __cluster_dims__(kScanCtas, 1, 1) __launch_bounds__(kScanThreads
         p.count[0] = L - A;
         p.count[1] = L;
     }
-    cl.sync();  // the pairs are complete, and no CTA leaves while another reads its sums
-    for (int k = rank * kScanThreads + tid; k < L - A; k += kScanCtas * kScanThreads) {
+    scan_sync<CTAS>();  // the pairs are complete, and no CTA leaves while another reads its sums
+    for (int k = rank * kScanThreads + tid; k < L - A; k += CTAS * kScanThreads) {
         const int from = p.pairs[2ll * k], to = p.pairs[2ll * k + 1];
         p.remap[from] = to;
         p.refs_out[to] = p.refs_in[from];
         p.refs_out[from] = 0;
     }
     if (!whole) return;  // (uniform)
-    cl.sync();  // remap is complete
-    for (int x = rank * kScanThreads + tid; x < p.rows * p.cols; x += kScanCtas * kScanThreads) remap_entry(p, x);
+    scan_sync<CTAS>();  // remap is complete
+    for (int x = rank * kScanThreads + tid; x < p.rows * p.cols; x += CTAS * kScanThreads) remap_entry(p, x);
 }
 
 // The entries of longer tables.
@@ -552,10 +580,12 @@ unsigned grid_for(long long items, int sms) {
 }  // namespace
 
 cudaError_t launch_fork_tables(const ForkParams& p, cudaStream_t stream) {
-    // up to four rows (or requests) for each of the cluster's warps: one launch instead of two (two beams of one
+    // up to four rows (or requests) for each of the scan's warps: one launch instead of two (two beams of one
     // request forked, rows too, 24.6 -> 18.3 us a call); 1920 rows are served better by a grid of their own
-    const bool whole = p.rows + p.batch <= 4 * kScanCtas * kScanThreads / 32;
-    fork_scan_kernel<<<kScanCtas, kScanThreads, 0, stream>>>(p, whole);
+    const int all = p.rows + p.batch, warps = kScanThreads / 32;
+    const bool small = p.num_pages <= kSmallPool && all <= 4 * warps, whole = all <= 4 * kScanCtas * warps;
+    if (small) fork_scan_kernel<1><<<1, kScanThreads, 0, stream>>>(p, true);
+    else fork_scan_kernel<kScanCtas><<<kScanCtas, kScanThreads, 0, stream>>>(p, whole);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || whole) return e;
     fork_tables_kernel<<<(p.rows + p.batch + 7) / 8, 256, 0, stream>>>(p);
@@ -581,7 +611,10 @@ cudaError_t launch_free_pages(const FreeParams& p, const int32_t* refs_in, int n
     // pages: 28.3 -> 21.3 us)
     const int few = 8 * kScanCtas * kScanThreads;
     if (refs_in != p.refs_out && p.num_pages <= few && total <= few) {
-        free_few_kernel<<<kScanCtas, kScanThreads, 0, stream>>>(p, refs_in);
+        if (p.num_pages <= kSmallPool && total <= 8 * kScanThreads)
+            free_few_kernel<1><<<1, kScanThreads, 0, stream>>>(p, refs_in);
+        else
+            free_few_kernel<kScanCtas><<<kScanCtas, kScanThreads, 0, stream>>>(p, refs_in);
         return cudaGetLastError();
     }
     if (refs_in != p.refs_out) {
@@ -596,8 +629,11 @@ cudaError_t launch_free_pages(const FreeParams& p, const int32_t* refs_in, int n
 
 cudaError_t launch_compact_tables(const CompactParams& p, int num_sms, cudaStream_t stream) {
     const long long total = static_cast<long long>(p.rows) * p.cols;
-    const bool whole = total <= 8 * kScanCtas * kScanThreads;  // eight for each of the cluster's threads
-    compact_scan_kernel<<<kScanCtas, kScanThreads, 0, stream>>>(p, whole);
+    // (eight entries for each of the scan's threads)
+    const bool small = p.num_pages <= kSmallPool && total <= 8 * kScanThreads;
+    const bool whole = total <= 8 * kScanCtas * kScanThreads;
+    if (small) compact_scan_kernel<1><<<1, kScanThreads, 0, stream>>>(p, true);
+    else compact_scan_kernel<kScanCtas><<<kScanCtas, kScanThreads, 0, stream>>>(p, whole);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || whole) return e;
     remap_tables_kernel<<<grid_for(total, num_sms), 256, 0, stream>>>(p);

@@ -296,3 +296,37 @@ def test_replayed_fork_follows_later_plans_and_refuses_others():
     g.replay()
     assert bsp.read_device_status(one) == (5, bsp.DEVFLAG_GRAPH)
     assert (f.out == -7).all()
+
+
+@pytest.mark.parametrize("pages", [1023, 1024, 1025, 2049])
+def test_pools_around_the_size_that_one_cta_scans(pages):
+    rs = np.random.RandomState(pages)
+    geo = bsp.geometry(2, 1, 64, 8, pages, "bf16")
+    ws = bsp.Workspace(geo, 1, 4, 1)
+    plan = ws.plan(geo, 1, 4, [3], [6], [[5]])   # nine positions: two fresh pages a fork
+    refs = rs.randint(0, 3, pages).astype(np.int32)
+    refs[5] = 1
+    gone = rs.randint(-1, pages, (9, 60)).astype(np.int32)
+    dev = torch.from_numpy(refs).cuda()
+    bsp.free_pages(plan, torch.from_numpy(gone).cuda(), dev, freed := torch.empty_like(dev))
+    want = cache.free_pages(refs, gone)
+    np.testing.assert_array_equal(freed.cpu().numpy(), want)
+    bsp.read_device_status(plan)                 # (more were given back than there were)
+    want[5] = 1
+    freed.copy_(torch.from_numpy(want))
+    beams = np.array([[0, 3, -1, 1]], np.int32)
+    table = torch.full((4, 3), -7, dtype=torch.int32, device="cuda")
+    bsp.fork_tables(plan, torch.from_numpy(beams).cuda(), freed, freed, table, bsp.fork_workspace(1, 4))
+    counts, out, _, _ = cache.fork_tables([3], [6], [[5]], beams, 4, 8, want, np.full((4, 3), -7))
+    np.testing.assert_array_equal(table.cpu().numpy(), out)
+    np.testing.assert_array_equal(freed.cpu().numpy(), counts)
+    moves, tables = bsp.PageMoves(pages), rs.randint(-1, pages, (7, 11)).astype(np.int32)
+    renamed = torch.from_numpy(tables).cuda()
+    bsp.compact_tables(plan, freed, freed, moves, renamed)
+    after, pairs, live, remap, named = cache.compact(counts, tables)
+    assert moves.count.tolist() == [len(pairs), live]
+    np.testing.assert_array_equal(moves.pairs[:len(pairs)].cpu().numpy(), np.array(pairs).reshape(-1, 2))
+    np.testing.assert_array_equal(freed.cpu().numpy(), after)
+    np.testing.assert_array_equal(moves.remap.cpu().numpy(), remap)
+    np.testing.assert_array_equal(renamed.cpu().numpy(), named)
+    assert bsp.read_device_status(plan) == (0, 0)
