@@ -13,7 +13,9 @@
  *                   returning O and LSE.
  * Around it: bsp_process_logits, bsp_beam_select and bsp_beam_advance take the
  * step's logits to the next step's beams; bsp_key_weights and bsp_evict_prefix
- * shorten the prompts' cache to the rows that the attention looked at.
+ * shorten the prompts' cache to the rows that the attention looked at. For the
+ * cache itself: appends that normalise and rotate, E4M3 pools with block scales
+ * and their attention, and pages forked, given back, compacted and copied.
  * The method: TensorRT-LLM PR #21738, "Add opt-in cascade attention for wide
  * beam search on KVCM V2" (description, "Solution"); the valid-prefix bound:
  * TensorRT-Model-Connect PR #2202, "prefill and decode over the cached prefix,
@@ -615,8 +617,10 @@ BSP_API bsp_status bsp_prefill_attn(const bsp_plan_t* plan, const void* q, const
 /*
  * Synchronises `stream`, then reads the workspace's device status word into
  * *flags_out (BSP_DEVFLAG_* bits set by kernels since the last clear) and
- * clears it when `clear` is non-zero. Returns BSP_ERR_PAGE_INDEX or
- * BSP_ERR_DEVICE_TIMEOUT when a bit is set, BSP_OK otherwise.
+ * clears it when `clear` is non-zero. Returns, for the bits that are set, the
+ * first of BSP_ERR_PAGE_INDEX, BSP_ERR_STALE_PLAN (BSP_DEVFLAG_GRAPH),
+ * BSP_ERR_CAPACITY (BSP_DEVFLAG_PAGES) and BSP_ERR_DEVICE_TIMEOUT; BSP_OK when
+ * there are none.
  */
 BSP_API bsp_status bsp_read_device_status(const bsp_plan_t* plan, void* stream, int32_t clear, int32_t* flags_out);
 
