@@ -93,12 +93,12 @@ __device__ __forceinline__ uint32_t block_factor(uint32_t e) {
         const uint32_t c = min(max(e, 112u), 134u);
         f = c == 112u ? 0x0200u : (c - 112u) << 10;  // 2^-15 is half of the smallest normal number
     }
-    return f | (f << 16);
+    return e == 0 ? 0u : f | (f << 16);  // (a block that nothing was written to reads as 0)
 }
 // The same scale in fp32 (0 for a block that nothing was written to).
 template <bool BF16>
 __device__ __forceinline__ float block_scale(uint32_t e) {
-    return __uint_as_float((BF16 ? min(e, 142u) : min(max(e, 112u), 134u)) << 23);
+    return e == 0 ? 0.f : __uint_as_float((BF16 ? min(e, 142u) : min(max(e, 112u), 134u)) << 23);
 }
 // e4m3x2_to_16 times a block's scale, exact where the product is a number of the type (bfloat16: all but the
 // smallest scales' products below 2^-133).

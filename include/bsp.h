@@ -512,7 +512,7 @@ BSP_API bsp_status bsp_decode_attn_fp8(const bsp_plan_t* plan, const void* q, co
 /*
  * E4M3 pools with block scales: each block of `block` consecutive slots of a (page, kv head) has a scale of its own
  * for K and for V, a power of two kept as its exponent byte E: element x of the block stands for
- * e4m3(x) * 2^(E - 127). E = 0 means that nothing has been written to the block (its codes are read as 0). An 8-bit
+ * e4m3(x) * 2^(E - 127). E = 0 means that nothing has been written to the block (its codes are read as 0, those of NaN as NaN). An 8-bit
  * float loses nothing by a power of two, so the scale only places its range; it can be changed without rounding the
  * codes again (but for those that leave the range below), and the product is exact in 16 bits: bf16 takes exponents
  * E - 127 up to 15, fp16 those in [-15, 7]; larger ones (fp16: smaller ones too) are read as the nearest of these.

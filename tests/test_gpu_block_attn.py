@@ -217,3 +217,22 @@ def test_refusals():
         call(st.scales, plan=p16)
     torch.cuda.synchronize()
     assert torch.isnan(st.o).all()
+
+
+@pytest.mark.parametrize("name,dtype", [("qwen3_0p6b_b64_w30", "bf16"), ("qwen3_0p6b_b64_w30", "fp16"),
+                                        ("wide_beam_b128_w96", "fp16"), ("qwen3_4b_fp16_d128", "fp16")])
+@pytest.mark.parametrize("tails", [None, 8])
+def test_blocks_that_were_never_written_read_as_zero_whatever_they_hold(name, dtype, tails):
+    """Cleared exponents over codes of the largest magnitude: values of 0 give rows of exactly 0, keys of 0 scores of 0."""
+    wl = synth.WORKLOADS[name].scaled(2).with_(dtype=dtype)
+    st = BlockStep(synth.make_case(wl, 41, full_step=False, device="cpu",
+                                   tail_lengths=None if tails is None else [tails] * wl.batch), 42, 8)
+    st.kd.fill_(0x7e)
+    st.vd.fill_(0x7e)
+    st.scales.k.zero_()
+    st.scales.v.zero_()
+    st.attend()
+    assert (st.o == 0).all()
+    keys = torch.from_numpy(np.repeat(st.case.prefix_len + st.case.tail_len, wl.beam_width)).cuda()
+    # a sum of up to 10^4 ones in fp32 parts, and two logarithms of a few units in the last place
+    assert (st.lse - keys.double().log()[:, None]).abs().max() <= 2.0 ** -18
