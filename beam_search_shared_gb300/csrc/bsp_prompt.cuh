@@ -84,16 +84,17 @@ __device__ __forceinline__ uint32_t e4m3x2_to_16(uint32_t two) {
 // bfloat16: 2^112 * 2^(E - 127), one exponent field of E + 112 (E up to 142, a scale of 2^15), so that the scale costs no
 // multiplication of its own. binary16: 2^(E - 127) for exponents in [-15, 7], with which every product is a number of
 // the type: |code| <= 448 * 2^7 < 2^16, and the smallest step of a code, 2^-9, gives a multiple of 2^-24.
+// A block that nothing was written to (E = 0) reads as 0.
 template <bool BF16>
 __device__ __forceinline__ uint32_t block_factor(uint32_t e) {
     uint32_t f;
     if constexpr (BF16) {
-        f = (min(e, 142u) + 112u) << 7;
+        f = (e == 0 ? 0u : min(e, 142u) + 112u) << 7;
     } else {
         const uint32_t c = min(max(e, 112u), 134u);
-        f = c == 112u ? 0x0200u : (c - 112u) << 10;  // 2^-15 is half of the smallest normal number
+        f = e == 0 ? 0u : c == 112u ? 0x0200u : (c - 112u) << 10;  // 2^-15 is half of the smallest normal number
     }
-    return e == 0 ? 0u : f | (f << 16);  // (a block that nothing was written to reads as 0)
+    return f | (f << 16);
 }
 // The same scale in fp32 (0 for a block that nothing was written to).
 template <bool BF16>
