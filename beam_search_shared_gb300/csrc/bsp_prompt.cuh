@@ -62,21 +62,29 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 
 // ---- E4M3 pools: the kernels load E4M3 tiles and widen them to the q dtype in shared memory
 
-// Two E4M3 codes (bits 0-7 and 8-15 of `two`) as a pair of 16-bit floats of the q dtype, the first in the
-// low half, exactly: every E4M3 value is a binary16 and a bfloat16 value. The hardware conversion gives
-// binary16; for bfloat16 the binary16 sign, exponent and fraction fields move into bfloat16 fields (the
-// exponent keeps its binary16 bias of 15 instead of 127: a factor 2^-112), and one multiplication by
-// 2^112 restores the value. E4M3-derived binary16 values are zero or normal (the smallest, 2^-9, has
-// exponent field 6), so the shifted bfloat16 value is zero or normal too and the product is exact.
+// Two E4M3 codes (bits 0-7 and 8-15 of `two`) as bfloat16 values times 2^-112, the first in the low half: the
+// hardware conversion gives binary16, and the binary16 sign, exponent and fraction fields move into bfloat16
+// fields (the exponent keeps its binary16 bias of 15 instead of 127). E4M3-derived binary16 values are zero or
+// normal (the smallest, 2^-9, has exponent field 6) with the fraction's low 7 bits zero, so the shifted values
+// are exact, zero or normal. A product with 0 gives each half's sign bit, and 0x7fff for a NaN code, whose
+// exponent field would be that of a number once shifted; the mask cuts what the upper half's fraction (of a
+// NaN) moves into the lower half.
+__device__ __forceinline__ uint32_t e4m3x2_shifted(uint32_t two) {
+    uint32_t h, z;
+    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h) : "r"(two));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(z) : "r"(h), "r"(0u));
+    return ((h >> 3) & 0x0fff0fffu) | z;
+}
+
+// Two E4M3 codes as a pair of 16-bit floats of the q dtype, exactly: every E4M3 value is a binary16 and a
+// bfloat16 value, and one multiplication by 2^112 restores the shifted one. NaN codes give NaN.
 template <bool BF16>
 __device__ __forceinline__ uint32_t e4m3x2_to_16(uint32_t two) {
-    uint32_t h;
-    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h) : "r"(two));
-    if constexpr (!BF16) return h;
-    // the fraction's low 7 bits are zero for these values, so nothing crosses from one half to the other
-    const uint32_t t = ((h & 0x7fff7fffu) >> 3) | (h & 0x80008000u);
     uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(t), "r"(0x77807780u));  // 2^112 in both halves
+    if constexpr (BF16)
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(e4m3x2_shifted(two)), "r"(0x77807780u));  // 2^112 in both halves
+    else
+        asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(r) : "r"(two));
     return r;
 }
 
@@ -102,17 +110,12 @@ __device__ __forceinline__ float block_scale(uint32_t e) {
     return e == 0 ? 0.f : __uint_as_float((BF16 ? min(e, 142u) : min(max(e, 112u), 134u)) << 23);
 }
 // e4m3x2_to_16 times a block's scale, exact where the product is a number of the type (bfloat16: all but the
-// smallest scales' products below 2^-133).
+// smallest scales' products below 2^-133). NaN codes give NaN under every factor, 0 among them.
 template <bool BF16>
 __device__ __forceinline__ uint32_t scaled_e4m3x2(uint32_t two, uint32_t factor) {
-    uint32_t h, r;
-    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h) : "r"(two));
-    if constexpr (BF16) {
-        const uint32_t t = ((h & 0x7fff7fffu) >> 3) | (h & 0x80008000u);
-        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(t), "r"(factor));
-    } else {
-        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(factor));
-    }
+    uint32_t r;
+    if constexpr (BF16) asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(e4m3x2_shifted(two)), "r"(factor));
+    else asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(e4m3x2_to_16<false>(two)), "r"(factor));
     return r;
 }
 // 8 E4M3 codes (bytes in order) -> one 16-byte chunk of 8 16-bit values

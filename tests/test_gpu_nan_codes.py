@@ -1,0 +1,137 @@
+"""NaN codes (0x7f, 0xff) of E4M3 pools: a NaN in a key that a row attends makes the row's output and log-sum-exp NaN, a
+NaN in a value the output's element of that column, whatever kernel reads the tile; every other number stays bit for bit
+what it is without the NaN. Blocks with an exponent of 0 keep their NaN codes too.
+"""
+import numpy as np
+import pytest
+import torch
+
+from beam_search_shared_gb300 import bsp, synth
+from test_gpu_block_attn import BlockStep
+from test_gpu_fp8_attn import Fp8Step
+
+pytestmark = pytest.mark.gpu
+
+
+def step(scales, name, batch, kw, **lengths):
+    """A BlockStep (block of 8 slots) or an Fp8Step. Beams that are even read beam 1's tail rows, the others beam 0's."""
+    wl = synth.WORKLOADS[name].scaled(batch).with_(**kw)
+    case = synth.make_case(wl, 900 + batch, full_step=False, device="cpu", **lengths)
+    for b in range(batch):
+        P, T = int(case.prefix_len[b]), int(case.tail_len[b])
+        case.cache_indirection[b, ::2, P:P + T] = min(1, wl.beam_width - 1)
+        case.cache_indirection[b, 1::2, P:P + T] = 0
+    return BlockStep(case, 901, 8) if scales == "blocks" else Fp8Step(case, 901, 0.5, 1.5)
+
+
+def attend(st):
+    st.o.fill_(-7.0)
+    st.lse.fill_(-7.0)
+    st.attend(flags=bsp.FLAG_CHECK)
+    return st.o.clone(), st.lse.clone()
+
+
+def prompt_slot(st, b, i):
+    ps = st.case.workload.page_size
+    return int(st.case.prefix_pages[b, i // ps]), i % ps
+
+
+def tail_slot(st, b, src, t):
+    ps, W = st.case.workload.page_size, st.case.workload.beam_width
+    pos = int(st.case.prefix_len[b]) + t
+    return int(st.case.beam_pages[b * W + src, pos // ps]), pos % ps
+
+
+def put(st, pool, at, head, col, code, cleared):
+    pool[at[0], head, at[1], col] = code
+    if cleared:
+        exps = st.scales.k if pool is st.kd else st.scales.v
+        exps[at[0], head, at[1] // 8] = 0
+
+
+def check(st, clean, got, rows=None, elements=None):
+    """NaN where `rows` [R, Hq] (output and log-sum-exp) and `elements` [R, Hq, D] (output) say, else as before."""
+    o, lse = got
+    rows = torch.zeros_like(lse, dtype=torch.bool) if rows is None else rows.cuda()
+    bad = rows[..., None].expand_as(o)
+    if elements is not None:
+        bad = bad | elements.cuda()
+    assert torch.isnan(lse[rows]).all() and torch.equal(lse[~rows], clean[1][~rows])
+    assert torch.isnan(o[bad]).all(), int((~torch.isnan(o[bad])).sum())
+    assert torch.equal(o[~bad], clean[0][~bad])
+
+
+# scales, workload, batch, changes to it: what a prompt tile is read by
+TILES = [
+    ("blocks", "qwen3_0p6b_b64_w30", 2, {}),                                        # one-set kernel
+    ("blocks", "qwen3_0p6b_b64_w30", 2, dict(dtype="fp16")),
+    ("blocks", "qwen3_0p6b_b64_w30", 2, dict(head_dim=64)),
+    ("blocks", "qwen3_0p6b_b64_w30", 2, dict(beam_width=42)),                       # alternating tiles
+    ("blocks", "qwen3_0p6b_b64_w30", 2, dict(beam_width=42, dtype="fp16")),
+    ("blocks", "qwen3_0p6b_b64_w30", 2, dict(beam_width=42, head_dim=64)),
+    ("blocks", "wide_beam_b128_w96", 2, {}),                                        # wide
+    ("blocks", "wide_beam_b128_w96", 2, dict(dtype="fp16")),
+    ("blocks", "wide_beam_b128_w96", 2, dict(head_dim=64)),
+    ("tensor", "qwen3_0p6b_b64_w30", 2, {}),                                        # alternating tiles
+    ("tensor", "qwen3_0p6b_b64_w30", 2, dict(dtype="fp16")),
+    ("tensor", "qwen3_0p6b_b64_w30", 2, dict(head_dim=64)),
+    ("tensor", "wide_beam_b128_w96", 2, {}),
+    ("tensor", "wide_beam_b128_w96", 2, dict(head_dim=64)),
+]
+WHOLE = [  # enough requests that none is split: several tiles of a unit, the output written by the prompt kernel
+    ("blocks", "qwen3_0p6b_b64_w30", 40, {}), ("blocks", "qwen3_0p6b_b64_w30", 40, dict(beam_width=42)),
+    ("blocks", "wide_beam_b128_w96", 40, {}), ("tensor", "qwen3_0p6b_b64_w30", 40, {}),
+]
+names = lambda c: "-".join(map(str, (*c[:3], *(f"{k}={v}" for k, v in c[3].items()))))  # noqa: E731
+
+
+@pytest.mark.parametrize("config", TILES + WHOLE, ids=names)
+@pytest.mark.parametrize("cleared", [False, True])
+def test_prompt_tiles(config, cleared):
+    if cleared and config[0] != "blocks":
+        pytest.skip("no block scales")
+    batch = config[2]
+    st = step(*config, prompt_lengths=[300, 200] * (batch // 2), tail_lengths=[2, 0] * (batch // 2))
+    assert (st.plan.tail_requests == 0) == (batch == 40)
+    wl = st.case.workload
+    W, Hq, Hkv, D = wl.beam_width, wl.num_q_heads, wl.num_kv_heads, wl.head_dim
+    G = Hq // Hkv
+    # key, column, code; a head of request 0 each
+    spots = [(0, 0, 0x7f), (130, 1, 0xff), (299, D - 1, 0x7f), (77, 36, 0xff)]
+    for which in ("k", "v"):
+        pool = st.kd if which == "k" else st.vd
+        if cleared:
+            for h, (key, _, _) in enumerate(spots):
+                put(st, pool, prompt_slot(st, 0, key), h, 0, 0x31, True)
+        clean = attend(st)
+        assert torch.isfinite(clean[0]).all()
+        kept = pool.clone()
+        rows, elements = torch.zeros((batch * W, Hq), dtype=torch.bool), torch.zeros((batch * W, Hq, D), dtype=torch.bool)
+        for h, (key, col, code) in enumerate(spots):
+            put(st, pool, prompt_slot(st, 0, key), h, col, code, cleared)
+            (rows if which == "k" else elements[..., col])[:W, h * G:(h + 1) * G] = True
+        check(st, clean, attend(st), rows, elements)
+        pool.copy_(kept)
+
+
+@pytest.mark.parametrize("config", TILES, ids=names)
+@pytest.mark.parametrize("cleared", [False, True])
+def test_keys_of_gathered_tails(config, cleared):
+    """Tail rows that the prompt kernel gathers: the beams that read the row, and no others."""
+    if cleared and config[0] != "blocks":
+        pytest.skip("no block scales")
+    st = step(*config, prompt_lengths=[100, 65], tail_lengths=[3, 1])
+    assert st.plan.tail_requests == 0
+    wl = st.case.workload
+    W, Hq, D = wl.beam_width, wl.num_q_heads, wl.head_dim
+    G = Hq // wl.num_kv_heads
+    spots = [(0, 0x7f), (1, 0xff), (D - 1, 0x7f)]
+    if cleared:
+        for h in range(len(spots)):
+            put(st, st.kd, tail_slot(st, 0, 1, 1), h, 0, 0x31, True)
+    clean = attend(st)
+    rows = torch.zeros((2 * W, Hq), dtype=torch.bool)
+    for h, (col, code) in enumerate(spots):
+        put(st, st.kd, tail_slot(st, 0, 1, 1), h, col, code, cleared)
+        rows[0:W:2, h * G:(h + 1) * G] = True
+    check(st, clean, attend(st), rows)
