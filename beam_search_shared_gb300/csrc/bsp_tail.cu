@@ -66,6 +66,14 @@ __device__ __forceinline__ void unpack8_e4m3(const uint2& u, float (&f)[8]) {
     }
 }
 
+// The larger of two numbers, NaN if one of them is (fmaxf passes a NaN over, and a maximum without the NaN would
+// take a tail or a split that holds one for empty).
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 template <bool BF16>
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
     uint32_t w[4];
@@ -211,7 +219,7 @@ __global__ void __launch_bounds__(kTailThreads) tail_merge_kernel(TailParams p) 
                     for (int off = LPR / 2; off >= 1; off >>= 1) dot += __shfl_xor_sync(FULL, dot, off);
                     if constexpr (BLK) dot *= kscale[t];
                     if (ok[t]) sc[t] = dot * p.scale_log2;
-                    m = fmaxf(m, sc[t]);
+                    m = max_nan(m, sc[t]);
                 }
             }
             float l = 0.f;
@@ -266,8 +274,8 @@ __global__ void __launch_bounds__(kTailThreads) tail_merge_kernel(TailParams p) 
             const bool active = pg + pi < passes && h < p.Hq;  // every lane still takes part in the shuffles
             const long long prow = (static_cast<long long>(part_off) * p.W + w) * p.Hq + (active ? h : 0);
             const float m = tm[pi], l = tl[pi];
-            float Lmax = (l > 0.f) ? m + log2f(l) : -INFINITY;
-            Lmax = fmaxf(Lmax, lse0[pi]);
+            float Lmax = l == 0.f ? -INFINITY : m + log2f(l);
+            Lmax = max_nan(Lmax, lse0[pi]);
             if (nsplit > 1) {  // block-uniform
                 float lsev[KMAX];
 #pragma unroll
@@ -276,13 +284,13 @@ __global__ void __launch_bounds__(kTailThreads) tail_merge_kernel(TailParams p) 
                     lsev[k] = (active && sp < nsplit) ? ld_dep(p.part_lse + prow + sp * pstride) : -INFINITY;
                 }
 #pragma unroll
-                for (int k = 0; k < KMAX; ++k) Lmax = fmaxf(Lmax, lsev[k]);
+                for (int k = 0; k < KMAX; ++k) Lmax = max_nan(Lmax, lsev[k]);
                 // a request may hold more splits when others of the batch have none (the planner's bound
                 // is batch + kExtraParts in all): the rest, one load per lane at a time
                 for (int sp = 1 + KMAX * LPR + li; active && sp < nsplit; sp += LPR)
-                    Lmax = fmaxf(Lmax, ld_dep(p.part_lse + prow + sp * pstride));
+                    Lmax = max_nan(Lmax, ld_dep(p.part_lse + prow + sp * pstride));
 #pragma unroll
-                for (int off = LPR / 2; off >= 1; off >>= 1) Lmax = fmaxf(Lmax, __shfl_xor_sync(FULL, Lmax, off));
+                for (int off = LPR / 2; off >= 1; off >>= 1) Lmax = max_nan(Lmax, __shfl_xor_sync(FULL, Lmax, off));
             }
             float out[8];
             float lse2;
@@ -291,8 +299,8 @@ __global__ void __launch_bounds__(kTailThreads) tail_merge_kernel(TailParams p) 
                 for (int e = 0; e < 8; ++e) out[e] = 0.f;
                 lse2 = -INFINITY;
             } else {
-                // tail weight exp2(m + log2 l - Lmax) times O_t = acc / l, then split 0
-                const float ft = (l > 0.f) ? exp2f(m - Lmax) : 0.f;
+                // tail weight exp2(m + log2 l - Lmax) times O_t = acc / l, then split 0 (Lmax NaN: all are)
+                const float ft = l == 0.f ? 0.f : exp2f(m - Lmax);
                 const float fv = ft * p.v_scale;          // the tail's values in their E4M3 scale (1 otherwise)
                 const float w0 = exp2f(lse0[pi] - Lmax);  // 0 without a prompt
                 float sum = l * ft + w0;

@@ -1,4 +1,4 @@
-"""NaN codes (0x7f, 0xff) of E4M3 pools: a NaN in a key that a row attends makes the row's output and log-sum-exp NaN, a
+"""NaN codes (0x7f, 0xff) of E4M3 pools, and NaN in 16-bit pools where splits and tails are merged: a NaN in a key that a row attends makes the row's output and log-sum-exp NaN, a
 NaN in a value the output's element of that column, whatever kernel reads the tile; every other number stays bit for bit
 what it is without the NaN. Blocks with an exponent of 0 keep their NaN codes too.
 """
@@ -13,14 +13,32 @@ from test_gpu_fp8_attn import Fp8Step
 pytestmark = pytest.mark.gpu
 
 
+class Step16:
+    """The same with the case's 16-bit pools (their NaN is put by value)."""
+
+    def __init__(self, case):
+        self.case, wl = case, case.workload
+        self.kd, self.vd, self.q = case.k_pool.cuda(), case.v_pool.cuda(), case.q.cuda()
+        self.ci, self.beam_pages = torch.from_numpy(case.cache_indirection).cuda(), torch.from_numpy(case.beam_pages).cuda()
+        self.o, self.lse = torch.empty_like(self.q), torch.empty(self.q.shape[:2], device="cuda")
+        self.geo = bsp.geometry(wl.num_q_heads, wl.num_kv_heads, wl.head_dim, wl.page_size, case.num_pages, wl.dtype)
+        self.ws = bsp.Workspace(self.geo, wl.batch, wl.beam_width, case.prefix_pages.shape[1])
+        self.plan = self.ws.plan(self.geo, wl.batch, wl.beam_width, case.prefix_len, case.tail_len, case.prefix_pages)
+
+    def attend(self, flags=0):
+        bsp.decode_attn(self.plan, self.q, self.kd, self.vd, self.beam_pages, self.ci, self.case.workload.head_dim ** -0.5, self.o, self.lse, flags=flags)
+
+
 def step(scales, name, batch, kw, **lengths):
-    """A BlockStep (block of 8 slots) or an Fp8Step. Beams that are even read beam 1's tail rows, the others beam 0's."""
+    """A BlockStep (block of 8 slots), an Fp8Step or a Step16. Beams that are even read beam 1's tail rows, the others beam 0's."""
     wl = synth.WORKLOADS[name].scaled(batch).with_(**kw)
     case = synth.make_case(wl, 900 + batch, full_step=False, device="cpu", **lengths)
     for b in range(batch):
         P, T = int(case.prefix_len[b]), int(case.tail_len[b])
         case.cache_indirection[b, ::2, P:P + T] = min(1, wl.beam_width - 1)
         case.cache_indirection[b, 1::2, P:P + T] = 0
+    if scales == "plain":
+        return Step16(case)
     return BlockStep(case, 901, 8) if scales == "blocks" else Fp8Step(case, 901, 0.5, 1.5)
 
 
@@ -134,4 +152,57 @@ def test_keys_of_gathered_tails(config, cleared):
     for h, (col, code) in enumerate(spots):
         put(st, st.kd, tail_slot(st, 0, 1, 1), h, col, code, cleared)
         rows[0:W:2, h * G:(h + 1) * G] = True
+    check(st, clean, attend(st), rows)
+
+
+MERGED = [(s, "qwen3_4b_fp16_d128", 6, kw) for s in ("blocks", "tensor", "plain") for kw in ({}, dict(dtype="bf16"), dict(head_dim=64))]
+MERGED.append(("plain", "qwen3_4b_fp16_d128", 6, dict(head_dim=256)))
+
+
+@pytest.mark.parametrize("config", MERGED, ids=names)
+def test_tails_and_splits_that_are_merged(config):
+    """The tail kernel: a NaN in some of a row's tail keys or in all of its keys, tail and splits, and in a value."""
+    st = step(*config, prompt_lengths=[3000, 129, 0, 0, 1, 517], tail_lengths=[8, 5, 3, 0, 1, 1])
+    assert st.plan.tail_requests >= 4
+    wl = st.case.workload
+    W, Hq, Hkv, D, ps = wl.beam_width, wl.num_q_heads, wl.num_kv_heads, wl.head_dim, wl.page_size
+    G = Hq // Hkv
+    nan = float("nan") if config[0] == "plain" else 0x7f
+    clean = attend(st)
+    kept = st.kd.clone()
+    rows = torch.zeros((6 * W, Hq), dtype=torch.bool)
+    for b, h in ((0, 0), (1, 3), (2, 5)):   # a key of a long prompt's, a short prompt's and an empty prompt's tail
+        at = tail_slot(st, b, 1, 2)
+        st.kd[at[0], h, at[1], (h + D - 1) % D] = nan
+        rows[b * W:(b + 1) * W:2, h * G:(h + 1) * G] = True
+    for t in range(3):                      # every key that there is, of an empty prompt
+        at = tail_slot(st, 2, 0, t)
+        st.kd[at[0], 2, at[1], 7] = nan
+    rows[2 * W + 1:3 * W:2, 2 * G:3 * G] = True
+    for i in range(517):                    # ... of a prompt in splits (its tail's keys stay numbers)
+        at = prompt_slot(st, 5, i)
+        st.kd[at[0], 1, at[1], 0] = nan
+    rows[5 * W:, G:2 * G] = True
+    check(st, clean, attend(st), rows)
+    st.kd.copy_(kept)
+    elements = torch.zeros((6 * W, Hq, D), dtype=torch.bool)
+    for b, col in ((0, 1), (1, D - 1), (2, 0)):
+        at = tail_slot(st, b, 0, 1)
+        st.vd[at[0], 4, at[1], col] = nan
+        elements[b * W + 1:(b + 1) * W:2, 4 * G:5 * G, col] = True
+    check(st, clean, attend(st), None, elements)
+
+
+@pytest.mark.parametrize("scales", ["blocks", "tensor", "plain"])
+def test_every_key_of_split_prompts_without_tails(scales):
+    st = step(scales, "qwen3_4b_fp16_d128", 2, {}, prompt_lengths=[900, 700], tail_lengths=[0, 0])
+    assert st.plan.tail_requests == 2
+    wl = st.case.workload
+    G = wl.num_q_heads // wl.num_kv_heads
+    clean = attend(st)
+    for i in range(900):
+        at = prompt_slot(st, 0, i)
+        st.kd[at[0], 2, at[1], 3] = float("nan") if scales == "plain" else 0xff
+    rows = torch.zeros((2 * wl.beam_width, wl.num_q_heads), dtype=torch.bool)
+    rows[:wl.beam_width, 2 * G:3 * G] = True
     check(st, clean, attend(st), rows)
