@@ -874,7 +874,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     // for its own reads
                     constexpr int kBatch = 8;
                     static_assert(C::TAIL_CHUNKS % kBatch == 0, "batches");
-                    uint32_t kfac = 0, vfac = 0;  // of the lane's resolved row
+                    uint32_t kfac = 0, vfac = 0, nan = 0;  // (the factors of the lane's resolved row)
                     if (myrow >= 0) {
                         kfac = block_factor<BF16>(__ldg(p.k_exp + (myrow >> p.block_log2)));
                         vfac = block_factor<BF16>(__ldg(p.v_exp + (myrow >> p.block_log2)));
@@ -898,7 +898,14 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             const uint32_t off = chunk_off(chunk_row(i0 + i));
                             const uint32_t kf = __shfl_sync(FULL, kfac, from), vf = __shfl_sync(FULL, vfac, from);
                             *reinterpret_cast<uint4*>(kt + off) = widen_e4m3x8<BF16, true>(kw[i], kf);
-                            *reinterpret_cast<uint4*>(vt + off) = widen_e4m3x8<BF16, true>(vw[i], vf);
+                            *reinterpret_cast<uint4*>(vt + off) = widen_values<BF16, true>(vw[i], vf, nan);
+                        }
+                    }
+                    if (seen_nan<BF16>(nan)) {
+#pragma unroll 1
+                        for (int i = 0; i < C::TAIL_CHUNKS; ++i) {
+                            const uint32_t off = chunk_off(chunk_row(i));
+                            spread_nan<BF16>(kt + off, vt + off);
                         }
                     }
                 } else {

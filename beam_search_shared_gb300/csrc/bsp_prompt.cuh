@@ -68,9 +68,9 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 // normal (the smallest, 2^-9, has exponent field 6) with the fraction's low 7 bits zero, so the shifted values
 // are exact, zero or normal. A product with 0 gives each half's sign bit, and 0x7fff for a NaN code, whose
 // exponent field would be that of a number once shifted; the mask cuts what the upper half's fraction (of a
-// NaN) moves into the lower half.
-__device__ __forceinline__ uint32_t e4m3x2_shifted(uint32_t two) {
-    uint32_t h, z;
+// NaN) moves into the lower half. z: that product.
+__device__ __forceinline__ uint32_t e4m3x2_shifted(uint32_t two, uint32_t& z) {
+    uint32_t h;
     asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(h) : "r"(two));
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(z) : "r"(h), "r"(0u));
     return ((h >> 3) & 0x0fff0fffu) | z;
@@ -80,9 +80,9 @@ __device__ __forceinline__ uint32_t e4m3x2_shifted(uint32_t two) {
 // bfloat16 value, and one multiplication by 2^112 restores the shifted one. NaN codes give NaN.
 template <bool BF16>
 __device__ __forceinline__ uint32_t e4m3x2_to_16(uint32_t two) {
-    uint32_t r;
+    uint32_t r, z;
     if constexpr (BF16)
-        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(e4m3x2_shifted(two)), "r"(0x77807780u));  // 2^112 in both halves
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(e4m3x2_shifted(two, z)), "r"(0x77807780u));  // 2^112 in both halves
     else
         asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(r) : "r"(two));
     return r;
@@ -113,8 +113,8 @@ __device__ __forceinline__ float block_scale(uint32_t e) {
 // smallest scales' products below 2^-133). NaN codes give NaN under every factor, 0 among them.
 template <bool BF16>
 __device__ __forceinline__ uint32_t scaled_e4m3x2(uint32_t two, uint32_t factor) {
-    uint32_t r;
-    if constexpr (BF16) asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(e4m3x2_shifted(two)), "r"(factor));
+    uint32_t r, z;
+    if constexpr (BF16) asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(e4m3x2_shifted(two, z)), "r"(factor));
     else asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(e4m3x2_to_16<false>(two)), "r"(factor));
     return r;
 }
@@ -133,6 +133,44 @@ __device__ __forceinline__ uint4 widen_e4m3x8(uint2 in, uint32_t factor) {
                           scaled_e4m3x2<BF16>(in.y & 0xffffu, factor), scaled_e4m3x2<BF16>(in.y >> 16, factor));
     else
         return e4m3x8_to_16<BF16>(in);
+}
+
+// A gathered tail tile holds rows of all beams of its block, and a probability of 0 times a NaN is a NaN: a value's NaN
+// would reach the beams that do not read it. So the gathering threads mark what they have seen in `nan` (widen_values,
+// seen_nan), and go over their chunks of the tile once more if there was one: 8 values with a NaN among them become
+// zeros, and the 8 elements of the key beside them NaNs (spread_nan). The mask keeps those from the other beams'
+// scores, and the rows that read the key become NaN, output and log-sum-exp.
+template <bool BF16, bool BLK>
+__device__ __forceinline__ uint4 widen_values(uint2 in, uint32_t factor, uint32_t& nan) {
+    if constexpr (BF16) {
+        const uint32_t f = BLK ? factor : 0x77807780u;
+        const uint32_t two[4] = {in.x & 0xffffu, in.x >> 16, in.y & 0xffffu, in.y >> 16};
+        uint32_t r[4], z[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r[i]) : "r"(e4m3x2_shifted(two[i], z[i])), "r"(f));
+        nan |= z[0] | z[1];
+        nan |= z[2] | z[3];
+        return make_uint4(r[0], r[1], r[2], r[3]);
+    } else {
+        // (a NaN code has all seven bits below its sign set: one more carries into the sign's place)
+        nan |= ((in.x & 0x7f7f7f7fu) + 0x01010101u) | ((in.y & 0x7f7f7f7fu) + 0x01010101u);
+        return widen_e4m3x8<BF16, BLK>(in, factor);
+    }
+}
+template <bool BF16>
+__device__ __forceinline__ bool seen_nan(uint32_t nan) {
+    return (nan & (BF16 ? 0x7fff7fffu : 0x80808080u)) != 0u;
+}
+template <bool BF16>
+__device__ __forceinline__ void spread_nan(uint8_t* key, uint8_t* value) {
+    const uint4 v = *reinterpret_cast<const uint4*>(value);
+    constexpr uint32_t inf = BF16 ? 0x7f80u : 0x7c00u;
+    bool nan = false;
+    for (uint32_t w : {v.x, v.y, v.z, v.w}) nan |= (w & 0x7fffu) > inf || (w >> 16 & 0x7fffu) > inf;
+    if (!nan) return;
+    *reinterpret_cast<uint4*>(key) = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+    *reinterpret_cast<uint4*>(value) = make_uint4(0u, 0u, 0u, 0u);
 }
 
 // The prompt tiles of a CTA's units in order, one ahead of the tile that is widened, so that the exponent bytes of the

@@ -558,6 +558,7 @@ prefix_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     if (ok) {
                         uint8_t* kt = k_tile(gtt);
                         uint8_t* vt = v_tile(gtt);
+                        uint32_t nan = 0;
 #pragma unroll 4
                         for (int i = 0; i < TK / RPS; ++i) {
                             const int c = rsub + i * RPS;
@@ -576,7 +577,7 @@ prefix_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                     const uint2 k8 = __ldg(reinterpret_cast<const uint2*>(k_pool + e));
                                     kw = widen_e4m3x8<BF16, BLK>(k8, kfac);
                                     const uint2 v8 = __ldg(reinterpret_cast<const uint2*>(v_pool + e));
-                                    vw = widen_e4m3x8<BF16, BLK>(v8, vfac);
+                                    vw = widen_values<BF16, BLK>(v8, vfac, nan);
                                 }
                                 *reinterpret_cast<uint4*>(kt + off) = kw;
                                 *reinterpret_cast<uint4*>(vt + off) = vw;
@@ -587,6 +588,11 @@ prefix_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                             }
                         }
                         if constexpr (!FP8) cp_async_commit_wait_all();
+                        if (FP8 && seen_nan<BF16>(nan)) {
+#pragma unroll 1
+                            for (int c = rsub; c < TK; c += RPS)
+                                spread_nan<BF16>(kt + sw128_chunk<TK>(kc, c), vt + sw128_chunk<TK>(kc, c));
+                        }
                         fence_proxy_async_smem();
                     }
                     ok = gather_sync_and(ok);

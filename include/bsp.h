@@ -467,6 +467,9 @@ BSP_API bsp_status bsp_norm_rope_append_kv_fp8(const bsp_plan_t* plan, const bsp
  * Each (request, kv head) reads its prompt keys a single time for all beams and query
  * heads (tensor cores), the tail per beam, and the two merge exactly by
  * log-sum-exp. Only the valid P_b prompt rows are read, never the allocation.
+ * Values are finite numbers: an infinity or NaN in a beam's tail may reach the
+ * outputs of the request's other beams, for which its probability is 0. In a
+ * key it stays with the rows that attend it.
  *   beam_pages_stride  entries per beam_pages row, >= ceil(max(P_b+T_b)/page_size)
  *   max_seq            innermost extent of cache_indirection, >= max(P_b + T_b)
  *   softmax_scale      > 0, typically 1/sqrt(head_dim)
@@ -497,9 +500,11 @@ BSP_API bsp_status bsp_decode_attn(const bsp_plan_t* plan, const void* q, const 
  * The kernels read the E4M3 tiles (half the bytes of the 16-bit pools) and
  * widen them exactly to the q dtype in shared memory (every E4M3 value is a
  * bf16 and a binary16 value), so the tensor-core products are those of the
- * 16-bit path. A NaN code (0x7f, 0xff) in a key or value row that is read
- * makes that row's output NaN. Other arguments, flags, events and errors as
- * bsp_decode_attn; a plan whose pools are not E4M3 is BSP_ERR_INVALID_ARG here,
+ * 16-bit path. A NaN code (0x7f, 0xff) in a key that a row of q attends makes
+ * the row's output and LSE NaN, one in a value the output's element of that
+ * column (in a tail row it may be all of the row's output and its LSE); rows
+ * that do not attend it are what they are without it. Other arguments, flags,
+ * events and errors as bsp_decode_attn; a plan whose pools are not E4M3 is BSP_ERR_INVALID_ARG here,
  * and an E4M3 plan is BSP_ERR_INVALID_ARG for bsp_decode_attn, bsp_append_kv
  * and bsp_rope_append_kv.
  */
@@ -512,10 +517,11 @@ BSP_API bsp_status bsp_decode_attn_fp8(const bsp_plan_t* plan, const void* q, co
 /*
  * E4M3 pools with block scales: each block of `block` consecutive slots of a (page, kv head) has a scale of its own
  * for K and for V, a power of two kept as its exponent byte E: element x of the block stands for
- * e4m3(x) * 2^(E - 127). E = 0 means that nothing has been written to the block (its codes are read as 0, those of NaN as NaN). An 8-bit
- * float loses nothing by a power of two, so the scale only places its range; it can be changed without rounding the
- * codes again (but for those that leave the range below), and the product is exact in 16 bits: bf16 takes exponents
- * E - 127 up to 15, fp16 those in [-15, 7]; larger ones (fp16: smaller ones too) are read as the nearest of these.
+ * e4m3(x) * 2^(E - 127). E = 0 means that nothing has been written to the block (its codes are read as 0, those of
+ * NaN as NaN). An 8-bit float loses nothing by a power of two, so the scale only places its range; it can be changed
+ * without rounding the codes again (but for those that leave the range below), and the product is exact in 16 bits:
+ * bf16 takes exponents E - 127 up to 15, fp16 those in [-15, 7]; larger ones (fp16: smaller ones too) are read as the
+ * nearest of these.
  * (These entry points have no counterpart on the pages the method comes from.)
  */
 #define BSP_MAX_SCALE_BLOCK 32
@@ -574,7 +580,8 @@ BSP_API bsp_status bsp_decode_attn_fp8_blocks(const bsp_plan_t* plan, const void
  * must lie in [0, num_pages), else BSP_ERR_PAGE_INDEX). With `causal` != 0,
  * prompt token i sees positions 0 .. cached_len[b] + i, else all
  * cached_len[b] + prompt_len[b] positions. Positions past those are never
- * read. The query rows are the prompt tokens of all requests in order (request
+ * read. Values are finite numbers: an infinity or NaN in one prompt token's may
+ * reach the outputs of tokens before it. The query rows are the prompt tokens of all requests in order (request
  * b's tokens start at the sum of the earlier prompt_len), `total_rows` in all.
  * A request whose longest work unit is above the launch's mean load per SM has
  * its cached rows cut into key ranges (every cut inside the cached rows, so

@@ -206,3 +206,46 @@ def test_every_key_of_split_prompts_without_tails(scales):
     rows = torch.zeros((2 * wl.beam_width, wl.num_q_heads), dtype=torch.bool)
     rows[:wl.beam_width, 2 * G:3 * G] = True
     check(st, clean, attend(st), rows)
+
+
+@pytest.mark.parametrize("config", TILES, ids=names)
+def test_values_of_gathered_tails(config):
+    """A beam's NaN value stays with the rows that read it, though the tile holds all beams' rows: their elements of its
+    column are NaN (the rest of them may be), the other rows are bit for bit what they were."""
+    st = step(*config, prompt_lengths=[100, 65], tail_lengths=[3, 1])
+    assert st.plan.tail_requests == 0
+    wl = st.case.workload
+    W, Hq, D = wl.beam_width, wl.num_q_heads, wl.head_dim
+    G = Hq // wl.num_kv_heads
+    clean = attend(st)
+    spots = [(0, 0x7f), (1, 0xff), (D - 1, 0x7f)]
+    rows = torch.zeros((2 * W, Hq), dtype=torch.bool)
+    for h, (col, code) in enumerate(spots):
+        put(st, st.vd, tail_slot(st, 0, 1, 2), h, col, code, False)
+        rows[0:W:2, h * G:(h + 1) * G] = True
+    o, lse = attend(st)
+    for h, (col, _) in enumerate(spots):
+        assert torch.isnan(o[0:W:2, h * G:(h + 1) * G, col]).all()
+    other = ~rows.cuda()
+    assert torch.equal(o[other], clean[0][other]) and torch.equal(lse[other], clean[1][other])
+
+
+@pytest.mark.parametrize("kw", [{}, dict(dtype="fp16"), dict(head_dim=64)], ids=str)
+def test_weights_of_keys(kw):
+    """bsp_key_weights_fp8: the weight of a key that holds a NaN, and no other's."""
+    st = step("tensor", "qwen3_0p6b_b64_w30", 2, kw, prompt_lengths=[300, 200], tail_lengths=[0, 0])
+    wl = st.case.workload
+    attend(st)
+
+    def weigh():
+        out = torch.full((2, wl.num_kv_heads, 300), -7.0, device="cuda")
+        bsp.key_weights_fp8(st.plan, st.q, st.kd, st.lse, st.scale, st.k_scale, out, flags=bsp.FLAG_CHECK)
+        return out
+
+    clean = weigh()
+    bad = torch.zeros(clean.shape, dtype=torch.bool)
+    for h, (key, col, code) in enumerate([(0, 0, 0x7f), (130, 1, 0xff), (299, wl.head_dim - 1, 0x7f)]):
+        put(st, st.kd, prompt_slot(st, 0, key), h, col, code, False)
+        bad[0, h, key] = True
+    got = weigh()
+    assert torch.isnan(got[bad]).all() and torch.equal(got[~bad], clean[~bad])
