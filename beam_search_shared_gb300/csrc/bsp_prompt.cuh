@@ -49,6 +49,9 @@ __device__ __forceinline__ int prompt_tiles(const UnitInfo& ui) {
     return (ui.key_end - ui.key_begin + TK - 1) / TK;
 }
 
+// Two values as a 16-bit pair. Probabilities go to P*V this way: the MMA's operands have one type, V's. Each is off by
+// half a step (bf16 2^-8 of the value, fp16 2^-11, or 2^-25 below 2^-14), so an output element by that share of
+// sum p |v| beside its own rounding. Row sums add the fp32 values.
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     if constexpr (BF16) {
