@@ -191,8 +191,8 @@ bsp_status bsp_append_kv_fp8_blocks(const bsp_plan_t* plan, const bsp_qk_norm* n
     p.ps_log2 = ilog2(geo.page_size);
     p.num_pages = geo.num_pages;
     p.block_log2 = ilog2(scales->block);
-    p.exp_lo = bf16 ? 27 : 112;  // 2^-100 .. 2^15, 2^-15 .. 2^7
-    p.exp_hi = bf16 ? 142 : 134;
+    p.exp_lo = bf16 ? 27 : kReadLo<false>;  // 2^-100 .. 2^15, 2^-15 .. 2^7
+    p.exp_hi = bf16 ? kReadHi<true> : kReadHi<false>;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (!record_event(events, 0, s)) return BSP_ERR_CUDA;
     st = launched(launch_norm_append(geo.head_dim, bf16, kPoolBlocks, plan->kind == 1, p, plan->num_sms, s));
@@ -311,6 +311,8 @@ bsp_status bsp_fork_rows(const bsp_plan_t* plan, const int32_t* beams, int64_t b
         p.k_exp = scales->k;
         p.v_exp = scales->v;
         p.block_log2 = ilog2(scales->block);
+        p.read_lo = geo.dtype == BSP_DTYPE_BF16 ? kReadLo<true> : kReadLo<false>;
+        p.read_hi = geo.dtype == BSP_DTYPE_BF16 ? kReadHi<true> : kReadHi<false>;
     }
     p.status = status_word(plan);
     p.shape = plan_shape(plan);

@@ -247,6 +247,13 @@ __device__ __forceinline__ long long pool_row(const NormAppendParams& p, int slo
     return ((static_cast<long long>(slot >> p.ps_log2) * p.Hkv + h) << p.ps_log2) + (slot & ((1 << p.ps_log2) - 1));
 }
 
+// A block's exponent byte as the attention reads it: the nearest one of its range; 0 as it is.
+template <bool BF16>
+__device__ __forceinline__ int held_exponent(int e) {
+    const int held = min(e, kReadHi<BF16>);
+    return BF16 || e == 0 ? held : max(held, kReadLo<BF16>);
+}
+static_assert(kReadLo<true> == 1, "bf16: no byte below the range but 0");
 // The exponent byte of a block whose new rows' largest magnitude has the bits `top` and whose own byte is `old` (0:
 // starts anew): the smallest E with top <= 448 * 2^(E - 127), 448 = 1.75 * 2^8, within the written range.
 __device__ __forceinline__ int block_exponent(const NormAppendParams& p, uint32_t top, int old) {
@@ -262,7 +269,8 @@ __device__ __forceinline__ float code_factor(int e) {  // 2^(127 - E)
 template <int D>
 __device__ __forceinline__ void raise_rows(uint8_t* row, int off, int old, int e, int c) {
     constexpr int CPR = D / 8;
-    const float mul = __uint_as_float(static_cast<uint32_t>(127 + old - e) << 23);
+    // (2^-126 brings every code to 0, as the smaller factors do)
+    const float mul = __uint_as_float(static_cast<uint32_t>(max(1, 127 + old - e)) << 23);
     for (int r = 0; r < off; ++r) {
         uint2* at = reinterpret_cast<uint2*>(row + static_cast<long long>(r) * D) + c;
         const uint2 v = *at;
@@ -404,13 +412,13 @@ __device__ __forceinline__ void kv_rows(const NormAppendParams& p, int i, int po
                 const float mul = IS_V ? p.v_mul : p.k_mul;
                 reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + row * D)[c] = quant8(f[j], mul);
             } else {
-                const int e = block_exponent(p, __float_as_uint(top[j]), old[k]);
+                const int was = held_exponent<BF16>(old[k]), e = block_exponent(p, __float_as_uint(top[j]), was);
                 reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + row * D)[c] = quant8(f[j], code_factor(e));
                 const long long head = row >> p.block_log2;
                 // (0: zeros that start it anew)
                 if (c == 0 && (e != old[k] || e == 0)) exps[head] = static_cast<uint8_t>(e);
-                if (old[k] != 0 && e != old[k])
-                    raise_rows<D>(static_cast<uint8_t*>(pool) + (head << p.block_log2) * D, off, old[k], e, c);
+                if (was != 0 && e != was)
+                    raise_rows<D>(static_cast<uint8_t*>(pool) + (head << p.block_log2) * D, off, was, e, c);
             }
         }
     }
@@ -430,7 +438,7 @@ __device__ __forceinline__ void run_rows(const NormAppendParams& p, int lead, in
     uint8_t* exps = is_v ? p.v_exp : p.k_exp;
     const int off = __ldg(a.loc + lead) & ((1 << p.block_log2) - 1);
     const long long head = live ? pool_row(p, slot, h) >> p.block_log2 : 0;  // the block's place in the table
-    const int old = live && off != 0 ? exps[head] : 0;
+    const int old = live && off != 0 ? held_exponent<BF16>(exps[head]) : 0;
     const uint16_t* src = static_cast<const uint16_t*>(is_v ? p.v_new : p.k_new);
     auto rows = [&](auto&& each) {
         for (int r = 0; r < length; ++r) {
@@ -660,7 +668,7 @@ __global__ void __launch_bounds__(256, 3) block_window_kernel(const NormAppendPa
         int e = 0, old = 0;
         if ((lead >> lane & 1) && hs < p.Hkv) {
             uint8_t* at = exps + (pool_row(p, slot[0], hs) >> p.block_log2);
-            if ((slot[0] & ((1 << p.block_log2) - 1)) != 0) old = *at;
+            if ((slot[0] & ((1 << p.block_log2) - 1)) != 0) old = held_exponent<BF16>(*at);
             e = block_exponent(p, s_top[lane][warp], old);
             *at = static_cast<uint8_t>(e);
         }

@@ -340,6 +340,7 @@ __global__ void __launch_bounds__(256) fork_rows_kernel(const ForkRowsParams p) 
                 int e = 0;
                 if (s < n && s_src[s] >= 0)
                     e = exps[(((static_cast<long long>(s_src[s]) * p.Hkv + h0 + h) << p.ps_log2) + s) >> p.block_log2];
+                if (e != 0) e = min(max(e, p.read_lo), p.read_hi);  // (as the attention reads it)
                 int m = e;
                 for (int o = 1; o < 1 << p.block_log2; o <<= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
                 if (s < ps) {

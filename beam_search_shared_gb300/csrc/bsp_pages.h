@@ -43,6 +43,7 @@ struct ForkRowsParams {
     int32_t* status;
     PlanShape shape;
     int W, num_forks, rows, num_pages, Hkv, ps_log2, row_bytes, block_log2, out_cols, beam_cols, max_seq;
+    int read_lo, read_hi;      // exponent bytes that the attention reads as they are
     int heads, per_row;        // set by launch_fork_rows: heads of a CTA, CTAs of a row
 };
 cudaError_t launch_fork_rows(ForkRowsParams p, int num_sms, cudaStream_t stream);

@@ -48,6 +48,12 @@ struct AppendFp8Params {
 cudaError_t launch_append_fp8(int src, const AppendFp8Params& p, cudaStream_t stream);
 cudaError_t prepare_append_fp8(int src);
 
+// Exponent bytes of block scales that the attention reads as they are; others, but 0, it takes as the nearest of them.
+template <bool BF16>
+constexpr int kReadLo = BF16 ? 1 : 112;
+template <bool BF16>
+constexpr int kReadHi = BF16 ? 142 : 134;
+
 // Normalised and rotated appends (bsp_norm.cu): what K and query rows go through, and the query rows.
 struct NormRope {
     const int32_t* loc;
@@ -76,14 +82,12 @@ struct NormAppendParams {
     int block_log2, exp_lo, exp_hi;
     float k_mul, v_mul;        // E4M3 pools with one multiplier per tensor
     // set by launch_norm_append: groups of heads that fill a warp, batches of K (and of V) of a token, all of its
-    // batches,
-    // warps of a token
+    // batches, warps of a token
     int groups, kv_batches, batches, units;
 };
 // runs: the tokens are prompts', many of a block next to one another (the kernels differ in speed only)
 cudaError_t launch_norm_append(int head_dim, bool bf16, PoolKind pools, bool runs, const NormAppendParams& p,
-                               int num_sms,
-                               cudaStream_t stream);
+                               int num_sms, cudaStream_t stream);
 cudaError_t launch_rope_scaled(int max_pos, int rot, double base, const bsp_rope_scaling& sc, float* cos_sin,
                                cudaStream_t stream);
 

@@ -542,9 +542,10 @@ typedef struct bsp_block_scales {
  *  - E is the smallest exponent byte with top <= 448 * 2^(E - 127), within 27 .. 142 (fp16: 112 .. 134): for all but
  *    the largest values nothing saturates; 0 if top is 0;
  *  - a run that begins at the block's first slot starts the block anew with E. Another keeps the rows before it: the
- *    block's exponent becomes the larger of E and its own, and if it grew, the codes of the slots before the run are
- *    brought to it (times a power of two, rounded to nearest even). So a page that is taken from another sequence and
- *    not written from a block's first slot on has its exponents cleared, or copied with its rows, first;
+ *    block's exponent becomes the larger of E and its own (as it is read, see above), and if it grew, the codes of the
+ *    slots before the run are brought to it (times a power of two, rounded to nearest even). So a page that is taken
+ *    from another sequence and not written from a block's first slot on has its exponents cleared, or copied with its
+ *    rows, first;
  *  - x is stored as the E4M3 value nearest to x * 2^(127 - E), ties to even, saturated to +-448; a NaN as a NaN code.
  * The plan may have either kv_dtype and any head_dim. Other arguments and errors as bsp_norm_rope_append_kv.
  */
@@ -896,8 +897,8 @@ BSP_API bsp_status bsp_fork_tables(const bsp_plan_t* plan, const int32_t* beams,
  * Rows whose table holds -1 are left out. The fresh pages' other slots keep what they held.
  *   beam_pages, cache_indirection  as bsp_decode_attn (both may be NULL for a plan without tails)
  *   scales         NULL, or the block scales of E4M3 pools: a block takes the largest exponent among those of the blocks
- *                  that its rows come from, rows of a smaller one are brought to it (times a power of two, rounded to
- *                  nearest even), and blocks without rows are cleared
+ *                  that its rows come from (as they are read), rows of a smaller one are brought to it (times a power of
+ *                  two, rounded to nearest even), and blocks without rows are cleared
  */
 BSP_API bsp_status bsp_fork_rows(const bsp_plan_t* plan, const int32_t* beams, int64_t beams_stride, int32_t num_forks,
                                  const int32_t* pages_out, int64_t pages_out_stride, int32_t pages_out_cols,
