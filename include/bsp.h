@@ -545,7 +545,8 @@ typedef struct bsp_block_scales {
  *    block's exponent becomes the larger of E and its own (as it is read, see above), and if it grew, the codes of the
  *    slots before the run are brought to it (times a power of two, rounded to nearest even). So a page that is taken
  *    from another sequence and not written from a block's first slot on has its exponents cleared, or copied with its
- *    rows, first;
+ *    rows, first. An exponent of 0 has no rows to keep: codes of slots that nothing was written to stay, and are read
+ *    as 0 no longer but at the new scale (no sequence reads such slots);
  *  - x is stored as the E4M3 value nearest to x * 2^(127 - E), ties to even, saturated to +-448; a NaN as a NaN code.
  * The plan may have either kv_dtype and any head_dim. Other arguments and errors as bsp_norm_rope_append_kv.
  */
