@@ -1061,6 +1061,9 @@ def compact_tables(plan_: Plan, refs: torch.Tensor, refs_out: torch.Tensor, move
     _counts(plan_, refs, refs_out)
     if moves.remap is None or moves.remap.shape[0] != plan_.geo.num_pages:
         raise ValueError(f"moves are not made for {plan_.geo.num_pages} pages")
+    if moves.count.shape[0] < 2 or moves.pairs.shape[0] < plan_.geo.num_pages // 2:
+        raise ValueError(f"count {list(moves.count.shape)} and pairs {list(moves.pairs.shape)} for two counts and "
+                         f"{plan_.geo.num_pages // 2} pairs")
     stride = rows = cols = 0
     if tables is not None:
         tables_out = tables if tables_out is None else tables_out
@@ -1076,6 +1079,8 @@ def compact_tables(plan_: Plan, refs: torch.Tensor, refs_out: torch.Tensor, move
 def copy_pages(plan_: Plan, moves: PageMoves, k_pool: torch.Tensor, v_pool: torch.Tensor,
                scales: Optional[BlockScales] = None, stream=None):
     """bsp_copy_pages: the first count[0] pairs of ``moves``, whole pages of both pools (and their scales)."""
+    if moves.count.shape[0] < 1:
+        raise ValueError("count is empty")
     _pools_ok(plan_, k_pool, v_pool)
     _check("bsp_copy_pages", load().bsp_copy_pages(
         ctypes.byref(plan_), moves.pairs.data_ptr(), moves.count.data_ptr(), moves.pairs.shape[0], k_pool.data_ptr(),
