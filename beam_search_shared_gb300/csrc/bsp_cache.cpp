@@ -21,6 +21,17 @@ bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
     return x < y + nb && y < x + na;
 }
 
+// Whether one of n rows of na bytes, sa apart from a on, shares a byte with one of n rows of nb bytes, sb apart from b
+// on. Rows of one stride are compared as they lie, so that column slices of one buffer pass; others by what they span.
+bool rows_overlap(const void* a, int64_t na, int64_t sa, const void* b, int64_t nb, int64_t sb, int64_t n) {
+    if (sa != sb) return overlap(a, (n - 1) * sa + na, b, (n - 1) * sb + nb);
+    // row i + k of b begins d + k sa behind row i of a: of the k within n rows, the largest that begins before a's row ends
+    const int64_t d = static_cast<int64_t>(reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a));
+    const int64_t room = na - 1 - d;
+    const int64_t k = std::min(room >= 0 ? room / sa : -((-room + sa - 1) / sa), n - 1);
+    return k > -n && d + k * sa + nb > 0;
+}
+
 // What the three appends share: the arguments but for the pools' own, checked, in *a. BSP_OK with a->n = 0: nothing
 // to do.
 bsp_status check_norm_append(const bsp_plan_t* plan, const bsp_qk_norm* norm, const bsp_rope_config* rope,
@@ -58,10 +69,20 @@ bsp_status check_norm_append(const bsp_plan_t* plan, const bsp_qk_norm* norm, co
     if (norm && (!optional_ptr(norm->q_weight, 16) || !optional_ptr(norm->k_weight, 16))) return BSP_ERR_INVALID_ARG;
     if (q && q_out == q && q_out_stride != q_row_stride) return BSP_ERR_INVALID_ARG;
     if (q && q_out != q) {
-        const int64_t out = ((n - 1) * q_out_stride + q_row) * 2, kv = ((n - 1) * src_row_stride + kv_row) * 2;
-        if (overlap(q_out, out, q, ((n - 1) * q_row_stride + q_row) * 2) || overlap(q_out, out, k_new, kv) ||
-            overlap(q_out, out, v_new, kv))
+        auto over_rows = [&](const void* x, int64_t row, int64_t stride) {
+            return rows_overlap(q_out, 2 * q_row, 2 * q_out_stride, x, 2 * row, 2 * stride, n);
+        };
+        auto over = [&](const void* x, int64_t bytes) {
+            return x && overlap(q_out, 2 * ((n - 1) * q_out_stride + q_row), x, bytes);
+        };
+        if (over_rows(q, q_row, q_row_stride) || over_rows(k_new, kv_row, src_row_stride) ||
+            over_rows(v_new, kv_row, src_row_stride) || over(loc, 4ll * n))
             return BSP_ERR_INVALID_ARG;
+        if (rope && (over(positions, 4ll * n) ||
+                     over(rope->cos_sin, 4ll * rope->max_position * rope->rotary_dim)))
+            return BSP_ERR_INVALID_ARG;
+        const int64_t weight = static_cast<int64_t>(D) * (norm && norm->weight_fp32 ? 4 : 2);
+        if (norm && (over(norm->q_weight, weight) || over(norm->k_weight, weight))) return BSP_ERR_INVALID_ARG;
     }
     a->loc = loc;
     if (rope) {

@@ -430,7 +430,9 @@ BSP_API bsp_status bsp_rope_cos_sin_scaled(int32_t max_position, int32_t rotary_
  *                   fp32 (weight_fp32 = 1), or NULL: ones (weight_offset is then not added); eps >= 0, finite
  *   q, q_row_stride NULL, or device [n] rows of num_q_heads * head_dim elements q_row_stride apart
  *   q_out, q_out_stride  where the query rows go (with q): q itself with its stride, or memory that overlaps none of the
- *                   call's inputs (BSP_ERR_INVALID_ARG); rows of decode_attn's q when q_out_stride = num_q_heads * head_dim
+ *                   call's inputs (BSP_ERR_INVALID_ARG; rows of q_out's stride are compared as they lie, so a column
+ *                   slice of the buffer that holds the inputs will do, rows of another stride by all that they span);
+ *                   rows of decode_attn's q when q_out_stride = num_q_heads * head_dim
  *   positions       device int32 [n]; NULL without rope
  *   other arguments, skipped tokens and errors: as bsp_rope_append_kv (events too)
  * The _fp8 form writes E4M3 pools with one multiplier per tensor. (No counterpart on the pages the method comes from.)
