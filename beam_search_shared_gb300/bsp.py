@@ -8,6 +8,7 @@ fails to load, every call raises ``NativeLibraryError``: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional
 
@@ -538,14 +539,33 @@ class BlockScales:
         return ctypes.byref(self.c)
 
 
+def _buffer(name: str, t: torch.Tensor, dtype, rows: int, row):
+    """A contiguous buffer of at least ``rows`` rows of shape ``row`` (or flat), whatever dimensions count the rows."""
+    if t.dtype is not dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype}, not {t.dtype} of strides {t.stride()}")
+    shape, width = tuple(t.shape), math.prod(row)
+    fits = shape[-len(row):] == row or shape[-1:] == (width,) or len(shape) == 1
+    if not fits or t.numel() < rows * width:
+        raise ValueError(f"{name} has shape {shape}, not [{rows}, {', '.join(map(str, row))}]")
+
+
 def decode_attn_fp8_blocks(plan_: Plan, q: torch.Tensor, k_pool: torch.Tensor, v_pool: torch.Tensor,
                            scales: BlockScales, beam_pages: Optional[torch.Tensor],
                            cache_indirection: Optional[torch.Tensor], softmax_scale: float, o: torch.Tensor,
                            lse: torch.Tensor, flags: int = 0, events=None, stream=None):
     """bsp_decode_attn_fp8_blocks: decode attention over uint8 E4M3 pools with block scales; writes o [R,Hq,D] in
     the q dtype and lse [R,Hq] (fp32)."""
+    g, rows = plan_.geo, plan_.total_rows
+    heads = (g.num_q_heads, g.head_dim)
+    _buffer("q", q, _ELEMENT[g.dtype], rows, heads)
+    _buffer("o", o, _ELEMENT[g.dtype], rows, heads)
+    _buffer("lse", lse, torch.float32, rows, heads[:1])
     bps = int(beam_pages.shape[-1]) if beam_pages is not None else 0
     max_seq = int(cache_indirection.shape[-1]) if cache_indirection is not None else 0
+    if plan_.max_tail_len > 0 or flags & FLAG_GRAPH:  # (they are read)
+        for name, t, width in (("beam_pages", beam_pages, bps), ("cache_indirection", cache_indirection, max_seq)):
+            if t is not None:
+                _buffer(name, t, torch.int32, rows, (width,))
     _pools_ok(plan_, k_pool, v_pool)
     _check("bsp_decode_attn_fp8_blocks", load().bsp_decode_attn_fp8_blocks(
         ctypes.byref(plan_), _dptr(q), _dptr(k_pool), _dptr(v_pool), scales._of(plan_), _dptr(beam_pages), bps,
