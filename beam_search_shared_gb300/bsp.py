@@ -1039,6 +1039,13 @@ def fork_rows(plan_: Plan, beams: torch.Tensor, pages_out: torch.Tensor, beam_pa
     cols = max_seq = 0
     if beam_pages is not None:
         cols = _table("beam_pages", beam_pages, i32, (plan_.total_rows, None))
+        if plan_.max_tail_len > 0 and beam_pages.shape[1] * plan_.geo.page_size < plan_.max_total_len:
+            raise ValueError(f"beam_pages has {beam_pages.shape[1]} columns for {plan_.max_total_len} positions")
+        if cols != beam_pages.shape[1] and torch.cuda.is_current_stream_capturing():
+            # (a replay reads as far as its plan's sequences and the stride allow)
+            end = beam_pages.storage_offset() + plan_.total_rows * cols
+            if 4 * end > beam_pages.untyped_storage().nbytes():
+                raise ValueError("the last row of beam_pages ends before its stride")
         if cache_indirection is not None:
             max_seq = cache_indirection.shape[-1]
             if _table("cache_indirection", cache_indirection, i32, (plan_.batch, plan_.beam_width, max_seq)) != max_seq:

@@ -73,3 +73,25 @@ def test_buffers_of_the_attention_over_blocks():
         call(plan=none.plan, pages=torch.zeros((1, 3), dtype=I32))
     with pytest.raises(ValueError):                              # a replay may have some
         call(plan=none.plan, pages=torch.zeros((1, 3), dtype=I32), flags=bsp.FLAG_GRAPH)
+
+
+def test_columns_of_the_forked_beams_pages(monkeypatch):
+    """A column slice of a wider table has its own columns only, though the library goes by the rows' stride."""
+    s = Staged(prefix=(64, 32), tail=(1, 0))   # 65 positions: 3 pages
+    beams, out = torch.zeros((2, 3), dtype=I32), torch.zeros((6, 4), dtype=I32)
+    ci = torch.zeros((2, 4, 65), dtype=I32)
+    pool = torch.zeros((100, 4, 32, 128), dtype=BF)
+    wide = torch.zeros((8, 10), dtype=I32)
+    call = lambda pages: bsp.fork_rows(s.plan, beams, out, pages, ci, pool, pool, stream=Stream)  # noqa: E731
+    for pages in (wide, wide[:, :3], wide[:, 2:5], wide[:, :3].contiguous()):
+        with pytest.raises(bsp.BspError, match="INVALID_ARG"):   # all right but for the memory
+            call(pages)
+    for pages in (wide[:, :2], wide[:, :2].contiguous()):
+        with pytest.raises(ValueError, match="columns"):
+            call(pages)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    for pages in (wide, wide[:, :3], wide[:, :3].contiguous()):
+        with pytest.raises(bsp.BspError, match="INVALID_ARG"):
+            call(pages)
+    with pytest.raises(ValueError, match="stride"):              # (a replay may read ten columns of the last row)
+        call(wide[:, 2:5])
