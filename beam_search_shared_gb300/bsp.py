@@ -1028,6 +1028,10 @@ def fork_tables(plan_: Plan, beams: torch.Tensor, refs: torch.Tensor, refs_out: 
         _stream(stream)))
 
 
+def _captured(t: torch.Tensor) -> bool:
+    return t.is_cuda and torch.cuda.is_current_stream_capturing()
+
+
 def fork_rows(plan_: Plan, beams: torch.Tensor, pages_out: torch.Tensor, beam_pages: Optional[torch.Tensor],
               cache_indirection: Optional[torch.Tensor], k_pool: torch.Tensor, v_pool: torch.Tensor,
               scales: Optional[BlockScales] = None, stream=None):
@@ -1041,7 +1045,7 @@ def fork_rows(plan_: Plan, beams: torch.Tensor, pages_out: torch.Tensor, beam_pa
         cols = _table("beam_pages", beam_pages, i32, (plan_.total_rows, None))
         if plan_.max_tail_len > 0 and beam_pages.shape[1] * plan_.geo.page_size < plan_.max_total_len:
             raise ValueError(f"beam_pages has {beam_pages.shape[1]} columns for {plan_.max_total_len} positions")
-        if cols != beam_pages.shape[1] and torch.cuda.is_current_stream_capturing():
+        if cols != beam_pages.shape[1] and _captured(beam_pages):
             # (a replay reads as far as its plan's sequences and the stride allow)
             end = beam_pages.storage_offset() + plan_.total_rows * cols
             if 4 * end > beam_pages.untyped_storage().nbytes():
