@@ -514,7 +514,9 @@ class _BlockScales(ctypes.Structure):
 
 class BlockScales:
     """Scales of E4M3 pools, one for each block of ``block`` slots of a (page, kv head): exponent bytes E of 2^(E - 127)
-    in uint8 tables k and v [num_pages, num_kv_heads, page_size // block] (made zeroed, or the given ones)."""
+    in uint8 tables k and v [num_pages, num_kv_heads, page_size // block] (made zeroed, or the given ones). Pools that have
+    them go through append_kv_fp8_blocks, decode_attn_fp8_blocks and, with ``scales``, fork_rows and copy_pages; no other
+    call knows of the scales, and none can tell."""
 
     def __init__(self, geo: Geometry, block: int, k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None,
                  device="cuda"):
@@ -967,7 +969,8 @@ def key_weights(plan_: Plan, q: torch.Tensor, k_pool: torch.Tensor, lse: torch.T
 
 def key_weights_fp8(plan_: Plan, q: torch.Tensor, k_pool: torch.Tensor, lse: torch.Tensor, softmax_scale: float,
                     k_scale: float, weights: torch.Tensor, window: int = 0, flags: int = 0, stream=None):
-    """bsp_key_weights_fp8: key_weights over a uint8 E4M3 pool (key = code x k_scale)."""
+    """bsp_key_weights_fp8: key_weights over a uint8 E4M3 pool (key = code x k_scale; not one with BlockScales, whose
+    exponents it would pass over)."""
     _rows_ok(plan_, q, lse)
     _pools_ok(plan_, k_pool)
     stride = _key_table(plan_, "weights", weights, torch.float32)
@@ -981,7 +984,8 @@ def evict_prefix(plan_: Plan, weights: torch.Tensor, keep_len: torch.Tensor, sin
                  positions: Optional[torch.Tensor] = None, weights_out: Optional[torch.Tensor] = None,
                  positions_out: Optional[torch.Tensor] = None, stream=None):
     """bsp_evict_prefix: per (request, kv head) the keep_len[b] rows of largest weight move to the front of the
-    request's pages, in place. weights fp32, positions and kept int32 [batch, num_kv_heads, >= longest prompt]."""
+    request's pages, in place. weights fp32, positions and kept int32 [batch, num_kv_heads, >= longest prompt]. Not for
+    pools with BlockScales: rows would leave their blocks' scales behind."""
     i32 = torch.int32
     stride = _key_table(plan_, "weights", weights, torch.float32)
     out_stride = _key_table(plan_, "kept", kept, i32)

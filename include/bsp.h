@@ -524,6 +524,10 @@ BSP_API bsp_status bsp_decode_attn_fp8(const bsp_plan_t* plan, const void* q, co
  * without rounding the codes again (but for those that leave the range below), and the product is exact in 16 bits:
  * bf16 takes exponents E - 127 up to 15, fp16 those in [-15, 7]; larger ones (fp16: smaller ones too) are read as the
  * nearest of these.
+ * Only calls that take a bsp_block_scales know of the scales, and no call can tell such pools from others:
+ * bsp_decode_attn_fp8, bsp_key_weights_fp8 and the appends with one multiplier per tensor pass the exponents over,
+ * bsp_evict_prefix moves codes between blocks without them, and so do bsp_fork_rows and bsp_copy_pages with scales NULL.
+ * Their results over such pools are wrong.
  * (These entry points have no counterpart on the pages the method comes from.)
  */
 #define BSP_MAX_SCALE_BLOCK 32
@@ -823,7 +827,8 @@ BSP_API bsp_status bsp_beam_advance(const bsp_plan_t* plan, const int32_t* paren
  *   weights       device fp32 [batch][num_kv_heads][weights_stride], weights_stride >= the plan's longest
  *                 prompt; entries past a request's keys (all entries of one without rows) stay as they were
  * One pass over K on the tensor cores; each sum is taken in one order, so repeated calls agree bit for bit.
- * The _fp8 form reads E4M3 pools (key = code * k_scale; head_dim 64 or 128, decode plans).
+ * The _fp8 form reads E4M3 pools with one scale per tensor (key = code * k_scale; head_dim 64 or 128, decode plans);
+ * of pools with block scales it would read the codes alone.
  */
 BSP_API bsp_status bsp_key_weights(const bsp_plan_t* plan, const void* q, const void* k_pool, const float* lse,
                                    float softmax_scale, int32_t window, int32_t flags, float* weights,
@@ -851,6 +856,7 @@ BSP_API bsp_status bsp_key_weights_fp8(const bsp_plan_t* plan, const void* q, co
  *                  was in slot kept[i]
  *   weights_out, positions_out   NULL, or [batch][num_kv_heads][out_stride]: the kept slots' weights and
  *                  positions (each may be its input when the strides agree)
+ * Not for pools with block scales (bsp_block_scales): a row moved to another block would be read at that block's scale.
  * Entries of the outputs from `keep` on stay as they were. weights_stride, out_stride >= the longest prompt. A replay
  * that finds a page id past the pools it was captured with does not copy that row and sets BSP_DEVFLAG_PAGE_INDEX.
  */
