@@ -746,6 +746,7 @@ bsp_status plan_build_core(const bsp_geometry* geo, int32_t batch, int32_t beam_
     // (a prefill request is the tail kernel's when its keys were split)
     for (int b = 0; b < batch; ++b) tail_requests += pf ? nsplit[b] > 1 : !fused(b);
     out->tail_requests = tail_requests;
+    out->max_splits = batch > 0 ? static_cast<int32_t>(*std::max_element(nsplit.begin(), nsplit.end())) : 0;
     out->total_rows = static_cast<int32_t>(total_rows);
     out->kind = pf ? 1 : 0;
     out->layout = layout;
@@ -1186,7 +1187,9 @@ bsp_status attn_launches(const bsp_plan_t* plan, uint8_t* ws, const void* q, con
                    : wide    ? prepare_wide(D, bf16, pools)
                              : prepare_prefix(D, bf16)) != cudaSuccess)
         return BSP_ERR_CUDA;
-    if (prepare_tail(D, bf16, graph ? plan->max_tail : plan->max_tail_len, Hq, pools) != cudaSuccess) return BSP_ERR_CUDA;
+    if (prepare_tail(D, bf16, graph ? plan->max_tail : plan->max_tail_len, Hq,
+                     static_cast<long long>(plan->batch) * plan->beam_width, plan->max_splits, pools) != cudaSuccess)
+        return BSP_ERR_CUDA;
     CUtensorMap tq, tk, tv;
     PrefixParams pp{};
     if (prefix) {
@@ -1296,8 +1299,8 @@ bsp_status attn_launches(const bsp_plan_t* plan, uint8_t* ws, const void* q, con
     if (!record(1)) return BSP_ERR_CUDA;
     // without timing events between them, the tail kernel overlaps the end of the prompt kernel
     if ((graph || plan->tail_requests > 0) &&
-        launch_tail(D, bf16, graph ? plan->max_tail : plan->max_tail_len, tp, prefix && events == nullptr, s, pools) !=
-            cudaSuccess)
+        launch_tail(D, bf16, graph ? plan->max_tail : plan->max_tail_len, tp, plan->max_splits,
+                    prefix && events == nullptr, s, pools) != cudaSuccess)
         return BSP_ERR_CUDA;
     if (!record(2)) return BSP_ERR_CUDA;
     return BSP_OK;

@@ -152,11 +152,13 @@ cudaError_t launch_prefix_blocks(int head_dim, bool bf16, int ctas, const CUtens
 // What a kernel's pools hold: elements of q's dtype, E4M3 bytes with one scale per tensor, or E4M3 bytes with block
 // scales.
 enum PoolKind { kPool16 = 0, kPoolE4m3 = 1, kPoolBlocks = 2 };
-cudaError_t prepare_tail(int head_dim, bool bf16, int max_tail_len, int num_q_heads, PoolKind pools = kPool16);
+// rows: beams of all requests; splits: the most partial states of a request (both choose among kernels of one result).
+cudaError_t prepare_tail(int head_dim, bool bf16, int max_tail_len, int num_q_heads, long long rows, int splits,
+                         PoolKind pools = kPool16);
 // after_prefix: the prompt kernel was the last launch on `stream`; the tail kernel is then a
 // programmatic dependent launch of it (it starts on SMs the prompt kernel has left, resolves and
 // prefetches its tail rows, and waits for the prompt kernel's partials before merging).
-cudaError_t launch_tail(int head_dim, bool bf16, int max_tail_len, const TailParams& p, bool after_prefix,
+cudaError_t launch_tail(int head_dim, bool bf16, int max_tail_len, const TailParams& p, int splits, bool after_prefix,
                         cudaStream_t stream, PoolKind pools = kPool16);
 // The alternating-tile prompt kernel (p.Wblk = beams per row block, p.bq = beams per quadrant). E4M3 pools:
 // tk, tv map one-byte elements without swizzle, boxes of min(page, 64) rows x head_dim bytes.

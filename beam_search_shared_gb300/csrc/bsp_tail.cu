@@ -93,7 +93,7 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 }  // namespace
 
 constexpr int kTailThreads = 128;
-constexpr int kFewMerge = 16, kMerge = 8, kRowMerge = 4;  // KB below: few CTAs, more, CTAs of whole rows
+constexpr int kFewMerge = 16, kMerge = 8, kRowMerge = 4;  // KB below (tail_choice_p)
 
 // MAXT: tail rows held in registers, the batch's longest tail rounded up to 2, 4 or 8.
 // MAXP: head passes whose tail state is held in registers across the wait for the prompt kernel
@@ -354,22 +354,6 @@ __global__ void __launch_bounds__(kTailThreads) tail_merge_kernel(TailParams p) 
     }
 }
 
-template <int D, bool BF16, int MAXT, int MAXP, int KB, PoolKind POOL>
-static cudaError_t launch_tail_k(const TailParams& p, bool after_prefix, int pass_ctas, cudaStream_t stream) {
-    const long long rows = static_cast<long long>(p.B) * p.W;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(rows), static_cast<unsigned>(pass_ctas));
-    cfg.blockDim = dim3(kTailThreads);
-    cfg.dynamicSmemBytes = 0;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = after_prefix ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, tail_merge_kernel<D, BF16, MAXT, MAXP, KB, POOL>, p);
-}
-
 // head passes of a 128-thread CTA: Hq / (4 warps x heads per warp pass)
 template <int D>
 static int tail_passes(int Hq) {
@@ -390,92 +374,88 @@ static int device_sms() {
     return cache[dev];
 }
 
+// The kernel for a launch, and its CTAs per row.
+struct TailChoice {
+    void (*kernel)(TailParams) = nullptr;
+    int pass_ctas = 1;
+};
+
 template <int D, bool BF16, int MAXT, PoolKind POOL>
-static cudaError_t launch_tail_p(const TailParams& p, bool after_prefix, cudaStream_t stream) {
-    const int passes = tail_passes<D>(p.Hq);
-    const long long rows = static_cast<long long>(p.B) * p.W;
-    // fewer rows than SMs: one CTA per (row, head pass), so a row's heads merge in parallel. With two CTAs an SM at
-    // most, registers are plenty, and each round over the partial states costs its latency: 16 in flight. 10000 keys
-    // of one request: 4 beams of 32 heads 32.9 us with 4 in flight, 26.2 with 8, 20.8 with 16, 96 beams of 16 heads
-    // 44.8, 37.0 and 31.0. More CTAs need the registers: 2 x 60 beams of 32 heads 39.9, 35.6 and 39.0.
+static TailChoice tail_choice_p(int Hq, long long rows, int splits) {
+    const int passes = tail_passes<D>(Hq);
+    // fewer rows than SMs: one CTA per (row, head pass), so a row's heads merge in parallel. With many splits each
+    // round over the partial states costs its latency, and with two CTAs an SM at most registers are plenty: 16 in
+    // flight. 10000 keys of one request: 4 beams of 32 heads 32.7 us with 4 in flight, 25.9 with 8, 20.7 with 16, 96
+    // beams of 16 heads 44.7, 36.9 and 31.0. More CTAs need the registers: 1 x 140 beams of 32 heads 56.8 with 4 and
+    // 55.3 with 8, 2 x 60 of 32 heads 39.9, 35.6 and (with 16) 39.0. Few splits leave the places empty, and CTAs of fewer
+    // registers start beside the prompt kernel: 10 x 30 beams of 8 heads over 300 keys (3 splits) 11.4 with 4, 12.6
+    // with 16; 3 x 96 of 16 heads of 64 over 5000 (8 splits) 28.1 and 26.0. So do CTAs of one pass for each of many
+    // rows: 64 x 60 beams of 4 heads of 256 31.4 with 4, 37.5 with 8.
     if (passes <= 1 || rows < device_sms()) {
-        if (rows * passes <= 2ll * device_sms())
-            return launch_tail_k<D, BF16, MAXT, 1, kFewMerge, POOL>(p, after_prefix, passes, stream);
-        return launch_tail_k<D, BF16, MAXT, 1, kMerge, POOL>(p, after_prefix, passes, stream);
+        if (splits > kRowMerge + 1) {  // (more than split 0 and one round)
+            if (rows * passes <= 2ll * device_sms()) return {tail_merge_kernel<D, BF16, MAXT, 1, kFewMerge, POOL>, passes};
+            if (passes > 1) return {tail_merge_kernel<D, BF16, MAXT, 1, kMerge, POOL>, passes};
+        }
+        return {tail_merge_kernel<D, BF16, MAXT, 1, kRowMerge, POOL>, passes};
     }
-    if (passes <= 2) return launch_tail_k<D, BF16, MAXT, 2, kRowMerge, POOL>(p, after_prefix, 1, stream);
-    return launch_tail_k<D, BF16, MAXT, 4, kRowMerge, POOL>(p, after_prefix, 1, stream);
+    if (passes <= 2) return {tail_merge_kernel<D, BF16, MAXT, 2, kRowMerge, POOL>, 1};
+    return {tail_merge_kernel<D, BF16, MAXT, 4, kRowMerge, POOL>, 1};
 }
 
 template <int D, bool BF16, PoolKind POOL>
-static cudaError_t launch_tail_t(const TailParams& p, int max_tail_len, bool after_prefix, cudaStream_t stream) {
-    const long long rows = static_cast<long long>(p.B) * p.W;
-    if (rows == 0) return cudaSuccess;
-    if (max_tail_len <= 2) return launch_tail_p<D, BF16, 2, POOL>(p, after_prefix, stream);
-    if (max_tail_len <= 4) return launch_tail_p<D, BF16, 4, POOL>(p, after_prefix, stream);
-    return launch_tail_p<D, BF16, 8, POOL>(p, after_prefix, stream);
+static TailChoice tail_choice_t(int max_tail_len, int Hq, long long rows, int splits) {
+    if (max_tail_len <= 2) return tail_choice_p<D, BF16, 2, POOL>(Hq, rows, splits);
+    if (max_tail_len <= 4) return tail_choice_p<D, BF16, 4, POOL>(Hq, rows, splits);
+    return tail_choice_p<D, BF16, 8, POOL>(Hq, rows, splits);
+}
+
+template <int D, PoolKind POOL>
+static TailChoice tail_choice_d(bool bf16, int max_tail_len, int Hq, long long rows, int splits) {
+    return bf16 ? tail_choice_t<D, true, POOL>(max_tail_len, Hq, rows, splits)
+                : tail_choice_t<D, false, POOL>(max_tail_len, Hq, rows, splits);
+}
+
+// E4M3 pools at head_dim 64 and 128 only
+static TailChoice tail_choice(int head_dim, bool bf16, int max_tail_len, int Hq, long long rows, int splits,
+                              PoolKind pools) {
+    switch (head_dim + pools) {
+        case 64 + kPool16: return tail_choice_d<64, kPool16>(bf16, max_tail_len, Hq, rows, splits);
+        case 64 + kPoolE4m3: return tail_choice_d<64, kPoolE4m3>(bf16, max_tail_len, Hq, rows, splits);
+        case 64 + kPoolBlocks: return tail_choice_d<64, kPoolBlocks>(bf16, max_tail_len, Hq, rows, splits);
+        case 128 + kPool16: return tail_choice_d<128, kPool16>(bf16, max_tail_len, Hq, rows, splits);
+        case 128 + kPoolE4m3: return tail_choice_d<128, kPoolE4m3>(bf16, max_tail_len, Hq, rows, splits);
+        case 128 + kPoolBlocks: return tail_choice_d<128, kPoolBlocks>(bf16, max_tail_len, Hq, rows, splits);
+        case 256 + kPool16: return tail_choice_d<256, kPool16>(bf16, max_tail_len, Hq, rows, splits);
+        default: return {};
+    }
 }
 
 // the same L1/shared split as the prompt kernel, so SMs are not reconfigured between the
 // kernels of a step
-template <int D, bool BF16, int MAXT, PoolKind POOL>
-static cudaError_t prepare_tail_p(int Hq) {
-    const cudaFuncAttribute a = cudaFuncAttributePreferredSharedMemoryCarveout;
-    const int passes = tail_passes<D>(Hq);
-    auto prepared = [&](auto kernel) { return cudaFuncSetAttribute(kernel, a, cudaSharedmemCarveoutMaxShared); };
-    // the one-pass variants also serve steps with fewer rows than SMs
-    cudaError_t e = prepared(tail_merge_kernel<D, BF16, MAXT, 1, kFewMerge, POOL>);
-    if (e == cudaSuccess) e = prepared(tail_merge_kernel<D, BF16, MAXT, 1, kMerge, POOL>);
-    if (e != cudaSuccess || passes <= 1) return e;
-    if (passes <= 2) return prepared(tail_merge_kernel<D, BF16, MAXT, 2, kRowMerge, POOL>);
-    return prepared(tail_merge_kernel<D, BF16, MAXT, 4, kRowMerge, POOL>);
+cudaError_t prepare_tail(int head_dim, bool bf16, int max_tail_len, int num_q_heads, long long rows, int splits,
+                         PoolKind pools) {
+    const TailChoice c = tail_choice(head_dim, bf16, max_tail_len, num_q_heads, rows, splits, pools);
+    if (!c.kernel) return cudaErrorInvalidValue;
+    return cudaFuncSetAttribute(c.kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
 }
 
-template <int D, bool BF16, PoolKind POOL>
-static cudaError_t prepare_tail_t(int max_tail_len, int Hq) {
-    if (max_tail_len <= 2) return prepare_tail_p<D, BF16, 2, POOL>(Hq);
-    if (max_tail_len <= 4) return prepare_tail_p<D, BF16, 4, POOL>(Hq);
-    return prepare_tail_p<D, BF16, 8, POOL>(Hq);
-}
-
-template <int D, PoolKind POOL>
-static cudaError_t prepare_tail_d(bool bf16, int max_tail_len, int Hq) {
-    return bf16 ? prepare_tail_t<D, true, POOL>(max_tail_len, Hq) : prepare_tail_t<D, false, POOL>(max_tail_len, Hq);
-}
-
-template <int D, PoolKind POOL>
-static cudaError_t launch_tail_d(bool bf16, int max_tail_len, const TailParams& p, bool after_prefix,
-                                 cudaStream_t stream) {
-    return bf16 ? launch_tail_t<D, true, POOL>(p, max_tail_len, after_prefix, stream)
-                : launch_tail_t<D, false, POOL>(p, max_tail_len, after_prefix, stream);
-}
-
-// E4M3 pools at head_dim 64 and 128 only
-cudaError_t prepare_tail(int head_dim, bool bf16, int max_tail_len, int num_q_heads, PoolKind pools) {
-    switch (head_dim + pools) {
-        case 64 + kPool16: return prepare_tail_d<64, kPool16>(bf16, max_tail_len, num_q_heads);
-        case 64 + kPoolE4m3: return prepare_tail_d<64, kPoolE4m3>(bf16, max_tail_len, num_q_heads);
-        case 64 + kPoolBlocks: return prepare_tail_d<64, kPoolBlocks>(bf16, max_tail_len, num_q_heads);
-        case 128 + kPool16: return prepare_tail_d<128, kPool16>(bf16, max_tail_len, num_q_heads);
-        case 128 + kPoolE4m3: return prepare_tail_d<128, kPoolE4m3>(bf16, max_tail_len, num_q_heads);
-        case 128 + kPoolBlocks: return prepare_tail_d<128, kPoolBlocks>(bf16, max_tail_len, num_q_heads);
-        case 256 + kPool16: return prepare_tail_d<256, kPool16>(bf16, max_tail_len, num_q_heads);
-        default: return cudaErrorInvalidValue;
-    }
-}
-
-cudaError_t launch_tail(int head_dim, bool bf16, int max_tail_len, const TailParams& p, bool after_prefix,
+cudaError_t launch_tail(int head_dim, bool bf16, int max_tail_len, const TailParams& p, int splits, bool after_prefix,
                         cudaStream_t stream, PoolKind pools) {
-    switch (head_dim + pools) {
-        case 64 + kPool16: return launch_tail_d<64, kPool16>(bf16, max_tail_len, p, after_prefix, stream);
-        case 64 + kPoolE4m3: return launch_tail_d<64, kPoolE4m3>(bf16, max_tail_len, p, after_prefix, stream);
-        case 64 + kPoolBlocks: return launch_tail_d<64, kPoolBlocks>(bf16, max_tail_len, p, after_prefix, stream);
-        case 128 + kPool16: return launch_tail_d<128, kPool16>(bf16, max_tail_len, p, after_prefix, stream);
-        case 128 + kPoolE4m3: return launch_tail_d<128, kPoolE4m3>(bf16, max_tail_len, p, after_prefix, stream);
-        case 128 + kPoolBlocks: return launch_tail_d<128, kPoolBlocks>(bf16, max_tail_len, p, after_prefix, stream);
-        case 256 + kPool16: return launch_tail_d<256, kPool16>(bf16, max_tail_len, p, after_prefix, stream);
-        default: return cudaErrorInvalidValue;
-    }
+    const long long rows = static_cast<long long>(p.B) * p.W;
+    const TailChoice c = tail_choice(head_dim, bf16, max_tail_len, p.Hq, rows, splits, pools);
+    if (!c.kernel) return cudaErrorInvalidValue;
+    if (rows == 0) return cudaSuccess;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(rows), static_cast<unsigned>(c.pass_ctas));
+    cfg.blockDim = dim3(kTailThreads);
+    cfg.dynamicSmemBytes = 0;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = after_prefix ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, c.kernel, p);
 }
 
 }  // namespace bsp

@@ -169,7 +169,8 @@ typedef struct bsp_plan_t {
                                     sets taking a unit's key tiles alternately (other decode steps at
                                     head_dim <= 128) */
     uint64_t off_cta;            /* byte offset of the per-CTA unit table */
-    uint64_t reserved;
+    int32_t max_splits;          /* the most prompt partial states of a request */
+    int32_t reserved;
 } bsp_plan_t;
 
 /* Human-readable name of a bsp_status value. Never NULL. */
