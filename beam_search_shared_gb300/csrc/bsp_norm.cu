@@ -24,7 +24,7 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 
-// Pairs of fp32, one instruction for both: the arithmetic of the rows is what bounds the larger steps.
+// Pairs of fp32, one instruction for both: norm and rotation are 9 of the 45 us of the largest steps (norm_append_kernel).
 using f2 = unsigned long long;
 __device__ __forceinline__ f2 pair(float x, float y) {
     f2 r;
@@ -480,10 +480,13 @@ __device__ __forceinline__ void run_rows(const NormAppendParams& p, int lead, in
 // run of one token (a decode step's) takes the same path, and finds its exponent by shuffles. The warps of a longer run
 // share its groups (run_rows). Nothing is shared between warps. Where a block's exponent grows, its rows before the
 // run are brought to the new one in place.
-// Bound by latency at a step's sizes (16 query and 8 K and V heads of 128: 4 tokens 2.6 us in a graph, the chain of
-// slot, position, angles and rows; 1920 tokens into 16-bit pools 7.8 us where the bytes take 4.6) and by the scattered
-// row writes at large ones (12288 tokens into 8-bit blocks 45 us, 26 for the bytes: writes of 128 bytes to rows of their
-// own run at about half of the copy rate, in bsp_append.cu too).
+// Times in a replayed graph, 16 query and 8 K and V heads of 128. Bound by latency at a step's sizes: 4 tokens 2.6 us, the
+// chain of slot, position, angles and rows; 1920 tokens into 16-bit pools 7.9 us where the bytes take 4.6, all CTAs
+// resident at once: K and V alone 4.6 (the plain append 4.1), without the rotation 6.7. Large ones have two parts: 12288
+// tokens into 8-bit blocks take 45 us, 26 for the bytes. K and V alone take 25, and the plain E4M3 append of the same
+// rows 24 (bsp_append.cu): writes of 128 bytes to pages of their own run at half of the copy rate. The query rows add
+// their bytes, and norm and rotation their instructions: without both it takes 35.5, K and V alone 21.
+// E4M3 pools with one scale: 12288 tokens 36.6 us, 3540 prompt tokens (32 query heads) 19.4.
 // Seven CTAs an SM: 1920 tokens 7.8 us, 12288 into blocks 44.8; six 9.0 and 45.3, eight 8.1 and 47.1 (spills).
 template <int D, bool BF16, int POOL>
 __global__ void __launch_bounds__(128, 7) norm_append_kernel(const NormAppendParams p) {
@@ -536,8 +539,9 @@ __global__ void __launch_bounds__(128, 7) norm_append_kernel(const NormAppendPar
 // tokens piece by piece, normalise and rotate their rows into shared memory (fp32) and find each run's largest
 // magnitude there; then the rows' codes follow. Each row is read and worked out once, and no CTA depends on another.
 // The query rows' CTAs are dealt between the others', which wait more than they move.
-// 3540 prompt tokens, 32 query and 8 K and V heads, blocks of 32: 27 us (12 for the bytes), 18 of them for K and V,
-// bound by the phases of a CTA one after another and a warp's chain for each of its tokens; runs by warps
+// 3540 prompt tokens, 32 query and 8 K and V heads, blocks of 32: 27 us (12 for the bytes), K and V alone 18 (12 without
+// norm and rotation, the plain E4M3 append 7), bound by the phases of a CTA one after another and a warp's chain for each
+// of its tokens; runs by warps
 // (norm_append_kernel), which read and normalise their rows twice, took 41. Windows of 16 tokens 34 us, four warps 38,
 // sixteen 33.
 constexpr int kWindow = 32;

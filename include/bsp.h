@@ -401,9 +401,11 @@ BSP_API bsp_status bsp_rope_append_kv_fp8(const bsp_plan_t* plan, const bsp_rope
  * value rounded once. Kinds:
  *   BSP_ROPE_LINEAR  theta_j / factor (position interpolation)
  *   BSP_ROPE_BASE    a base of base * factor^(rotary_dim / (rotary_dim - 2)); rotary_dim > 2
- *   BSP_ROPE_BANDS   by the turns t_j = original_positions * theta_j / (2 pi) that a pair makes over the trained length:
- *                    theta_j * ((1 - s) / factor + s), s = clamp((t_j - low) / (high - low), 0, 1)
- *   BSP_ROPE_RAMP    by the pair's index (Peng et al., YaRN, section 3.2): theta_j / factor * s + theta_j * (1 - s),
+ *   BSP_ROPE_BANDS   by the turns t_j = original_positions * theta_j / (2 pi) that a pair makes over the trained length
+ *                    (as Peng et al., YaRN, section 3.2): theta_j * ((1 - s) / factor + s),
+ *                    s = clamp((t_j - low) / (high - low), 0, 1)
+ *   BSP_ROPE_RAMP    by the pair's index, linear between the indices of the two turns, rounded outwards (the form that
+ *                    implementations of YaRN use): theta_j / factor * s + theta_j * (1 - s),
  *                    s = clamp((j - lo) / max(hi - lo, 0.001), 0, 1) with i(t) = rotary_dim * ln(original_positions /
  *                    (2 pi t)) / (2 ln base), lo = max(floor(i(high)), 0), hi = min(ceil(i(low)), rotary_dim - 1)
  * factor > 0, amplitude > 0 finite; BANDS and RAMP: original_positions > 0 and 0 < low < high, finite (not read
